@@ -1,73 +1,785 @@
-// kda_paged_attention.cu -- attention of new tokens over a paged cache.
+// kda_paged_attention.cu -- attention of new tokens over a paged cache, on
+// the tcgen05 tensor cores.
 //
-// One warp per (token, query head) walks the token's keys with the running
-// maximum and sum of a softmax: lanes hold D / 32 channels each.
+//   o = softmax(scale q K^T, causal from the cache's end) V
+//
+// Tiles. The query heads of one key/value head share its keys, so their rows
+// (token, head of the group) fill one 128-row tile: a decode step of a
+// grouped head reads K and V once for the whole group, and a chunk of tokens
+// fills the tensor cores' 128 rows. Keys come in tiles of 128: S = Q K^T and
+// O += P V are 128 x 128 x D and 128 x D x 128 products with fp32 sums in
+// TMEM; P goes back to TMEM as bf16 over its own S and is the A operand of
+// the second product from there.
+//
+// Two streams. Even and odd key tiles of a segment go to two warpgroups, each
+// with its own S, running maximum, sum and O: while one forms its
+// probabilities (a thread owns a row) the tensor cores run the other's
+// products. The two are joined once, at the end. A row's O is rescaled
+// only when its maximum has grown by more than 2^8 (probabilities then stay
+// below 2^8, far inside bf16's and fp32's range; the division by the sum
+// takes the factor out).
+//
+// Split. A call's work is counted in key tiles over all (sequence, key/value
+// head, row tile) items, and each CTA takes an equal run of them, cutting
+// items where the runs end: ragged lengths, one long sequence and many short
+// ones all load every SM alike. An item cut over several CTAs leaves its
+// parts (maximum, sum, O in fp32) in the workspace; the CTA that finishes
+// last adds them in the order of the keys, so the result does not depend on
+// which one it was.
+//
+// Loads. One warp fetches K and V by TMA into a ring of 128-row slots, in the
+// order the products need them and across item ends. A copy stays inside a
+// page: boxes of gcd(page_size, 128) rows. Rows past what an item sees are
+// masked out of S by selection and set to zero in V, so stale cache rows (NaN
+// among them) have no part in the result.
+//
+// Bound: decode steps by HBM (K and V once), chunks by the exponentials and
+// the tensor cores: a 128 x 128 tile takes about 1024 cycles of either.
+#include <math.h>
+
 #include "kda_paged.cuh"
+#include "kda_tc_common.cuh"
 
 namespace kda {
+namespace tc {
+
+// 64 consecutive 32-bit columns of the thread's TMEM lane, complete on return.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,"
+      "%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+        "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+}
+// Another 32 of them.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// Stores 32 consecutive 32-bit columns of the thread's TMEM lane (tmem_st_wait completes it).
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+        "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// D (+)= A B, kind::f16: A (16-bit, two K elements a 32-bit column) from TMEM.
+__device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(id), "r"(acc));
+}
+// TMA: a 4-D tile (channel, head, row of the page, page).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+}  // namespace tc
+
 namespace {
 
-template <int D>
-__global__ void __launch_bounds__(128) kda_paged_attention_kernel(const PagedArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t job = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (job >= a.S * a.Hq) return;
-  const int64_t tok = job / a.Hq;
-  const int h = static_cast<int>(job % a.Hq), hk = h / (a.Hq / a.Hkv);
-  int n = 0, bad = a.cu[0] != 0 || a.cu[a.N] != a.S;
-  for (int i = lane; i < a.N; i += 32) {
-    n += a.cu[i + 1] <= tok;
-    bad |= a.cu[i + 1] < a.cu[i];
+using namespace tc;
+
+constexpr int kRows = 128;               // query rows of an item, keys of a tile
+constexpr int kSoftmaxWarps = 8;         // two warpgroups
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kThreads = 320;
+constexpr int kMaxCtas = 152;            // one per SM
+constexpr int kMinTiles = 2;             // key tiles that are worth a CTA of their own
+constexpr int kRingBytes = 6 * 32768;    // K and V slots
+constexpr float kRescale = 8.f;          // log2 growth of a maximum that rescales O
+
+// One item's part that a CTA works on.
+struct Segment {
+  int n, hk, mt;      // sequence, key/value head, row tile
+  int j0, j1;         // key tiles [j0, j1); j0 == j1: no key is seen
+  int tiles;          // of the whole item (0: none)
+  int rows;           // rows of the tile in use
+  int lo, L;          // first token and number of tokens of the sequence
+  int seen;           // keys that the tile's last row sees
+  int first;          // keys that token 0 of the sequence sees (may be <= 0)
+};
+
+// Walks a CTA's segments; every role keeps its own copy.
+struct Walk {
+  const PagedArgs* a;
+  int64_t left;       // tiles of the run that remain (an empty item counts as one)
+  int n, hk, mt, j;   // next item and its first tile
+  int lo, L, len;     // of sequence n
+  int group;
+
+  __device__ __forceinline__ int row_tiles() const { return (L * group + kRows - 1) / kRows; }
+  __device__ __forceinline__ int seen_of(int m) const {
+    const int last = min((m + 1) * kRows, L * group) - 1;
+    return max(len - L + last / group + 1, 0);
   }
-  n = __reduce_add_sync(~0u, n);
-  bad = __reduce_or_sync(~0u, bad);
-  __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(a.o) + job * D + lane * E;
-  bool ok = !bad && n < a.N;
-  int64_t keys = 0;
-  if (ok) {
-    keys = static_cast<int64_t>(a.lens[n]) - (a.cu[n + 1] - tok) + 1;
-    ok = a.lens[n] >= 0 && a.lens[n] <= static_cast<int64_t>(a.width) * a.page;
+  __device__ __forceinline__ int tiles_of(int m) const { return (seen_of(m) + kRows - 1) / kRows; }
+  __device__ __forceinline__ void sequence(int i) {
+    n = i;
+    lo = a->cu[i];
+    L = a->cu[i + 1] - lo;
+    len = a->lens[i];
+    if (len < 0 || static_cast<int64_t>(len) > static_cast<int64_t>(a->width) * a->page) len = 0;
   }
-  if (!ok && lane == 0) set_status(a.status, KDA_ERR_DEVICE_CHECK);
-  float q[E], acc[E], m = -INFINITY, l = 0.f;
-  for (int i = 0; i < E; ++i) {
-    q[i] = ldf(static_cast<const __nv_bfloat16*>(a.q) + job * D + lane * E + i) * a.scale;
-    acc[i] = 0.f;
+  __device__ __forceinline__ int64_t head_tiles() const {  // one key/value head of the sequence
+    int64_t t = 0;
+    for (int m = 0, e = row_tiles(); m < e; ++m) t += max(tiles_of(m), 1);
+    return t;
   }
-  for (int64_t t = 0; ok && t < keys; ++t) {
-    const int64_t page = a.table[static_cast<int64_t>(n) * a.width + t / a.page];
-    if (page < 0 || page >= a.pages) {
-      if (lane == 0) set_status(a.status, KDA_ERR_DEVICE_CHECK);
-      l = 0.f;
+  __device__ bool next(Segment& s) {
+    if (left <= 0) return false;
+    while (mt >= row_tiles()) {  // past the sequence's last row tile
+      mt = 0;
+      if (++hk >= a->Hkv || L == 0) {
+        hk = 0;
+        if (n + 1 >= a->N) return false;
+        sequence(n + 1);
+      }
+    }
+    s.n = n; s.hk = hk; s.mt = mt; s.lo = lo; s.L = L;
+    s.tiles = tiles_of(mt);
+    s.seen = seen_of(mt);
+    s.first = len - L + 1;
+    s.rows = min(kRows, L * group - mt * kRows);
+    const int weight = max(s.tiles, 1);
+    const int take = static_cast<int>(min(static_cast<int64_t>(weight - j), left));
+    s.j0 = min(j, s.tiles);
+    s.j1 = min(j + take, s.tiles);
+    left -= take;
+    j += take;
+    if (j >= weight) {
+      j = 0;
+      ++mt;
+    }
+    return true;
+  }
+};
+
+struct Shared {
+  uint64_t full[12], empty[12];       // ring slots
+  uint64_t s_full[2], p_ready[2];     // per stream
+  uint64_t q_ready, done, drain;
+  uint32_t tmem;
+  int abort_, last;
+  int bad_page[16];                   // of the last 16 segments
+  int64_t sum[kThreads / 32];
+  int64_t run, total, start_base;
+  int start_n;
+  int bad;
+  float m[2][kRows], l[2][kRows];
+};
+
+struct Parts {        // the workspace behind the status header
+  uint32_t* count;    // [kMaxCtas] parts of a cut item that are done, by the CTA of its first part
+  float* ml;          // [2 * kMaxCtas][2][kRows]
+  float* o;           // [2 * kMaxCtas][kRows][D]
+  int* bad;           // [2 * kMaxCtas]
+};
+constexpr size_t kCountBytes = 1024, kBadBytes = 2048;
+static_assert(kMaxCtas * 4 <= kCountBytes && 2 * kMaxCtas * 4 <= kBadBytes, "");
+__host__ __device__ inline Parts parts_of(void* scratch) {
+  Parts p;
+  p.count = static_cast<uint32_t*>(scratch);
+  p.bad = reinterpret_cast<int*>(static_cast<char*>(scratch) + kCountBytes);
+  p.ml = reinterpret_cast<float*>(static_cast<char*>(scratch) + kCountBytes + kBadBytes);
+  p.o = p.ml + 2 * kMaxCtas * 2 * kRows;
+  return p;
+}
+
+// Bounded wait; false when it ran out (the CTA's abort flag is then set) or
+// another role gave up. After an abort every role still walks through its
+// segments and barriers, but issues no copy and no product any more.
+__device__ __forceinline__ bool wait(Shared* sh, uint64_t* bar, uint32_t parity, int* status) {
+  const uint32_t at = smem_addr(bar);
+  for (int it = 0; it < (1 << 22); ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((it & 15) == 15 && *const_cast<volatile int*>(&sh->abort_)) return false;
+  }
+  *const_cast<volatile int*>(&sh->abort_) = 1;
+  set_status(status, KDA_ERR_TIMEOUT);
+  return false;
+}
+
+// Waits, at most so long, without giving up.
+__device__ __forceinline__ void settle(uint64_t* bar, uint32_t parity) {
+  const uint32_t at = smem_addr(bar);
+  for (int it = 0; it < (1 << 20); ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (ok) return;
+  }
+}
+
+// wait() of a whole warp, with one answer.
+__device__ __forceinline__ bool wait_warp(Shared* sh, uint64_t* bar, uint32_t parity, int* status) {
+  return __all_sync(~0u, wait(sh, bar, parity, status));
+}
+
+// Every CTA adds up the call's tiles and finds the start of its run.
+__device__ void plan(const PagedArgs& a, Shared* sh, Walk& w) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.N + kThreads - 1) / kThreads;
+  const int n0 = min(tid * per, a.N), n1 = min(n0 + per, a.N);
+  int bad = 0;
+  int64_t mine = 0;
+  for (int n = n0; n < n1; ++n) {
+    const int lo = a.cu[n], hi = a.cu[n + 1], len = a.lens[n];
+    if (lo < 0 || hi < lo || hi > a.S || (n == 0 && lo != 0) || (n == a.N - 1 && hi != a.S)) {
+      bad = 1;
       break;
     }
-    const int64_t at = ((page * a.page + t % a.page) * a.Hkv + hk) * D + lane * E;
-    float s = 0.f;
-    for (int i = 0; i < E; ++i) s += q[i] * ldf(static_cast<const __nv_bfloat16*>(a.k) + at + i);
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s), f = mn == m ? 1.f : expf(m - mn), p = s == -INFINITY ? 0.f : expf(s - mn);
-    m = mn;
-    l = l * f + p;
-    for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + p * ldf(static_cast<const __nv_bfloat16*>(a.v) + at + i);
+    if ((len < 0 || static_cast<int64_t>(len) > static_cast<int64_t>(a.width) * a.page) && blockIdx.x == 0)
+      set_status(a.status, KDA_ERR_DEVICE_CHECK);
+    w.sequence(n);
+    mine += w.head_tiles() * a.Hkv;
   }
-  for (int i = 0; i < E; ++i) stf(o + i, l == 0.f ? 0.f : acc[i] / l);
+  bad = __syncthreads_or(bad);
+  int64_t upto = mine;  // inclusive sum over the threads of the warp, then over the warps
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int64_t t = __shfl_up_sync(~0u, upto, m);
+    if (lane >= m) upto += t;
+  }
+  if (lane == 31) sh->sum[warp] = upto;
+  __syncthreads();
+  int64_t total = 0;
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) upto += sh->sum[i];
+    total += sh->sum[i];
+  }
+  int64_t run = (total + gridDim.x - 1) / gridDim.x;
+  if (run < kMinTiles) run = kMinTiles;
+  if (bad) total = 0;
+  const int64_t start = static_cast<int64_t>(blockIdx.x) * run;
+  if (start < total && start >= upto - mine && start < upto) {
+    int64_t base = upto - mine;
+    for (int n = n0; n < n1; ++n) {
+      w.sequence(n);
+      const int64_t t = w.head_tiles() * a.Hkv;
+      if (start < base + t) {
+        sh->start_n = n;
+        sh->start_base = base;
+        break;
+      }
+      base += t;
+    }
+  }
+  if (tid == 0) {
+    sh->run = run;
+    sh->total = total;
+    if (bad && blockIdx.x == 0) set_status(a.status, KDA_ERR_DEVICE_CHECK);
+  }
+  __syncthreads();
+  w.left = total - start < run ? total - start : run;
+  if (w.left <= 0) return;
+  w.sequence(sh->start_n);
+  int64_t rest = start - sh->start_base;
+  const int64_t head = w.head_tiles();
+  w.hk = static_cast<int>(rest / head);
+  rest -= w.hk * head;
+  w.mt = 0;
+  for (int t; rest >= (t = max(w.tiles_of(w.mt), 1)); ++w.mt) rest -= t;
+  w.j = static_cast<int>(rest);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    kda_paged_attention_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap,
+                               const __grid_constant__ CUtensorMap vmap, const int box, const float sc,
+                               const uint32_t keep, const uint32_t sign) {
+  constexpr int kSlot = kRows * D * 2;       // bytes of a ring slot
+  constexpr int kSlots = kRingBytes / kSlot;  // 6 at D = 128, 12 at D = 64
+  constexpr int kHalf = kRows * 128;          // bytes of a 64-channel block
+  extern __shared__ __align__(1024) uint8_t ring[];
+  uint8_t* const qtile = ring + kRingBytes;
+  Shared* const sh = reinterpret_cast<Shared*>(qtile + kSlot);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = a.Hq / a.Hkv;
+
+  if (smem_addr(ring) & 1023) {  // the swizzle needs it; no static shared memory comes before the ring
+    if (tid == 0) set_status(a.status, KDA_ERR_DEVICE_CHECK);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->s_full[i], 1);
+      mbar_init(&sh->p_ready[i], 4);
+    }
+    mbar_init(&sh->q_ready, kSoftmaxWarps);
+    mbar_init(&sh->done, 1);
+    mbar_init(&sh->drain, 1);
+    sh->abort_ = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) tmem_alloc(&sh->tmem, 512);
+  Walk w{};
+  w.a = &a;
+  w.group = group;
+  plan(a, sh, w);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = sh->tmem;
+  const uint32_t tmem_s = tmem, tmem_o = tmem + 256;  // S (P over it) of stream i at + 128 i, O at + 128 i
+  Segment s;
+
+  if (warp == kLoadWarp) {
+    // ---- loads: lane i copies box i of a tile ----
+    const int boxes = kRows / box;
+    int64_t pos = 0;  // slots used so far
+    auto page_of = [&](const Segment& g, int j) {
+      const int64_t t = static_cast<int64_t>(j) * kRows + lane * box;
+      return lane < boxes && j < g.j1 && t < g.seen ? a.table[static_cast<int64_t>(g.n) * a.width + t / a.page] : 0;
+    };
+    bool ok = true;
+    auto copy = [&](const CUtensorMap* map, const Segment& g, int j, int page) {
+      const int slot = static_cast<int>(pos % kSlots);
+      const int64_t turn = pos / kSlots;
+      if (turn > 0) ok = ok && wait_warp(sh, &sh->empty[slot], static_cast<uint32_t>((turn - 1) & 1), a.status);
+      if (!ok) return;
+      ++pos;
+      const int t = j * kRows + lane * box;
+      const int here = min(boxes, (g.seen - j * kRows + box - 1) / box);  // boxes with a key that is seen
+      if (lane == 0) mbar_expect_tx(&sh->full[slot], static_cast<uint32_t>(here * box * D * 2));
+      __syncwarp();
+      if (lane < here) {
+        const uint32_t dst = smem_addr(ring) + slot * kSlot + lane * box * 128;
+#pragma unroll
+        for (int x = 0; x < D; x += 64)
+          tma_load_4d(dst + (x / 64) * kHalf, map, x, g.hk, t % a.page, page, &sh->full[slot]);
+      }
+    };
+    for (uint32_t seg = 0; w.next(s);) {
+      if (s.j0 == s.j1) continue;
+      int* const flag = &sh->bad_page[seg++ & 15];
+      // a page outside the cache is recorded, and the item's rows become zero (the copy itself writes zeros)
+      auto check = [&](int page, int j) {
+        if (lane < boxes && j < s.j1 && j * kRows + lane * box < s.seen && (page < 0 || page >= a.pages)) {
+          *const_cast<volatile int*>(flag) = 1;
+          set_status(a.status, KDA_ERR_DEVICE_CHECK);
+        }
+      };
+      int cur = page_of(s, s.j0), nxt = page_of(s, s.j0 + 1);
+      if (lane == 0) *const_cast<volatile int*>(flag) = 0;
+      __syncwarp();
+      check(cur, s.j0);
+      copy(&kmap, s, s.j0, cur);
+      for (int j = s.j0; j < s.j1; ++j) {
+        check(nxt, j + 1);
+        if (j + 1 < s.j1) copy(&kmap, s, j + 1, nxt);
+        copy(&vmap, s, j, cur);
+        cur = nxt;
+        nxt = page_of(s, j + 2);
+      }
+    }
+    // after an abort: the copies in flight land before the CTA ends
+    if (!ok)
+      for (int64_t p = pos > kSlots ? pos - kSlots : 0; p < pos; ++p)
+        settle(&sh->full[p % kSlots], static_cast<uint32_t>((p / kSlots) & 1));
+  } else if (warp == kMmaWarp) {
+    // ---- products: one thread issues QK(0), QK(1), then PV(j), QK(j + 2) ----
+    if (lane == 0) {
+      constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // bf16 A and B
+      constexpr uint32_t id_qk = idesc(kRows, kRows) | kBf16, id_pv = idesc(kRows, D, false, true) | kBf16;
+      const uint32_t q0 = smem_addr(qtile), r0 = smem_addr(ring);
+      int64_t pos = 0;
+      uint32_t turn_p[2] = {0, 0};
+      uint32_t turn = 0;
+      bool ok = true;
+      auto qk = [&](int i) {
+        const int slot = static_cast<int>(pos % kSlots);
+        ok = ok && wait(sh, &sh->full[slot], static_cast<uint32_t>((pos / kSlots) & 1), a.status);
+        if (!ok) return;
+        ++pos;
+        fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma(tmem_s + 128 * (i & 1), desc_kmajor(q0, kRows, 0, k), desc_kmajor(r0 + slot * kSlot, kRows, 0, k), id_qk,
+              k > 0);
+        mma_commit(&sh->empty[slot]);
+        mma_commit(&sh->s_full[i & 1]);
+      };
+      while (ok && w.next(s)) {
+        const int nt = s.j1 - s.j0;
+        if (nt == 0) continue;
+        ok = wait(sh, &sh->q_ready, turn++ & 1, a.status);
+        if (!ok) break;
+        fence_after_sync();
+        qk(0);
+        if (nt > 1) qk(1);
+        for (int i = 0; ok && i < nt; ++i) {
+          const int st = i & 1, slot = static_cast<int>(pos % kSlots);
+          ok = wait(sh, &sh->p_ready[st], turn_p[st]++ & 1, a.status) &&
+               wait(sh, &sh->full[slot], static_cast<uint32_t>((pos / kSlots) & 1), a.status);
+          if (!ok) break;
+          ++pos;
+          fence_after_sync();
+#pragma unroll
+          for (int k = 0; k < kRows / 16; ++k)
+            mma_ta(tmem_o + 128 * st, tmem_s + 128 * st + 8 * k, desc_mnmajor(r0 + slot * kSlot, kHalf, k), id_pv,
+                   (i > 1 || k > 0) ? 1u : 0u);
+          mma_commit(&sh->empty[slot]);
+          if (i + 2 < nt) qk(i + 2);
+        }
+        if (ok) mma_commit(&sh->done);
+      }
+      // nothing of this thread may be in flight when TMEM is freed
+      mma_commit(&sh->drain);
+      settle(&sh->drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax: thread = row, warpgroup = stream ----
+    const int st = warp >> 2, row = tid & 127;
+    const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
+    const uint32_t my_s = tmem_s + 128 * st + lane_base;
+    const uint32_t my_o = tmem_o + 128 * st + lane_base;
+    uint32_t turn_s = 0, turn_d = 0;
+    int64_t pos0 = 0;  // ring position of the segment's first slot
+    const Parts parts = parts_of(a.scratch);
+    uint32_t seg = 0;
+    while (w.next(s)) {
+      const int nt = s.j1 - s.j0;
+      const int at = s.mt * kRows + row;  // row of the sequence: token * group + head
+      const bool used = row < s.rows;
+      const int token = at / group, head = s.hk * group + at % group;
+      __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o) +
+                                 (static_cast<int64_t>(s.lo + token) * a.Hq + head) * D;
+      if (nt == 0) {  // nothing to see for any row of the tile
+        if (used)
+          for (int c = st * (D / 2); c < (st + 1) * (D / 2); c += 8)
+            *reinterpret_cast<uint4*>(out + c) = make_uint4(0u, 0u, 0u, 0u);
+        continue;
+      }
+      const int limit = used ? s.first + token : 0;  // keys this row sees
+      {
+        // Q rows into the tile, 16-byte chunks in the 128-byte swizzle; this
+        // warpgroup's half of the channels
+        if (used) {
+          const uint4* const src = reinterpret_cast<const uint4*>(
+              static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(s.lo + token) * a.Hq + head) * D);
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint4 x = src[st * (D / 16) + c];
+            x.x = (x.x & keep) ^ sign; x.y = (x.y & keep) ^ sign; x.z = (x.z & keep) ^ sign; x.w = (x.w & keep) ^ sign;
+            *reinterpret_cast<uint4*>(qtile + sw128_chunk(row, st * (D / 16) + c, kRows)) = x;
+          }
+        }
+        fence_async_smem();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->q_ready);
+      }
+      float m = -INFINITY, l = 0.f;
+      const bool warp_used = (row & ~31) < s.rows;
+      for (int i = st; i < nt; i += 2) {
+        wait_warp(sh, &sh->s_full[st], turn_s++ & 1, a.status);
+        fence_after_sync();
+        const int k0 = (s.j0 + i) * kRows;
+        if (k0 + kRows > s.seen) {
+          // keys past what any row of the tile sees: V rows to zero (their
+          // probabilities are zero, but zero times a stale NaN is not)
+          const int64_t vpos = pos0 + (i + 1 < nt ? 2 * i + 2 : 2 * nt - 1);
+          const int slot = static_cast<int>(vpos % kSlots);
+          const bool here = wait_warp(sh, &sh->full[slot], static_cast<uint32_t>((vpos / kSlots) & 1), a.status);
+          if (here && k0 + row >= s.seen) {
+            uint8_t* const v = ring + slot * kSlot + row * 128;
+#pragma unroll
+            for (int c = 0; c < D * 2; c += 16)
+              *reinterpret_cast<uint4*>(v + (c / 128) * kHalf + c % 128) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_async_smem();
+        }
+        if (warp_used) {
+          // The row is read twice, half by half (its maximum, then its
+          // probabilities), so that a thread never holds all 128 scores.
+          uint32_t x[64];
+          const int open = limit - k0;  // keys of the tile that the row sees
+          const bool masked = __any_sync(~0u, open < kRows);
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tmem_ld(my_s + 64 * h, x);
+            if (masked) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                if (64 * h + c >= open) x[c] = 0xff800000u;  // -inf
+            }
+#pragma unroll
+            for (int c = 0; c < 64; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(x[c]));
+          }
+          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          const float mn = mx * sc;
+          const bool grow = mn > m + kRescale;  // m = -inf: any finite maximum
+          if (__any_sync(~0u, grow)) {
+            const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - mn)) : 1.f;
+            if (grow) m = mn;
+            l *= f;
+            if (i >= 2) {  // the stream's O exists, and is complete: S of this tile was issued after it
+#pragma unroll
+              for (int c = 0; c < D; c += 32) {
+                uint32_t y[32];
+                tmem_ld(my_o + c, y);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+                tmem_st(my_o + c, y);
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t p[32];
+            tmem_ld(my_s + 64 * h, x);
+            if (masked) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                if (64 * h + c >= open) x[c] = 0xff800000u;
+            }
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              const float e0 = ex2(fmaf(__uint_as_float(x[c]), sc, -ref));
+              const float e1 = ex2(fmaf(__uint_as_float(x[c + 1]), sc, -ref));
+              sum[c / 2 & 1] += e0;
+              sum[2 + (c / 2 & 1)] += e1;
+              p[c / 2] = pack_bf16(e0, e1);
+            }
+            tmem_st(my_s + 32 * h, p);  // over the half of S that is read by now
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+        }
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->p_ready[st]);
+      }
+      wait_warp(sh, &sh->done, turn_d++ & 1, a.status);
+      fence_after_sync();
+      // join the two streams: this warpgroup writes its half of the channels
+      sh->m[st][row] = m;
+      sh->l[st][row] = l;
+      named_bar_sync(1, 256);
+      const float m0 = sh->m[0][row], m1 = sh->m[1][row];
+      const float mm = fmaxf(m0, m1);
+      const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - mm), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - mm);
+      const float ll = sh->l[0][row] * f0 + sh->l[1][row] * f1;
+      const bool whole = nt == s.tiles;
+      const int bad = *const_cast<volatile int*>(&sh->bad_page[seg++ & 15]);
+      const int part = 2 * static_cast<int>(blockIdx.x) + (s.j0 == 0 ? 1 : 0);
+      const float inv = whole ? (ll == 0.f || bad ? 0.f : 1.f / ll) : 1.f;
+      if (warp_used) {
+#pragma unroll
+        for (int c = st * (D / 2); c < (st + 1) * (D / 2); c += 32) {
+          uint32_t x[32], y[32];
+          tmem_ld(tmem_o + lane_base + c, x);
+          if (nt > 1) tmem_ld(tmem_o + 128 + lane_base + c, y);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            // a stream without a key of this row: its O holds nothing to add
+            float v = m0 == -INFINITY ? 0.f : __uint_as_float(x[k]) * f0;
+            if (nt > 1 && m1 != -INFINITY) v = fmaf(__uint_as_float(y[k]), f1, v);
+            x[k] = __float_as_uint(inv == 0.f ? 0.f : v * inv);
+          }
+          if (used && whole) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              uint4 o;
+              o.x = pack_bf16(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+              o.y = pack_bf16(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+              o.z = pack_bf16(__uint_as_float(x[k + 4]), __uint_as_float(x[k + 5]));
+              o.w = pack_bf16(__uint_as_float(x[k + 6]), __uint_as_float(x[k + 7]));
+              *reinterpret_cast<uint4*>(out + c + k) = o;
+            }
+          } else if (used) {
+            float* const po = parts.o + (static_cast<int64_t>(part) * kRows + row) * D + c;
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<uint4*>(po + k) = make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+          }
+        }
+      }
+      pos0 += 2 * nt;
+      if (!whole) {
+        if (st == 0 && used) {
+          parts.ml[part * 2 * kRows + row] = mm;
+          parts.ml[part * 2 * kRows + kRows + row] = ll;
+        }
+        if (tid == 0) parts.bad[part] = bad;
+        // The CTAs of this item: the run that holds its first tile, and those after it.
+        const int64_t run_end = min((static_cast<int64_t>(blockIdx.x) + 1) * sh->run, sh->total);
+        const int64_t item0 = run_end - w.left - s.j1, item1 = item0 + s.tiles;
+        const int c0 = static_cast<int>(item0 / sh->run), c1 = static_cast<int>((item1 - 1) / sh->run);
+        __threadfence();
+        named_bar_sync(1, 256);
+        if (tid == 0) {
+          __threadfence();
+          sh->last = atomicAdd(&parts.count[c0], 1u) == static_cast<uint32_t>(c1 - c0);
+          __threadfence();
+        }
+        named_bar_sync(1, 256);
+        if (sh->last) {
+          __threadfence();
+          // parts c0 (its slot 1) .. c1 (their slot 0), in the order of the keys
+          int any = 0;
+          for (int c = c0; c <= c1; ++c) any |= __ldcg(&parts.bad[2 * c + (c == c0)]);
+          if (st == 0 && used) {
+            float top = -INFINITY, sum = 0.f;
+            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(&parts.ml[(2 * c + (c == c0)) * 2 * kRows + row]));
+            for (int c = c0; c <= c1; ++c) {
+              const float* const q = &parts.ml[(2 * c + (c == c0)) * 2 * kRows + row];
+              const float pm = __ldcg(q);
+              sum += __ldcg(q + kRows) * (pm == -INFINITY ? 0.f : ex2(pm - top));
+            }
+            sh->m[0][row] = top;
+            sh->l[0][row] = sum == 0.f || any ? 0.f : 1.f / sum;
+          }
+          named_bar_sync(1, 256);
+          for (int e = tid; e < s.rows * (D / 8); e += 256) {
+            const int r = e / (D / 8), c8 = e % (D / 8) * 8;
+            const float top = sh->m[0][r], scale = sh->l[0][r];
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            for (int c = c0; c <= c1; ++c) {
+              const int p = 2 * c + (c == c0);
+              const float pm = __ldcg(&parts.ml[p * 2 * kRows + r]);
+              if (pm == -INFINITY) continue;
+              const float f = ex2(pm - top);
+              const float4* const q = reinterpret_cast<const float4*>(parts.o + (static_cast<int64_t>(p) * kRows + r) * D + c8);
+              const float4 x = __ldcg(q), y = __ldcg(q + 1);
+              v[0] = fmaf(x.x, f, v[0]); v[1] = fmaf(x.y, f, v[1]); v[2] = fmaf(x.z, f, v[2]); v[3] = fmaf(x.w, f, v[3]);
+              v[4] = fmaf(y.x, f, v[4]); v[5] = fmaf(y.y, f, v[5]); v[6] = fmaf(y.z, f, v[6]); v[7] = fmaf(y.w, f, v[7]);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = scale == 0.f ? 0.f : v[k] * scale;
+            const int ar = s.mt * kRows + r;
+            __nv_bfloat16* const po = static_cast<__nv_bfloat16*>(a.o) +
+                                      (static_cast<int64_t>(s.lo + ar / group) * a.Hq + s.hk * group + ar % group) * D + c8;
+            *reinterpret_cast<uint4*>(po) =
+                make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+          }
+        }
+      }
+      // O, m and l are read: the next segment may start
+      named_bar_sync(1, 256);
+    }
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<EncodeFn>(p)
+               : nullptr;
+  }();
+  return fn;
+}
+
+// Pages [pages][page][Hkv][D]; box: 64 channels of one head, `box` rows of one page.
+bool page_map(CUtensorMap* m, const void* base, const PagedArgs& a, int box) {
+  const EncodeFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.Hkv, (cuuint64_t)a.page, (cuuint64_t)a.pages};
+  const cuuint64_t row = (cuuint64_t)a.D * 2;
+  const cuuint64_t strides[3] = {row, row * a.Hkv, row * a.Hkv * a.page};
+  const cuuint32_t boxes[4] = {64, 1, (cuuint32_t)box, 1}, ones[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, boxes, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const PagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, int box, int ctas, cudaStream_t s) {
+  const size_t smem = kRingBytes + kRows * D * 2 + sizeof(Shared);
+  auto* const kernel = kda_paged_attention_kernel<D>;
+  static const cudaError_t set =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (set != cudaSuccess) return set;
+  // Exponentials are taken in base 2. sc > 0, so that masked scores stay -inf:
+  // a negative scale moves to the queries' sign, a scale of 0 to zero queries.
+  float sc = fabsf(a.scale) * 1.4426950408889634f;
+  const uint32_t keep = sc > 0.f ? ~0u : 0u, sign = a.scale < 0.f ? 0x80008000u : 0u;
+  if (!(sc > 0.f)) sc = 1.f;
+  kernel<<<ctas, kThreads, smem, s>>>(a, k, v, box, sc, keep, sign);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t paged_attention_scratch_bytes(const PagedArgs&) { return 0; }
+size_t paged_attention_scratch_bytes(const PagedArgs& a) {
+  return kCountBytes + kBadBytes + sizeof(float) * 2 * kMaxCtas * kRows * (2 + a.D);
+}
 
 kda_status launch_paged_attention(const PagedArgs& a, cudaStream_t s) {
-  cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(int), s);
-  const unsigned grid = static_cast<unsigned>((a.S * a.Hq + 3) / 4);
-  if (e == cudaSuccess) {
-    if (a.D == 128)
-      kda_paged_attention_kernel<128><<<grid, 128, 0, s>>>(a);
-    else
-      kda_paged_attention_kernel<64><<<grid, 128, 0, s>>>(a);
-    e = cudaGetLastError();
-  }
+  int box = kRows;
+  while (a.page % box) box /= 2;  // the largest power of two up to 128 that divides the page: at least 8
+  CUtensorMap k, v;
+  if (!page_map(&k, a.k, a, box) || !page_map(&v, a.v, a, box))
+    return set_error(KDA_ERR_CUDA, "the tensor maps of the cache could not be made");
+  static const int sms = [] {
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n;
+  }();
+  // the status word and the counters that follow it
+  cudaError_t e = cudaMemsetAsync(a.status, 0, kHeaderBytes + kCountBytes, s);
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  if (e == cudaSuccess) e = a.D == 128 ? launch<128>(a, k, v, box, ctas, s) : launch<64>(a, k, v, box, ctas, s);
   return e == cudaSuccess ? KDA_OK : set_error(KDA_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
 }
 

@@ -26,9 +26,10 @@ def check(x, ref, bar, what):
     fine = torch.isfinite(ref)
     assert torch.equal(torch.isfinite(got), fine), f"{what}: not finite in other places"
     rms = ref[fine].pow(2).mean().sqrt() if fine.any() else torch.tensor(0.0)
-    over = (got - ref).abs() - half_ulp(ref, x.dtype) - (bar if torch.is_tensor(bar) else bar * rms)
+    bar = bar if torch.is_tensor(bar) else bar * rms
+    # the computed value, up to ``bar`` from ref, is what is rounded: half an ulp of the largest it may be
+    over = (got - ref).abs() - half_ulp(ref.abs() + bar, x.dtype) - bar
     worst = over[fine].max().item() if fine.any() else 0.0
-    # a value that rounds across a power of two has the larger ulp of the two
     assert worst <= 1e-6 * rms + 1e-30, f"{what}: {worst:.3e} over the bar (RMS {rms:.3e})"
 
 
@@ -130,9 +131,10 @@ def attention(q, k_pages, v_pages, table, lens, cu, scale):
 
 
 def attention_bar(size):
-    """Probabilities are rounded to bf16 (2^-9 relative each); scores and sums
-    are fp32 (below 2^-15 of a probability for the sizes tested)."""
-    return size * (2.0 ** -9 + 2.0 ** -14)
+    """Probabilities are rounded to bf16 (8 significant bits: 2^-8 of each at
+    most); scores and sums are fp32 (below 2^-15 of a probability for the
+    sizes tested)."""
+    return size * (2.0 ** -8 + 2.0 ** -14)
 
 
 def cu_of(lengths):

@@ -1,6 +1,6 @@
 """The paged cache: append and attention against float64 softmax attention.
 
-Bars (tests/_serving_ref.py attention_bar): 2^-9 of sum p |v| for the bf16
+Bars (tests/_serving_ref.py attention_bar): 2^-8 of sum p |v| for the bf16
 probabilities, and the output's own rounding."""
 import pytest
 import torch
