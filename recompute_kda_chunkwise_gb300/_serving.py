@@ -52,19 +52,31 @@ def library():
 check = _kda._check
 
 
-def ptr(t):
-    return None if t is None else t.data_ptr()
+# The raw handle of the current stream of a device index: these calls take a
+# few microseconds on the GPU, so their host side is kept as short.
+stream = torch._C._cuda_getCurrentRawStream
 
 
-def stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+def off(t, dtype, device, shape) -> bool:
+    """Whether ``t`` is not the contiguous tensor of ``dtype`` and ``shape`` on
+    CUDA device ``device`` (an index) that the kernels index."""
+    return t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous()
+
+
+def refuse(named, dtype, device, shape):
+    """Raises for the first of the (name, tensor) pairs that is off()."""
+    shape = tuple(shape)
+    for name, t in named:
+        if device < 0 or off(t, dtype, device, shape):
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {shape}"
+                             f"{f' on cuda:{device}' if device >= 0 else ''} (got {t.dtype} {tuple(t.shape)} on "
+                             f"{t.device}{'' if t.is_contiguous() else ', strided'})")
 
 
 def need(t, name, shape, dtype, device):
-    """A tensor the kernels index by ``shape``: contiguous, on ``device``."""
-    if t.dtype != dtype or t.device != device or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {shape} on {device} "
-                         f"(got {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', strided'})")
+    """The address of a tensor the kernels index by ``shape``."""
+    if device < 0 or off(t, dtype, device, shape):
+        refuse(((name, t),), dtype, device, shape)
     return t.data_ptr()
 
 

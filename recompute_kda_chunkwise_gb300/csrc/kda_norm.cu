@@ -54,44 +54,114 @@ template <>
 struct alignas(16) Raw<float, 4> {
   float4 u;
 };
-template <typename T, int V>
-__device__ __forceinline__ void unpack(const Raw<T, V>& r, float (&x)[V]) {
-#pragma unroll
-  for (int i = 0; i < V; ++i) x[i] = ldf(&r.x[i]);
+// Arithmetic on the values of a vector: pairs where V is even (one
+// instruction for two fp32 operations), single values otherwise.
+struct F2 {
+  uint64_t u;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.u) : "f"(x), "f"(y));
+  return r;
 }
-__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 8>& r, float (&x)[8]) {
+__device__ __forceinline__ float2 both(F2 p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p.u));
+  return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+  return r;
+}
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float sum(F2 a) { return both(a).x + both(a).y; }
+__device__ __forceinline__ float sum(float a) { return a; }
+template <int V>
+struct PackOf {
+  using type = F2;
+  static constexpr int n = V / 2;
+  static __device__ __forceinline__ F2 all(float x) { return f2(x, x); }
+};
+template <>
+struct PackOf<1> {
+  using type = float;
+  static constexpr int n = 1;
+  static __device__ __forceinline__ float all(float x) { return x; }
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw<T, 1>& r, float (&x)[1]) {
+  x[0] = ldf(&r.x[0]);
+}
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 8>& r, F2 (&x)[4]) {
   const uint32_t u[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = f2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
 }
-__device__ __forceinline__ void unpack(const Raw<float, 4>& r, float (&x)[4]) {
-  x[0] = r.u.x; x[1] = r.u.y; x[2] = r.u.z; x[3] = r.u.w;
+__device__ __forceinline__ void unpack(const Raw<float, 4>& r, F2 (&x)[2]) {
+  x[0] = f2(r.u.x, r.u.y);
+  x[1] = f2(r.u.z, r.u.w);
 }
-template <typename T, int V>
-__device__ __forceinline__ void put(T* p, const float (&x)[V]) {
-#pragma unroll
-  for (int i = 0; i < V; ++i) stf(p + i, x[i]);
+template <typename T>
+__device__ __forceinline__ void put(T* p, const float (&x)[1]) {
+  stf(p, x[0]);
 }
-__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&x)[8]) {
+__device__ __forceinline__ void put(__nv_bfloat16* p, const F2 (&x)[4]) {
   uint32_t u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    __nv_bfloat162 t = __float22bfloat162_rn(both(x[i]));
     u[i] = *reinterpret_cast<uint32_t*>(&t);
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ void put(float* p, const float (&x)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+__device__ __forceinline__ void put(float* p, const F2 (&x)[2]) {
+  const float2 a = both(x[0]), b = both(x[1]);
+  *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
 }
-template <int V>
-__device__ __forceinline__ void weights(const float* w, int c, int width, float (&x)[V]) {
+// Weights c .. c + V - 1 (c < width; 1 without weights).
+__device__ __forceinline__ void weights(const float* w, int c, float (&x)[1]) { x[0] = w ? w[c] : 1.f; }
+template <int N>
+__device__ __forceinline__ void weights(const float* w, int c, F2 (&x)[N]) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) x[i] = (w && c < width) ? w[c + i] : 1.f;
+  for (int i = 0; i < N; i += 2) {
+    const float4 t = w ? *reinterpret_cast<const float4*>(w + c + 2 * i) : make_float4(1.f, 1.f, 1.f, 1.f);
+    x[i] = f2(t.x, t.y);
+    x[i + 1] = f2(t.z, t.w);
+  }
 }
+
+// A thread's weights: in registers for all its rows where it holds one vector
+// of a row (read every row they cost the L1 more than the row itself: 4 bytes
+// an element against 2), from L1 each time where it holds more.
+template <int V, int NV, int G>
+struct Weights {
+  using F = typename PackOf<V>::type;
+  static constexpr bool kKept = V > 1 && NV == 1;
+  const float* w;
+  int c0;
+  F kept[kKept ? PackOf<V>::n : 1];
+  __device__ __forceinline__ Weights(const float* p, int lane, int width) : w(p), c0(lane * V) {
+    if constexpr (kKept) {
+      if (c0 < width) weights(w, c0, kept);
+    }
+  }
+  __device__ __forceinline__ void get(int j, F (&x)[PackOf<V>::n]) const {
+    if constexpr (kKept) {
+#pragma unroll
+      for (int i = 0; i < PackOf<V>::n; ++i) x[i] = kept[i];
+    } else {
+      weights(w, c0 + j * G * V, x);
+    }
+  }
+};
 
 // Sums of N values over a group of G threads (G <= 32: lanes; else the whole
 // CTA of G threads, through `sh`, whose halves alternate so that one barrier
@@ -122,78 +192,172 @@ __device__ __forceinline__ void group_sum(float (&x)[N], float* sh, int& turn) {
   }
 }
 
+// sigmoid(z) and sigmoid(-z) from one exponential of -|z| (at most 1: neither
+// overflows, and neither is a difference that cancels).
+__device__ __forceinline__ void gate(float z, float& s, float& n) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(z) * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  const float er = e * r;
+  s = z < 0.f ? er : r;
+  n = z < 0.f ? r : er;
+}
+__device__ __forceinline__ void gate(F2 z, F2& s, F2& n) {
+  const float2 t = both(z);
+  float2 a, b;
+  gate(t.x, a.x, b.x);
+  gate(t.y, a.y, b.y);
+  s = f2(a.x, a.y);
+  n = f2(b.x, b.y);
+}
+
+// How a thread gets its share of its group's rows. 16-byte vectors go by
+// asynchronous copies, up to four rows ahead, into a ring of shared memory
+// in which a thread reads only what it copied itself: the rows ahead hold no
+// registers and need no barrier. Single elements (odd widths) are loaded when
+// their row's turn comes. Tensors that are absent are not read.
+enum Which { kY, kZ, kDho, kH, kDn };  // a backward without the next norm has no kH, kDn; a forward the first two and kH
+template <typename T, int V, int NV, int G, int NT, int SLOTS>
+struct Rows {
+  static constexpr int kStage = SLOTS * NV * NT * 16;  // bytes
+  static constexpr int kFit = 200 * 1024 / kStage;
+  static constexpr int kDepth = V == 1 ? 1 : (kFit < 4 ? kFit : 4);
+  static constexpr size_t kBytes = V == 1 ? 0 : static_cast<size_t>(kDepth) * kStage;
+  static_assert(kDepth >= 1, "");
+  const NormArgs& a;
+  const void* const (&from)[SLOTS];
+  uint8_t* ring;
+  int64_t step, ahead;  // rows between two turns; the next row to copy
+  int in, out;          // ring positions
+  int lane;
+  Raw<T, V> direct[V == 1 ? SLOTS : 1][V == 1 ? NV : 1];
+
+  __device__ __forceinline__ Rows(const NormArgs& args, const void* const (&f)[SLOTS], uint8_t* sm, int64_t row,
+                                  int64_t st, int ln)
+      : a(args), from(f), ring(sm), step(st), ahead(row), in(0), out(kDepth - 1), lane(ln) {
+    if constexpr (V > 1)
+      for (int i = 0; i + 1 < kDepth; ++i) copy();
+  }
+  __device__ __forceinline__ void copy() {
+    if (ahead < a.rows) {
+      const int64_t base = ahead * a.width;
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s)
+        if (from[s])
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            const int c = (j * G + lane) * V;
+            if (c < a.width) {
+              const uint32_t dst =
+                  static_cast<uint32_t>(__cvta_generic_to_shared(ring + in * kStage + ((s * NV + j) * NT + threadIdx.x) * 16));
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                           "l"(static_cast<const T*>(from[s]) + base + c)
+                           : "memory");
+            }
+          }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ahead += step;
+    if (++in == kDepth) in = 0;
+  }
+  // The next row of this group is at hand afterwards.
+  __device__ __forceinline__ void turn() {
+    if constexpr (V > 1) {
+      copy();
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+      if (++out == kDepth) out = 0;
+    } else {
+      if (ahead < a.rows) {
+        const int64_t base = ahead * a.width;
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+          if (from[s])
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+              if (j * G + lane < a.width) direct[s][j].x[0] = static_cast<const T*>(from[s])[base + j * G + lane];
+      }
+      ahead += step;
+    }
+  }
+  __device__ __forceinline__ Raw<T, V> get(int s, int j) const {
+    if constexpr (V > 1)
+      return *reinterpret_cast<const Raw<T, V>*>(ring + out * kStage + ((s * NV + j) * NT + threadIdx.x) * 16);
+    else
+      return direct[s][j];
+  }
+};
+
 template <typename T, int V, int NV, int G, int NT>
 __global__ void __launch_bounds__(NT) norm_fwd_kernel(const NormArgs a) {
-  constexpr int kGroups = NT / G;
+  using P = PackOf<V>;
+  using F = typename P::type;
+  constexpr int kGroups = NT / G, NP = P::n;
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float sh[2 * 3 * 32];
   int turn = 0;
   const int lane = static_cast<int>(threadIdx.x) % G;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / G;
   const float inv = 1.f / static_cast<float>(a.width);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / G;
+  const Weights<V, NV, G> wpost(a.wpost, lane, a.width), wpre(a.wpre, lane, a.width);
+  const void* const from[3] = {a.y, a.z, a.h};
+  Rows<T, V, NV, G, NT, 3> in(a, from, ring, row, step, lane);
   // every group of a CTA makes the same number of turns (the reductions are collective)
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGroups; r0 < a.rows;
-       r0 += static_cast<int64_t>(gridDim.x) * kGroups) {
-    const int64_t row = r0 + (first - static_cast<int64_t>(blockIdx.x) * kGroups);
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGroups; r0 < a.rows; r0 += step, row += step) {
+    in.turn();
     const bool live = row < a.rows;
     const int64_t base = row * a.width;
-    Raw<T, V> ry[NV], rz[NV], rh[NV];
+    F x[NV][NP], hh = P::all(0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (live && (j * G + lane) * V < a.width) {
+        unpack(in.get(kY, j), x[j]);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) hh = fma(x[j][i], x[j][i], hh);
+      }
+    float yy[1] = {sum(hh)};
+    group_sum<G>(yy, sh, turn);
+    const F scale = P::all(rsqrtf(yy[0] * inv + a.eps) * a.b), keep = P::all(a.a);
+    hh = P::all(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * G + lane) * V;
       if (live && c < a.width) {
-        ry[j] = *reinterpret_cast<const Raw<T, V>*>(static_cast<const T*>(a.y) + base + c);
-        if (a.z) rz[j] = *reinterpret_cast<const Raw<T, V>*>(static_cast<const T*>(a.z) + base + c);
-        if (a.h) rh[j] = *reinterpret_cast<const Raw<T, V>*>(static_cast<const T*>(a.h) + base + c);
-      }
-    }
-    float x[NV][V], sum[1] = {0.f};
+        F w[NP], t[NP];
+        wpost.get(j, w);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool in = live && (j * G + lane) * V < a.width;
-      if (in) unpack(ry[j], x[j]);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (!in) x[j][i] = 0.f;
-        sum[0] += x[j][i] * x[j][i];
-      }
-    }
-    group_sum<G>(sum, sh, turn);
-    const float scale = rsqrtf(sum[0] * inv + a.eps) * a.b;
-    sum[0] = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * G + lane) * V;
-      if (live && c < a.width) {
-        float w[V], t[V];
-        weights(a.wpost, c, a.width, w);
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[j][i] *= scale * w[i];
+        for (int i = 0; i < NP; ++i) x[j][i] = mul(x[j][i], mul(scale, w[i]));
         if (a.z) {
-          unpack(rz[j], t);
+          unpack(in.get(kZ, j), t);
 #pragma unroll
-          for (int i = 0; i < V; ++i) x[j][i] *= sigmoidf_(t[i]);
+          for (int i = 0; i < NP; ++i) {
+            F s, n;
+            gate(t[i], s, n);
+            x[j][i] = mul(x[j][i], s);
+          }
         }
         if (a.h) {
-          unpack(rh[j], t);
+          unpack(in.get(2, j), t);
 #pragma unroll
-          for (int i = 0; i < V; ++i) x[j][i] = fmaf(a.a, t[i], x[j][i]);
+          for (int i = 0; i < NP; ++i) x[j][i] = fma(keep, t[i], x[j][i]);
         }
         put(static_cast<T*>(a.ho) + base + c, x[j]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum[0] += x[j][i] * x[j][i];
+        for (int i = 0; i < NP; ++i) hh = fma(x[j][i], x[j][i], hh);
       }
     }
     if (a.n) {
-      group_sum<G>(sum, sh, turn);
-      const float r = rsqrtf(sum[0] * inv + a.eps);
+      float two[1] = {sum(hh)};
+      group_sum<G>(two, sh, turn);
+      const F r = P::all(rsqrtf(two[0] * inv + a.eps));
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = (j * G + lane) * V;
         if (live && c < a.width) {
-          float w[V];
-          weights(a.wpre, c, a.width, w);
+          F w[NP];
+          wpre.get(j, w);
 #pragma unroll
-          for (int i = 0; i < V; ++i) x[j][i] *= r * w[i];
+          for (int i = 0; i < NP; ++i) x[j][i] = mul(x[j][i], mul(r, w[i]));
           put(static_cast<T*>(a.n) + base + c, x[j]);
         }
       }
@@ -201,179 +365,182 @@ __global__ void __launch_bounds__(NT) norm_fwd_kernel(const NormArgs a) {
   }
 }
 
-template <typename T, int V, int NV, int G, int NT>
-__global__ void __launch_bounds__(NT) norm_bwd_kernel(const NormArgs a) {
-  constexpr int kGroups = NT / G;
+// PRE: the next norm takes part (dn and w_pre are given).
+template <typename T, int V, int NV, int G, int NT, bool PRE>
+__global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_kernel(const NormArgs a) {
+  using P = PackOf<V>;
+  using F = typename P::type;
+  constexpr int kGroups = NT / G, NP = P::n;
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float sh[2 * 3 * 32];
   int turn = 0;
   const int lane = static_cast<int>(threadIdx.x) % G, group = static_cast<int>(threadIdx.x) / G;
   const float inv = 1.f / static_cast<float>(a.width);
-  float gpost[NV][V], gpre[NV][V];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+  const bool one = a.width == 1;
+  F gpost[NV][NP], gpre[PRE ? NV : 1][NP];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int i = 0; i < V; ++i) gpost[j][i] = gpre[j][i] = 0.f;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGroups; r0 < a.rows;
-       r0 += static_cast<int64_t>(gridDim.x) * kGroups) {
-    const int64_t row = r0 + group;
+    for (int i = 0; i < NP; ++i) gpost[j][i] = gpre[PRE ? j : 0][i] = P::all(0.f);
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + group;
+  const Weights<V, NV, G> wpost(a.wpost, lane, a.width), wpre(PRE ? a.wpre : nullptr, lane, a.width);
+  constexpr int kSlots = PRE ? 5 : 3;
+  const void* const all[5] = {a.y, a.z, a.dho, a.h, a.dn};
+  const void* const(&from)[kSlots] = reinterpret_cast<const void* const(&)[kSlots]>(all);
+  Rows<T, V, NV, G, NT, kSlots> in(a, from, ring, row, step, lane);
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGroups; r0 < a.rows; r0 += step, row += step) {
+    in.turn();
     const bool live = row < a.rows;
     const int64_t base = row * a.width;
-    Raw<T, V> ry[NV], rz[NV], rh[NV], ro[NV], rn[NV];
-    auto load = [&](const void* p, int c) {
-      return *reinterpret_cast<const Raw<T, V>*>(static_cast<const T*>(p) + base + c);
-    };
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * G + lane) * V;
-      if (live && c < a.width) {
-        ry[j] = load(a.y, c);
-        if (a.z) rz[j] = load(a.z, c);
-        if (a.h) rh[j] = load(a.h, c);
-        if (a.dho) ro[j] = load(a.dho, c);
-        if (a.dn) rn[j] = load(a.dn, c);
-      }
-    }
-    float s1[1] = {0.f};
+    auto here = [&](int j) { return live && (j * G + lane) * V < a.width; };
+    F yt = P::all(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (live && (j * G + lane) * V < a.width) {
-        float y[V];
-        unpack(ry[j], y);
+      if (here(j)) {
+        F y[NP];
+        unpack(in.get(kY, j), y);
 #pragma unroll
-        for (int i = 0; i < V; ++i) s1[0] += y[i] * y[i];
+        for (int i = 0; i < NP; ++i) yt = fma(y[i], y[i], yt);
       }
-    group_sum<G>(s1, sh, turn);
-    const float iy = rsqrtf(s1[0] * inv + a.eps);
-    float ih = 0.f, proj = 0.f;
-    auto hidden = [&](int j, int c, float (&hp)[V]) {  // h' of this thread's vector j
-      float t[V], w[V];
-      unpack(ry[j], hp);
-      weights(a.wpost, c, a.width, w);
-#pragma unroll
-      for (int i = 0; i < V; ++i) hp[i] *= iy * a.b * w[i];
-      if (a.z) {
-        unpack(rz[j], t);
-#pragma unroll
-        for (int i = 0; i < V; ++i) hp[i] *= sigmoidf_(t[i]);
-      }
-      if (a.h) {
-        unpack(rh[j], t);
-#pragma unroll
-        for (int i = 0; i < V; ++i) hp[i] = fmaf(a.a, t[i], hp[i]);
-      }
-    };
-    if (a.dn) {
-      float s2[2] = {0.f, 0.f};
+    float yy[1] = {sum(yt)};
+    group_sum<G>(yy, sh, turn);
+    const float iy = rsqrtf(yy[0] * inv + a.eps);
+    // yn, the gates and what follows from them are formed again in each stage
+    // from the row at hand: registers, not instructions, limit the warps here.
+    F hp[PRE ? NV : 1][NP];  // h'
+    F hh = P::all(0.f), hd = P::all(0.f);
+    if constexpr (PRE) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = (j * G + lane) * V;
-        if (live && c < a.width) {
-          float hp[V], d[V], w[V];
-          hidden(j, c, hp);
-          unpack(rn[j], d);
-          weights(a.wpre, c, a.width, w);
+        if (here(j)) {
+          F t[NP], w[NP];
+          unpack(in.get(kY, j), t);
+          wpost.get(j, w);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            s2[0] += hp[i] * hp[i];
-            s2[1] += hp[i] * d[i] * w[i];
+          for (int i = 0; i < NP; ++i) hp[j][i] = mul(mul(t[i], P::all(iy * a.b)), w[i]);
+          if (a.z) {
+            unpack(in.get(kZ, j), t);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+              F s, n;
+              gate(t[i], s, n);
+              hp[j][i] = mul(hp[j][i], s);
+            }
+          }
+          if (a.h) {
+            unpack(in.get(kH, j), t);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) hp[j][i] = fma(P::all(a.a), t[i], hp[j][i]);
+          }
+          unpack(in.get(kDn, j), t);
+          wpre.get(j, w);
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            hh = fma(hp[j][i], hp[j][i], hh);
+            hd = fma(hp[j][i], mul(t[i], w[i]), hd);
           }
         }
       }
-      group_sum<G>(s2, sh, turn);
-      ih = rsqrtf(s2[0] * inv + a.eps);
-      proj = s2[1] * inv * ih * ih;  // mean(d hn) rh
     }
-    float s3[1] = {0.f};
-    float q[NV][V];  // du, the gradient of u, until dy is formed
+    F ih = P::all(0.f), dk = ih, dp = ih;  // dh' = dh_out + dk d - dp h'
+    if constexpr (PRE) {
+      float two[2] = {sum(hh), sum(hd)};
+      group_sum<G>(two, sh, turn);
+      const float r = rsqrtf(two[0] * inv + a.eps);
+      ih = P::all(r);
+      dk = P::all(r * (one ? a.eps * r * r : 1.f));
+      dp = P::all(one ? 0.f : -(r * r * r) * (two[1] * inv));
+    }
+    F ty = P::all(0.f);
+    F q[NV][NP];  // the gradient of yn, until dy is formed
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * G + lane) * V;
-      if (live && c < a.width) {
-        float D[V], y[V], w[V];
+      if (here(j)) {
+        F d[NP], w[NP], t[NP];
         if (a.dho)
-          unpack(ro[j], D);
+          unpack(in.get(kDho, j), d);
         else
 #pragma unroll
-          for (int i = 0; i < V; ++i) D[i] = 0.f;
-        if (a.dn) {
-          float hp[V], d[V];
-          hidden(j, c, hp);
-          unpack(rn[j], d);
-          weights(a.wpre, c, a.width, w);
+          for (int i = 0; i < NP; ++i) d[i] = P::all(0.f);
+        if constexpr (PRE) {
+          unpack(in.get(kDn, j), t);
+          wpre.get(j, w);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            gpre[j][i] += d[i] * hp[i] * ih;
-            const float dw = d[i] * w[i];
-            D[i] += ih * (a.width == 1 ? dw * (a.eps * ih * ih) : dw - hp[i] * proj);
+          for (int i = 0; i < NP; ++i) {
+            gpre[j][i] = fma(t[i], mul(hp[j][i], ih), gpre[j][i]);
+            d[i] = fma(hp[j][i], dp, fma(mul(t[i], w[i]), dk, d[i]));
           }
         }
         if (a.dh) {
-          float t[V];
 #pragma unroll
-          for (int i = 0; i < V; ++i) t[i] = a.a * D[i];
+          for (int i = 0; i < NP; ++i) t[i] = mul(P::all(a.a), d[i]);
           put(static_cast<T*>(a.dh) + base + c, t);
         }
-        unpack(ry[j], y);
-        weights(a.wpost, c, a.width, w);
-        if (a.z) {
-          float z[V], t[V];
-          unpack(rz[j], z);
+        F yn[NP];
+        unpack(in.get(kY, j), yn);
+        wpost.get(j, w);
+        F z[NP];
+        if (a.z) unpack(in.get(kZ, j), z);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float sg = sigmoidf_(z[i]), du = a.b * D[i];
-            t[i] = du * (y[i] * iy) * w[i] * (sg * sigmoidf_(-z[i]));
-            q[j][i] = du * sg;
-          }
-          put(static_cast<T*>(a.dz) + base + c, t);
-        } else {
-#pragma unroll
-          for (int i = 0; i < V; ++i) q[j][i] = a.b * D[i];
+        for (int i = 0; i < NP; ++i) {
+          F sg = P::all(1.f), sn = sg;
+          if (a.z) gate(z[i], sg, sn);
+          yn[i] = mul(yn[i], P::all(iy));
+          const F du = mul(d[i], mul(sg, P::all(a.b)));
+          gpost[j][i] = fma(du, yn[i], gpost[j][i]);
+          q[j][i] = mul(du, w[i]);
+          ty = fma(q[j][i], yn[i], ty);
+          z[i] = mul(mul(q[j][i], yn[i]), sn);
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          gpost[j][i] += q[j][i] * (y[i] * iy);
-          q[j][i] *= w[i];
-          s3[0] += q[j][i] * (y[i] * iy);
-        }
+        if (a.z) put(static_cast<T*>(a.dz) + base + c, z);
       }
     }
-    group_sum<G>(s3, sh, turn);
-    const float m = s3[0] * inv;
+    float two[1] = {sum(ty)};
+    group_sum<G>(two, sh, turn);
+    const F yk = P::all(iy * (one ? a.eps * iy * iy : 1.f)), yp = P::all(one ? 0.f : -iy * iy * (two[0] * inv));
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * G + lane) * V;
-      if (live && c < a.width) {
-        float y[V];
-        unpack(ry[j], y);
+    for (int j = 0; j < NV; ++j)
+      if (here(j)) {
+        F y[NP];
+        unpack(in.get(kY, j), y);
 #pragma unroll
-        for (int i = 0; i < V; ++i) q[j][i] = iy * (a.width == 1 ? q[j][i] * (a.eps * iy * iy) : q[j][i] - (y[i] * iy) * m);
-        put(static_cast<T*>(a.dy) + base + c, q[j]);
+        for (int i = 0; i < NP; ++i) q[j][i] = fma(y[i], yp, mul(q[j][i], yk));
+        put(static_cast<T*>(a.dy) + base + (j * G + lane) * V, q[j]);
       }
-    }
   }
   // This CTA's share of the weight gradients: its groups' sums, in order.
+  // (Without dn, w_pre's gradient is zero: gpre was never added to.)
   if (!a.part) return;
-  extern __shared__ float acc[];  // [groups][G * NV * V], only where a CTA has several groups
+  float* const acc = reinterpret_cast<float*>(ring);  // [groups][G * NV * V], where a CTA has several groups
+  if constexpr (kGroups > 1) __syncthreads();         // every group is done with the ring
   const int64_t half = static_cast<int64_t>(gridDim.x) * a.width;
   float* const out = a.part + static_cast<int64_t>(blockIdx.x) * a.width;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     if ((which == 0 ? a.wpost : a.wpre) == nullptr) continue;
-    if constexpr (kGroups == 1) {
+    constexpr int W = G * NV * V;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * G + lane) * V;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int c = (j * G + lane) * V + i;
-          if (c < a.width) out[which * half + c] = which == 0 ? gpost[j][i] : gpre[j][i];
+      for (int i = 0; i < V; ++i) {
+        float v;
+        if constexpr (V == 1) {
+          v = which == 0 ? gpost[j][0] : gpre[PRE ? j : 0][0];
+        } else {
+          const float2 t = both(which == 0 ? gpost[j][i / 2] : gpre[PRE ? j : 0][i / 2]);
+          v = i % 2 ? t.y : t.x;
         }
-    } else {
-      constexpr int W = G * NV * V;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          acc[group * W + (j * G + lane) * V + i] = which == 0 ? gpost[j][i] : gpre[j][i];
+        if constexpr (kGroups > 1)
+          acc[group * W + c + i] = v;
+        else if (c < a.width)
+          out[which * half + c + i] = v;
+      }
+    }
+    if constexpr (kGroups > 1) {
       __syncthreads();
       for (int c = static_cast<int>(threadIdx.x); c < a.width; c += NT) {
         float t = 0.f;
@@ -405,15 +572,28 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* part, in
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// CTAs of a launch: what the SMs hold at once (the loop takes the rest).
+// CTAs that the SMs hold at once (a launch's loop takes the rest of the rows), at most `most`.
 template <typename K>
-int grid_of(K kernel, int threads, size_t smem, int64_t blocks, int most) {
+int64_t resident(K kernel, int threads, size_t smem, int most) {
   int dev = 0, sms = 0, per = 0;
+  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
-  const int64_t fit = static_cast<int64_t>(sms) * (per < 1 ? 1 : per);
-  return static_cast<int>(blocks < fit ? blocks : (fit < most ? fit : most));
+  const int fit = (sms < 1 ? 1 : sms) * (per < 1 ? 1 : per);
+  return fit < most ? fit : most;
+}
+
+template <typename T, int V, int NV, int G, int NT, bool PRE>
+void run_bwd(const NormArgs& a, int64_t blocks, float* dpost, float* dpre, cudaStream_t s) {
+  auto k = norm_bwd_kernel<T, V, NV, G, NT, PRE>;
+  constexpr size_t rows = Rows<T, V, NV, G, NT, PRE ? 5 : 3>::kBytes, sums = NT / G > 1 ? sizeof(float) * NT * NV * V : 0;
+  constexpr size_t smem = rows > sums ? rows : sums;
+  static const int64_t fit = resident(k, NT, smem, kMaxCtas);
+  const int grid = static_cast<int>(blocks < fit ? blocks : fit);
+  k<<<grid, NT, smem, s>>>(a);
+  if (a.part)
+    norm_weight_kernel<<<dim3((a.width + 31) / 32, 2), dim3(32, 32), 0, s>>>(a.part, grid, a.width, dpost, dpre);
 }
 
 template <typename T, int V, int NV, int G, int NT>
@@ -421,14 +601,13 @@ kda_status run(const NormArgs& a, bool bwd, float* dpost, float* dpre, cudaStrea
   const int64_t blocks = ceil_div(a.rows, NT / G);
   if (!bwd) {
     auto k = norm_fwd_kernel<T, V, NV, G, NT>;
-    k<<<grid_of(k, NT, 0, blocks, 1 << 30), NT, 0, s>>>(a);
+    constexpr size_t smem = Rows<T, V, NV, G, NT, 3>::kBytes;
+    static const int64_t fit = resident(k, NT, smem, 1 << 30);
+    k<<<static_cast<int>(blocks < fit ? blocks : fit), NT, smem, s>>>(a);
+  } else if (a.dn) {
+    run_bwd<T, V, NV, G, NT, true>(a, blocks, dpost, dpre, s);
   } else {
-    auto k = norm_bwd_kernel<T, V, NV, G, NT>;
-    const size_t smem = NT / G > 1 && a.part ? sizeof(float) * NT * NV * V : 0;
-    const int grid = grid_of(k, NT, smem, blocks, kMaxCtas);
-    k<<<grid, NT, smem, s>>>(a);
-    if (a.part)
-      norm_weight_kernel<<<dim3((a.width + 31) / 32, 2), dim3(32, 32), 0, s>>>(a.part, grid, a.width, dpost, dpre);
+    run_bwd<T, V, NV, G, NT, false>(a, blocks, dpost, dpre, s);
   }
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? KDA_OK : set_error(KDA_ERR_CUDA, "block norm launch failed: %s", cudaGetErrorString(e));

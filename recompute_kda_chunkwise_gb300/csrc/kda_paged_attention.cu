@@ -27,11 +27,12 @@
 // last adds them in the order of the keys, so the result does not depend on
 // which one it was.
 //
-// Loads. One warp fetches K and V by TMA into a ring of 128-row slots, in the
-// order the products need them and across item ends. A copy stays inside a
-// page: boxes of gcd(page_size, 128) rows. Rows past what an item sees are
-// masked out of S by selection and set to zero in V, so stale cache rows (NaN
-// among them) have no part in the result.
+// Loads. One warp fetches K and one V, by TMA into a ring of 128-row slots
+// each, ahead of the products and across item ends. A copy stays inside a
+// page: boxes of gcd(page_size, 128) rows, whose pages a warp looks up 32 at a
+// time, a batch ahead. Rows past what an item sees are masked out of S by
+// selection and set to zero in V, so stale cache rows (NaN among them) have no
+// part in the result.
 //
 // Bound: decode steps by HBM (K and V once), chunks by the exponentials and
 // the tensor cores: a 128 x 128 tile takes about 1024 cycles of either.
@@ -102,6 +103,27 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
       : "memory");
 }
+// Two fp32 operations at once.
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(x));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -114,11 +136,11 @@ using namespace tc;
 
 constexpr int kRows = 128;               // query rows of an item, keys of a tile
 constexpr int kSoftmaxWarps = 8;         // two warpgroups
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;  // kLoadWarp: K, the one after it: V
+constexpr int kThreads = 352;
 constexpr int kMaxCtas = 152;            // one per SM
 constexpr int kMinTiles = 2;             // key tiles that are worth a CTA of their own
-constexpr int kRingBytes = 6 * 32768;    // K and V slots
+constexpr int kRingBytes = 6 * 32768;    // K slots, then V slots
 constexpr float kRescale = 8.f;          // log2 growth of a maximum that rescales O
 
 // One item's part that a CTA works on.
@@ -188,7 +210,7 @@ struct Walk {
 };
 
 struct Shared {
-  uint64_t full[12], empty[12];       // ring slots
+  uint64_t full[2][6], empty[2][6];   // ring slots of K, of V
   uint64_t s_full[2], p_ready[2];     // per stream
   uint64_t q_ready, done, drain;
   uint32_t tmem;
@@ -330,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                const __grid_constant__ CUtensorMap vmap, const int box, const float sc,
                                const uint32_t keep, const uint32_t sign) {
   constexpr int kSlot = kRows * D * 2;       // bytes of a ring slot
-  constexpr int kSlots = kRingBytes / kSlot;  // 6 at D = 128, 12 at D = 64
+  constexpr int kSlots = kRingBytes / kSlot / 2;  // of K, and of V: 3 at D = 128, 6 at D = 64
   constexpr int kHalf = kRows * 128;          // bytes of a 64-channel block
   extern __shared__ __align__(1024) uint8_t ring[];
   uint8_t* const qtile = ring + kRingBytes;
@@ -343,9 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&sh->full[i], 1);
-      mbar_init(&sh->empty[i], 1);
+    for (int i = 0; i < 2 * kSlots; ++i) {
+      mbar_init(&sh->full[i / kSlots][i % kSlots], 1);
+      mbar_init(&sh->empty[i / kSlots][i % kSlots], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->s_full[i], 1);
@@ -369,81 +391,106 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_s = tmem, tmem_o = tmem + 256;  // S (P over it) of stream i at + 128 i, O at + 128 i
   Segment s;
 
-  if (warp == kLoadWarp) {
-    // ---- loads: lane i copies box i of a tile ----
-    const int boxes = kRows / box;
-    int64_t pos = 0;  // slots used so far
-    auto page_of = [&](const Segment& g, int j) {
-      const int64_t t = static_cast<int64_t>(j) * kRows + lane * box;
-      return lane < boxes && j < g.j1 && t < g.seen ? a.table[static_cast<int64_t>(g.n) * a.width + t / a.page] : 0;
-    };
+  if (warp >= kLoadWarp) {
+    // ---- loads ----
+    const int which = warp - kLoadWarp;  // 0: K, 1: V
+    const CUtensorMap* const map = which ? &vmap : &kmap;
+    const uint32_t dst0 = smem_addr(ring) + which * (kRingBytes / 2);
+    const int boxes = kRows / box;         // of a tile
+    const int batch = 32 / boxes;          // tiles whose pages the lanes hold
+    const uint32_t per_page = a.page / box;  // boxes of a page
+    int slot = 0;
+    uint32_t turn = 0;  // times the ring has been gone round
+    int64_t copies = 0;
     bool ok = true;
-    auto copy = [&](const CUtensorMap* map, const Segment& g, int j, int page) {
-      const int slot = static_cast<int>(pos % kSlots);
-      const int64_t turn = pos / kSlots;
-      if (turn > 0) ok = ok && wait_warp(sh, &sh->empty[slot], static_cast<uint32_t>((turn - 1) & 1), a.status);
-      if (!ok) return;
-      ++pos;
-      const int t = j * kRows + lane * box;
-      const int here = min(boxes, (g.seen - j * kRows + box - 1) / box);  // boxes with a key that is seen
-      if (lane == 0) mbar_expect_tx(&sh->full[slot], static_cast<uint32_t>(here * box * D * 2));
-      __syncwarp();
-      if (lane < here) {
-        const uint32_t dst = smem_addr(ring) + slot * kSlot + lane * box * 128;
-#pragma unroll
-        for (int x = 0; x < D; x += 64)
-          tma_load_4d(dst + (x / 64) * kHalf, map, x, g.hk, t % a.page, page, &sh->full[slot]);
+    int page = 0, line = 0, nonempty = 0;
+    // lane i: page and first line of box i of the batch that starts at tile j
+    auto look_up = [&](const Segment& g, int j) {
+      const uint32_t at = static_cast<uint32_t>(j * boxes + lane);
+      const bool in = lane < batch * boxes && j + lane / boxes < g.j1 && at * box < static_cast<uint32_t>(g.seen);
+      const uint32_t col = at / per_page;
+      line = static_cast<int>((at - col * per_page) * box);
+      page = in ? a.table[static_cast<int64_t>(g.n) * a.width + col] : 0;
+    };
+    // a page outside the cache is recorded, and the item's rows become zero (the copy itself writes zeros)
+    auto check = [&](int* flag) {
+      if (which == 0 && (page < 0 || page >= a.pages)) {
+        *const_cast<volatile int*>(flag) = 1;
+        set_status(a.status, KDA_ERR_DEVICE_CHECK);
       }
     };
-    for (uint32_t seg = 0; w.next(s);) {
-      if (s.j0 == s.j1) continue;
-      int* const flag = &sh->bad_page[seg++ & 15];
-      // a page outside the cache is recorded, and the item's rows become zero (the copy itself writes zeros)
-      auto check = [&](int page, int j) {
-        if (lane < boxes && j < s.j1 && j * kRows + lane * box < s.seen && (page < 0 || page >= a.pages)) {
-          *const_cast<volatile int*>(flag) = 1;
-          set_status(a.status, KDA_ERR_DEVICE_CHECK);
+    auto next_segment = [&]() {  // the next one with keys, its first pages on their way
+      while (w.next(s))
+        if (s.j0 != s.j1) {
+          look_up(s, s.j0);
+          return true;
         }
-      };
-      int cur = page_of(s, s.j0), nxt = page_of(s, s.j0 + 1);
-      if (lane == 0) *const_cast<volatile int*>(flag) = 0;
+      return false;
+    };
+    for (bool more = next_segment(); more;) {
+      const Segment g = s;
+      int* const flag = &sh->bad_page[nonempty++ & 15];
+      if (which == 0 && lane == 0) *const_cast<volatile int*>(flag) = 0;
       __syncwarp();
-      check(cur, s.j0);
-      copy(&kmap, s, s.j0, cur);
-      for (int j = s.j0; j < s.j1; ++j) {
-        check(nxt, j + 1);
-        if (j + 1 < s.j1) copy(&kmap, s, j + 1, nxt);
-        copy(&vmap, s, j, cur);
-        cur = nxt;
-        nxt = page_of(s, j + 2);
+      for (int j = g.j0; j < g.j1; j += batch) {
+        check(flag);
+        const int now_page = page, now_line = line;
+        if (j + batch < g.j1)
+          look_up(g, j + batch);
+        else
+          more = next_segment();
+        for (int t = j; t < min(j + batch, g.j1); ++t) {
+          if (turn > 0) ok = ok && wait_warp(sh, &sh->empty[which][slot], (turn - 1) & 1, a.status);
+          if (!ok) continue;
+          uint64_t* const bar = &sh->full[which][slot];
+          const int here = min(boxes, (g.seen - t * kRows + box - 1) / box);  // boxes with a key that is seen
+          if (lane == 0) mbar_expect_tx(bar, static_cast<uint32_t>(here * box * D * 2));
+          for (int i = 0; i < here; ++i) {
+            const int from = (t - j) * boxes + i;
+            const int pg = __shfl_sync(~0u, now_page, from), ln = __shfl_sync(~0u, now_line, from);
+            if (lane == 0) {
+              const uint32_t dst = dst0 + slot * kSlot + i * box * 128;
+#pragma unroll
+              for (int x = 0; x < D; x += 64) tma_load_4d(dst + (x / 64) * kHalf, map, x, g.hk, ln, pg, bar);
+            }
+          }
+          ++copies;
+          if (++slot == kSlots) {
+            slot = 0;
+            ++turn;
+          }
+        }
       }
     }
     // after an abort: the copies in flight land before the CTA ends
     if (!ok)
-      for (int64_t p = pos > kSlots ? pos - kSlots : 0; p < pos; ++p)
-        settle(&sh->full[p % kSlots], static_cast<uint32_t>((p / kSlots) & 1));
+      for (int64_t p = copies > kSlots ? copies - kSlots : 0; p < copies; ++p)
+        settle(&sh->full[which][p % kSlots], static_cast<uint32_t>((p / kSlots) & 1));
   } else if (warp == kMmaWarp) {
     // ---- products: one thread issues QK(0), QK(1), then PV(j), QK(j + 2) ----
     if (lane == 0) {
       constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // bf16 A and B
       constexpr uint32_t id_qk = idesc(kRows, kRows) | kBf16, id_pv = idesc(kRows, D, false, true) | kBf16;
-      const uint32_t q0 = smem_addr(qtile), r0 = smem_addr(ring);
-      int64_t pos = 0;
+      const uint32_t q0 = smem_addr(qtile), k0 = smem_addr(ring), v0 = k0 + kRingBytes / 2;
+      int kslot = 0, vslot = 0;
+      uint32_t kturn = 0, vturn = 0;
       uint32_t turn_p[2] = {0, 0};
       uint32_t turn = 0;
       bool ok = true;
       auto qk = [&](int i) {
-        const int slot = static_cast<int>(pos % kSlots);
-        ok = ok && wait(sh, &sh->full[slot], static_cast<uint32_t>((pos / kSlots) & 1), a.status);
+        ok = ok && wait(sh, &sh->full[0][kslot], kturn & 1, a.status);
         if (!ok) return;
-        ++pos;
         fence_after_sync();
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma(tmem_s + 128 * (i & 1), desc_kmajor(q0, kRows, 0, k), desc_kmajor(r0 + slot * kSlot, kRows, 0, k), id_qk,
+          mma(tmem_s + 128 * (i & 1), desc_kmajor(q0, kRows, 0, k), desc_kmajor(k0 + kslot * kSlot, kRows, 0, k), id_qk,
               k > 0);
-        mma_commit(&sh->empty[slot]);
+        mma_commit(&sh->empty[0][kslot]);
         mma_commit(&sh->s_full[i & 1]);
+        if (++kslot == kSlots) {
+          kslot = 0;
+          ++kturn;
+        }
       };
       while (ok && w.next(s)) {
         const int nt = s.j1 - s.j0;
@@ -454,17 +501,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         qk(0);
         if (nt > 1) qk(1);
         for (int i = 0; ok && i < nt; ++i) {
-          const int st = i & 1, slot = static_cast<int>(pos % kSlots);
-          ok = wait(sh, &sh->p_ready[st], turn_p[st]++ & 1, a.status) &&
-               wait(sh, &sh->full[slot], static_cast<uint32_t>((pos / kSlots) & 1), a.status);
+          const int st = i & 1;
+          ok = wait(sh, &sh->full[1][vslot], vturn & 1, a.status) &&
+               wait(sh, &sh->p_ready[st], turn_p[st]++ & 1, a.status);
           if (!ok) break;
-          ++pos;
           fence_after_sync();
 #pragma unroll
           for (int k = 0; k < kRows / 16; ++k)
-            mma_ta(tmem_o + 128 * st, tmem_s + 128 * st + 8 * k, desc_mnmajor(r0 + slot * kSlot, kHalf, k), id_pv,
+            mma_ta(tmem_o + 128 * st, tmem_s + 128 * st + 64 + 8 * k, desc_mnmajor(v0 + vslot * kSlot, kHalf, k), id_pv,
                    (i > 1 || k > 0) ? 1u : 0u);
-          mma_commit(&sh->empty[slot]);
+          mma_commit(&sh->empty[1][vslot]);
+          if (++vslot == kSlots) {
+            vslot = 0;
+            ++vturn;
+          }
           if (i + 2 < nt) qk(i + 2);
         }
         if (ok) mma_commit(&sh->done);
@@ -481,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t my_s = tmem_s + 128 * st + lane_base;
     const uint32_t my_o = tmem_o + 128 * st + lane_base;
     uint32_t turn_s = 0, turn_d = 0;
-    int64_t pos0 = 0;  // ring position of the segment's first slot
+    int64_t tiles0 = 0;  // tiles before the segment
     const Parts parts = parts_of(a.scratch);
     uint32_t seg = 0;
     while (w.next(s)) {
@@ -525,11 +575,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (k0 + kRows > s.seen) {
           // keys past what any row of the tile sees: V rows to zero (their
           // probabilities are zero, but zero times a stale NaN is not)
-          const int64_t vpos = pos0 + (i + 1 < nt ? 2 * i + 2 : 2 * nt - 1);
+          const int64_t vpos = tiles0 + i;
           const int slot = static_cast<int>(vpos % kSlots);
-          const bool here = wait_warp(sh, &sh->full[slot], static_cast<uint32_t>((vpos / kSlots) & 1), a.status);
+          const bool here = wait_warp(sh, &sh->full[1][slot], static_cast<uint32_t>((vpos / kSlots) & 1), a.status);
           if (here && k0 + row >= s.seen) {
-            uint8_t* const v = ring + slot * kSlot + row * 128;
+            uint8_t* const v = ring + kRingBytes / 2 + slot * kSlot + row * 128;
 #pragma unroll
             for (int c = 0; c < D * 2; c += 16)
               *reinterpret_cast<uint4*>(v + (c / 128) * kHalf + c % 128) = make_uint4(0u, 0u, 0u, 0u);
@@ -537,22 +587,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_smem();
         }
         if (warp_used) {
-          // The row is read twice, half by half (its maximum, then its
-          // probabilities), so that a thread never holds all 128 scores.
+          // Half by half, so that a thread never holds all 128 scores: both
+          // for the maximum, then the second half, still at hand, and the
+          // first again for their probabilities. P takes the columns of the
+          // second half.
           uint32_t x[64];
           const int open = limit - k0;  // keys of the tile that the row sees
           const bool masked = __any_sync(~0u, open < kRows);
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          auto load = [&](int h) {
             tmem_ld(my_s + 64 * h, x);
             if (masked) {
 #pragma unroll
               for (int c = 0; c < 64; ++c)
                 if (64 * h + c >= open) x[c] = 0xff800000u;  // -inf
             }
+          };
 #pragma unroll
-            for (int c = 0; c < 64; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(x[c]));
+          for (int h = 0; h < 2; ++h) {
+            load(h);
+#pragma unroll
+            for (int c = 0; c < 64; c += 2)
+              top[c / 2 & 3] = fmaxf(fmaxf(top[c / 2 & 3], __uint_as_float(x[c])), __uint_as_float(x[c + 1]));
           }
           const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
           const float mn = mx * sc;
@@ -573,27 +629,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t sc2 = pack2(__float_as_uint(sc), __float_as_uint(sc));
+          const uint64_t ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
+          uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 1; h >= 0; --h) {
+            if (h == 0) load(0);
             uint32_t p[32];
-            tmem_ld(my_s + 64 * h, x);
-            if (masked) {
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (64 * h + c >= open) x[c] = 0xff800000u;
-            }
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
-              const float e0 = ex2(fmaf(__uint_as_float(x[c]), sc, -ref));
-              const float e1 = ex2(fmaf(__uint_as_float(x[c + 1]), sc, -ref));
-              sum[c / 2 & 1] += e0;
-              sum[2 + (c / 2 & 1)] += e1;
+              const float2 t = unpack2(fma2(pack2(x[c], x[c + 1]), sc2, ref2));
+              const float e0 = ex2(t.x), e1 = ex2(t.y);
+              sum[c / 2 & 3] = add2(sum[c / 2 & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
               p[c / 2] = pack_bf16(e0, e1);
             }
-            tmem_st(my_s + 32 * h, p);  // over the half of S that is read by now
+            tmem_st(my_s + 64 + 32 * h, p);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          const float2 all = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+          l += all.x + all.y;
           tmem_st_wait();
         }
         fence_before_sync();
@@ -645,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      pos0 += 2 * nt;
+      tiles0 += nt;
       if (!whole) {
         if (st == 0 && used) {
           parts.ml[part * 2 * kRows + row] = mm;
