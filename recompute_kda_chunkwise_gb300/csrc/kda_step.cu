@@ -71,6 +71,57 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
   *reinterpret_cast<uint2*>(p) = u;
 }
 
+// Exponentials and quotients of the gates from the hardware's approximations
+// (each within 2^-22 of the value): one warp forms them for a token's 128
+// channels before the others can go on, and the full-precision functions made
+// that the longest part of a token.
+__device__ __forceinline__ float exp2_(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sigmoid_(float x) {  // 0 and 1 in the limits: 1 / inf, 1 / 1
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + exp2_(x * -1.4426950408889634f)));
+  return y;
+}
+
+// Four columns as two pairs of fp32 values: one instruction works on a pair.
+struct alignas(16) F4 {
+  uint64_t a, b;
+};
+__device__ __forceinline__ uint64_t twice(float x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t add(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ F4 add(F4 x, F4 y) { return {add(x.a, y.a), add(x.b, y.b)}; }
+__device__ __forceinline__ F4 mul(F4 x, float y) {
+  const uint64_t t = twice(y);
+  F4 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.a) : "l"(x.a), "l"(t));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(x.b), "l"(t));
+  return r;
+}
+__device__ __forceinline__ F4 fma(F4 x, float y, F4 z) {
+  const uint64_t t = twice(y);
+  F4 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.a) : "l"(x.a), "l"(t), "l"(z.a));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.b) : "l"(x.b), "l"(t), "l"(z.b));
+  return r;
+}
+__device__ __forceinline__ float4 values(F4 x) {
+  float4 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.a));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.z), "=f"(r.w) : "l"(x.b));
+  return r;
+}
+
 // CG: GDN-2's channel gates (b: erase on key channels, w: write on value
 // channels); otherwise beta scales r.
 template <typename T, int D, bool CG>
@@ -78,17 +129,22 @@ __global__ void __launch_bounds__(kThreads) kda_step_kernel(const StepArgs a) {
   constexpr int R = D / 16;        // rows of a thread
   constexpr int E = D / 32;        // channels of a lane in the staged vectors
   constexpr int kSplit = D / kCols;
-  __shared__ float s_q[kBatch][D], s_k[kBatch][D], s_a[kBatch][D], s_b[CG ? kBatch : 1][D];
+  // Per key channel: decay, key, query, and the key under GDN-2's erase gate,
+  // at place(channel): a lane writes E consecutive channels and reads rows four
+  // apart, and neither falls on a few banks only.
+  constexpr int kSkew = 32 + 8 / E;
+  __shared__ float4 s_c[kBatch][E * kSkew];
+  auto place = [](int c) { return c / E + c % E * kSkew; };
   __shared__ __align__(16) float s_v[kBatch][kCols];
   __shared__ float s_beta[kBatch];
-  __shared__ __align__(16) float4 s_pk[2][4][8], s_pq[2][4][8];
+  __shared__ __align__(16) float s_pk[2][4][kCols], s_pq[2][4][kCols];
   __shared__ float s_kq[2][4];
 
   const int cb = static_cast<int>(blockIdx.x) % kSplit;
   const int item = static_cast<int>(blockIdx.x) / kSplit;
   const int n = item / a.H, h = item % a.H;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-  const int cg = lane & 7, row0 = warp * 4 + (lane >> 3);
+  const int cg = lane & 7, row0 = warp * 4 + (lane >> 3), at0 = place(row0);
 
   const int64_t lo = a.cu[n], hi = a.cu[n + 1];
   const int64_t slot = a.index ? a.index[n] : n;
@@ -109,9 +165,9 @@ __global__ void __launch_bounds__(kThreads) kda_step_kernel(const StepArgs a) {
     return;
   }
   float* const state = a.states + ((slot * a.H + h) * D + row0) * D + cb * kCols + cg * 4;
-  float4 S[R];
+  F4 S[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) S[i] = *reinterpret_cast<const float4*>(state + i * 16 * D);
+  for (int i = 0; i < R; ++i) S[i] = *reinterpret_cast<const F4*>(state + i * 16 * D);
 
   const int64_t base = (lo * a.H + h) * D;
   const T* const q = static_cast<const T*>(a.q) + base;
@@ -120,103 +176,113 @@ __global__ void __launch_bounds__(kThreads) kda_step_kernel(const StepArgs a) {
   const T* const g = static_cast<const T*>(a.g) + base;
   const T* const er = static_cast<const T*>(a.b) + (CG ? base : 0);
   const T* const wr = CG ? static_cast<const T*>(a.w) + base + cb * kCols : nullptr;
-  const float rate = expf(a.A_log[h]);
+  const float rate = expf(a.A_log[h]), lower2 = a.lower * 1.4426950408889634f;
 
   for (int64_t t0 = 0; t0 < count; t0 += kBatch) {
     const int nb = static_cast<int>(count - t0 < kBatch ? count - t0 : kBatch);
-    // Channel vectors of the next nb tokens: one warp normalises the queries,
-    // one the keys, one forms the decays, one the values and gates.
-    for (int t = 0; t < nb; ++t) {
+    // Channel vectors of the next nb tokens. A single token is shared out: one
+    // warp normalises the query, one the key, one forms the decays, one the
+    // values and gates. Of several, each warp takes a token, so that the loads
+    // of all of them are in flight together.
+    const bool shared_out = nb == 1;
+    const int t = shared_out ? 0 : warp;
+    if (t < nb) {
       const int64_t at = (t0 + t) * tok;
-      if (warp == 0 || warp == 1) {
-        float x[E], e[E];
-        load_row<E>((warp == 0 ? q : k) + at, lane, x);
-        if (CG && warp == 1) load_row<E>(er + at, lane, e);
+      float xq[E], xk[E], xe[E], xg[E], bias[E], xv = 0.f, xw = 0.f;
+      const bool do_q = !shared_out || warp == 0, do_k = !shared_out || warp == 1, do_g = !shared_out || warp == 2,
+                 do_v = !shared_out || warp == 3;
+      if (do_q) load_row<E>(q + at, lane, xq);
+      if (do_k) {
+        load_row<E>(k + at, lane, xk);
+        if (CG) load_row<E>(er + at, lane, xe);
+      }
+      if (do_g) {
+        load_row<E>(g + at, lane, xg);
+        load_row<E>(a.dt_bias + h * D, lane, bias);
+      }
+      if (do_v) {
+        xv = ldf(v + at + lane);
+        xw = CG ? ldf(wr + at + lane) : ldf(static_cast<const T*>(a.b) + (lo + t0 + t) * a.H + h);
+      }
+      if (do_q) {
         float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < E; ++i) ss += x[i] * x[i];
-        const float inv = rsqrtf(warp_sum(ss) + a.eps) * (warp == 0 ? a.scale : 1.f);
+        for (int i = 0; i < E; ++i) ss += xq[i] * xq[i];
+        const float inv = rsqrtf(warp_sum(ss) + a.eps) * a.scale;
+#pragma unroll
+        for (int i = 0; i < E; ++i) s_c[t][lane + i * kSkew].z = xq[i] * inv;
+      }
+      if (do_k) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) ss += xk[i] * xk[i];
+        const float inv = rsqrtf(warp_sum(ss) + a.eps);
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-          const float y = x[i] * inv;
-          (warp == 0 ? s_q : s_k)[t][lane * E + i] = y;
-          if (CG && warp == 1) s_b[t][lane * E + i] = y * sigmoidf_(e[i]);
+          s_c[t][lane + i * kSkew].y = xk[i] * inv;
+          if (CG) s_c[t][lane + i * kSkew].w = xk[i] * inv * sigmoid_(xe[i]);
         }
-      } else if (warp == 2) {
-        float x[E], bias[E];
-        load_row<E>(g + at, lane, x);
-        load_row<E>(a.dt_bias + h * D, lane, bias);
+      }
+      if (do_g) {
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-          s_a[t][lane * E + i] = expf(a.lower * sigmoidf_(rate * (x[i] + bias[i])));
-      } else {
-        float x = ldf(v + at + lane);
-        if (CG)
-          x *= sigmoidf_(ldf(wr + at + lane));
-        else if (lane == 0)
-          s_beta[t] = sigmoidf_(ldf(static_cast<const T*>(a.b) + (lo + t0 + t) * a.H + h));
-        s_v[t][lane] = x;
+        for (int i = 0; i < E; ++i) s_c[t][lane + i * kSkew].x = exp2_(lower2 * sigmoid_(rate * (xg[i] + bias[i])));
+      }
+      if (do_v) {
+        const float w = sigmoid_(xw);
+        s_v[t][lane] = CG ? xv * w : xv;
+        if (!CG && lane == 0) s_beta[t] = w;
       }
     }
     __syncthreads();
 
     for (int t = 0; t < nb; ++t) {
-      float4 pk = make_float4(0.f, 0.f, 0.f, 0.f), pq = pk;
+      F4 pk = {0, 0}, pq = {0, 0};
       float kq = 0.f;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const int row = row0 + i * 16;
-        const float al = s_a[t][row], kr = s_k[t][row], qr = s_q[t][row];
-        const float br = CG ? s_b[CG ? t : 0][row] : kr;
-        S[i].x *= al; S[i].y *= al; S[i].z *= al; S[i].w *= al;
-        pk.x = fmaf(S[i].x, br, pk.x); pk.y = fmaf(S[i].y, br, pk.y);
-        pk.z = fmaf(S[i].z, br, pk.z); pk.w = fmaf(S[i].w, br, pk.w);
-        pq.x = fmaf(S[i].x, qr, pq.x); pq.y = fmaf(S[i].y, qr, pq.y);
-        pq.z = fmaf(S[i].z, qr, pq.z); pq.w = fmaf(S[i].w, qr, pq.w);
-        kq = fmaf(kr, qr, kq);
+        const float4 c = s_c[t][at0 + i * (16 / E)];
+        S[i] = mul(S[i], c.x);
+        pk = fma(S[i], CG ? c.w : c.y, pk);
+        pq = fma(S[i], c.z, pq);
+        kq = fmaf(c.y, c.z, kq);
       }
-      // Sum over the 4 row lanes of the warp, then over the 4 warps; two
-      // buffers, so that one barrier a token is enough.
-#pragma unroll
-      for (int m = 8; m <= 16; m <<= 1) {
-        pk.x += __shfl_xor_sync(~0u, pk.x, m); pk.y += __shfl_xor_sync(~0u, pk.y, m);
-        pk.z += __shfl_xor_sync(~0u, pk.z, m); pk.w += __shfl_xor_sync(~0u, pk.w, m);
-        pq.x += __shfl_xor_sync(~0u, pq.x, m); pq.y += __shfl_xor_sync(~0u, pq.y, m);
-        pq.z += __shfl_xor_sync(~0u, pq.z, m); pq.w += __shfl_xor_sync(~0u, pq.w, m);
-        kq += __shfl_xor_sync(~0u, kq, m);
-      }
+      // Sums over the 4 row lanes of the warp: a lane passes on what its
+      // partner keeps, pk against pq, then one pair of columns against the
+      // other, so that lane 8 j + cg ends with pair j % 2 of pk (j < 2) or pq.
+      const bool hi = lane & 16, odd = lane & 8;
+      const F4 keep = hi ? pq : pk, give = hi ? pk : pq;
+      F4 w;
+      w.a = add(keep.a, __shfl_xor_sync(~0u, give.a, 16));
+      w.b = add(keep.b, __shfl_xor_sync(~0u, give.b, 16));
+      const uint64_t pair = add(odd ? w.b : w.a, __shfl_xor_sync(~0u, odd ? w.a : w.b, 8));
+      kq += __shfl_xor_sync(~0u, kq, 8);
+      kq += __shfl_xor_sync(~0u, kq, 16);
+      // then over the 4 warps; two buffers, so that one barrier a token is enough
       const int buf = t & 1;
-      if (lane < 8) {
-        s_pk[buf][warp][cg] = pk;
-        s_pq[buf][warp][cg] = pq;
-        if (lane == 0) s_kq[buf][warp] = kq;
-      }
+      *reinterpret_cast<uint64_t*>(&(hi ? s_pq : s_pk)[buf][warp][cg * 4 + (odd ? 2 : 0)]) = pair;
+      if (lane == 0) s_kq[buf][warp] = kq;
       __syncthreads();
-      pk = s_pk[buf][0][cg];
-      pq = s_pq[buf][0][cg];
-      kq = s_kq[buf][0];
+      pk = *reinterpret_cast<const F4*>(&s_pk[buf][0][cg * 4]);
 #pragma unroll
-      for (int j = 1; j < 4; ++j) {
-        const float4 x = s_pk[buf][j][cg], y = s_pq[buf][j][cg];
-        pk.x += x.x; pk.y += x.y; pk.z += x.z; pk.w += x.w;
-        pq.x += y.x; pq.y += y.y; pq.z += y.z; pq.w += y.w;
-        kq += s_kq[buf][j];
-      }
-      const float4 x = *reinterpret_cast<const float4*>(&s_v[t][cg * 4]);
+      for (int j = 1; j < 4; ++j) pk = add(pk, *reinterpret_cast<const F4*>(&s_pk[buf][j][cg * 4]));
+      // r = w v - pk (KDA: beta (v - pk))
       const float beta = CG ? 1.f : s_beta[t];
-      const float4 r = make_float4(beta * (x.x - pk.x), beta * (x.y - pk.y), beta * (x.z - pk.z), beta * (x.w - pk.w));
+      const F4 r = mul(fma(pk, -1.f, *reinterpret_cast<const F4*>(&s_v[t][cg * 4])), beta);
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const float kr = s_k[t][row0 + i * 16];
-        S[i].x = fmaf(kr, r.x, S[i].x); S[i].y = fmaf(kr, r.y, S[i].y);
-        S[i].z = fmaf(kr, r.z, S[i].z); S[i].w = fmaf(kr, r.w, S[i].w);
+      for (int i = 0; i < R; ++i) S[i] = fma(r, s_c[t][at0 + i * (16 / E)].y, S[i]);
+      if (row0 == 0) {
+        pq = *reinterpret_cast<const F4*>(&s_pq[buf][0][cg * 4]);
+        kq = s_kq[buf][0];
+#pragma unroll
+        for (int j = 1; j < 4; ++j) {
+          pq = add(pq, *reinterpret_cast<const F4*>(&s_pq[buf][j][cg * 4]));
+          kq += s_kq[buf][j];
+        }
+        store4(o + (t0 + t) * tok + cg * 4, values(fma(r, kq, pq)));
       }
-      if (row0 == 0)
-        store4(o + (t0 + t) * tok + cg * 4, make_float4(fmaf(kq, r.x, pq.x), fmaf(kq, r.y, pq.y), fmaf(kq, r.z, pq.z),
-                                                        fmaf(kq, r.w, pq.w)));
       if (t0 + t + 1 == kept) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) *reinterpret_cast<float4*>(state + i * 16 * D) = S[i];
+        for (int i = 0; i < R; ++i) *reinterpret_cast<F4*>(state + i * 16 * D) = S[i];
       }
     }
     __syncthreads();  // the staged vectors are read: the next batch may replace them

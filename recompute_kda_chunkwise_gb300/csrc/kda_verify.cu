@@ -26,6 +26,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512;
+constexpr int kSms = 152;
 
 struct VerifyArgs {
   const float *target, *draft, *u, *noise;
@@ -48,40 +49,65 @@ __device__ __forceinline__ void take(Best& a, float score, int idx) {
 
 // Largest r / e of this CTA's part of the row. Q: subtract the draft row;
 // skip: the entry to leave out (a draft without a distribution), or -1.
+//
+// Divisions are few: an entry can only win if r >= thr e, with thr just below
+// the warp's best quotient so far (by 2^-20: the rounding of the product and
+// of the quotients is far smaller), so a batch without such an entry costs one
+// subtraction, one product and one comparison an entry. A warp meets new
+// bests about ln(entries) times.
 template <bool Q, int VEC>
 __device__ Best scan(const float* p, const float* q, const float* e, int V, int skip, int rank, int ranks) {
   Best best{-1.f, INT32_MAX};
-  auto one = [&](float pi, float qi, float ei, int i) {
-    const float r = Q ? pi - qi : pi;
-    if (r > 0.f && i != skip) take(best, r / ei, i);
-  };
-  const int units = V / VEC;
-  constexpr int kUnroll = VEC == 4 ? 4 : 8;
-  const int step = ranks * kThreads;
+  float thr = -1.f;
+  constexpr int kUnroll = VEC == 4 ? 2 : 8;  // loads of a row in flight a thread: more would cost threads
+  const int units = V / VEC, step = ranks * kThreads;
+  const int turns = (units + step * kUnroll - 1) / (step * kUnroll);  // the same for every lane
   int i = rank * kThreads + static_cast<int>(threadIdx.x);
-  for (; i + (kUnroll - 1) * step < units; i += kUnroll * step) {
+  for (int t = 0; t < turns; ++t, i += kUnroll * step) {
     float pv[kUnroll][VEC], qv[kUnroll][VEC], ev[kUnroll][VEC];
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
       const int at = i + j * step;
-      if constexpr (VEC == 4) {
-        *reinterpret_cast<float4*>(pv[j]) = __ldcs(reinterpret_cast<const float4*>(p) + at);
-        if (Q) *reinterpret_cast<float4*>(qv[j]) = __ldcs(reinterpret_cast<const float4*>(q) + at);
-        *reinterpret_cast<float4*>(ev[j]) = __ldcs(reinterpret_cast<const float4*>(e) + at);
+      if (at < units) {
+        if constexpr (VEC == 4) {
+          *reinterpret_cast<float4*>(pv[j]) = __ldcs(reinterpret_cast<const float4*>(p) + at);
+          if (Q) *reinterpret_cast<float4*>(qv[j]) = __ldcs(reinterpret_cast<const float4*>(q) + at);
+          *reinterpret_cast<float4*>(ev[j]) = __ldcs(reinterpret_cast<const float4*>(e) + at);
+        } else {
+          pv[j][0] = __ldcs(p + at);
+          if (Q) qv[j][0] = __ldcs(q + at);
+          ev[j][0] = __ldcs(e + at);
+        }
       } else {
-        pv[j][0] = __ldcs(p + at);
-        if (Q) qv[j][0] = __ldcs(q + at);
-        ev[j][0] = __ldcs(e + at);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) pv[j][c] = qv[j][c] = 0.f, ev[j][c] = 1.f;
       }
     }
+    bool any = false;
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j)
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) one(pv[j][c], Q ? qv[j][c] : 0.f, ev[j][c], (i + j * step) * VEC + c);
-  }
-  for (; i < units; i += step)
+      for (int c = 0; c < VEC; ++c) {
+        if (Q) pv[j][c] -= qv[j][c];  // r from here on
+        any |= pv[j][c] > 0.f && pv[j][c] >= thr * ev[j][c];
+      }
+    if (__any_sync(~0u, any)) {
+      if (any) {
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) one(p[i * VEC + c], Q ? q[i * VEC + c] : 0.f, e[i * VEC + c], i * VEC + c);
+        for (int j = 0; j < kUnroll; ++j)
+#pragma unroll
+          for (int c = 0; c < VEC; ++c) {
+            const float r = pv[j][c];
+            const int idx = (i + j * step) * VEC + c;
+            if (r > 0.f && r >= thr * ev[j][c] && idx != skip) take(best, r / ev[j][c], idx);
+          }
+      }
+      // quotients are never negative, so their order is that of their bits; -1: none yet
+      const uint32_t top = __reduce_max_sync(~0u, best.score < 0.f ? 0u : __float_as_uint(best.score));
+      const bool some = __any_sync(~0u, best.score >= 0.f);
+      thr = some ? __uint_as_float(top) * (1.f - 0x1p-20f) : -1.f;
+    }
+  }
   return best;
 }
 
@@ -110,7 +136,7 @@ __device__ Best over_cluster(Best b, Best* warps, Best* mine) {
 }
 
 template <int VEC>
-__global__ void __launch_bounds__(kThreads) kda_verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) kda_verify_kernel(const VerifyArgs a) {
   auto cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
   const int n = static_cast<int>(blockIdx.x) / ranks;
@@ -193,9 +219,14 @@ extern "C" kda_status kda_verify_drafts(int32_t num_seqs, int32_t max_drafts, in
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 8;
+  // CTAs of a sequence: at most 8, and no more than give every SM one over the
+  // call (256 x 131072: 54 us with 1, 57 with 2, 64 with 4 CTAs a sequence; a
+  // cluster's CTAs have to find room together).
+  unsigned ranks = 8;
+  while (ranks > 1 && (int64_t)num_seqs * ranks / 2 >= kSms) ranks /= 2;
+  attr.val.clusterDim.x = ranks;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)num_seqs * 8u);
+  cfg.gridDim = dim3((unsigned)num_seqs * ranks);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = (cudaStream_t)stream;
   cfg.attrs = &attr;
