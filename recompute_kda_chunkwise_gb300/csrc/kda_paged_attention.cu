@@ -44,30 +44,12 @@
 namespace kda {
 namespace tc {
 
-// 64 consecutive 32-bit columns of the thread's TMEM lane, complete on return.
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[64]) {
+// 32 consecutive 32-bit columns of the thread's TMEM lane, in two steps: the
+// load is on its way after the first, its values are there after the second.
+__device__ __forceinline__ void tmem_ask(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,"
-      "%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
-        "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
-        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
-        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
-        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-      : "r"(taddr)
-      : "memory");
-}
-// Another 32 of them.
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
@@ -75,15 +57,33 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
-// Stores 32 consecutive 32-bit columns of the thread's TMEM lane (tmem_st_wait completes it).
+__device__ __forceinline__ void tmem_got(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+// Stores consecutive 32-bit columns of the thread's TMEM lane (tmem_st_wait completes it).
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
       :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
         "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
         "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 
@@ -471,7 +471,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // bf16 A and B
       constexpr uint32_t id_qk = idesc(kRows, kRows) | kBf16, id_pv = idesc(kRows, D, false, true) | kBf16;
-      const uint32_t q0 = smem_addr(qtile), k0 = smem_addr(ring), v0 = k0 + kRingBytes / 2;
+      // matrix descriptors: the low words are sums that never carry
+      const uint64_t q0 = desc_kmajor(smem_addr(qtile), kRows, 0, 0), k0 = desc_kmajor(smem_addr(ring), kRows, 0, 0),
+                     v0 = desc_mnmajor(smem_addr(ring) + kRingBytes / 2, kHalf, 0);
+      const uint32_t hi = static_cast<uint32_t>(q0 >> 32);
+      const uint32_t qlo = static_cast<uint32_t>(q0), klo = static_cast<uint32_t>(k0), vlo = static_cast<uint32_t>(v0);
       int kslot = 0, vslot = 0;
       uint32_t kturn = 0, vturn = 0;
       uint32_t turn_p[2] = {0, 0};
@@ -481,10 +485,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = ok && wait(sh, &sh->full[0][kslot], kturn & 1, a.status);
         if (!ok) return;
         fence_after_sync();
+        const uint32_t kd = klo + kslot * (kSlot >> 4), ts = tmem_s + 128 * (i & 1);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma(tmem_s + 128 * (i & 1), desc_kmajor(q0, kRows, 0, k), desc_kmajor(k0 + kslot * kSlot, kRows, 0, k), id_qk,
-              k > 0);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t step = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
+          mma(ts, pack2(qlo + step, hi), pack2(kd + step, hi), id_qk, k > 0);
+        }
         mma_commit(&sh->empty[0][kslot]);
         mma_commit(&sh->s_full[i & 1]);
         if (++kslot == kSlots) {
@@ -506,10 +512,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                wait(sh, &sh->p_ready[st], turn_p[st]++ & 1, a.status);
           if (!ok) break;
           fence_after_sync();
+          const uint32_t vd = vlo + vslot * (kSlot >> 4), ts = tmem_s + 128 * st + 64, to = tmem_o + 128 * st;
 #pragma unroll
           for (int k = 0; k < kRows / 16; ++k)
-            mma_ta(tmem_o + 128 * st, tmem_s + 128 * st + 64 + 8 * k, desc_mnmajor(v0 + vslot * kSlot, kHalf, k), id_pv,
-                   (i > 1 || k > 0) ? 1u : 0u);
+            mma_ta(to, ts + 8 * k, pack2(vd + k * 128, hi), id_pv, (i > 1 || k > 0) ? 1u : 0u);
           mma_commit(&sh->empty[1][vslot]);
           if (++vslot == kSlots) {
             vslot = 0;
@@ -587,28 +593,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_smem();
         }
         if (warp_used) {
-          // Half by half, so that a thread never holds all 128 scores: both
-          // for the maximum, then the second half, still at hand, and the
-          // first again for their probabilities. P takes the columns of the
-          // second half.
-          uint32_t x[64];
+          // The row is read twice, 32 scores at a time with the next 32 on
+          // their way: for its maximum, then for its probabilities. Short
+          // loops on purpose: unrolled, this code drove that of the issuing
+          // and loading warps out of the instruction cache.
           const int open = limit - k0;  // keys of the tile that the row sees
           const bool masked = __any_sync(~0u, open < kRows);
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto load = [&](int h) {
-            tmem_ld(my_s + 64 * h, x);
+          auto mask = [&](uint32_t(&x)[32], int c0) {
             if (masked) {
 #pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (64 * h + c >= open) x[c] = 0xff800000u;  // -inf
+              for (int c = 0; c < 32; ++c)
+                if (c0 + c >= open) x[c] = 0xff800000u;  // -inf
             }
           };
+          uint32_t xa[32], xb[32];
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto most = [&](const uint32_t(&x)[32]) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            load(h);
-#pragma unroll
-            for (int c = 0; c < 64; c += 2)
+            for (int c = 0; c < 32; c += 2)
               top[c / 2 & 3] = fmaxf(fmaxf(top[c / 2 & 3], __uint_as_float(x[c])), __uint_as_float(x[c + 1]));
+          };
+          tmem_ask(my_s, xa);
+#pragma unroll 1
+          for (int c0 = 0; c0 < kRows; c0 += 64) {
+            tmem_got(xa);
+            tmem_ask(my_s + c0 + 32, xb);
+            mask(xa, c0);
+            most(xa);
+            tmem_got(xb);
+            if (c0 + 64 < kRows) tmem_ask(my_s + c0 + 64, xa);
+            mask(xb, c0 + 32);
+            most(xb);
           }
           const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
           const float mn = mx * sc;
@@ -618,13 +633,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (grow) m = mn;
             l *= f;
             if (i >= 2) {  // the stream's O exists, and is complete: S of this tile was issued after it
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D; c += 32) {
-                uint32_t y[32];
-                tmem_ld(my_o + c, y);
+                tmem_ask(my_o + c, xa);
+                tmem_got(xa);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
-                tmem_st(my_o + c, y);
+                for (int k = 0; k < 32; ++k) xa[k] = __float_as_uint(__uint_as_float(xa[k]) * f);
+                tmem_st(my_o + c, xa);
               }
             }
           }
@@ -632,18 +647,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t sc2 = pack2(__float_as_uint(sc), __float_as_uint(sc));
           const uint64_t ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
           uint64_t sum[4] = {0, 0, 0, 0};
+          // P takes the columns of the second half, from its end: each store is over scores that are read
+          auto probabilities = [&](const uint32_t(&x)[32], int c0) {
+            uint32_t p[16];
 #pragma unroll
-          for (int h = 1; h >= 0; --h) {
-            if (h == 0) load(0);
-            uint32_t p[32];
-#pragma unroll
-            for (int c = 0; c < 64; c += 2) {
+            for (int c = 0; c < 32; c += 2) {
               const float2 t = unpack2(fma2(pack2(x[c], x[c + 1]), sc2, ref2));
               const float e0 = ex2(t.x), e1 = ex2(t.y);
               sum[c / 2 & 3] = add2(sum[c / 2 & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
               p[c / 2] = pack_bf16(e0, e1);
             }
-            tmem_st(my_s + 64 + 32 * h, p);
+            tmem_st(my_s + 64 + c0 / 2, p);
+          };
+          tmem_ask(my_s + 96, xb);
+#pragma unroll 1
+          for (int c0 = 64; c0 >= 0; c0 -= 64) {
+            tmem_got(xb);
+            tmem_ask(my_s + c0, xa);
+            mask(xb, c0 + 32);
+            probabilities(xb, c0 + 32);
+            tmem_got(xa);
+            if (c0 > 0) tmem_ask(my_s + 32, xb);
+            mask(xa, c0);
+            probabilities(xa, c0);
           }
           const float2 all = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
           l += all.x + all.y;
@@ -668,11 +694,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int part = 2 * static_cast<int>(blockIdx.x) + (s.j0 == 0 ? 1 : 0);
       const float inv = whole ? (ll == 0.f || bad ? 0.f : 1.f / ll) : 1.f;
       if (warp_used) {
-#pragma unroll
+#pragma unroll 1
         for (int c = st * (D / 2); c < (st + 1) * (D / 2); c += 32) {
           uint32_t x[32], y[32];
-          tmem_ld(tmem_o + lane_base + c, x);
-          if (nt > 1) tmem_ld(tmem_o + 128 + lane_base + c, y);
+          tmem_ask(tmem_o + lane_base + c, x);
+          tmem_got(x);
+          if (nt > 1) {
+            tmem_ask(tmem_o + 128 + lane_base + c, y);
+            tmem_got(y);
+          }
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
             // a stream without a key of this row: its O holds nothing to add
