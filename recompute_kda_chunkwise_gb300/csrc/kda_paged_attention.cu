@@ -87,12 +87,29 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16])
       : "memory");
 }
 
-// D (+)= A B, kind::f16: A (16-bit, two K elements a 32-bit column) from TMEM.
-__device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
+// Products and their commit, issued by the one lane of a converged warp that
+// has `lead` set: the warp's control flow, and with it the descriptors, stay
+// uniform. D (+)= A B, kind::f16, A and B in shared memory ...
+__device__ __forceinline__ void mma_by(uint32_t lead, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(id), "r"(acc));
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(lead));
+}
+// ... or A (16-bit, two K elements a 32-bit column) in TMEM.
+__device__ __forceinline__ void mma_ta_by(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id,
+                                          uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(id), "r"(acc), "r"(lead));
+}
+__device__ __forceinline__ void commit_by(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar)),
+      "r"(lead)
+      : "memory");
 }
 // TMA: a 4-D tile (channel, head, row of the page, page).
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
@@ -274,7 +291,8 @@ __device__ __forceinline__ void settle(uint64_t* bar, uint32_t parity) {
   }
 }
 
-// wait() of a whole warp, with one answer.
+// wait() of a whole warp, with one answer. Lanes may wait for barriers of
+// their own: the warp goes on when all of them are through.
 __device__ __forceinline__ bool wait_warp(Shared* sh, uint64_t* bar, uint32_t parity, int* status) {
   return __all_sync(~0u, wait(sh, bar, parity, status));
 }
@@ -467,68 +485,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int64_t p = copies > kSlots ? copies - kSlots : 0; p < copies; ++p)
         settle(&sh->full[which][p % kSlots], static_cast<uint32_t>((p / kSlots) & 1));
   } else if (warp == kMmaWarp) {
-    // ---- products: one thread issues QK(0), QK(1), then PV(j), QK(j + 2) ----
-    if (lane == 0) {
-      constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // bf16 A and B
-      constexpr uint32_t id_qk = idesc(kRows, kRows) | kBf16, id_pv = idesc(kRows, D, false, true) | kBf16;
-      // matrix descriptors: the low words are sums that never carry
-      const uint64_t q0 = desc_kmajor(smem_addr(qtile), kRows, 0, 0), k0 = desc_kmajor(smem_addr(ring), kRows, 0, 0),
-                     v0 = desc_mnmajor(smem_addr(ring) + kRingBytes / 2, kHalf, 0);
-      const uint32_t hi = static_cast<uint32_t>(q0 >> 32);
-      const uint32_t qlo = static_cast<uint32_t>(q0), klo = static_cast<uint32_t>(k0), vlo = static_cast<uint32_t>(v0);
-      int kslot = 0, vslot = 0;
-      uint32_t kturn = 0, vturn = 0;
-      uint32_t turn_p[2] = {0, 0};
-      uint32_t turn = 0;
-      bool ok = true;
-      auto qk = [&](int i) {
-        ok = ok && wait(sh, &sh->full[0][kslot], kturn & 1, a.status);
-        if (!ok) return;
-        fence_after_sync();
-        const uint32_t kd = klo + kslot * (kSlot >> 4), ts = tmem_s + 128 * (i & 1);
+    // ---- products: QK(0), QK(1), then PV(i) and QK(i + 2) for each tile i ----
+    // One warp issues for both streams, and that takes it longer than the
+    // tensor cores need unless it is kept short: PV(i) and QK(i + 2) go out
+    // after one wait, in which a lane each looks at P(i), V(i) and K(i + 2).
+    constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // bf16 A and B
+    constexpr uint32_t id_qk = idesc(kRows, kRows) | kBf16, id_pv = idesc(kRows, D, false, true) | kBf16;
+    // matrix descriptors: the low words are sums that never carry
+    const uint64_t q0 = desc_kmajor(smem_addr(qtile), kRows, 0, 0), k0 = desc_kmajor(smem_addr(ring), kRows, 0, 0),
+                   v0 = desc_mnmajor(smem_addr(ring) + kRingBytes / 2, kHalf, 0);
+    const uint32_t hi = static_cast<uint32_t>(q0 >> 32);
+    const uint32_t qlo = static_cast<uint32_t>(q0), klo = static_cast<uint32_t>(k0), vlo = static_cast<uint32_t>(v0);
+    const uint32_t lead = lane == 0;
+    int kslot = 0, vslot = 0;
+    uint32_t kturn = 0, vturn = 0, turn = 0, turn_p[2] = {0, 0};
+    bool ok = true;
+    auto qk = [&](int st) {
+      const uint32_t kd = klo + kslot * (kSlot >> 4), ts = tmem_s + 128 * st;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t step = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
-          mma(ts, pack2(qlo + step, hi), pack2(kd + step, hi), id_qk, k > 0);
-        }
-        mma_commit(&sh->empty[0][kslot]);
-        mma_commit(&sh->s_full[i & 1]);
-        if (++kslot == kSlots) {
-          kslot = 0;
-          ++kturn;
-        }
-      };
-      while (ok && w.next(s)) {
-        const int nt = s.j1 - s.j0;
-        if (nt == 0) continue;
-        ok = wait(sh, &sh->q_ready, turn++ & 1, a.status);
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t step = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
+        mma_by(lead, ts, pack2(qlo + step, hi), pack2(kd + step, hi), id_qk, k > 0);
+      }
+      commit_by(lead, &sh->s_full[st]);
+      commit_by(lead, &sh->empty[0][kslot]);
+      if (++kslot == kSlots) {
+        kslot = 0;
+        ++kturn;
+      }
+    };
+    while (ok && w.next(s)) {
+      const int nt = s.j1 - s.j0;
+      if (nt == 0) continue;
+      ok = wait_warp(sh, lane == 0 ? &sh->q_ready : &sh->full[0][kslot], (lane == 0 ? turn : kturn) & 1, a.status);
+      ++turn;
+      if (!ok) break;
+      fence_after_sync();
+      qk(0);
+      if (nt > 1) {
+        ok = wait_warp(sh, &sh->full[0][kslot], kturn & 1, a.status);
         if (!ok) break;
         fence_after_sync();
-        qk(0);
-        if (nt > 1) qk(1);
-        for (int i = 0; ok && i < nt; ++i) {
-          const int st = i & 1;
-          ok = wait(sh, &sh->full[1][vslot], vturn & 1, a.status) &&
-               wait(sh, &sh->p_ready[st], turn_p[st]++ & 1, a.status);
-          if (!ok) break;
-          fence_after_sync();
-          const uint32_t vd = vlo + vslot * (kSlot >> 4), ts = tmem_s + 128 * st + 64, to = tmem_o + 128 * st;
-#pragma unroll
-          for (int k = 0; k < kRows / 16; ++k)
-            mma_ta(to, ts + 8 * k, pack2(vd + k * 128, hi), id_pv, (i > 1 || k > 0) ? 1u : 0u);
-          mma_commit(&sh->empty[1][vslot]);
-          if (++vslot == kSlots) {
-            vslot = 0;
-            ++vturn;
-          }
-          if (i + 2 < nt) qk(i + 2);
-        }
-        if (ok) mma_commit(&sh->done);
+        qk(1);
       }
-      // nothing of this thread may be in flight when TMEM is freed
-      mma_commit(&sh->drain);
-      settle(&sh->drain, 0);
+      for (int i = 0; i < nt; ++i) {
+        const int st = i & 1;
+        const bool more = i + 2 < nt;
+        uint64_t* const bar = lane == 1 ? &sh->full[1][vslot] : lane == 2 && more ? &sh->full[0][kslot] : &sh->p_ready[st];
+        const uint32_t par = lane == 1 ? vturn : lane == 2 && more ? kturn : turn_p[st];
+        ok = wait_warp(sh, bar, par & 1, a.status);
+        ++turn_p[st];
+        if (!ok) break;
+        fence_after_sync();
+        const uint32_t vd = vlo + vslot * (kSlot >> 4), ts = tmem_s + 128 * st + 64, to = tmem_o + 128 * st;
+#pragma unroll
+        for (int k = 0; k < kRows / 16; ++k)
+          mma_ta_by(lead, to, ts + 8 * k, pack2(vd + k * 128, hi), id_pv, (i > 1 || k > 0) ? 1u : 0u);
+        commit_by(lead, &sh->empty[1][vslot]);
+        if (++vslot == kSlots) {
+          vslot = 0;
+          ++vturn;
+        }
+        if (more) qk(st);
+      }
+      if (ok) commit_by(lead, &sh->done);
     }
+    // nothing of this warp may be in flight when TMEM is freed
+    commit_by(lead, &sh->drain);
+    settle(&sh->drain, 0);
     __syncwarp();
   } else {
     // ---- softmax: thread = row, warpgroup = stream ----
