@@ -111,13 +111,15 @@ __device__ __forceinline__ void commit_by(uint32_t lead, uint64_t* bar) {
       "r"(lead)
       : "memory");
 }
-// TMA: a 4-D tile (channel, head, row of the page, page).
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
-                                            uint64_t* bar) {
+// TMA: a 5-D tile (channel of 64, row of 8, 64-channel block, group of 8 rows,
+// page), by the lane with `lead` set.
+__device__ __forceinline__ void tma_load_by(uint32_t lead, uint32_t dst, const CUtensorMap* map, int block, int group,
+                                            int page, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
-          "r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      "{\n.reg .pred q;\nsetp.ne.b32 q, %7, 0;\n"
+      "@q cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4, %5}], "
+      "[%6];\n}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(block), "r"(group), "r"(page), "r"(bar), "r"(lead)
       : "memory");
 }
 // Two fp32 operations at once.
@@ -371,7 +373,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                const uint32_t keep, const uint32_t sign) {
   constexpr int kSlot = kRows * D * 2;       // bytes of a ring slot
   constexpr int kSlots = kRingBytes / kSlot / 2;  // of K, and of V: 3 at D = 128, 6 at D = 64
-  constexpr int kHalf = kRows * 128;          // bytes of a 64-channel block
+  // A slot holds its rows in groups of eight, each 64-channel block of a group
+  // as 8 x 128 swizzled bytes: one copy then brings every channel of a box.
+  // (The query tile is the usual one, a block of all 128 rows after another.)
+  constexpr int kGroup = 8 * D * 2;  // bytes of eight rows
+  constexpr int kHalf = kRows * 128;  // bytes of a 64-channel block of the query tile
   extern __shared__ __align__(1024) uint8_t ring[];
   uint8_t* const qtile = ring + kRingBytes;
   Shared* const sh = reinterpret_cast<Shared*>(qtile + kSlot);
@@ -417,18 +423,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int boxes = kRows / box;         // of a tile
     const int batch = 32 / boxes;          // tiles whose pages the lanes hold
     const uint32_t per_page = a.page / box;  // boxes of a page
+    const uint32_t lead = lane == 0;
     int slot = 0;
     uint32_t turn = 0;  // times the ring has been gone round
     int64_t copies = 0;
     bool ok = true;
-    int page = 0, line = 0, nonempty = 0;
-    // lane i: page and first line of box i of the batch that starts at tile j
+    int page = 0, nonempty = 0;
+    // lane i: page of box i of the batch that starts at tile j
     auto look_up = [&](const Segment& g, int j) {
       const uint32_t at = static_cast<uint32_t>(j * boxes + lane);
       const bool in = lane < batch * boxes && j + lane / boxes < g.j1 && at * box < static_cast<uint32_t>(g.seen);
-      const uint32_t col = at / per_page;
-      line = static_cast<int>((at - col * per_page) * box);
-      page = in ? a.table[static_cast<int64_t>(g.n) * a.width + col] : 0;
+      page = in ? a.table[static_cast<int64_t>(g.n) * a.width + at / per_page] : 0;
     };
     // a page outside the cache is recorded, and the item's rows become zero (the copy itself writes zeros)
     auto check = [&](int* flag) {
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       for (int j = g.j0; j < g.j1; j += batch) {
         check(flag);
-        const int now_page = page, now_line = line;
+        const int pages = page;
         if (j + batch < g.j1)
           look_up(g, j + batch);
         else
@@ -460,17 +465,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = j; t < min(j + batch, g.j1); ++t) {
           if (turn > 0) ok = ok && wait_warp(sh, &sh->empty[which][slot], (turn - 1) & 1, a.status);
           if (!ok) continue;
-          uint64_t* const bar = &sh->full[which][slot];
           const int here = min(boxes, (g.seen - t * kRows + box - 1) / box);  // boxes with a key that is seen
-          if (lane == 0) mbar_expect_tx(bar, static_cast<uint32_t>(here * box * D * 2));
+          if (lane == 0) mbar_expect_tx(&sh->full[which][slot], static_cast<uint32_t>(here * box * D * 2));
+          __syncwarp();
+          const uint32_t bar = smem_addr(&sh->full[which][slot]);
+          uint32_t dst = dst0 + slot * kSlot;
+          uint32_t part = static_cast<uint32_t>(t * boxes) % per_page;  // box within its page
           for (int i = 0; i < here; ++i) {
-            const int from = (t - j) * boxes + i;
-            const int pg = __shfl_sync(~0u, now_page, from), ln = __shfl_sync(~0u, now_line, from);
-            if (lane == 0) {
-              const uint32_t dst = dst0 + slot * kSlot + i * box * 128;
-#pragma unroll
-              for (int x = 0; x < D; x += 64) tma_load_4d(dst + (x / 64) * kHalf, map, x, g.hk, ln, pg, bar);
-            }
+            const int pg = __shfl_sync(~0u, pages, (t - j) * boxes + i);
+            tma_load_by(lead, dst, map, g.hk * (D / 64), static_cast<int>(part) * (box / 8), pg, bar);
+            dst += box * D * 2;
+            if (++part == per_page) part = 0;
           }
           ++copies;
           if (++slot == kSlots) {
@@ -492,9 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // bf16 A and B
     constexpr uint32_t id_qk = idesc(kRows, kRows) | kBf16, id_pv = idesc(kRows, D, false, true) | kBf16;
     // matrix descriptors: the low words are sums that never carry
-    const uint64_t q0 = desc_kmajor(smem_addr(qtile), kRows, 0, 0), k0 = desc_kmajor(smem_addr(ring), kRows, 0, 0),
-                   v0 = desc_mnmajor(smem_addr(ring) + kRingBytes / 2, kHalf, 0);
-    const uint32_t hi = static_cast<uint32_t>(q0 >> 32);
+    const uint64_t q0 = sdesc(smem_addr(qtile), 16), k0 = sdesc(smem_addr(ring), 16),
+                   v0 = sdesc(smem_addr(ring) + kRingBytes / 2, 1024);
+    // high words: the bytes from one group of eight rows to the next, with the layout's constant bits
+    const uint32_t hi = static_cast<uint32_t>(q0 >> 32), hi_kv = hi - (1024 >> 4) + (kGroup >> 4);
     const uint32_t qlo = static_cast<uint32_t>(q0), klo = static_cast<uint32_t>(k0), vlo = static_cast<uint32_t>(v0);
     const uint32_t lead = lane == 0;
     int kslot = 0, vslot = 0;
@@ -504,8 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t kd = klo + kslot * (kSlot >> 4), ts = tmem_s + 128 * st;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const uint32_t step = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
-        mma_by(lead, ts, pack2(qlo + step, hi), pack2(kd + step, hi), id_qk, k > 0);
+        mma_by(lead, ts, pack2(qlo + (k >> 2) * (kHalf >> 4) + (k & 3) * 2, hi),
+               pack2(kd + (k >> 2) * (1024 >> 4) + (k & 3) * 2, hi_kv), id_qk, k > 0);
       }
       commit_by(lead, &sh->s_full[st]);
       commit_by(lead, &sh->empty[0][kslot]);
@@ -540,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t vd = vlo + vslot * (kSlot >> 4), ts = tmem_s + 128 * st + 64, to = tmem_o + 128 * st;
 #pragma unroll
         for (int k = 0; k < kRows / 16; ++k)
-          mma_ta_by(lead, to, ts + 8 * k, pack2(vd + k * 128, hi), id_pv, (i > 1 || k > 0) ? 1u : 0u);
+          mma_ta_by(lead, to, ts + 8 * k, pack2(vd + k * (2 * kGroup >> 4), hi_kv), id_pv, (i > 1 || k > 0) ? 1u : 0u);
         commit_by(lead, &sh->empty[1][vslot]);
         if (++vslot == kSlots) {
           vslot = 0;
@@ -609,10 +615,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int slot = static_cast<int>(vpos % kSlots);
           const bool here = wait_warp(sh, &sh->full[1][slot], static_cast<uint32_t>((vpos / kSlots) & 1), a.status);
           if (here && k0 + row >= s.seen) {
-            uint8_t* const v = ring + kRingBytes / 2 + slot * kSlot + row * 128;
+            uint8_t* const v = ring + kRingBytes / 2 + slot * kSlot + (row >> 3) * kGroup + (row & 7) * 128;
 #pragma unroll
             for (int c = 0; c < D * 2; c += 16)
-              *reinterpret_cast<uint4*>(v + (c / 128) * kHalf + c % 128) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(v + (c / 128) * 1024 + c % 128) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_async_smem();
         }
@@ -836,15 +842,18 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// Pages [pages][page][Hkv][D]; box: 64 channels of one head, `box` rows of one page.
+// Pages [pages][page][Hkv][D] as (64 channels, row of 8, 64-channel block of
+// any head, group of 8 rows, page); box: every channel of one head, `box` rows
+// of one page.
 bool page_map(CUtensorMap* m, const void* base, const PagedArgs& a, int box) {
   const EncodeFn enc = encode_fn();
   if (enc == nullptr) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.Hkv, (cuuint64_t)a.page, (cuuint64_t)a.pages};
-  const cuuint64_t row = (cuuint64_t)a.D * 2;
-  const cuuint64_t strides[3] = {row, row * a.Hkv, row * a.Hkv * a.page};
-  const cuuint32_t boxes[4] = {64, 1, (cuuint32_t)box, 1}, ones[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, boxes, ones,
+  const cuuint32_t blocks = (cuuint32_t)a.D / 64;
+  const cuuint64_t row = (cuuint64_t)a.D * 2 * a.Hkv;
+  const cuuint64_t dims[5] = {64, 8, (cuuint64_t)blocks * a.Hkv, (cuuint64_t)a.page / 8, (cuuint64_t)a.pages};
+  const cuuint64_t strides[4] = {row, 128, row * 8, row * a.page};
+  const cuuint32_t boxes[5] = {64, 8, blocks, (cuuint32_t)box / 8, 1}, ones[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, boxes, ones,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
