@@ -87,39 +87,28 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16])
       : "memory");
 }
 
-// Products and their commit, issued by the one lane of a converged warp that
-// has `lead` set: the warp's control flow, and with it the descriptors, stay
-// uniform. D (+)= A B, kind::f16, A and B in shared memory ...
-__device__ __forceinline__ void mma_by(uint32_t lead, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(lead));
+// One lane of the converged warp, the same one every time. What is issued by
+// one thread for the CTA stands behind this: the compiler then knows that a
+// single thread issues it, and leaves out a loop over the active ones.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
-// ... or A (16-bit, two K elements a 32-bit column) in TMEM.
-__device__ __forceinline__ void mma_ta_by(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id,
-                                          uint32_t acc) {
+// D (+)= A B, kind::f16: A (16-bit, two K elements a 32-bit column) from TMEM.
+__device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(id), "r"(acc), "r"(lead));
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(id), "r"(acc));
 }
-__device__ __forceinline__ void commit_by(uint32_t lead, uint64_t* bar) {
+// TMA: a 5-D tile (channel of 64, row of 8, 64-channel block, group of 8 rows, page).
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int block, int group, int page,
+                                            uint32_t bar) {
   asm volatile(
-      "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar)),
-      "r"(lead)
-      : "memory");
-}
-// TMA: a 5-D tile (channel of 64, row of 8, 64-channel block, group of 8 rows,
-// page), by the lane with `lead` set.
-__device__ __forceinline__ void tma_load_by(uint32_t lead, uint32_t dst, const CUtensorMap* map, int block, int group,
-                                            int page, uint32_t bar) {
-  asm volatile(
-      "{\n.reg .pred q;\nsetp.ne.b32 q, %7, 0;\n"
-      "@q cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4, %5}], "
-      "[%6];\n}\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(block), "r"(group), "r"(page), "r"(bar), "r"(lead)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(block), "r"(group), "r"(page), "r"(bar)
       : "memory");
 }
 // Two fp32 operations at once.
@@ -423,7 +412,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int boxes = kRows / box;         // of a tile
     const int batch = 32 / boxes;          // tiles whose pages the lanes hold
     const uint32_t per_page = a.page / box;  // boxes of a page
-    const uint32_t lead = lane == 0;
     int slot = 0;
     uint32_t turn = 0;  // times the ring has been gone round
     int64_t copies = 0;
@@ -473,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t part = static_cast<uint32_t>(t * boxes) % per_page;  // box within its page
           for (int i = 0; i < here; ++i) {
             const int pg = __shfl_sync(~0u, pages, (t - j) * boxes + i);
-            tma_load_by(lead, dst, map, g.hk * (D / 64), static_cast<int>(part) * (box / 8), pg, bar);
+            if (elect()) tma_load_5d(dst, map, g.hk * (D / 64), static_cast<int>(part) * (box / 8), pg, bar);
             dst += box * D * 2;
             if (++part == per_page) part = 0;
           }
@@ -502,19 +490,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // high words: the bytes from one group of eight rows to the next, with the layout's constant bits
     const uint32_t hi = static_cast<uint32_t>(q0 >> 32), hi_kv = hi - (1024 >> 4) + (kGroup >> 4);
     const uint32_t qlo = static_cast<uint32_t>(q0), klo = static_cast<uint32_t>(k0), vlo = static_cast<uint32_t>(v0);
-    const uint32_t lead = lane == 0;
     int kslot = 0, vslot = 0;
     uint32_t kturn = 0, vturn = 0, turn = 0, turn_p[2] = {0, 0};
     bool ok = true;
     auto qk = [&](int st) {
       const uint32_t kd = klo + kslot * (kSlot >> 4), ts = tmem_s + 128 * st;
+      if (elect()) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        mma_by(lead, ts, pack2(qlo + (k >> 2) * (kHalf >> 4) + (k & 3) * 2, hi),
-               pack2(kd + (k >> 2) * (1024 >> 4) + (k & 3) * 2, hi_kv), id_qk, k > 0);
+        for (int k = 0; k < D / 16; ++k)
+          mma(ts, pack2(qlo + (k >> 2) * (kHalf >> 4) + (k & 3) * 2, hi),
+              pack2(kd + (k >> 2) * (1024 >> 4) + (k & 3) * 2, hi_kv), id_qk, k > 0);
+        mma_commit(&sh->s_full[st]);
+        mma_commit(&sh->empty[0][kslot]);
       }
-      commit_by(lead, &sh->s_full[st]);
-      commit_by(lead, &sh->empty[0][kslot]);
       if (++kslot == kSlots) {
         kslot = 0;
         ++kturn;
@@ -544,20 +532,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         fence_after_sync();
         const uint32_t vd = vlo + vslot * (kSlot >> 4), ts = tmem_s + 128 * st + 64, to = tmem_o + 128 * st;
+        if (elect()) {
 #pragma unroll
-        for (int k = 0; k < kRows / 16; ++k)
-          mma_ta_by(lead, to, ts + 8 * k, pack2(vd + k * (2 * kGroup >> 4), hi_kv), id_pv, (i > 1 || k > 0) ? 1u : 0u);
-        commit_by(lead, &sh->empty[1][vslot]);
+          for (int k = 0; k < kRows / 16; ++k)
+            mma_ta(to, ts + 8 * k, pack2(vd + k * (2 * kGroup >> 4), hi_kv), id_pv, (i > 1 || k > 0) ? 1u : 0u);
+          mma_commit(&sh->empty[1][vslot]);
+        }
         if (++vslot == kSlots) {
           vslot = 0;
           ++vturn;
         }
         if (more) qk(st);
       }
-      if (ok) commit_by(lead, &sh->done);
+      if (ok && elect()) mma_commit(&sh->done);
     }
     // nothing of this warp may be in flight when TMEM is freed
-    commit_by(lead, &sh->drain);
+    if (elect()) mma_commit(&sh->drain);
     settle(&sh->drain, 0);
     __syncwarp();
   } else {
