@@ -613,84 +613,68 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_smem();
         }
         if (warp_used) {
-          // The row is read twice, 32 scores at a time with the next 32 on
-          // their way: for its maximum, then for its probabilities. Short
-          // loops on purpose: unrolled, this code drove that of the issuing
-          // and loading warps out of the instruction cache.
+          // One pass over the row, 32 scores at a time with the next 32 on
+          // their way: probabilities against the maximum so far, and the
+          // maximum of this tile with them. P stays in registers until that
+          // has not grown by more than 2^8 (else the pass is made again from
+          // S, which is still there: in a stream's first tile, and rarely after).
           const int open = limit - k0;  // keys of the tile that the row sees
-          const bool masked = __any_sync(~0u, open < kRows);
-          auto mask = [&](uint32_t(&x)[32], int c0) {
-            if (masked) {
+          if (__any_sync(~0u, open < kRows)) {  // an item's last tiles: -inf into S first, off the common path
+#pragma unroll 1
+            for (int c0 = 0; c0 < kRows; c0 += 32) {
+              uint32_t y[32];
+              tmem_ask(my_s + c0, y);
+              tmem_got(y);
 #pragma unroll
               for (int c = 0; c < 32; ++c)
-                if (c0 + c >= open) x[c] = 0xff800000u;  // -inf
+                if (c0 + c >= open) y[c] = 0xff800000u;
+              tmem_st(my_s + c0, y);
             }
-          };
-          uint32_t xa[32], xb[32];
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto most = [&](const uint32_t(&x)[32]) {
-#pragma unroll
-            for (int c = 0; c < 32; c += 2)
-              top[c / 2 & 3] = fmaxf(fmaxf(top[c / 2 & 3], __uint_as_float(x[c])), __uint_as_float(x[c + 1]));
-          };
-          tmem_ask(my_s, xa);
-#pragma unroll 1
-          for (int c0 = 0; c0 < kRows; c0 += 64) {
-            tmem_got(xa);
-            tmem_ask(my_s + c0 + 32, xb);
-            mask(xa, c0);
-            most(xa);
-            tmem_got(xb);
-            if (c0 + 64 < kRows) tmem_ask(my_s + c0 + 64, xa);
-            mask(xb, c0 + 32);
-            most(xb);
+            tmem_st_wait();
           }
-          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-          const float mn = mx * sc;
-          const bool grow = mn > m + kRescale;  // m = -inf: any finite maximum
-          if (__any_sync(~0u, grow)) {
+          const uint64_t sc2 = pack2(__float_as_uint(sc), __float_as_uint(sc));
+          uint32_t p[2][32];
+          uint64_t sum[4];
+          for (bool first = true;; first = false) {
+            const float ref = m == -INFINITY ? 0.f : m;
+            const uint64_t ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            uint32_t x[2][32];
+            sum[0] = sum[1] = sum[2] = sum[3] = 0;
+            tmem_ask(my_s, x[0]);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              uint32_t(&y)[32] = x[h & 1];
+              tmem_got(y);
+              if (h < 3) tmem_ask(my_s + 32 * (h + 1), x[(h + 1) & 1]);
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                top[c / 2 & 3] = fmaxf(fmaxf(top[c / 2 & 3], __uint_as_float(y[c])), __uint_as_float(y[c + 1]));
+                const float2 t = unpack2(fma2(pack2(y[c], y[c + 1]), sc2, ref2));
+                const float e0 = ex2(t.x), e1 = ex2(t.y);
+                sum[c / 2 & 3] = add2(sum[c / 2 & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
+                p[h / 2][16 * (h & 1) + c / 2] = pack_bf16(e0, e1);
+              }
+            }
+            const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+            const bool grow = first && mn > m + kRescale;  // m = -inf: any finite maximum
+            if (!__any_sync(~0u, grow)) break;
             const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - mn)) : 1.f;
             if (grow) m = mn;
             l *= f;
             if (i >= 2) {  // the stream's O exists, and is complete: S of this tile was issued after it
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
-                tmem_ask(my_o + c, xa);
-                tmem_got(xa);
+                tmem_ask(my_o + c, x[0]);
+                tmem_got(x[0]);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) xa[k] = __float_as_uint(__uint_as_float(xa[k]) * f);
-                tmem_st(my_o + c, xa);
+                for (int k = 0; k < 32; ++k) x[0][k] = __float_as_uint(__uint_as_float(x[0][k]) * f);
+                tmem_st(my_o + c, x[0]);
               }
             }
           }
-          const float ref = m == -INFINITY ? 0.f : m;
-          const uint64_t sc2 = pack2(__float_as_uint(sc), __float_as_uint(sc));
-          const uint64_t ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
-          uint64_t sum[4] = {0, 0, 0, 0};
-          // P takes the columns of the second half, from its end: each store is over scores that are read
-          auto probabilities = [&](const uint32_t(&x)[32], int c0) {
-            uint32_t p[16];
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const float2 t = unpack2(fma2(pack2(x[c], x[c + 1]), sc2, ref2));
-              const float e0 = ex2(t.x), e1 = ex2(t.y);
-              sum[c / 2 & 3] = add2(sum[c / 2 & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
-              p[c / 2] = pack_bf16(e0, e1);
-            }
-            tmem_st(my_s + 64 + c0 / 2, p);
-          };
-          tmem_ask(my_s + 96, xb);
-#pragma unroll 1
-          for (int c0 = 64; c0 >= 0; c0 -= 64) {
-            tmem_got(xb);
-            tmem_ask(my_s + c0, xa);
-            mask(xb, c0 + 32);
-            probabilities(xb, c0 + 32);
-            tmem_got(xa);
-            if (c0 > 0) tmem_ask(my_s + 32, xb);
-            mask(xa, c0);
-            probabilities(xa, c0);
-          }
+          tmem_st(my_s + 64, p[0]);
+          tmem_st(my_s + 96, p[1]);
           const float2 all = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
           l += all.x + all.y;
           tmem_st_wait();
