@@ -12,10 +12,16 @@
 // The backward forms yn, s and h' again from y, z and h: it reads those rows
 // anyway, and needs no statistics or h' from the forward.
 //
-// Bound: HBM; each tensor is read or written once. A row stays in registers
-// between its reductions. A group of kGroup threads takes a row; a thread
-// holds kVecs vectors of kVec elements (16 bytes where width and dtype allow,
-// one element otherwise: rows of an odd width start unaligned).
+// Bound: HBM; each tensor is read or written once. A row stays at hand between
+// its reductions. A group of kGroup threads takes a row; a thread holds kVecs
+// 16-byte vectors of it.
+//
+// Rows of an odd width start anywhere within 16 bytes. There a group works on
+// the aligned vectors that cover its row, `shift` elements before its start;
+// what lies outside the row is set to zero as it is read and not written. The
+// rows of a group are a multiple of the vector's elements apart, so its shift
+// is the same for all of them, and with it a thread's columns: weights and
+// their gradients stay in registers as for other widths.
 //
 // x - xn mean(x xn) takes x's part along the row out. In a row of one element
 // that is all of x but the share eps r^2 that eps keeps, far below the
@@ -43,9 +49,7 @@ struct NormArgs {
 
 // kVec consecutive elements as loaded.
 template <typename T, int V>
-struct Raw {
-  T x[V];
-};
+struct Raw;
 template <>
 struct alignas(16) Raw<__nv_bfloat16, 8> {
   uint4 u;
@@ -79,27 +83,9 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
   return r;
 }
-__device__ __forceinline__ float mul(float a, float b) { return a * b; }
-__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
 __device__ __forceinline__ float sum(F2 a) { return both(a).x + both(a).y; }
-__device__ __forceinline__ float sum(float a) { return a; }
-template <int V>
-struct PackOf {
-  using type = F2;
-  static constexpr int n = V / 2;
-  static __device__ __forceinline__ F2 all(float x) { return f2(x, x); }
-};
-template <>
-struct PackOf<1> {
-  using type = float;
-  static constexpr int n = 1;
-  static __device__ __forceinline__ float all(float x) { return x; }
-};
+__device__ __forceinline__ F2 all(float x) { return f2(x, x); }
 
-template <typename T>
-__device__ __forceinline__ void unpack(const Raw<T, 1>& r, float (&x)[1]) {
-  x[0] = ldf(&r.x[0]);
-}
 __device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 8>& r, F2 (&x)[4]) {
   const uint32_t u[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
 #pragma unroll
@@ -108,10 +94,6 @@ __device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, 8>& r, F2 (&x)[4
 __device__ __forceinline__ void unpack(const Raw<float, 4>& r, F2 (&x)[2]) {
   x[0] = f2(r.u.x, r.u.y);
   x[1] = f2(r.u.z, r.u.w);
-}
-template <typename T>
-__device__ __forceinline__ void put(T* p, const float (&x)[1]) {
-  stf(p, x[0]);
 }
 __device__ __forceinline__ void put(__nv_bfloat16* p, const F2 (&x)[4]) {
   uint32_t u[4];
@@ -126,39 +108,84 @@ __device__ __forceinline__ void put(float* p, const F2 (&x)[2]) {
   const float2 a = both(x[0]), b = both(x[1]);
   *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
 }
-// Weights c .. c + V - 1 (c < width; 1 without weights).
-__device__ __forceinline__ void weights(const float* w, int c, float (&x)[1]) { x[0] = w ? w[c] : 1.f; }
-template <int N>
-__device__ __forceinline__ void weights(const float* w, int c, F2 (&x)[N]) {
+// A thread's vectors of a row: vector j starts at column at(j). ODD: rows
+// start `shift` elements into an aligned vector, and the first and last one
+// may reach over the row's ends.
+template <int V, int G, bool ODD>
+struct Span {
+  int c0, width;
+  __device__ __forceinline__ Span(int lane, int64_t row, int w)
+      : c0(lane * V - (ODD ? static_cast<int>(row % V * (w % V) % V) : 0)), width(w) {}
+  __device__ __forceinline__ int at(int j) const { return c0 + j * G * V; }
+  __device__ __forceinline__ bool any(int j) const { return at(j) < width; }
+  __device__ __forceinline__ bool whole(int j) const { return !ODD || (at(j) >= 0 && at(j) + V <= width); }
+  // x's values outside the row set to zero
+  template <int N>
+  __device__ __forceinline__ void clip(int j, F2 (&x)[N]) const {
+    if (whole(j)) return;
 #pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    const float4 t = w ? *reinterpret_cast<const float4*>(w + c + 2 * i) : make_float4(1.f, 1.f, 1.f, 1.f);
-    x[i] = f2(t.x, t.y);
-    x[i + 1] = f2(t.z, t.w);
+    for (int i = 0; i < N; ++i) {
+      const float2 t = both(x[i]);
+      const int c = at(j) + 2 * i;
+      x[i] = f2(c >= 0 && c < width ? t.x : 0.f, c >= -1 && c + 1 < width ? t.y : 0.f);
+    }
   }
-}
+  template <typename T, int N>
+  __device__ __forceinline__ void store(T* row, int j, const F2 (&x)[N]) const {
+    if (whole(j)) {
+      put(row + at(j), x);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 t = both(x[i]);
+      const int c = at(j) + 2 * i;
+      if (c >= 0 && c < width) stf(row + c, t.x);
+      if (c >= -1 && c + 1 < width) stf(row + c + 1, t.y);
+    }
+  }
+  // weights of vector j (1 without weights)
+  template <int N>
+  __device__ __forceinline__ void weights(const float* w, int j, F2 (&x)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      float t[4] = {1.f, 1.f, 1.f, 1.f};
+      const int c = at(j) + 2 * i;
+      if (w != nullptr) {
+        if constexpr (ODD) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) t[k] = c + k >= 0 && c + k < width ? w[c + k] : 0.f;
+        } else {
+          *reinterpret_cast<float4*>(t) = *reinterpret_cast<const float4*>(w + c);
+        }
+      }
+      x[i] = f2(t[0], t[1]);
+      x[i + 1] = f2(t[2], t[3]);
+    }
+  }
+};
 
 // A thread's weights: in registers for all its rows where it holds one vector
 // of a row (read every row they cost the L1 more than the row itself: 4 bytes
 // an element against 2), from L1 each time where it holds more.
-template <int V, int NV, int G>
+template <int V, int NV, int G, bool ODD>
 struct Weights {
-  using F = typename PackOf<V>::type;
-  static constexpr bool kKept = V > 1 && NV == 1;
+  static constexpr int N = V / 2;
+  static constexpr bool kKept = NV == 1;
   const float* w;
-  int c0;
-  F kept[kKept ? PackOf<V>::n : 1];
-  __device__ __forceinline__ Weights(const float* p, int lane, int width) : w(p), c0(lane * V) {
+  const Span<V, G, ODD>& span;
+  F2 kept[kKept ? N : 1];
+  __device__ __forceinline__ Weights(const float* p, const Span<V, G, ODD>& sp) : w(p), span(sp) {
     if constexpr (kKept) {
-      if (c0 < width) weights(w, c0, kept);
+      if (span.any(0)) span.weights(w, 0, kept);
     }
   }
-  __device__ __forceinline__ void get(int j, F (&x)[PackOf<V>::n]) const {
+  __device__ __forceinline__ void get(int j, F2 (&x)[N]) const {
     if constexpr (kKept) {
 #pragma unroll
-      for (int i = 0; i < PackOf<V>::n; ++i) x[i] = kept[i];
+      for (int i = 0; i < N; ++i) x[i] = kept[i];
     } else {
-      weights(w, c0 + j * G * V, x);
+      span.weights(w, j, x);
     }
   }
 };
@@ -211,50 +238,52 @@ __device__ __forceinline__ void gate(F2 z, F2& s, F2& n) {
   n = f2(b.x, b.y);
 }
 
-// How a thread gets its share of its group's rows. 16-byte vectors go by
-// asynchronous copies, up to four rows ahead, into a ring of shared memory
-// in which a thread reads only what it copied itself: the rows ahead hold no
-// registers and need no barrier. Single elements (odd widths) are loaded when
-// their row's turn comes. Tensors that are absent are not read.
+// How a thread gets its share of its group's rows: 16-byte vectors by
+// asynchronous copies, up to four rows ahead, into a ring of shared memory in
+// which a thread reads only what it copied itself. The rows ahead hold no
+// registers and need no barrier. Tensors that are absent are not read.
 enum Which { kY, kZ, kDho, kH, kDn };  // a backward without the next norm has no kH, kDn; a forward the first two and kH
-template <typename T, int V, int NV, int G, int NT, int SLOTS>
+template <typename T, int V, int NV, int G, int NT, bool ODD, int SLOTS>
 struct Rows {
   static constexpr int kStage = SLOTS * NV * NT * 16;  // bytes
   static constexpr int kFit = 200 * 1024 / kStage;
-  static constexpr int kDepth = V == 1 ? 1 : (kFit < 4 ? kFit : 4);
-  static constexpr size_t kBytes = V == 1 ? 0 : static_cast<size_t>(kDepth) * kStage;
+  static constexpr int kDepth = kFit < 4 ? kFit : 4;
+  static constexpr size_t kBytes = static_cast<size_t>(kDepth) * kStage;
   static_assert(kDepth >= 1, "");
   const NormArgs& a;
+  const Span<V, G, ODD>& span;
   const void* const (&from)[SLOTS];
   uint8_t* ring;
   int64_t step, ahead;  // rows between two turns; the next row to copy
   int in, out;          // ring positions
-  int lane;
-  Raw<T, V> direct[V == 1 ? SLOTS : 1][V == 1 ? NV : 1];
 
-  __device__ __forceinline__ Rows(const NormArgs& args, const void* const (&f)[SLOTS], uint8_t* sm, int64_t row,
-                                  int64_t st, int ln)
-      : a(args), from(f), ring(sm), step(st), ahead(row), in(0), out(kDepth - 1), lane(ln) {
-    if constexpr (V > 1)
-      for (int i = 0; i + 1 < kDepth; ++i) copy();
+  __device__ __forceinline__ Rows(const NormArgs& args, const Span<V, G, ODD>& sp, const void* const (&f)[SLOTS],
+                                  uint8_t* sm, int64_t row, int64_t st)
+      : a(args), span(sp), from(f), ring(sm), step(st), ahead(row), in(0), out(kDepth - 1) {
+    for (int i = 0; i + 1 < kDepth; ++i) copy();
+  }
+  __device__ __forceinline__ uint8_t* slot(int stage, int s, int j) const {
+    return ring + stage * kStage + ((s * NV + j) * NT + threadIdx.x) * 16;
   }
   __device__ __forceinline__ void copy() {
     if (ahead < a.rows) {
       const int64_t base = ahead * a.width;
 #pragma unroll
-      for (int s = 0; s < SLOTS; ++s)
-        if (from[s])
-#pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            const int c = (j * G + lane) * V;
-            if (c < a.width) {
-              const uint32_t dst =
-                  static_cast<uint32_t>(__cvta_generic_to_shared(ring + in * kStage + ((s * NV + j) * NT + threadIdx.x) * 16));
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
-                           "l"(static_cast<const T*>(from[s]) + base + c)
-                           : "memory");
-            }
+      for (int j = 0; j < NV; ++j)
+        if (span.any(j)) {
+          int bytes = 16;
+          if constexpr (ODD) {  // the last vector of the tensor may be short
+            const int64_t left = (a.rows * a.width - base - span.at(j)) * static_cast<int64_t>(sizeof(T));
+            if (left < 16) bytes = static_cast<int>(left);
           }
+#pragma unroll
+          for (int s = 0; s < SLOTS; ++s)
+            if (from[s])
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                               static_cast<uint32_t>(__cvta_generic_to_shared(slot(in, s, j)))),
+                           "l"(static_cast<const T*>(from[s]) + base + span.at(j)), "r"(bytes)
+                           : "memory");
+        }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     ahead += step;
@@ -262,36 +291,20 @@ struct Rows {
   }
   // The next row of this group is at hand afterwards.
   __device__ __forceinline__ void turn() {
-    if constexpr (V > 1) {
-      copy();
-      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
-      if (++out == kDepth) out = 0;
-    } else {
-      if (ahead < a.rows) {
-        const int64_t base = ahead * a.width;
-#pragma unroll
-        for (int s = 0; s < SLOTS; ++s)
-          if (from[s])
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-              if (j * G + lane < a.width) direct[s][j].x[0] = static_cast<const T*>(from[s])[base + j * G + lane];
-      }
-      ahead += step;
-    }
+    copy();
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    if (++out == kDepth) out = 0;
   }
-  __device__ __forceinline__ Raw<T, V> get(int s, int j) const {
-    if constexpr (V > 1)
-      return *reinterpret_cast<const Raw<T, V>*>(ring + out * kStage + ((s * NV + j) * NT + threadIdx.x) * 16);
-    else
-      return direct[s][j];
+  __device__ __forceinline__ void get(int s, int j, F2 (&x)[V / 2]) const {
+    unpack(*reinterpret_cast<const Raw<T, V>*>(slot(out, s, j)), x);
+    span.clip(j, x);
   }
 };
 
-template <typename T, int V, int NV, int G, int NT>
+template <typename T, int V, int NV, int G, int NT, bool ODD>
 __global__ void __launch_bounds__(NT) norm_fwd_kernel(const NormArgs a) {
-  using P = PackOf<V>;
-  using F = typename P::type;
-  constexpr int kGroups = NT / G, NP = P::n;
+  using F = F2;
+  constexpr int kGroups = NT / G, NP = V / 2;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float sh[2 * 3 * 32];
   int turn = 0;
@@ -299,36 +312,37 @@ __global__ void __launch_bounds__(NT) norm_fwd_kernel(const NormArgs a) {
   const float inv = 1.f / static_cast<float>(a.width);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
   int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / G;
-  const Weights<V, NV, G> wpost(a.wpost, lane, a.width), wpre(a.wpre, lane, a.width);
+  const Span<V, G, ODD> span(lane, row, a.width);
+  const Weights<V, NV, G, ODD> wpost(a.wpost, span), wpre(a.wpre, span);
   const void* const from[3] = {a.y, a.z, a.h};
-  Rows<T, V, NV, G, NT, 3> in(a, from, ring, row, step, lane);
+  Rows<T, V, NV, G, NT, ODD, 3> in(a, span, from, ring, row, step);
   // every group of a CTA makes the same number of turns (the reductions are collective)
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGroups; r0 < a.rows; r0 += step, row += step) {
     in.turn();
     const bool live = row < a.rows;
     const int64_t base = row * a.width;
-    F x[NV][NP], hh = P::all(0.f);
+    auto here = [&](int j) { return live && span.any(j); };
+    F x[NV][NP], hh = all(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (live && (j * G + lane) * V < a.width) {
-        unpack(in.get(kY, j), x[j]);
+      if (here(j)) {
+        in.get(kY, j, x[j]);
 #pragma unroll
         for (int i = 0; i < NP; ++i) hh = fma(x[j][i], x[j][i], hh);
       }
     float yy[1] = {sum(hh)};
     group_sum<G>(yy, sh, turn);
-    const F scale = P::all(rsqrtf(yy[0] * inv + a.eps) * a.b), keep = P::all(a.a);
-    hh = P::all(0.f);
+    const F scale = all(rsqrtf(yy[0] * inv + a.eps) * a.b), keep = all(a.a);
+    hh = all(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * G + lane) * V;
-      if (live && c < a.width) {
+      if (here(j)) {
         F w[NP], t[NP];
         wpost.get(j, w);
 #pragma unroll
         for (int i = 0; i < NP; ++i) x[j][i] = mul(x[j][i], mul(scale, w[i]));
         if (a.z) {
-          unpack(in.get(kZ, j), t);
+          in.get(kZ, j, t);
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
             F s, n;
@@ -337,11 +351,11 @@ __global__ void __launch_bounds__(NT) norm_fwd_kernel(const NormArgs a) {
           }
         }
         if (a.h) {
-          unpack(in.get(2, j), t);
+          in.get(2, j, t);
 #pragma unroll
           for (int i = 0; i < NP; ++i) x[j][i] = fma(keep, t[i], x[j][i]);
         }
-        put(static_cast<T*>(a.ho) + base + c, x[j]);
+        span.store(static_cast<T*>(a.ho) + base, j, x[j]);
 #pragma unroll
         for (int i = 0; i < NP; ++i) hh = fma(x[j][i], x[j][i], hh);
       }
@@ -349,16 +363,15 @@ __global__ void __launch_bounds__(NT) norm_fwd_kernel(const NormArgs a) {
     if (a.n) {
       float two[1] = {sum(hh)};
       group_sum<G>(two, sh, turn);
-      const F r = P::all(rsqrtf(two[0] * inv + a.eps));
+      const F r = all(rsqrtf(two[0] * inv + a.eps));
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (j * G + lane) * V;
-        if (live && c < a.width) {
+        if (here(j)) {
           F w[NP];
           wpre.get(j, w);
 #pragma unroll
           for (int i = 0; i < NP; ++i) x[j][i] = mul(x[j][i], mul(r, w[i]));
-          put(static_cast<T*>(a.n) + base + c, x[j]);
+          span.store(static_cast<T*>(a.n) + base, j, x[j]);
         }
       }
     }
@@ -366,11 +379,10 @@ __global__ void __launch_bounds__(NT) norm_fwd_kernel(const NormArgs a) {
 }
 
 // PRE: the next norm takes part (dn and w_pre are given).
-template <typename T, int V, int NV, int G, int NT, bool PRE>
+template <typename T, int V, int NV, int G, int NT, bool ODD, bool PRE>
 __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_kernel(const NormArgs a) {
-  using P = PackOf<V>;
-  using F = typename P::type;
-  constexpr int kGroups = NT / G, NP = P::n;
+  using F = F2;
+  constexpr int kGroups = NT / G, NP = V / 2;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float sh[2 * 3 * 32];
   int turn = 0;
@@ -382,24 +394,25 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int i = 0; i < NP; ++i) gpost[j][i] = gpre[PRE ? j : 0][i] = P::all(0.f);
+    for (int i = 0; i < NP; ++i) gpost[j][i] = gpre[PRE ? j : 0][i] = all(0.f);
   int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + group;
-  const Weights<V, NV, G> wpost(a.wpost, lane, a.width), wpre(PRE ? a.wpre : nullptr, lane, a.width);
+  const Span<V, G, ODD> span(lane, row, a.width);
+  const Weights<V, NV, G, ODD> wpost(a.wpost, span), wpre(PRE ? a.wpre : nullptr, span);
   constexpr int kSlots = PRE ? 5 : 3;
-  const void* const all[5] = {a.y, a.z, a.dho, a.h, a.dn};
-  const void* const(&from)[kSlots] = reinterpret_cast<const void* const(&)[kSlots]>(all);
-  Rows<T, V, NV, G, NT, kSlots> in(a, from, ring, row, step, lane);
+  const void* const five[5] = {a.y, a.z, a.dho, a.h, a.dn};
+  const void* const(&from)[kSlots] = reinterpret_cast<const void* const(&)[kSlots]>(five);
+  Rows<T, V, NV, G, NT, ODD, kSlots> in(a, span, from, ring, row, step);
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGroups; r0 < a.rows; r0 += step, row += step) {
     in.turn();
     const bool live = row < a.rows;
     const int64_t base = row * a.width;
-    auto here = [&](int j) { return live && (j * G + lane) * V < a.width; };
-    F yt = P::all(0.f);
+    auto here = [&](int j) { return live && span.any(j); };
+    F yt = all(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (here(j)) {
         F y[NP];
-        unpack(in.get(kY, j), y);
+        in.get(kY, j, y);
 #pragma unroll
         for (int i = 0; i < NP; ++i) yt = fma(y[i], y[i], yt);
       }
@@ -409,19 +422,18 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
     // yn, the gates and what follows from them are formed again in each stage
     // from the row at hand: registers, not instructions, limit the warps here.
     F hp[PRE ? NV : 1][NP];  // h'
-    F hh = P::all(0.f), hd = P::all(0.f);
+    F hh = all(0.f), hd = all(0.f);
     if constexpr (PRE) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (j * G + lane) * V;
         if (here(j)) {
           F t[NP], w[NP];
-          unpack(in.get(kY, j), t);
+          in.get(kY, j, t);
           wpost.get(j, w);
 #pragma unroll
-          for (int i = 0; i < NP; ++i) hp[j][i] = mul(mul(t[i], P::all(iy * a.b)), w[i]);
+          for (int i = 0; i < NP; ++i) hp[j][i] = mul(mul(t[i], all(iy * a.b)), w[i]);
           if (a.z) {
-            unpack(in.get(kZ, j), t);
+            in.get(kZ, j, t);
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
               F s, n;
@@ -430,11 +442,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
             }
           }
           if (a.h) {
-            unpack(in.get(kH, j), t);
+            in.get(kH, j, t);
 #pragma unroll
-            for (int i = 0; i < NP; ++i) hp[j][i] = fma(P::all(a.a), t[i], hp[j][i]);
+            for (int i = 0; i < NP; ++i) hp[j][i] = fma(all(a.a), t[i], hp[j][i]);
           }
-          unpack(in.get(kDn, j), t);
+          in.get(kDn, j, t);
           wpre.get(j, w);
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
@@ -444,29 +456,28 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
         }
       }
     }
-    F ih = P::all(0.f), dk = ih, dp = ih;  // dh' = dh_out + dk d - dp h'
+    F ih = all(0.f), dk = ih, dp = ih;  // dh' = dh_out + dk d - dp h'
     if constexpr (PRE) {
       float two[2] = {sum(hh), sum(hd)};
       group_sum<G>(two, sh, turn);
       const float r = rsqrtf(two[0] * inv + a.eps);
-      ih = P::all(r);
-      dk = P::all(r * (one ? a.eps * r * r : 1.f));
-      dp = P::all(one ? 0.f : -(r * r * r) * (two[1] * inv));
+      ih = all(r);
+      dk = all(r * (one ? a.eps * r * r : 1.f));
+      dp = all(one ? 0.f : -(r * r * r) * (two[1] * inv));
     }
-    F ty = P::all(0.f);
+    F ty = all(0.f);
     F q[NV][NP];  // the gradient of yn, until dy is formed
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * G + lane) * V;
       if (here(j)) {
         F d[NP], w[NP], t[NP];
         if (a.dho)
-          unpack(in.get(kDho, j), d);
+          in.get(kDho, j, d);
         else
 #pragma unroll
-          for (int i = 0; i < NP; ++i) d[i] = P::all(0.f);
+          for (int i = 0; i < NP; ++i) d[i] = all(0.f);
         if constexpr (PRE) {
-          unpack(in.get(kDn, j), t);
+          in.get(kDn, j, t);
           wpre.get(j, w);
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
@@ -476,39 +487,39 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
         }
         if (a.dh) {
 #pragma unroll
-          for (int i = 0; i < NP; ++i) t[i] = mul(P::all(a.a), d[i]);
-          put(static_cast<T*>(a.dh) + base + c, t);
+          for (int i = 0; i < NP; ++i) t[i] = mul(all(a.a), d[i]);
+          span.store(static_cast<T*>(a.dh) + base, j, t);
         }
         F yn[NP];
-        unpack(in.get(kY, j), yn);
+        in.get(kY, j, yn);
         wpost.get(j, w);
         F z[NP];
-        if (a.z) unpack(in.get(kZ, j), z);
+        if (a.z) in.get(kZ, j, z);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          F sg = P::all(1.f), sn = sg;
+          F sg = all(1.f), sn = sg;
           if (a.z) gate(z[i], sg, sn);
-          yn[i] = mul(yn[i], P::all(iy));
-          const F du = mul(d[i], mul(sg, P::all(a.b)));
+          yn[i] = mul(yn[i], all(iy));
+          const F du = mul(d[i], mul(sg, all(a.b)));
           gpost[j][i] = fma(du, yn[i], gpost[j][i]);
           q[j][i] = mul(du, w[i]);
           ty = fma(q[j][i], yn[i], ty);
           z[i] = mul(mul(q[j][i], yn[i]), sn);
         }
-        if (a.z) put(static_cast<T*>(a.dz) + base + c, z);
+        if (a.z) span.store(static_cast<T*>(a.dz) + base, j, z);
       }
     }
     float two[1] = {sum(ty)};
     group_sum<G>(two, sh, turn);
-    const F yk = P::all(iy * (one ? a.eps * iy * iy : 1.f)), yp = P::all(one ? 0.f : -iy * iy * (two[0] * inv));
+    const F yk = all(iy * (one ? a.eps * iy * iy : 1.f)), yp = all(one ? 0.f : -iy * iy * (two[0] * inv));
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (here(j)) {
         F y[NP];
-        unpack(in.get(kY, j), y);
+        in.get(kY, j, y);
 #pragma unroll
         for (int i = 0; i < NP; ++i) q[j][i] = fma(y[i], yp, mul(q[j][i], yk));
-        put(static_cast<T*>(a.dy) + base + (j * G + lane) * V, q[j]);
+        span.store(static_cast<T*>(a.dy) + base, j, q[j]);
       }
   }
   // This CTA's share of the weight gradients: its groups' sums, in order.
@@ -524,27 +535,23 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
     constexpr int W = G * NV * V;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * G + lane) * V;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        float v;
-        if constexpr (V == 1) {
-          v = which == 0 ? gpost[j][0] : gpre[PRE ? j : 0][0];
-        } else {
-          const float2 t = both(which == 0 ? gpost[j][i / 2] : gpre[PRE ? j : 0][i / 2]);
-          v = i % 2 ? t.y : t.x;
-        }
+        const float2 t = both(which == 0 ? gpost[j][i / 2] : gpre[PRE ? j : 0][i / 2]);
+        const float v = i % 2 ? t.y : t.x;
+        const int c = span.at(j) + i;
         if constexpr (kGroups > 1)
-          acc[group * W + c + i] = v;
-        else if (c < a.width)
-          out[which * half + c + i] = v;
+          acc[group * W + (j * G + lane) * V + i] = v;
+        else if (c >= 0 && c < a.width)
+          out[which * half + c] = v;
       }
     }
     if constexpr (kGroups > 1) {
       __syncthreads();
       for (int c = static_cast<int>(threadIdx.x); c < a.width; c += NT) {
         float t = 0.f;
-        for (int g = 0; g < kGroups; ++g) t += acc[g * W + c];
+        for (int g = 0; g < kGroups; ++g)
+          t += acc[g * W + c - Span<V, G, ODD>(0, static_cast<int64_t>(blockIdx.x) * kGroups + g, a.width).at(0)];
         out[which * half + c] = t;
       }
       __syncthreads();
@@ -580,14 +587,15 @@ int64_t resident(K kernel, int threads, size_t smem, int most) {
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
-  const int fit = (sms < 1 ? 1 : sms) * (per < 1 ? 1 : per);
-  return fit < most ? fit : most;
+  const int fit = (sms < 8 ? 8 : sms) * (per < 1 ? 1 : per);
+  return (fit < most ? fit : most) / 8 * 8;  // a group's rows are a multiple of the vector's elements apart
 }
 
-template <typename T, int V, int NV, int G, int NT, bool PRE>
+template <typename T, int V, int NV, int G, int NT, bool ODD, bool PRE>
 void run_bwd(const NormArgs& a, int64_t blocks, float* dpost, float* dpre, cudaStream_t s) {
-  auto k = norm_bwd_kernel<T, V, NV, G, NT, PRE>;
-  constexpr size_t rows = Rows<T, V, NV, G, NT, PRE ? 5 : 3>::kBytes, sums = NT / G > 1 ? sizeof(float) * NT * NV * V : 0;
+  auto k = norm_bwd_kernel<T, V, NV, G, NT, ODD, PRE>;
+  constexpr size_t rows = Rows<T, V, NV, G, NT, ODD, PRE ? 5 : 3>::kBytes;
+  constexpr size_t sums = NT / G > 1 ? sizeof(float) * NT * NV * V : 0;
   constexpr size_t smem = rows > sums ? rows : sums;
   static const int64_t fit = resident(k, NT, smem, kMaxCtas);
   const int grid = static_cast<int>(blocks < fit ? blocks : fit);
@@ -596,51 +604,50 @@ void run_bwd(const NormArgs& a, int64_t blocks, float* dpost, float* dpre, cudaS
     norm_weight_kernel<<<dim3((a.width + 31) / 32, 2), dim3(32, 32), 0, s>>>(a.part, grid, a.width, dpost, dpre);
 }
 
-template <typename T, int V, int NV, int G, int NT>
+template <typename T, int V, int NV, int G, int NT, bool ODD>
 kda_status run(const NormArgs& a, bool bwd, float* dpost, float* dpre, cudaStream_t s) {
   const int64_t blocks = ceil_div(a.rows, NT / G);
   if (!bwd) {
-    auto k = norm_fwd_kernel<T, V, NV, G, NT>;
-    constexpr size_t smem = Rows<T, V, NV, G, NT, 3>::kBytes;
+    auto k = norm_fwd_kernel<T, V, NV, G, NT, ODD>;
+    constexpr size_t smem = Rows<T, V, NV, G, NT, ODD, 3>::kBytes;
     static const int64_t fit = resident(k, NT, smem, 1 << 30);
     k<<<static_cast<int>(blocks < fit ? blocks : fit), NT, smem, s>>>(a);
   } else if (a.dn) {
-    run_bwd<T, V, NV, G, NT, true>(a, blocks, dpost, dpre, s);
+    run_bwd<T, V, NV, G, NT, ODD, true>(a, blocks, dpost, dpre, s);
   } else {
-    run_bwd<T, V, NV, G, NT, false>(a, blocks, dpost, dpre, s);
+    run_bwd<T, V, NV, G, NT, ODD, false>(a, blocks, dpost, dpre, s);
   }
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? KDA_OK : set_error(KDA_ERR_CUDA, "block norm launch failed: %s", cudaGetErrorString(e));
 }
 
-// The smallest group that holds a row.
-template <typename T, int V>
+// The smallest group that holds a row (with the elements before its start, where they may be any number).
+template <typename T, int V, bool ODD>
 kda_status dispatch(const NormArgs& a, bool bwd, float* dpost, float* dpre, cudaStream_t s) {
-  const int vecs = (a.width + V - 1) / V;
-  if (vecs <= 8) return run<T, V, 1, 8, 256>(a, bwd, dpost, dpre, s);
-  if (vecs <= 16) return run<T, V, 1, 16, 256>(a, bwd, dpost, dpre, s);
-  if (vecs <= 32) return run<T, V, 1, 32, 256>(a, bwd, dpost, dpre, s);
-  if (vecs <= 64) return run<T, V, 1, 64, 64>(a, bwd, dpost, dpre, s);
-  if (vecs <= 128) return run<T, V, 1, 128, 128>(a, bwd, dpost, dpre, s);
-  if (vecs <= 256) return run<T, V, 1, 256, 256>(a, bwd, dpost, dpre, s);
-  if (vecs <= 512) return run<T, V, 1, 512, 512>(a, bwd, dpost, dpre, s);
-  if (vecs <= 1024) return run<T, V, 2, 512, 512>(a, bwd, dpost, dpre, s);
-  if constexpr (V <= 4) {
-    if (vecs <= 2048) return run<T, V, 4, 512, 512>(a, bwd, dpost, dpre, s);
+  const int vecs = (a.width + (ODD ? V - 1 : 0) + V - 1) / V;
+  if (vecs <= 8) return run<T, V, 1, 8, 256, ODD>(a, bwd, dpost, dpre, s);
+  if (vecs <= 16) return run<T, V, 1, 16, 256, ODD>(a, bwd, dpost, dpre, s);
+  if (vecs <= 32) return run<T, V, 1, 32, 256, ODD>(a, bwd, dpost, dpre, s);
+  if (vecs <= 64) return run<T, V, 1, 64, 64, ODD>(a, bwd, dpost, dpre, s);
+  if (vecs <= 128) return run<T, V, 1, 128, 128, ODD>(a, bwd, dpost, dpre, s);
+  if (vecs <= 256) return run<T, V, 1, 256, 256, ODD>(a, bwd, dpost, dpre, s);
+  if (vecs <= 512) return run<T, V, 1, 512, 512, ODD>(a, bwd, dpost, dpre, s);
+  if (vecs <= 1024) return run<T, V, 2, 512, 512, ODD>(a, bwd, dpost, dpre, s);
+  if constexpr (V == 4) {
+    if (vecs <= 2048) return run<T, V, 4, 512, 512, ODD>(a, bwd, dpost, dpre, s);
   }
-  if constexpr (V == 1) {
-    if (vecs <= 4096) return run<T, V, 8, 512, 512>(a, bwd, dpost, dpre, s);
-    return run<T, V, 16, 512, 512>(a, bwd, dpost, dpre, s);
-  }
+  // widths from 8186 (fp32: 8190), whose first elements need one vector more
+  if constexpr (ODD) return run<T, V, V == 4 ? 5 : 3, 512, 512, ODD>(a, bwd, dpost, dpre, s);
   return set_error(KDA_ERR_UNSUPPORTED, "width %d", a.width);
 }
 
 kda_status launch_norm(const kda_norm_problem* p, const NormArgs& a, bool bwd, float* dpost, float* dpre,
                        cudaStream_t s) {
   if (p->dtype == KDA_DTYPE_BF16)
-    return p->width % 8 == 0 ? dispatch<__nv_bfloat16, 8>(a, bwd, dpost, dpre, s)
-                             : dispatch<__nv_bfloat16, 1>(a, bwd, dpost, dpre, s);
-  return p->width % 4 == 0 ? dispatch<float, 4>(a, bwd, dpost, dpre, s) : dispatch<float, 1>(a, bwd, dpost, dpre, s);
+    return p->width % 8 == 0 ? dispatch<__nv_bfloat16, 8, false>(a, bwd, dpost, dpre, s)
+                             : dispatch<__nv_bfloat16, 8, true>(a, bwd, dpost, dpre, s);
+  return p->width % 4 == 0 ? dispatch<float, 4, false>(a, bwd, dpost, dpre, s)
+                           : dispatch<float, 4, true>(a, bwd, dpost, dpre, s);
 }
 
 kda_status validate_norm(const kda_norm_problem* p) {
