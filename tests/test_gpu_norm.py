@@ -61,6 +61,15 @@ def test_every_part(rows, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,D", [(9001, 3), (30000, 65), (5003, 130), (3000, 257), (1501, 1001), (1300, 2050),
+                                    (700, 4093), (400, 8189), (321, 8186)])
+def test_odd_widths_with_several_rows_a_group(rows, D, dtype):
+    """More rows than groups are resident: a group's rows keep their shift."""
+    x, dho, dn = make(rows, D, dtype, "zhpn", seed=rows)
+    compare(x, dho, dn, 0.9, 0.5)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("parts", ["", "p", "z", "zp", "h", "hp", "hn", "n", "zn", "zhn", "hpn"])
 @pytest.mark.parametrize("rows,D", [(300, 128), (40, 1024), (7, 33)])
 def test_parts_left_out(rows, D, parts, dtype):
@@ -110,18 +119,36 @@ def test_autograd_wrapper_and_leading_dimensions():
     R.check(u, reference({**x, "h": None, "w_pre": None}, dho, None, 1.0, 1.0)[0], BAR, "u")
 
 
-def test_in_place_buffers_and_no_rows():
-    x, dho, dn = make(30, 512, torch.bfloat16, "zhpn", seed=5)
+@pytest.mark.parametrize("D", [512, 517])
+def test_in_place_buffers_and_no_rows(D):
+    x, dho, dn = make(3000, D, torch.bfloat16, "zhpn", seed=5)
     kw = dict(residual_scale=0.9, block_scale=0.5, **{k: x[k] for k in ("z", "w_post", "w_pre")})
     ho, n = norm.block_norm_fwd(x["y"], h=x["h"], **kw)
     h = x["h"].clone()
     ho2, n2 = norm.block_norm_fwd(x["y"], h=h, out=(h, torch.empty_like(h)), **kw)
     assert torch.equal(ho, ho2) and torch.equal(n, n2) and ho2 is h
-    e = torch.empty(0, 512, dtype=torch.bfloat16).cuda()
+    e = torch.empty(0, D, dtype=torch.bfloat16).cuda()
     ho, n = norm.block_norm_fwd(e, w_pre=x["w_pre"])
-    assert ho.shape == n.shape == (0, 512)
+    assert ho.shape == n.shape == (0, D)
     g = norm.block_norm_bwd(e, w_pre=x["w_pre"], dn=e)
     assert not g["dw_pre"].any()
+
+
+def test_neighbouring_rows_do_not_touch_each_other():
+    """Rows of an odd width share 16-byte vectors: NaN and infinities stay in their row."""
+    x, dho, dn = make(2000, 129, torch.bfloat16, "zhpn", seed=11)
+    kw = dict(residual_scale=0.9, block_scale=0.5)
+    clean = norm.block_norm_fwd(x["y"], **kw, **{k: x[k] for k in ("z", "h", "w_post", "w_pre")})
+    grads = norm.block_norm_bwd(x["y"], dh_out=dho, dn=dn, **kw, **{k: x[k] for k in ("z", "h", "w_post", "w_pre")})
+    bad = torch.arange(1, 2000, 3).cuda()
+    for t in (x["y"], x["z"], x["h"], dho, dn):
+        t[bad] = float("nan")
+    out = norm.block_norm_fwd(x["y"], **kw, **{k: x[k] for k in ("z", "h", "w_post", "w_pre")})
+    g = norm.block_norm_bwd(x["y"], dh_out=dho, dn=dn, **kw, **{k: x[k] for k in ("z", "h", "w_post", "w_pre")})
+    good = torch.ones(2000, dtype=torch.bool).cuda()
+    good[bad] = False
+    for a, b in [*zip(clean, out), *((grads[k], g[k]) for k in ("dy", "dz", "dh"))]:
+        assert torch.equal(a[good], b[good]) and torch.isnan(b[bad]).all()
 
 
 def test_extreme_rows():
