@@ -1,10 +1,12 @@
-"""ctypes declarations of include/kda_serving.h, shared by the bindings in
-``decode`` and ``norm``. As in ``kda``: argument marshalling only, no CPU path."""
+"""What the bindings in ``decode`` and ``norm`` share: the ctypes declarations of
+include/kda_serving.h and the compiled host side. As in ``kda``: argument
+marshalling only, no CPU path."""
 from __future__ import annotations
 
 import ctypes
-
-import torch
+import importlib.machinery
+import importlib.util
+import os
 
 from . import kda as _kda
 
@@ -52,33 +54,30 @@ def library():
 check = _kda._check
 
 
-# The raw handle of the current stream of a device index: these calls take a
-# few microseconds on the GPU, so their host side is kept as short.
-stream = torch._C._cuda_getCurrentRawStream
+_bind = None
 
 
-def off(t, dtype, device, shape) -> bool:
-    """Whether ``t`` is not the contiguous tensor of ``dtype`` and ``shape`` on
-    CUDA device ``device`` (an index) that the kernels index."""
-    return t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous()
+def bind():
+    """The binding's compiled host side (csrc/kda_bind.cpp), joined to the library's entry points."""
+    global _bind
+    if _bind is None:
+        lib = library()
+        path = os.path.join(os.path.dirname(_kda.LIB_PATH), "_kda_bind.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"KDA binding not built: {path} is missing "
+                               "(run recompute_kda_chunkwise_gb300.build.build())")
+        loader = importlib.machinery.ExtensionFileLoader("_kda_bind", path)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kda_bind", loader))
+        loader.exec_module(m)
+        m.init(*(ctypes.cast(getattr(lib, n), _vp).value for n in (
+            "kda_step", "kda_gdn2_step", "kda_block_norm_fwd", "kda_block_norm_workspace_bytes", "kda_block_norm_bwd",
+            "kda_verify_drafts", "kda_paged_append", "kda_paged_attention_workspace_bytes", "kda_paged_attention")))
+        _bind = m
+    return _bind
 
 
-def refuse(named, dtype, device, shape):
-    """Raises for the first of the (name, tensor) pairs that is off()."""
-    shape = tuple(shape)
-    for name, t in named:
-        if device < 0 or off(t, dtype, device, shape):
-            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {shape}"
-                             f"{f' on cuda:{device}' if device >= 0 else ''} (got {t.dtype} {tuple(t.shape)} on "
-                             f"{t.device}{'' if t.is_contiguous() else ', strided'})")
-
-
-def need(t, name, shape, dtype, device):
-    """The address of a tensor the kernels index by ``shape``."""
-    if device < 0 or off(t, dtype, device, shape):
-        refuse(((name, t),), dtype, device, shape)
-    return t.data_ptr()
-
-
-def maybe(t, name, shape, dtype, device):
-    return None if t is None else need(t, name, shape, dtype, device)
+def done(result, where):
+    """What a function of bind() returned; an int is the entry point's error status."""
+    if type(result) is int:
+        check(result, where)
+    return result

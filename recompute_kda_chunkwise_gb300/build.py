@@ -4,6 +4,8 @@ Each translation unit under ``csrc/`` is compiled by nvcc in parallel with
 ``-gencode arch=compute_103a,code=sm_103a -lineinfo -O3`` and linked with the
 static CUDA runtime, so loading the library needs no libcudart on the path
 (and loading it on a host without a GPU works; calling into the GPU does not).
+``csrc/kda_bind.cpp``, the host side of the serving operators' binding, is
+compiled by g++ against torch into ``_build/_kda_bind.so``.
 """
 from __future__ import annotations
 
@@ -21,6 +23,7 @@ LIB = os.path.join(BUILD, "libkda_gb300.so")
 # (-DKDA_STAGE_TIMERS), in a directory of its own
 STAGE_BUILD = os.path.join(HERE, "_build_stage_timers")
 STAGE_LIB = os.path.join(STAGE_BUILD, "libkda_gb300.so")
+BIND = os.path.join(BUILD, "_kda_bind.so")
 INCLUDE = os.path.join(ROOT, "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -40,6 +43,32 @@ def _headers():
     hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     hs += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
     return hs
+
+
+def _build_bind(force: bool = False) -> str:
+    """Compiles the binding's host side (links to torch only; the kernel
+    library's entry points are handed to it at run time)."""
+    import sysconfig
+
+    import torch
+    src = os.path.join(CSRC, "kda_bind.cpp")
+    newest = max(os.path.getmtime(f) for f in [src, *(h for h in _headers() if h.startswith(INCLUDE)), torch.__file__])
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= newest:
+        return BIND
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = BIND + f".tmp{os.getpid()}"
+    lib = os.path.join(at, "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", src, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+           "-isystem", os.path.join(at, "include"), "-isystem", os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), stage_timers: bool = False) -> str:
@@ -72,8 +101,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), stage_time
         os.replace(tmp, obj)
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        bind = None if stage_timers else ex.submit(_build_bind, force)
         results = list(ex.map(compile_one, srcs))
+        if bind is not None:
+            bind.result()
     if verbose:
         for _, log in results:
             if log:

@@ -11,15 +11,7 @@ from __future__ import annotations
 
 import torch
 
-from . import kda as _kda
-from ._serving import NormProblem, check, library, maybe, need, stream
-
-
-def _problem(y, a, b, eps):
-    if y.dim() < 1 or y.dtype not in _kda._DTYPE_CODE:
-        raise ValueError(f"y must be [..., width] in bfloat16 or float32 (got {y.dtype} {tuple(y.shape)})")
-    D = y.shape[-1]
-    return NormProblem(y.numel() // D if D else 0, D, _kda._DTYPE_CODE[y.dtype], a, b, eps), y.shape, D
+from ._serving import bind, done
 
 
 def block_norm_fwd(y, *, z=None, h=None, w_post=None, w_pre=None, residual_scale: float = 1.0, block_scale: float = 1.0,
@@ -27,20 +19,8 @@ def block_norm_fwd(y, *, z=None, h=None, w_post=None, w_pre=None, residual_scale
     """Forward. y, z, h: [..., width] in one dtype; w_post, w_pre: [width]
     fp32. Returns (h_out, n); n is None without w_pre. ``out`` may hold
     (h_out, n) and h_out may be h."""
-    p, shape, D = _problem(y, residual_scale, block_scale, eps)
-    dev, dt, f32 = y.get_device(), y.dtype, torch.float32
-    args = [need(y, "y", shape, dt, dev), maybe(z, "z", shape, dt, dev), maybe(h, "h", shape, dt, dev),
-            maybe(w_post, "w_post", (D,), f32, dev), maybe(w_pre, "w_pre", (D,), f32, dev)]
-    if out is None:
-        h_out = torch.empty_like(y)
-        n = torch.empty_like(y) if w_pre is not None else None
-    else:
-        h_out, n = out
-    st = library().kda_block_norm_fwd(p, *args, need(h_out, "h_out", shape, dt, dev),
-                                      maybe(n, "n", shape, dt, dev), stream(dev))
-    if st:
-        check(st, "kda_block_norm_fwd")
-    return h_out, n
+    h_out, n = (None, None) if out is None else out
+    return done(bind().norm_fwd(y, z, h, w_post, w_pre, residual_scale, block_scale, eps, h_out, n), "kda_block_norm_fwd")
 
 
 def block_norm_bwd(y, *, z=None, h=None, w_post=None, w_pre=None, dh_out=None, dn=None, residual_scale: float = 1.0,
@@ -48,26 +28,9 @@ def block_norm_bwd(y, *, z=None, h=None, w_post=None, w_pre=None, dh_out=None, d
     """Backward, from the forward's inputs and the gradients of h_out and n
     (zero when None). Returns dict dy, dz, dh, dw_post, dw_pre (None for what
     was not given)."""
-    p, shape, D = _problem(y, residual_scale, block_scale, eps)
-    dev, dt, f32 = y.get_device(), y.dtype, torch.float32
-    args = [need(y, "y", shape, dt, dev), maybe(z, "z", shape, dt, dev), maybe(h, "h", shape, dt, dev),
-            maybe(w_post, "w_post", (D,), f32, dev), maybe(w_pre, "w_pre", (D,), f32, dev),
-            maybe(dh_out, "dh_out", shape, dt, dev), maybe(dn, "dn", shape, dt, dev)]
-    g = {"dy": torch.empty_like(y), "dz": None if z is None else torch.empty_like(z),
-         "dh": None if h is None else torch.empty_like(h),
-         "dw_post": None if w_post is None else torch.empty_like(w_post),
-         "dw_pre": None if w_pre is None else torch.empty_like(w_pre)}
-    lib = library()
-    size = lib.kda_block_norm_workspace_bytes(p, w_post is not None, w_pre is not None)
-    if workspace is None:
-        workspace = torch.empty(size, dtype=torch.uint8, device=y.device) if size else None
-    else:
-        _kda._check_buffer(workspace, size, y, "workspace")
-    st = lib.kda_block_norm_bwd(p, *args, *(None if t is None else t.data_ptr() for t in g.values()),
-                                None if workspace is None else workspace.data_ptr(), stream(dev))
-    if st:
-        check(st, "kda_block_norm_bwd")
-    return g
+    r = done(bind().norm_bwd(y, z, h, w_post, w_pre, dh_out, dn, residual_scale, block_scale, eps, workspace),
+             "kda_block_norm_bwd")
+    return dict(zip(("dy", "dz", "dh", "dw_post", "dw_pre"), r))
 
 
 class BlockNormFunction(torch.autograd.Function):
