@@ -147,7 +147,6 @@ constexpr int kSoftmaxWarps = 8;         // two warpgroups
 constexpr int kMmaWarp = 8, kLoadWarp = 9;  // kLoadWarp: K, the one after it: V
 constexpr int kThreads = 352;
 constexpr int kMaxCtas = 152;            // one per SM
-constexpr int kMinTiles = 2;             // key tiles that are worth a CTA of their own
 constexpr int kRingBytes = 6 * 32768;    // K slots, then V slots
 constexpr float kRescale = 8.f;          // log2 growth of a maximum that rescales O
 
@@ -288,6 +287,12 @@ __device__ __forceinline__ bool wait_warp(Shared* sh, uint64_t* bar, uint32_t pa
   return __all_sync(~0u, wait(sh, bar, parity, status));
 }
 
+// a / b of non-negative numbers, in 32 bits where both fit (nearly always: a
+// 64-bit division is a long chain of instructions at the start of every call).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+
 // Every CTA adds up the call's tiles and finds the start of its run.
 __device__ void plan(const PagedArgs& a, Shared* sh, Walk& w) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -320,9 +325,8 @@ __device__ void plan(const PagedArgs& a, Shared* sh, Walk& w) {
     if (i < warp) upto += sh->sum[i];
     total += sh->sum[i];
   }
-  int64_t run = (total + gridDim.x - 1) / gridDim.x;
-  if (run < kMinTiles) run = kMinTiles;
   if (bad) total = 0;
+  const int64_t run = quotient(total + gridDim.x - 1, gridDim.x);  // one tile may be a CTA's run
   const int64_t start = static_cast<int64_t>(blockIdx.x) * run;
   if (start < total && start >= upto - mine && start < upto) {
     int64_t base = upto - mine;
@@ -348,7 +352,7 @@ __device__ void plan(const PagedArgs& a, Shared* sh, Walk& w) {
   w.sequence(sh->start_n);
   int64_t rest = start - sh->start_base;
   const int64_t head = w.head_tiles();
-  w.hk = static_cast<int>(rest / head);
+  w.hk = static_cast<int>(quotient(rest, head));
   rest -= w.hk * head;
   w.mt = 0;
   for (int t; rest >= (t = max(w.tiles_of(w.mt), 1)); ++w.mt) rest -= t;
@@ -743,16 +747,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t run_end = min((static_cast<int64_t>(blockIdx.x) + 1) * sh->run, sh->total);
         const int64_t item0 = run_end - w.left - s.j1, item1 = item0 + s.tiles;
         const int c0 = static_cast<int>(item0 / sh->run), c1 = static_cast<int>((item1 - 1) / sh->run);
-        __threadfence();
         named_bar_sync(1, 256);
         if (tid == 0) {
-          __threadfence();
+          __threadfence();  // this CTA's part, written before the barrier, ...
           sh->last = atomicAdd(&parts.count[c0], 1u) == static_cast<uint32_t>(c1 - c0);
-          __threadfence();
+          __threadfence();  // ... and the others' before what follows it
         }
         named_bar_sync(1, 256);
         if (sh->last) {
-          __threadfence();
           // parts c0 (its slot 1) .. c1 (their slot 0), in the order of the keys
           int any = 0;
           for (int c = c0; c <= c1; ++c) any |= __ldcg(&parts.bad[2 * c + (c == c0)]);
