@@ -83,6 +83,11 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
   return r;
 }
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+  return r;
+}
 __device__ __forceinline__ float sum(F2 a) { return both(a).x + both(a).y; }
 __device__ __forceinline__ F2 all(float x) { return f2(x, x); }
 
@@ -219,23 +224,21 @@ __device__ __forceinline__ void group_sum(float (&x)[N], float* sh, int& turn) {
   }
 }
 
-// sigmoid(z) and sigmoid(-z) from one exponential of -|z| (at most 1: neither
-// overflows, and neither is a difference that cancels).
-__device__ __forceinline__ void gate(float z, float& s, float& n) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(z) * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  const float er = e * r;
-  s = z < 0.f ? er : r;
-  n = z < 0.f ? r : er;
-}
+// s = sigmoid(z) = 1 / (1 + e) and n = sigmoid(-z) = e s with e = exp(-z), so
+// that neither is a difference that cancels. e stops at 2^125, where 1 + e is
+// still finite: below z = -86.6 both stay at what they are there (2^-125, 1).
 __device__ __forceinline__ void gate(F2 z, F2& s, F2& n) {
-  const float2 t = both(z);
-  float2 a, b;
-  gate(t.x, a.x, b.x);
-  gate(t.y, a.y, b.y);
-  s = f2(a.x, a.y);
-  n = f2(b.x, b.y);
+  const float2 t = both(mul(z, all(-1.4426950408889634f)));
+  float ex, ey;
+  asm("{.reg .f32 t;\n min.NaN.f32 t, %1, 0f42FA0000;\n ex2.approx.ftz.f32 %0, t;\n}" : "=f"(ex) : "f"(t.x));
+  asm("{.reg .f32 t;\n min.NaN.f32 t, %1, 0f42FA0000;\n ex2.approx.ftz.f32 %0, t;\n}" : "=f"(ey) : "f"(t.y));
+  const F2 e = f2(ex, ey);
+  const float2 d = both(add(e, all(1.f)));
+  float rx, ry;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rx) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ry) : "f"(d.y));
+  s = f2(rx, ry);
+  n = mul(e, s);
 }
 
 // How a thread gets its share of its group's rows: 16-byte vectors by
