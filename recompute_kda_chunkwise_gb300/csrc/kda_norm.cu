@@ -227,18 +227,19 @@ __device__ __forceinline__ void group_sum(float (&x)[N], float* sh, int& turn) {
 // s = sigmoid(z) = 1 / (1 + e) and n = sigmoid(-z) = e s with e = exp(-z), so
 // that neither is a difference that cancels. e stops at 2^125, where 1 + e is
 // still finite: below z = -86.6 both stay at what they are there (2^-125, 1).
-__device__ __forceinline__ void gate(F2 z, F2& s, F2& n) {
+__device__ __forceinline__ F2 gate_exp(F2 z) {
   const float2 t = both(mul(z, all(-1.4426950408889634f)));
   float ex, ey;
   asm("{.reg .f32 t;\n min.NaN.f32 t, %1, 0f42FA0000;\n ex2.approx.ftz.f32 %0, t;\n}" : "=f"(ex) : "f"(t.x));
   asm("{.reg .f32 t;\n min.NaN.f32 t, %1, 0f42FA0000;\n ex2.approx.ftz.f32 %0, t;\n}" : "=f"(ey) : "f"(t.y));
-  const F2 e = f2(ex, ey);
+  return f2(ex, ey);
+}
+__device__ __forceinline__ F2 gate_of(F2 e) {
   const float2 d = both(add(e, all(1.f)));
-  float rx, ry;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rx) : "f"(d.x));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ry) : "f"(d.y));
-  s = f2(rx, ry);
-  n = mul(e, s);
+  float x, y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d.y));
+  return f2(x, y);
 }
 
 // How a thread gets its share of its group's rows: 16-byte vectors by
@@ -347,11 +348,7 @@ __global__ void __launch_bounds__(NT) norm_fwd_kernel(const NormArgs a) {
         if (a.z) {
           in.get(kZ, j, t);
 #pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            F s, n;
-            gate(t[i], s, n);
-            x[j][i] = mul(x[j][i], s);
-          }
+          for (int i = 0; i < NP; ++i) x[j][i] = mul(x[j][i], gate_of(gate_exp(t[i])));
         }
         if (a.h) {
           in.get(2, j, t);
@@ -422,9 +419,10 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
     float yy[1] = {sum(yt)};
     group_sum<G>(yy, sh, turn);
     const float iy = rsqrtf(yy[0] * inv + a.eps);
-    // yn, the gates and what follows from them are formed again in each stage
-    // from the row at hand: registers, not instructions, limit the warps here.
+    // yn and d are formed again in each stage from the row at hand: registers,
+    // not instructions, limit the warps here.
     F hp[PRE ? NV : 1][NP];  // h'
+    F q[NV][NP];             // exp(-z) of the gate, then the gradient of yn, until dy is formed
     F hh = all(0.f), hd = all(0.f);
     if constexpr (PRE) {
 #pragma unroll
@@ -439,9 +437,8 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
             in.get(kZ, j, t);
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-              F s, n;
-              gate(t[i], s, n);
-              hp[j][i] = mul(hp[j][i], s);
+              q[j][i] = gate_exp(t[i]);
+              hp[j][i] = mul(hp[j][i], gate_of(q[j][i]));
             }
           }
           if (a.h) {
@@ -469,7 +466,6 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
       dp = all(one ? 0.f : -(r * r * r) * (two[1] * inv));
     }
     F ty = all(0.f);
-    F q[NV][NP];  // the gradient of yn, until dy is formed
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (here(j)) {
@@ -497,11 +493,20 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
         in.get(kY, j, yn);
         wpost.get(j, w);
         F z[NP];
-        if (a.z) in.get(kZ, j, z);
+        if constexpr (!PRE) {
+          if (a.z) {
+            in.get(kZ, j, z);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) q[j][i] = gate_exp(z[i]);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           F sg = all(1.f), sn = sg;
-          if (a.z) gate(z[i], sg, sn);
+          if (a.z) {
+            sg = gate_of(q[j][i]);
+            sn = mul(q[j][i], sg);
+          }
           yn[i] = mul(yn[i], all(iy));
           const F du = mul(d[i], mul(sg, all(a.b)));
           gpost[j][i] = fma(du, yn[i], gpost[j][i]);
