@@ -216,9 +216,9 @@ __device__ __forceinline__ void group_sum(float (&x)[N], float* sh, int& turn) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float t = lane < W ? s[i * 32 + lane] : 0.f;
+      float t = s[i * 32 + lane % W];
 #pragma unroll
-      for (int m = 16; m > 0; m >>= 1) t += __shfl_xor_sync(~0u, t, m);
+      for (int m = W / 2; m > 0; m >>= 1) t += __shfl_xor_sync(~0u, t, m);
       x[i] = t;
     }
   }
@@ -246,13 +246,23 @@ __device__ __forceinline__ F2 gate_of(F2 e) {
 // asynchronous copies, up to four rows ahead, into a ring of shared memory in
 // which a thread reads only what it copied itself. The rows ahead hold no
 // registers and need no barrier. Tensors that are absent are not read.
+// FILL: the ring holds zeros in their place (the gate's: infinities, whose
+// sigmoid is 1), and whoever reads it need not ask which there are.
 enum Which { kY, kZ, kDho, kH, kDn };  // a backward without the next norm has no kH, kDn; a forward the first two and kH
-template <typename T, int V, int NV, int G, int NT, bool ODD, int SLOTS>
+template <typename T>
+__device__ __forceinline__ uint4 infinities() {
+  const uint32_t u = sizeof(T) == 2 ? 0x7f807f80u : 0x7f800000u;
+  return make_uint4(u, u, u, u);
+}
+template <typename T, int V, int NV, int G, int NT, bool ODD, int SLOTS, bool FILL>
 struct Rows {
   static constexpr int kStage = SLOTS * NV * NT * 16;  // bytes
   static constexpr int kFit = 200 * 1024 / kStage;
   static constexpr int kDepth = kFit < 4 ? kFit : 4;
   static constexpr size_t kBytes = static_cast<size_t>(kDepth) * kStage;
+  // The next row is at hand too: where a reduction is a barrier of the CTA,
+  // its first one shares the last one of the row before.
+  static constexpr bool kNext = G > 32 && kDepth >= 3;
   static_assert(kDepth >= 1, "");
   const NormArgs& a;
   const Span<V, G, ODD>& span;
@@ -264,6 +274,13 @@ struct Rows {
   __device__ __forceinline__ Rows(const NormArgs& args, const Span<V, G, ODD>& sp, const void* const (&f)[SLOTS],
                                   uint8_t* sm, int64_t row, int64_t st)
       : a(args), span(sp), from(f), ring(sm), step(st), ahead(row), in(0), out(kDepth - 1) {
+    if constexpr (FILL) {
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s)
+        if (!from[s])
+          for (int i = 0; i < kDepth * NV; ++i)
+            *reinterpret_cast<uint4*>(slot(i / NV, s, i % NV)) = s == kZ ? infinities<T>() : make_uint4(0, 0, 0, 0);
+    }
     for (int i = 0; i + 1 < kDepth; ++i) copy();
   }
   __device__ __forceinline__ uint8_t* slot(int stage, int s, int j) const {
@@ -293,15 +310,29 @@ struct Rows {
     ahead += step;
     if (++in == kDepth) in = 0;
   }
-  // The next row of this group is at hand afterwards.
+  // The next row of this group (kNext: and the one after it) is at hand afterwards.
   __device__ __forceinline__ void turn() {
     copy();
-    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - (kNext ? 2 : 1)) : "memory");
     if (++out == kDepth) out = 0;
   }
-  __device__ __forceinline__ void get(int s, int j, F2 (&x)[V / 2]) const {
-    unpack(*reinterpret_cast<const Raw<T, V>*>(slot(out, s, j)), x);
+  __device__ __forceinline__ void get(int s, int j, F2 (&x)[V / 2], bool next = false) const {
+    const int stage = !next ? out : out + 1 == kDepth ? 0 : out + 1;
+    unpack(*reinterpret_cast<const Raw<T, V>*>(slot(stage, s, j)), x);
     span.clip(j, x);
+  }
+  // This thread's share of the sum of y^2 over `row`, the one at hand or the next.
+  __device__ __forceinline__ float squares(int64_t row, bool next) const {
+    F2 t = all(0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (row < a.rows && span.any(j)) {
+        F2 y[V / 2];
+        get(kY, j, y, next);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) t = fma(y[i], y[i], t);
+      }
+    return sum(t);
   }
 };
 
@@ -319,25 +350,29 @@ __global__ void __launch_bounds__(NT) norm_fwd_kernel(const NormArgs a) {
   const Span<V, G, ODD> span(lane, row, a.width);
   const Weights<V, NV, G, ODD> wpost(a.wpost, span), wpre(a.wpre, span);
   const void* const from[3] = {a.y, a.z, a.h};
-  Rows<T, V, NV, G, NT, ODD, 3> in(a, span, from, ring, row, step);
+  Rows<T, V, NV, G, NT, ODD, 3, false> in(a, span, from, ring, row, step);
+  constexpr bool kNext = in.kNext;
+  float yy[1];
+  if constexpr (kNext) {
+    in.turn();
+    yy[0] = in.squares(row, false);
+    group_sum<G>(yy, sh, turn);
+  }
   // every group of a CTA makes the same number of turns (the reductions are collective)
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGroups; r0 < a.rows; r0 += step, row += step) {
-    in.turn();
+    if constexpr (!kNext) in.turn();
     const bool live = row < a.rows;
     const int64_t base = row * a.width;
     auto here = [&](int j) { return live && span.any(j); };
     F x[NV][NP], hh = all(0.f);
+    if constexpr (!kNext) {
+      yy[0] = in.squares(row, false);
+      group_sum<G>(yy, sh, turn);
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (here(j)) {
-        in.get(kY, j, x[j]);
-#pragma unroll
-        for (int i = 0; i < NP; ++i) hh = fma(x[j][i], x[j][i], hh);
-      }
-    float yy[1] = {sum(hh)};
-    group_sum<G>(yy, sh, turn);
+      if (here(j)) in.get(kY, j, x[j]);
     const F scale = all(rsqrtf(yy[0] * inv + a.eps) * a.b), keep = all(a.a);
-    hh = all(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (here(j)) {
@@ -361,8 +396,10 @@ __global__ void __launch_bounds__(NT) norm_fwd_kernel(const NormArgs a) {
       }
     }
     if (a.n) {
-      float two[1] = {sum(hh)};
+      float two[kNext ? 2 : 1] = {sum(hh)};
+      if constexpr (kNext) two[1] = in.squares(row + step, true);
       group_sum<G>(two, sh, turn);
+      if constexpr (kNext) yy[0] = two[1];
       const F r = all(rsqrtf(two[0] * inv + a.eps));
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -374,7 +411,11 @@ __global__ void __launch_bounds__(NT) norm_fwd_kernel(const NormArgs a) {
           span.store(static_cast<T*>(a.n) + base, j, x[j]);
         }
       }
+    } else if constexpr (kNext) {
+      yy[0] = in.squares(row + step, true);
+      group_sum<G>(yy, sh, turn);
     }
+    if constexpr (kNext) in.turn();
   }
 }
 
@@ -401,23 +442,23 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
   constexpr int kSlots = PRE ? 5 : 3;
   const void* const five[5] = {a.y, a.z, a.dho, a.h, a.dn};
   const void* const(&from)[kSlots] = reinterpret_cast<const void* const(&)[kSlots]>(five);
-  Rows<T, V, NV, G, NT, ODD, kSlots> in(a, span, from, ring, row, step);
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGroups; r0 < a.rows; r0 += step, row += step) {
+  Rows<T, V, NV, G, NT, ODD, kSlots, PRE> in(a, span, from, ring, row, step);
+  constexpr bool kNext = in.kNext;
+  float yy[1];
+  if constexpr (kNext) {
     in.turn();
+    yy[0] = in.squares(row, false);
+    group_sum<G>(yy, sh, turn);
+  }
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGroups; r0 < a.rows; r0 += step, row += step) {
+    if constexpr (!kNext) in.turn();
     const bool live = row < a.rows;
     const int64_t base = row * a.width;
     auto here = [&](int j) { return live && span.any(j); };
-    F yt = all(0.f);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (here(j)) {
-        F y[NP];
-        in.get(kY, j, y);
-#pragma unroll
-        for (int i = 0; i < NP; ++i) yt = fma(y[i], y[i], yt);
-      }
-    float yy[1] = {sum(yt)};
-    group_sum<G>(yy, sh, turn);
+    if constexpr (!kNext) {
+      yy[0] = in.squares(row, false);
+      group_sum<G>(yy, sh, turn);
+    }
     const float iy = rsqrtf(yy[0] * inv + a.eps);
     // yn and d are formed again in each stage from the row at hand: registers,
     // not instructions, limit the warps here.
@@ -433,7 +474,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
           wpost.get(j, w);
 #pragma unroll
           for (int i = 0; i < NP; ++i) hp[j][i] = mul(mul(t[i], all(iy * a.b)), w[i]);
-          if (a.z) {
+          {
             in.get(kZ, j, t);
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
@@ -441,7 +482,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
               hp[j][i] = mul(hp[j][i], gate_of(q[j][i]));
             }
           }
-          if (a.h) {
+          {
             in.get(kH, j, t);
 #pragma unroll
             for (int i = 0; i < NP; ++i) hp[j][i] = fma(all(a.a), t[i], hp[j][i]);
@@ -470,7 +511,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
     for (int j = 0; j < NV; ++j) {
       if (here(j)) {
         F d[NP], w[NP], t[NP];
-        if (a.dho)
+        if (PRE || a.dho)
           in.get(kDho, j, d);
         else
 #pragma unroll
@@ -503,7 +544,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           F sg = all(1.f), sn = sg;
-          if (a.z) {
+          if (PRE || a.z) {
             sg = gate_of(q[j][i]);
             sn = mul(q[j][i], sg);
           }
@@ -517,8 +558,10 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
         if (a.z) span.store(static_cast<T*>(a.dz) + base, j, z);
       }
     }
-    float two[1] = {sum(ty)};
+    float two[kNext ? 2 : 1] = {sum(ty)};
+    if constexpr (kNext) two[1] = in.squares(row + step, true);
     group_sum<G>(two, sh, turn);
+    if constexpr (kNext) yy[0] = two[1];
     const F yk = all(iy * (one ? a.eps * iy * iy : 1.f)), yp = all(one ? 0.f : -iy * iy * (two[0] * inv));
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -529,6 +572,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
         for (int i = 0; i < NP; ++i) q[j][i] = fma(y[i], yp, mul(q[j][i], yk));
         span.store(static_cast<T*>(a.dy) + base, j, q[j]);
       }
+    if constexpr (kNext) in.turn();
   }
   // This CTA's share of the weight gradients: its groups' sums, in order.
   // (Without dn, w_pre's gradient is zero: gpre was never added to.)
@@ -602,7 +646,7 @@ int64_t resident(K kernel, int threads, size_t smem, int most) {
 template <typename T, int V, int NV, int G, int NT, bool ODD, bool PRE>
 void run_bwd(const NormArgs& a, int64_t blocks, float* dpost, float* dpre, cudaStream_t s) {
   auto k = norm_bwd_kernel<T, V, NV, G, NT, ODD, PRE>;
-  constexpr size_t rows = Rows<T, V, NV, G, NT, ODD, PRE ? 5 : 3>::kBytes;
+  constexpr size_t rows = Rows<T, V, NV, G, NT, ODD, PRE ? 5 : 3, PRE>::kBytes;
   constexpr size_t sums = NT / G > 1 ? sizeof(float) * NT * NV * V : 0;
   constexpr size_t smem = rows > sums ? rows : sums;
   static const int64_t fit = resident(k, NT, smem, kMaxCtas);
@@ -617,7 +661,7 @@ kda_status run(const NormArgs& a, bool bwd, float* dpost, float* dpre, cudaStrea
   const int64_t blocks = ceil_div(a.rows, NT / G);
   if (!bwd) {
     auto k = norm_fwd_kernel<T, V, NV, G, NT, ODD>;
-    constexpr size_t smem = Rows<T, V, NV, G, NT, ODD, 3>::kBytes;
+    constexpr size_t smem = Rows<T, V, NV, G, NT, ODD, 3, false>::kBytes;
     static const int64_t fit = resident(k, NT, smem, 1 << 30);
     k<<<static_cast<int>(blocks < fit ? blocks : fit), NT, smem, s>>>(a);
   } else if (a.dn) {
