@@ -243,9 +243,12 @@ __device__ __forceinline__ F2 gate_of(F2 e) {
 }
 
 // How a thread gets its share of its group's rows: 16-byte vectors by
-// asynchronous copies, up to four rows ahead, into a ring of shared memory in
+// asynchronous copies, one or two rows ahead, into a ring of shared memory in
 // which a thread reads only what it copied itself. The rows ahead hold no
-// registers and need no barrier. Tensors that are absent are not read.
+// registers and need no barrier. More of them do not pay: head norms of 128 in
+// training take 254 us with one row ahead, 264 with two, 275 with three, and
+// rows of 4096 163, 164 and 173 with two, three and four. Tensors that are
+// absent are not read.
 // FILL: the ring holds zeros in their place (the gate's: infinities, whose
 // sigmoid is 1), and whoever reads it need not ask which there are.
 enum Which { kY, kZ, kDho, kH, kDn };  // a backward without the next norm has no kH, kDn; a forward the first two and kH
@@ -258,7 +261,8 @@ template <typename T, int V, int NV, int G, int NT, bool ODD, int SLOTS, bool FI
 struct Rows {
   static constexpr int kStage = SLOTS * NV * NT * 16;  // bytes
   static constexpr int kFit = 200 * 1024 / kStage;
-  static constexpr int kDepth = kFit < 4 ? kFit : 4;
+  static constexpr int kWant = G > 32 ? 3 : 2;
+  static constexpr int kDepth = kFit < kWant ? kFit : kWant;
   static constexpr size_t kBytes = static_cast<size_t>(kDepth) * kStage;
   // The next row is at hand too: where a reduction is a barrier of the CTA,
   // its first one shares the last one of the row before.
