@@ -67,6 +67,49 @@ __device__ __forceinline__ void tmem_got(uint32_t (&r)[32]) {
                :
                : "memory");
 }
+__device__ __forceinline__ void tmem_ask(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_got(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15])
+               :
+               : "memory");
+}
+// The same across the turns of a loop: registers that the kernel declares
+// (score_regs) take the values, so that nothing can move them before they are there.
+__device__ __forceinline__ void score_regs() { asm volatile(".reg .b32 sx<32>;"); }
+__device__ __forceinline__ void score_ask(uint32_t taddr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {sx0,sx1,sx2,sx3,sx4,sx5,sx6,sx7,sx8,sx9,sx10,sx11,sx12,sx13,sx14,sx15,"
+      "sx16,sx17,sx18,sx19,sx20,sx21,sx22,sx23,sx24,sx25,sx26,sx27,sx28,sx29,sx30,sx31}, [%0];" ::"r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void score_got(uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;\n"
+      "mov.b32 %0, sx0; mov.b32 %1, sx1; mov.b32 %2, sx2; mov.b32 %3, sx3;\n"
+      "mov.b32 %4, sx4; mov.b32 %5, sx5; mov.b32 %6, sx6; mov.b32 %7, sx7;\n"
+      "mov.b32 %8, sx8; mov.b32 %9, sx9; mov.b32 %10, sx10; mov.b32 %11, sx11;\n"
+      "mov.b32 %12, sx12; mov.b32 %13, sx13; mov.b32 %14, sx14; mov.b32 %15, sx15;\n"
+      "mov.b32 %16, sx16; mov.b32 %17, sx17; mov.b32 %18, sx18; mov.b32 %19, sx19;\n"
+      "mov.b32 %20, sx20; mov.b32 %21, sx21; mov.b32 %22, sx22; mov.b32 %23, sx23;\n"
+      "mov.b32 %24, sx24; mov.b32 %25, sx25; mov.b32 %26, sx26; mov.b32 %27, sx27;\n"
+      "mov.b32 %28, sx28; mov.b32 %29, sx29; mov.b32 %30, sx30; mov.b32 %31, sx31;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      :
+      : "memory");
+}
 // Stores consecutive 32-bit columns of the thread's TMEM lane (tmem_st_wait completes it).
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -144,8 +187,9 @@ using namespace tc;
 
 constexpr int kRows = 128;               // query rows of an item, keys of a tile
 constexpr int kSoftmaxWarps = 8;         // two warpgroups
-constexpr int kMmaWarp = 8, kLoadWarp = 9;  // kLoadWarp: K, the one after it: V
-constexpr int kThreads = 352;
+constexpr int kMmaWarp = 0, kLoadWarp = 1;  // kLoadWarp: K, the one after it: V
+constexpr int kSoftmaxWarp = 4;             // the first; the warp before it is idle
+constexpr int kThreads = 32 * (kSoftmaxWarp + kSoftmaxWarps);
 constexpr int kMaxCtas = 152;            // one per SM
 constexpr int kRingBytes = 6 * 32768;    // K slots, then V slots
 constexpr float kRescale = 8.f;          // log2 growth of a maximum that rescales O
@@ -371,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (The query tile is the usual one, a block of all 128 rows after another.)
   constexpr int kGroup = 8 * D * 2;  // bytes of eight rows
   constexpr int kHalf = kRows * 128;  // bytes of a 64-channel block of the query tile
+  score_regs();
   extern __shared__ __align__(1024) uint8_t ring[];
   uint8_t* const qtile = ring + kRingBytes;
   Shared* const sh = reinterpret_cast<Shared*>(qtile + kSlot);
@@ -408,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_s = tmem, tmem_o = tmem + 256;  // S (P over it) of stream i at + 128 i, O at + 128 i
   Segment s;
 
-  if (warp >= kLoadWarp) {
+  if (warp == kLoadWarp || warp == kLoadWarp + 1) {
     // ---- loads ----
     const int which = warp - kLoadWarp;  // 0: K, 1: V
     const CUtensorMap* const map = which ? &vmap : &kmap;
@@ -535,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++turn_p[st];
         if (!ok) break;
         fence_after_sync();
-        const uint32_t vd = vlo + vslot * (kSlot >> 4), ts = tmem_s + 128 * st + 64, to = tmem_o + 128 * st;
+        const uint32_t vd = vlo + vslot * (kSlot >> 4), ts = tmem_s + 128 * st, to = tmem_o + 128 * st;
         if (elect()) {
 #pragma unroll
           for (int k = 0; k < kRows / 16; ++k)
@@ -554,9 +599,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect()) mma_commit(&sh->drain);
     settle(&sh->drain, 0);
     __syncwarp();
-  } else {
+  } else if (warp >= kSoftmaxWarp) {
     // ---- softmax: thread = row, warpgroup = stream ----
-    const int st = warp >> 2, row = tid & 127;
+    const int st = (warp - kSoftmaxWarp) >> 2, row = tid & 127;
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
     const uint32_t my_s = tmem_s + 128 * st + lane_base;
     const uint32_t my_o = tmem_o + 128 * st + lane_base;
@@ -617,11 +662,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_smem();
         }
         if (warp_used) {
-          // One pass over the row, 32 scores at a time with the next 32 on
-          // their way: probabilities against the maximum so far, and the
-          // maximum of this tile with them. P stays in registers until that
-          // has not grown by more than 2^8 (else the pass is made again from
-          // S, which is still there: in a stream's first tile, and rarely after).
           const int open = limit - k0;  // keys of the tile that the row sees
           if (__any_sync(~0u, open < kRows)) {  // an item's last tiles: -inf into S first, off the common path
 #pragma unroll 1
@@ -636,49 +676,81 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_st_wait();
           }
+          // One pass over the row, 32 scores at a time with the next 32 on
+          // their way: probabilities against the maximum so far, written over
+          // scores that have been read. Where the maximum has grown by more
+          // than 2^8 (in a stream's first scores, and rarely after) the row
+          // goes over to it first, and what there is of the row is scaled.
+          // The loop stays rolled: its code and that of the warp that issues
+          // the products then both stay in the instruction cache.
           const uint64_t sc2 = pack2(__float_as_uint(sc), __float_as_uint(sc));
-          uint32_t p[2][32];
-          uint64_t sum[4];
-          for (bool first = true;; first = false) {
+          uint64_t sum[4] = {0, 0, 0, 0};
+          uint32_t x[32];
+          auto highest = [&]() {
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 32; c += 2)
+              top[c / 2 & 3] = fmaxf(fmaxf(top[c / 2 & 3], __uint_as_float(x[c])), __uint_as_float(x[c + 1]));
+            return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+          };
+          score_ask(my_s);
+          score_got(x);
+          float mn = highest();
+#pragma unroll 1
+          for (int h = 0; h < 4; ++h) {
+            const bool grow = mn > m + kRescale;  // m = -inf: any finite maximum
+            if (__any_sync(~0u, grow)) {
+              // by a whole number of octaves: the factor is exact, for P too
+              const float k = ceilf(mn - m);
+              const float f = !grow ? 1.f : k < 126.f ? __uint_as_float((127u - static_cast<uint32_t>(k)) << 23) : 0.f;
+              if (grow) m = m == -INFINITY ? mn : m + k;
+              l *= f;
+              const uint64_t f2 = pack2(__float_as_uint(f), __float_as_uint(f));
+#pragma unroll
+              for (int c = 0; c < 4; ++c) sum[c] = fma2(sum[c], f2, 0);
+              tmem_st_wait();
+              uint32_t y[16];
+#pragma unroll 1
+              for (int c = 0; c < 16 * h; c += 16) {
+                tmem_ask(my_s + c, y);
+                tmem_got(y);
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                  y[q] = pack_bf16(__uint_as_float(y[q] << 16) * f, __uint_as_float(y[q] & 0xffff0000u) * f);
+                tmem_st(my_s + c, y);
+              }
+              if (i >= 2) {  // the stream's O exists, and is complete: S of this tile was issued after it
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                  tmem_ask(my_o + c, y);
+                  tmem_got(y);
+#pragma unroll
+                  for (int q = 0; q < 16; ++q) y[q] = __float_as_uint(__uint_as_float(y[q]) * f);
+                  tmem_st(my_o + c, y);
+                }
+              }
+            }
             const float ref = m == -INFINITY ? 0.f : m;
             const uint64_t ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            uint32_t x[2][32];
-            sum[0] = sum[1] = sum[2] = sum[3] = 0;
-            tmem_ask(my_s, x[0]);
+            uint64_t t[16];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              uint32_t(&y)[32] = x[h & 1];
-              tmem_got(y);
-              if (h < 3) tmem_ask(my_s + 32 * (h + 1), x[(h + 1) & 1]);
+            for (int c = 0; c < 16; ++c) t[c] = fma2(pack2(x[2 * c], x[2 * c + 1]), sc2, ref2);
+            score_ask(my_s + (32 * (h + 1) & 96));  // after the last: not used
+            uint32_t p[16];
+            auto exps = [&](int c) {
+              const float2 e = unpack2(t[c]);
+              const float e0 = ex2(e.x), e1 = ex2(e.y);
+              sum[c & 3] = add2(sum[c & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
+              p[c] = pack_bf16(e0, e1);
+            };
 #pragma unroll
-              for (int c = 0; c < 32; c += 2) {
-                top[c / 2 & 3] = fmaxf(fmaxf(top[c / 2 & 3], __uint_as_float(y[c])), __uint_as_float(y[c + 1]));
-                const float2 t = unpack2(fma2(pack2(y[c], y[c + 1]), sc2, ref2));
-                const float e0 = ex2(t.x), e1 = ex2(t.y);
-                sum[c / 2 & 3] = add2(sum[c / 2 & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
-                p[h / 2][16 * (h & 1) + c / 2] = pack_bf16(e0, e1);
-              }
-            }
-            const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
-            const bool grow = first && mn > m + kRescale;  // m = -inf: any finite maximum
-            if (!__any_sync(~0u, grow)) break;
-            const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - mn)) : 1.f;
-            if (grow) m = mn;
-            l *= f;
-            if (i >= 2) {  // the stream's O exists, and is complete: S of this tile was issued after it
-#pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                tmem_ask(my_o + c, x[0]);
-                tmem_got(x[0]);
+            for (int c = 0; c < 8; ++c) exps(c);
+            score_got(x);
+            mn = highest();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) x[0][k] = __float_as_uint(__uint_as_float(x[0][k]) * f);
-                tmem_st(my_o + c, x[0]);
-              }
-            }
+            for (int c = 8; c < 16; ++c) exps(c);
+            tmem_st(my_s + 16 * h, p);
           }
-          tmem_st(my_s + 64, p[0]);
-          tmem_st(my_s + 96, p[1]);
           const float2 all = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
           l += all.x + all.y;
           tmem_st_wait();
@@ -742,13 +814,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           parts.ml[part * 2 * kRows + row] = mm;
           parts.ml[part * 2 * kRows + kRows + row] = ll;
         }
-        if (tid == 0) parts.bad[part] = bad;
+        if (warp == kSoftmaxWarp && lane == 0) parts.bad[part] = bad;
         // The CTAs of this item: the run that holds its first tile, and those after it.
         const int64_t run_end = min((static_cast<int64_t>(blockIdx.x) + 1) * sh->run, sh->total);
         const int64_t item0 = run_end - w.left - s.j1, item1 = item0 + s.tiles;
-        const int c0 = static_cast<int>(item0 / sh->run), c1 = static_cast<int>((item1 - 1) / sh->run);
+        const int c0 = static_cast<int>(quotient(item0, sh->run)), c1 = static_cast<int>(quotient(item1 - 1, sh->run));
         named_bar_sync(1, 256);
-        if (tid == 0) {
+        if (warp == kSoftmaxWarp && lane == 0) {
           __threadfence();  // this CTA's part, written before the barrier, ...
           sh->last = atomicAdd(&parts.count[c0], 1u) == static_cast<uint32_t>(c1 - c0);
           __threadfence();  // ... and the others' before what follows it
@@ -770,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sh->l[0][row] = sum == 0.f || any ? 0.f : 1.f / sum;
           }
           named_bar_sync(1, 256);
-          for (int e = tid; e < s.rows * (D / 8); e += 256) {
+          for (int e = tid - 32 * kSoftmaxWarp; e < s.rows * (D / 8); e += 256) {
             const int r = e / (D / 8), c8 = e % (D / 8) * 8;
             const float top = sh->m[0][r], scale = sh->l[0][r];
             float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
