@@ -138,7 +138,12 @@ __global__ void __launch_bounds__(kThreads) kda_step_kernel(const StepArgs a) {
   __shared__ __align__(16) float s_v[kBatch][kCols];
   __shared__ float s_beta[kBatch];
   __shared__ __align__(16) float s_pk[2][4][kCols], s_pq[2][4][kCols];
-  __shared__ float s_kq[2][4];
+  // kh . qh: of each staged token by one warp, or a part of every warp's sums.
+  // Each is the faster way where it is taken: with one token for 128 x 96 states
+  // of 128, once a token takes KDA 247 us against 261, but GDN-2
+  // 269 against 263, and states of 64 lose a tenth by it.
+  constexpr bool kOnce = !CG && D == 128;
+  __shared__ float s_kq[kOnce ? 1 : 2][4];
 
   const int cb = static_cast<int>(blockIdx.x) % kSplit;
   const int item = static_cast<int>(blockIdx.x) / kSplit;
@@ -234,6 +239,16 @@ __global__ void __launch_bounds__(kThreads) kda_step_kernel(const StepArgs a) {
       }
     }
     __syncthreads();
+    if (kOnce && warp < nb) {  // read after the next barrier
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float4 c = s_c[warp][lane + i * kSkew];
+        ss = fmaf(c.y, c.z, ss);
+      }
+      ss = warp_sum(ss);
+      if (lane == 0) s_kq[0][warp] = ss;
+    }
 
     for (int t = 0; t < nb; ++t) {
       F4 pk = {0, 0}, pq = {0, 0};
@@ -244,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) kda_step_kernel(const StepArgs a) {
         S[i] = mul(S[i], c.x);
         pk = fma(S[i], CG ? c.w : c.y, pk);
         pq = fma(S[i], c.z, pq);
-        kq = fmaf(c.y, c.z, kq);
+        if (!kOnce) kq = fmaf(c.y, c.z, kq);
       }
       // Sums over the 4 row lanes of the warp: a lane passes on what its
       // partner keeps, pk against pq, then one pair of columns against the
@@ -255,12 +270,14 @@ __global__ void __launch_bounds__(kThreads) kda_step_kernel(const StepArgs a) {
       w.a = add(keep.a, __shfl_xor_sync(~0u, give.a, 16));
       w.b = add(keep.b, __shfl_xor_sync(~0u, give.b, 16));
       const uint64_t pair = add(odd ? w.b : w.a, __shfl_xor_sync(~0u, odd ? w.a : w.b, 8));
-      kq += __shfl_xor_sync(~0u, kq, 8);
-      kq += __shfl_xor_sync(~0u, kq, 16);
+      if (!kOnce) {
+        kq += __shfl_xor_sync(~0u, kq, 8);
+        kq += __shfl_xor_sync(~0u, kq, 16);
+      }
       // then over the 4 warps; two buffers, so that one barrier a token is enough
       const int buf = t & 1;
       *reinterpret_cast<uint64_t*>(&(hi ? s_pq : s_pk)[buf][warp][cg * 4 + (odd ? 2 : 0)]) = pair;
-      if (lane == 0) s_kq[buf][warp] = kq;
+      if (!kOnce && lane == 0) s_kq[buf][warp] = kq;
       __syncthreads();
       pk = *reinterpret_cast<const F4*>(&s_pk[buf][0][cg * 4]);
 #pragma unroll
@@ -272,11 +289,11 @@ __global__ void __launch_bounds__(kThreads) kda_step_kernel(const StepArgs a) {
       for (int i = 0; i < R; ++i) S[i] = fma(r, s_c[t][at0 + i * (16 / E)].y, S[i]);
       if (row0 == 0) {
         pq = *reinterpret_cast<const F4*>(&s_pq[buf][0][cg * 4]);
-        kq = s_kq[buf][0];
+        kq = kOnce ? s_kq[0][t] : s_kq[buf][0];
 #pragma unroll
         for (int j = 1; j < 4; ++j) {
           pq = add(pq, *reinterpret_cast<const F4*>(&s_pq[buf][j][cg * 4]));
-          kq += s_kq[buf][j];
+          if (!kOnce) kq += s_kq[buf][j];
         }
         store4(o + (t0 + t) * tok + cg * 4, values(fma(r, kq, pq)));
       }
