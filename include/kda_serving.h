@@ -181,7 +181,10 @@ kda_status kda_paged_append(const kda_paged_problem* p, const void* k, const voi
 /* q, o: [S, Hq, D]; k_pages, v_pages: [num_pages, page_size, Hkv, D]. The
  * call's status word is the head of workspace (kda_query_device_status):
  * lengths that do not fit S or the table, and pages outside [0, num_pages)
- * within a sequence's length; such a sequence's rows of o are zero. */
+ * within a sequence's length. A kv_lens entry outside the table's reach makes
+ * its sequence's rows of o zero, a page outside the pool those rows that look
+ * it up (with the others of their tile of 128 rows), and cu_seqlens entries
+ * that decrease or leave [0, S] leave o unwritten. */
 size_t kda_paged_attention_workspace_bytes(const kda_paged_problem* p);
 kda_status kda_paged_attention(const kda_paged_problem* p, const void* q,
                                const void* k_pages, const void* v_pages,

@@ -13,8 +13,12 @@
 // anyway, and needs no statistics or h' from the forward.
 //
 // Bound: HBM; each tensor is read or written once. A row stays at hand between
-// its reductions. A group of kGroup threads takes a row; a thread holds kVecs
-// 16-byte vectors of it.
+// its reductions. A group of G threads takes a row; a thread holds NV 16-byte
+// vectors of it. Forward and backward together, bf16: head norms of 128 with a
+// gate take 253 us, 94% of the measured copy rate; 8192 rows of 4096 with the
+// next norm 162 us, 79%. There a row is spread over a CTA and its reductions
+// are barriers: between them the SM waits for the slowest warp, and the weight
+// gradients' registers leave room for one CTA.
 //
 // Rows of an odd width start anywhere within 16 bytes. There a group works on
 // the aligned vectors that cover its row, `shift` elements before its start;

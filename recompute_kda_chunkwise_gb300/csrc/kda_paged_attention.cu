@@ -8,8 +8,8 @@
 // grouped head reads K and V once for the whole group, and a chunk of tokens
 // fills the tensor cores' 128 rows. Keys come in tiles of 128: S = Q K^T and
 // O += P V are 128 x 128 x D and 128 x D x 128 products with fp32 sums in
-// TMEM; P goes back to TMEM as bf16 over its own S and is the A operand of
-// the second product from there.
+// TMEM; P goes back to TMEM as bf16, over those of its own scores that have
+// been read, and is the A operand of the second product from there.
 //
 // Two streams. Even and odd key tiles of a segment go to two warpgroups, each
 // with its own S, running maximum, sum and O: while one forms its
@@ -34,8 +34,16 @@
 // selection and set to zero in V, so stale cache rows (NaN among them) have no
 // part in the result.
 //
-// Bound: decode steps by HBM (K and V once), chunks by the exponentials and
-// the tensor cores: a 128 x 128 tile takes about 1024 cycles of either.
+// Bound: decode steps by HBM (K and V once): 32 sequences of 16384 keys, 64
+// query heads on 8 of 128 channels, take 235 us with their append, 87% of the
+// measured copy rate; about 13 us of it is the start, the cuts and the joins.
+// Chunks by the tensor cores, in principle: a 128 x 128 tile is 1024 cycles of
+// theirs and 512 of exponentials. Chunks of up to 2048 tokens over 8192 keys
+// take 720 us, 57% of the measured bf16 rate, a tile every 1655 cycles: each
+// stream's scores, probabilities (1725 cycles of latency for a thread's 128)
+// and products (1585) wait for one another, and two streams hide half of that.
+// Without the loads that stays as it is; without the exponentials it is 1555,
+// which is what the one issuing warp takes.
 #include <math.h>
 
 #include "kda_paged.cuh"
