@@ -85,6 +85,22 @@ def test_large_scores_and_a_negative_scale():
     compare(x, scale=0.0)
 
 
+@pytest.mark.parametrize("octaves", [10.0, -10.0, 3.0])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,lens", [([1], [600]), ([140, 2], [600, 333])])
+def test_maxima_that_move_all_along_the_keys(new, lens, D, octaves):
+    """Scores that rise (or fall) by so many octaves every 32 keys, with noise:
+    the running maximum moves inside every tile. The scores stay below 190
+    octaves, so three fp32 roundings of them are below 2^-14 of a probability."""
+    x = make(new, lens, 2, 1, D, 8, seed=9, std=0.25)
+    x["q"][..., 0] = 8.0
+    step = octaves / 32 / (8.0 * D ** -0.5 * 1.4426950408889634)
+    for n, total in enumerate(lens):
+        t = torch.arange(total, device="cuda")
+        x["kp"][x["table"][n, t // 8].long(), t % 8, :, 0] = (t * step).to(torch.bfloat16)[:, None]
+    compare(x)
+
+
 def test_rows_that_see_nothing_are_zero():
     """A sequence shorter than its new tokens: the first of them have no position."""
     x = make([6, 4, 150], [2, 0, 20], 4, 2, 64, 16, seed=5)
