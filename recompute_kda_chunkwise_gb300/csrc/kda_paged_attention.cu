@@ -32,7 +32,10 @@
 // page: boxes of gcd(page_size, 128) rows, whose pages a warp looks up 32 at a
 // time, a batch ahead. Rows past what an item sees are masked out of S by
 // selection and set to zero in V, so stale cache rows (NaN among them) have no
-// part in the result.
+// part in the result. A key that only some of the tile's rows see is masked out
+// of S for the others, and where its V holds an infinity or a NaN (zero times
+// which is not zero) that V row is zeroed too and added afterwards, to the rows
+// that see it.
 //
 // Bound: decode steps by HBM (K and V once): 32 sequences of 16384 keys, 64
 // query heads on 8 of 128 channels, take 235 us with their append, 87% of the
@@ -279,6 +282,7 @@ struct Shared {
   int64_t run, total, start_base;
   int start_n;
   int bad;
+  uint32_t held[8];                   // a segment's held keys (see add_held): 256 of them, from a tile's start
   float m[2][kRows], l[2][kRows];
 };
 
@@ -411,9 +415,71 @@ __device__ void plan(const PagedArgs& a, Shared* sh, Walk& w) {
   w.j = static_cast<int>(rest);
 }
 
+// Whether one of eight bf16 values is an infinity or a NaN: adding 1 to an
+// exponent of all ones carries into the sign's place.
+__device__ __forceinline__ bool not_finite(uint4 x) {
+  uint32_t top = 0;
+  for (uint32_t u : {x.x, x.y, x.z, x.w}) top |= (u & 0x7f807f80u) + 0x00800080u;
+  return (top & 0x80008000u) != 0;
+}
+
+// Adds a stream's held keys to its O in TMEM: keys that some rows of the tile see
+// and others do not, whose V row is not finite and was zero in the product. They
+// lie in key tile `tile` + `odd`, the one of the two that is this stream's. Each
+// row that sees one forms its probability again, in fp32 (its sum has it
+// already), and takes the V row from the cache; the other rows' O stays as it
+// was. Rare, and kept out of the loops' code and registers.
+template <int D>
+__device__ __noinline__ void add_held(const PagedArgs& a, const uint32_t* held, int n, int hk, int tile, int odd, int limit,
+                                      const uint4* q, float m, float sc, uint32_t keep, uint32_t sign, uint32_t my_o) {
+  const float ref = m == -INFINITY ? 0.f : m;
+  for (int w = 4 * odd; w < 4 * odd + 4; ++w) {
+    for (uint32_t left = held[w]; left; left &= left - 1) {
+      const int key = tile * kRows + 32 * w + __ffs(left) - 1;
+      const int64_t page = a.table[static_cast<int64_t>(n) * a.width + key / a.page];
+      if (page < 0 || page >= a.pages) continue;
+      const int64_t at = ((page * a.page + key % a.page) * a.Hkv + hk) * D;
+      const uint4* const k = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + at);
+      const uint32_t* const v = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.v) + at);
+      const bool sees = key < limit;
+      float p = 0.f;
+      if (sees) {
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 x = q[c], y = k[c];
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t u = (xs[i] & keep) ^ sign;
+            p = fmaf(__uint_as_float(u << 16), __uint_as_float(ys[i] << 16), p);
+            p = fmaf(__uint_as_float(u & 0xffff0000u), __uint_as_float(ys[i] & 0xffff0000u), p);
+          }
+        }
+        p = ex2(fmaf(p, sc, -ref));
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        uint32_t x[16];
+        tmem_ask(my_o + c, x);
+        tmem_got(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t u = v[c / 2 + i];
+          const float lo = fmaf(p, __uint_as_float(u << 16), __uint_as_float(x[2 * i]));
+          const float hi = fmaf(p, __uint_as_float(u & 0xffff0000u), __uint_as_float(x[2 * i + 1]));
+          x[2 * i] = sees ? __float_as_uint(lo) : x[2 * i];
+          x[2 * i + 1] = sees ? __float_as_uint(hi) : x[2 * i + 1];
+        }
+        tmem_st(my_o + c, x);
+        tmem_st_wait();
+      }
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    kda_paged_attention_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap,
+    kda_paged_attention_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ CUtensorMap kmap,
                                const __grid_constant__ CUtensorMap vmap, const int box, const float sc,
                                const uint32_t keep, const uint32_t sign) {
   constexpr int kSlot = kRows * D * 2;       // bytes of a ring slot
@@ -631,6 +697,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const int limit = used ? s.first + token : 0;  // keys this row sees
+      // Keys from `some` on are not seen by the tile's first row, those before
+      // by every row in use: at most 127, in this tile of keys and the next.
+      const int some = max(s.first + s.mt * kRows / group, 0);
+      if (lane == 0) sh->held[4 * ((s.j0 + st + some / kRows) & 1) + (warp & 3)] = 0;  // of the one that is this stream's
       {
         // Q rows into the tile, 16-byte chunks in the 128-byte swizzle; this
         // warpgroup's half of the channels
@@ -655,20 +725,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_warp(sh, &sh->s_full[st], turn_s++ & 1, a.status);
         fence_after_sync();
         const int k0 = (s.j0 + i) * kRows;
-        if (k0 + kRows > s.seen) {
-          // keys past what any row of the tile sees: V rows to zero (their
-          // probabilities are zero, but zero times a stale NaN is not)
-          const int64_t vpos = tiles0 + i;
-          const int slot = static_cast<int>(vpos % kSlots);
-          const bool here = wait_warp(sh, &sh->full[1][slot], static_cast<uint32_t>((vpos / kSlots) & 1), a.status);
-          if (here && k0 + row >= s.seen) {
-            uint8_t* const v = ring + kRingBytes / 2 + slot * kSlot + (row >> 3) * kGroup + (row & 7) * 128;
-#pragma unroll
-            for (int c = 0; c < D * 2; c += 16)
-              *reinterpret_cast<uint4*>(v + (c / 128) * 1024 + c % 128) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_async_smem();
-        }
         if (warp_used) {
           const int open = limit - k0;  // keys of the tile that the row sees
           if (__any_sync(~0u, open < kRows)) {  // an item's last tiles: -inf into S first, off the common path
@@ -763,6 +819,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           l += all.x + all.y;
           tmem_st_wait();
         }
+        if (k0 + kRows > some) {
+          // keys that not every row of the tile sees: V rows past what any row
+          // sees to zero, and those that are not finite (the probabilities of
+          // rows that do not see them are zero, but zero times a NaN is not).
+          // Behind the probabilities, when V has long arrived.
+          const int64_t vpos = tiles0 + i;
+          const int slot = static_cast<int>(vpos % kSlots), key = k0 + row;
+          const bool here = wait_warp(sh, &sh->full[1][slot], static_cast<uint32_t>((vpos / kSlots) & 1), a.status);
+          uint8_t* const v = ring + kRingBytes / 2 + slot * kSlot + (row >> 3) * kGroup + (row & 7) * 128;
+          auto chunk = [&](int c) {  // each lane from another one on: eight rows are a multiple of 128 bytes apart
+            const int x = (c + lane) % (D / 8);
+            return reinterpret_cast<uint4*>(v + x / 8 * 1024 + x % 8 * 16);
+          };
+          bool hold = false;
+          if (here && key >= some && key < s.seen) {
+#pragma unroll 8
+            for (int c = 0; c < D / 8; ++c) hold |= not_finite(*chunk(c));
+          }
+          if (here && (hold || key >= s.seen)) {
+#pragma unroll 8
+            for (int c = 0; c < D / 8; ++c) *chunk(c) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_async_smem();
+          if (hold) atomicOr(&sh->held[((key - some / kRows * kRows) >> 5) & 7], 1u << lane);
+        }
         fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->p_ready[st]);
@@ -773,6 +854,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       sh->m[st][row] = m;
       sh->l[st][row] = l;
       named_bar_sync(1, 256);
+      {
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) any |= sh->held[i];
+        if (any) {  // the same for all 256 threads
+          if (warp_used)
+            add_held<D>(a, sh->held, s.n, s.hk, some / kRows, (s.j0 + st + some / kRows) & 1, limit,
+                        reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                       (static_cast<int64_t>(s.lo + token) * a.Hq + head) * D),
+                        m, sc, keep, sign, my_o);
+          fence_before_sync();
+          named_bar_sync(1, 256);
+          fence_after_sync();
+        }
+      }
       const float m0 = sh->m[0][row], m1 = sh->m[1][row];
       const float mm = fmaxf(m0, m1);
       const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - mm), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - mm);
