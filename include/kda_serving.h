@@ -151,7 +151,8 @@ kda_status kda_verify_drafts(int32_t num_seqs, int32_t max_drafts, int32_t vocab
  * position kv_lens[n] - L + i and attends to the positions up to its own,
  *     o = softmax(scale * q K^T) V     per query head; heads h * Hq / Hkv ..
  *                                      share key/value head h.
- * A token whose position is negative (kv_lens[n] < L) sees nothing: o = 0.
+ * A token whose position is negative (kv_lens[n] < L) sees nothing: o = 0
+ * (while one whose scores are all -inf has o = NaN, from 0 / 0).
  * Cache rows past kv_lens[n] are never used, whatever they hold, and a key or
  * value that is not finite reaches the tokens that see it and no other. bf16,
  * head_dim 64 or 128, Hq a multiple of Hkv, page_size a multiple of 8; fp32

@@ -876,7 +876,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = nt == s.tiles;
       const int bad = *const_cast<volatile int*>(&sh->bad_page[seg++ & 15]);
       const int part = 2 * static_cast<int>(blockIdx.x) + (s.j0 == 0 ? 1 : 0);
-      const float inv = whole ? (ll == 0.f || bad ? 0.f : 1.f / ll) : 1.f;
+      // A sum of zero: no key is seen (zeros), or every score that is was -inf (0 / 0, as the definition has it).
+      const float none = limit > 0 ? __uint_as_float(0x7fc00000u) : 0.f;
+      const float inv = !whole ? 1.f : bad ? 0.f : ll == 0.f ? none : 1.f / ll;
       if (warp_used) {
 #pragma unroll 1
         for (int c = st * (D / 2); c < (st + 1) * (D / 2); c += 32) {
@@ -943,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum += __ldcg(q + kRows) * (pm == -INFINITY ? 0.f : ex2(pm - top));
             }
             sh->m[0][row] = top;
-            sh->l[0][row] = sum == 0.f || any ? 0.f : 1.f / sum;
+            sh->l[0][row] = any ? 0.f : sum == 0.f ? none : 1.f / sum;
           }
           named_bar_sync(1, 256);
           for (int e = tid - 32 * kSoftmaxWarp; e < s.rows * (D / 8); e += 256) {

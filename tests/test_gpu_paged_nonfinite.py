@@ -57,3 +57,15 @@ def test_values_that_every_row_sees(new, lens):
     spoil(x, "vp", 0, 200, float("nan"), channel=90)
     o = compare(x)
     assert torch.isinf(o[..., 3]).all() and torch.isnan(o[..., 90]).all() and torch.isfinite(o[..., :3]).all()
+
+
+@pytest.mark.parametrize("new,lens", [([1], [1]), ([3], [2]), ([130, 1], [131, 700]), ([1], [40000])])
+def test_scores_that_are_all_minus_infinity(new, lens):
+    """exp(-inf - (-inf)): NaN, unlike a row that sees no key, which is zero."""
+    x = make(new, lens, 4, 2, 64, 16, seed=3)
+    x["q"][..., 7] = -1.0
+    x["kp"][..., 7] = float("inf")
+    o = compare(x)
+    assert torch.isnan(o[x["cu"][1] - 1]).all()
+    if lens[0] < new[0]:
+        assert not o[0].any()
