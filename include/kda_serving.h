@@ -176,7 +176,8 @@ typedef struct {
 
 /* Writes the new tokens' k and v [S, Hkv, D] to their cache rows. A token
  * whose position is negative, past the table, or whose page is outside
- * [0, num_pages) is skipped and recorded in status. */
+ * [0, num_pages), and one that cu_seqlens (where it decreases) puts into no
+ * sequence, is skipped and recorded in status. */
 kda_status kda_paged_append(const kda_paged_problem* p, const void* k, const void* v,
                             void* k_pages, void* v_pages, int32_t* status, void* stream);
 

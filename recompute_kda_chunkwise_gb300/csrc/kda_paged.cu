@@ -28,7 +28,8 @@ __global__ void __launch_bounds__(128) kda_paged_append_kernel(const PagedArgs a
   int64_t at = -1;
   if (ok) {
     const int64_t pos = static_cast<int64_t>(a.lens[n]) - (a.cu[n + 1] - tok);
-    ok = tok >= a.cu[n] && pos >= 0 && pos / a.page < a.width;
+    // where cu_seqlens decreases, sequence n need not hold the token
+    ok = tok >= a.cu[n] && tok < a.cu[n + 1] && pos >= 0 && pos / a.page < a.width;
     if (ok) {
       const int64_t page = a.table[static_cast<int64_t>(n) * a.width + pos / a.page];
       ok = page >= 0 && page < a.pages;
