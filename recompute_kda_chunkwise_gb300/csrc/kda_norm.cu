@@ -511,8 +511,9 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (PRE ? 2 : 3) : 1) norm_bwd_ke
       group_sum<G>(two, sh, turn);
       const float r = rsqrtf(two[0] * inv + a.eps);
       ih = all(r);
+      // r^3 alone leaves fp32's range long before r^2 mean(d hn) does: r times each factor in turn
       dk = all(r * (one ? a.eps * r * r : 1.f));
-      dp = all(one ? 0.f : -(r * r * r) * (two[1] * inv));
+      dp = all(one ? 0.f : -r * (r * (r * (two[1] * inv))));
     }
     F ty = all(0.f);
 #pragma unroll
