@@ -229,13 +229,14 @@ __device__ __forceinline__ void group_sum(float (&x)[N], float* sh, int& turn) {
 }
 
 // s = sigmoid(z) = 1 / (1 + e) and n = sigmoid(-z) = e s with e = exp(-z), so
-// that neither is a difference that cancels. e stops at 2^125, where 1 + e is
-// still finite: below z = -86.6 both stay at what they are there (2^-125, 1).
+// that neither is a difference that cancels. e stops at 2^127, where 1 + e is
+// still finite and its reciprocal, below fp32's normal numbers, is 0: from
+// z = -87.4 down to -inf the gate is shut, and the gradient through it is 0.
 __device__ __forceinline__ F2 gate_exp(F2 z) {
   const float2 t = both(mul(z, all(-1.4426950408889634f)));
   float ex, ey;
-  asm("{.reg .f32 t;\n min.NaN.f32 t, %1, 0f42FA0000;\n ex2.approx.ftz.f32 %0, t;\n}" : "=f"(ex) : "f"(t.x));
-  asm("{.reg .f32 t;\n min.NaN.f32 t, %1, 0f42FA0000;\n ex2.approx.ftz.f32 %0, t;\n}" : "=f"(ey) : "f"(t.y));
+  asm("{.reg .f32 t;\n min.NaN.f32 t, %1, 0f42FE0000;\n ex2.approx.ftz.f32 %0, t;\n}" : "=f"(ex) : "f"(t.x));
+  asm("{.reg .f32 t;\n min.NaN.f32 t, %1, 0f42FE0000;\n ex2.approx.ftz.f32 %0, t;\n}" : "=f"(ey) : "f"(t.y));
   return f2(ex, ey);
 }
 __device__ __forceinline__ F2 gate_of(F2 e) {
