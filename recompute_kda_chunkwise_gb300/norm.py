@@ -10,6 +10,7 @@ h and w_pre it is the gated output norm of a delta-rule layer.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from ._serving import bind, done
 
@@ -34,7 +35,8 @@ def block_norm_bwd(y, *, z=None, h=None, w_post=None, w_pre=None, dh_out=None, d
 
 
 class BlockNormFunction(torch.autograd.Function):
-    """Autograd wrapper: saves the inputs only."""
+    """Autograd wrapper: saves the inputs only. Differentiable once: a second
+    derivative through it raises."""
 
     @staticmethod
     def forward(ctx, y, z, h, w_post, w_pre, residual_scale, block_scale, eps):
@@ -46,6 +48,7 @@ class BlockNormFunction(torch.autograd.Function):
         return h_out if n is None else (h_out, n)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh_out, dn=None):
         y, z, h, w_post, w_pre = ctx.saved_tensors
         c = lambda t: None if t is None else t.contiguous()  # noqa: E731
@@ -55,5 +58,5 @@ class BlockNormFunction(torch.autograd.Function):
 
 def block_norm(y, *, z=None, h=None, w_post=None, w_pre=None, residual_scale: float = 1.0, block_scale: float = 1.0,
                eps: float = 1e-5):
-    """Differentiable block norm. Returns h_out, or (h_out, n) with w_pre."""
+    """Differentiable (once) block norm. Returns h_out, or (h_out, n) with w_pre."""
     return BlockNormFunction.apply(y, z, h, w_post, w_pre, residual_scale, block_scale, eps)
