@@ -12,6 +12,7 @@ import os
 import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libkda_gb300.so")
@@ -434,7 +435,8 @@ def state_prefix(A, B, x0=None, *, direction: int, layout: str, x_end=None):
 
 
 class GDN2Function(torch.autograd.Function):
-    """Autograd wrapper of the GDN-2 operator (saves the inputs and ctx only)."""
+    """Autograd wrapper of the GDN-2 operator (saves the inputs and ctx only).
+    Differentiable once: a second derivative through it raises."""
 
     @staticmethod
     def forward(actx, q, k, v, g, erase, write, A_log, dt_bias, cu_seqlens, h0, output_final_state,
@@ -447,6 +449,7 @@ class GDN2Function(torch.autograd.Function):
         return (r[0], r[2]) if output_final_state else r[0]
 
     @staticmethod
+    @once_differentiable
     def backward(actx, dO, dht=None):
         q, k, v, g, erase, write, A_log, dt_bias, cu_seqlens, ctx = actx.saved_tensors
         scale, lower_bound, eps, has_h0 = actx.args
@@ -468,7 +471,8 @@ def gdn2(q, k, v, g, erase, write, A_log, dt_bias, cu_seqlens, scale: float = 1.
 
 
 class KDAFunction(torch.autograd.Function):
-    """Autograd wrapper: forward saves the inputs and the checkpoint ctx only."""
+    """Autograd wrapper: forward saves the inputs and the checkpoint ctx only.
+    Differentiable once: a second derivative through it raises."""
 
     @staticmethod
     def forward(actx, q, k, v, g, beta, A_log, dt_bias, cu_seqlens, h0, output_final_state, scale,
@@ -481,6 +485,7 @@ class KDAFunction(torch.autograd.Function):
         return (o, r[2]) if output_final_state else o
 
     @staticmethod
+    @once_differentiable
     def backward(actx, dO, dht=None):
         q, k, v, g, beta, A_log, dt_bias, cu_seqlens, ctx = actx.saved_tensors
         scale, lower_bound, eps, has_h0, _ = actx.args
