@@ -32,6 +32,7 @@
 // rounding of the two terms: width 1 multiplies by that share instead.
 #include <math.h>
 
+#include "kda_device.cuh"
 #include "kda_internal.cuh"
 #include "kda_serving.h"
 
@@ -641,45 +642,54 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* part, in
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// CTAs that the SMs hold at once (a launch's loop takes the rest of the rows), at most `most`.
+// CTAs that a device's SMs hold at once (a launch's loop takes the rest of the rows), at most `most`.
 template <typename K>
-int64_t resident(K kernel, int threads, size_t smem, int most) {
-  int dev = 0, sms = 0, per = 0;
-  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
+cudaError_t resident(K kernel, int threads, size_t smem, int most, int dev, int64_t* ctas) {
+  int sms = 0, per = 0;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
   const int fit = (sms < 8 ? 8 : sms) * (per < 1 ? 1 : per);
-  return (fit < most ? fit : most) / 8 * 8;  // a group's rows are a multiple of the vector's elements apart
+  *ctas = (fit < most ? fit : most) / 8 * 8;  // a group's rows are a multiple of the vector's elements apart
+  return e;
 }
 
 template <typename T, int V, int NV, int G, int NT, bool ODD, bool PRE>
-void run_bwd(const NormArgs& a, int64_t blocks, float* dpost, float* dpre, cudaStream_t s) {
+cudaError_t run_bwd(const NormArgs& a, int64_t blocks, float* dpost, float* dpre, cudaStream_t s) {
   auto k = norm_bwd_kernel<T, V, NV, G, NT, ODD, PRE>;
   constexpr size_t rows = Rows<T, V, NV, G, NT, ODD, PRE ? 5 : 3, PRE>::kBytes;
   constexpr size_t sums = NT / G > 1 ? sizeof(float) * NT * NV * V : 0;
   constexpr size_t smem = rows > sums ? rows : sums;
-  static const int64_t fit = resident(k, NT, smem, kMaxCtas);
+  static PerDevice kept;
+  int64_t fit = 0;
+  const cudaError_t e =
+      kept.get(&fit, [&](int dev, int64_t* n) { return resident(k, NT, smem, kMaxCtas, dev, n); });
+  if (e != cudaSuccess) return e;
   const int grid = static_cast<int>(blocks < fit ? blocks : fit);
   k<<<grid, NT, smem, s>>>(a);
   if (a.part)
     norm_weight_kernel<<<dim3((a.width + 31) / 32, 2), dim3(32, 32), 0, s>>>(a.part, grid, a.width, dpost, dpre);
+  return cudaGetLastError();
+}
+
+template <typename T, int V, int NV, int G, int NT, bool ODD>
+cudaError_t run_fwd(const NormArgs& a, int64_t blocks, cudaStream_t s) {
+  auto k = norm_fwd_kernel<T, V, NV, G, NT, ODD>;
+  constexpr size_t smem = Rows<T, V, NV, G, NT, ODD, 3, false>::kBytes;
+  static PerDevice kept;
+  int64_t fit = 0;
+  const cudaError_t e = kept.get(&fit, [&](int dev, int64_t* n) { return resident(k, NT, smem, 1 << 30, dev, n); });
+  if (e != cudaSuccess) return e;
+  k<<<static_cast<int>(blocks < fit ? blocks : fit), NT, smem, s>>>(a);
+  return cudaGetLastError();
 }
 
 template <typename T, int V, int NV, int G, int NT, bool ODD>
 kda_status run(const NormArgs& a, bool bwd, float* dpost, float* dpre, cudaStream_t s) {
   const int64_t blocks = ceil_div(a.rows, NT / G);
-  if (!bwd) {
-    auto k = norm_fwd_kernel<T, V, NV, G, NT, ODD>;
-    constexpr size_t smem = Rows<T, V, NV, G, NT, ODD, 3, false>::kBytes;
-    static const int64_t fit = resident(k, NT, smem, 1 << 30);
-    k<<<static_cast<int>(blocks < fit ? blocks : fit), NT, smem, s>>>(a);
-  } else if (a.dn) {
-    run_bwd<T, V, NV, G, NT, ODD, true>(a, blocks, dpost, dpre, s);
-  } else {
-    run_bwd<T, V, NV, G, NT, ODD, false>(a, blocks, dpost, dpre, s);
-  }
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = !bwd  ? run_fwd<T, V, NV, G, NT, ODD>(a, blocks, s)
+                        : a.dn ? run_bwd<T, V, NV, G, NT, ODD, true>(a, blocks, dpost, dpre, s)
+                               : run_bwd<T, V, NV, G, NT, ODD, false>(a, blocks, dpost, dpre, s);
   return e == cudaSuccess ? KDA_OK : set_error(KDA_ERR_CUDA, "block norm launch failed: %s", cudaGetErrorString(e));
 }
 

@@ -49,6 +49,7 @@
 // which is what the one issuing warp takes.
 #include <math.h>
 
+#include "kda_device.cuh"
 #include "kda_paged.cuh"
 #include "kda_tc_common.cuh"
 
@@ -985,14 +986,18 @@ typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void
                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeFn encode_fn() {
-  static const EncodeFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-                   q == cudaDriverEntryPointSuccess
-               ? reinterpret_cast<EncodeFn>(p)
-               : nullptr;
-  }();
+  static std::atomic<EncodeFn> kept{nullptr};
+  EncodeFn fn = kept.load(std::memory_order_relaxed);
+  if (fn != nullptr) return fn;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  fn = reinterpret_cast<EncodeFn>(p);
+  kept.store(fn, std::memory_order_relaxed);
   return fn;
 }
 
@@ -1013,12 +1018,22 @@ bool page_map(CUtensorMap* m, const void* base, const PagedArgs& a, int box) {
 }
 
 template <int D>
-cudaError_t launch(const PagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, int box, int ctas, cudaStream_t s) {
+cudaError_t launch(const PagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, int box, cudaStream_t s) {
   const size_t smem = kRingBytes + kRows * D * 2 + sizeof(Shared);
   auto* const kernel = kda_paged_attention_kernel<D>;
-  static const cudaError_t set =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (set != cudaSuccess) return set;
+  static PerDevice kept;
+  int64_t sms = 0;
+  cudaError_t e = kept.get(&sms, [&](int dev, int64_t* n) {
+    const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    int count = 0;
+    const cudaError_t got = cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev);
+    *n = count;
+    return set != cudaSuccess ? set : got;
+  });
+  // the status word and the counters that follow it
+  if (e == cudaSuccess) e = cudaMemsetAsync(a.status, 0, kHeaderBytes + kCountBytes, s);
+  if (e != cudaSuccess) return e;
+  const int ctas = static_cast<int>(sms < kMaxCtas ? sms : kMaxCtas);
   // Exponentials are taken in base 2. sc > 0, so that masked scores stay -inf:
   // a negative scale moves to the queries' sign, a scale of 0 to zero queries.
   float sc = fabsf(a.scale) * 1.4426950408889634f;
@@ -1040,16 +1055,7 @@ kda_status launch_paged_attention(const PagedArgs& a, cudaStream_t s) {
   CUtensorMap k, v;
   if (!page_map(&k, a.k, a, box) || !page_map(&v, a.v, a, box))
     return set_error(KDA_ERR_CUDA, "the tensor maps of the cache could not be made");
-  static const int sms = [] {
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n;
-  }();
-  // the status word and the counters that follow it
-  cudaError_t e = cudaMemsetAsync(a.status, 0, kHeaderBytes + kCountBytes, s);
-  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  if (e == cudaSuccess) e = a.D == 128 ? launch<128>(a, k, v, box, ctas, s) : launch<64>(a, k, v, box, ctas, s);
+  const cudaError_t e = a.D == 128 ? launch<128>(a, k, v, box, s) : launch<64>(a, k, v, box, s);
   return e == cudaSuccess ? KDA_OK : set_error(KDA_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
 }
 
