@@ -88,6 +88,11 @@ void* fit(const Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarTy
                   (t.is_cuda() ? "" : " on the CPU") + (t.is_contiguous() ? ")" : ", strided)"));
   return t.data_ptr();
 }
+// A size as the entry points take it: one past 32 bits is refused, not cut.
+int32_t size32(int64_t n, const char* name) {
+  if (n > INT32_MAX) throw Refused(std::string(name) + " " + std::to_string(n) + " is past 32 bits");
+  return static_cast<int32_t>(n);
+}
 void on_cuda(const Tensor& t, const char* name) {
   if (!t.is_cuda()) throw Refused(std::string(name) + " must be a contiguous CUDA tensor");
 }
@@ -138,9 +143,11 @@ PyObject* step(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     const Tensor q = a.at(0, "q"), cu = a.at(8, "cu_seqlens"), states = a.at(9, "states");
     if (q.dim() != 3) throw Refused("q must be [S, H, D] (got " + text(q.sizes()) + ")");
     const int32_t code = activation(q, "q must be [S, H, D]");
-    on_cuda(q, "q");
     if (states.dim() != 4) throw Refused("states must be [slots, H, D, D]");
     const int64_t S = q.size(0), H = q.size(1), D = q.size(2), N = cu.numel() - 1, slots = states.size(0);
+    const int32_t num_seqs = size32(N, "the number of sequences of cu_seqlens,"), heads = size32(H, "the number of heads"),
+                  head_dim = size32(D, "head_dim");
+    on_cuda(q, "q");
     const auto dev = q.get_device();
     const auto dt = q.scalar_type();
     const auto all = q.sizes();
@@ -148,9 +155,9 @@ PyObject* step(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     Tensor out = a.maybe(15, "out");
     kda_problem p{};
     p.total_tokens = S;
-    p.num_seqs = static_cast<int32_t>(N);
-    p.num_heads = static_cast<int32_t>(H);
-    p.head_dim = static_cast<int32_t>(D);
+    p.num_seqs = num_seqs;
+    p.num_heads = heads;
+    p.head_dim = head_dim;
     p.dtype = code;
     p.scale = static_cast<float>(a.number(12));
     p.gate_lower_bound = static_cast<float>(a.number(13));
@@ -185,8 +192,8 @@ kda_norm_problem norm_problem(const Tensor& y, double a, double b, double eps) {
   if (y.dim() < 1) throw Refused("y must be [..., width]");
   kda_norm_problem p{};
   p.dtype = activation(y, "y must be [..., width]");
+  p.width = size32(y.size(-1), "width");
   on_cuda(y, "y");
-  p.width = static_cast<int32_t>(y.size(-1));
   p.rows = p.width ? y.numel() / p.width : 0;
   p.residual_scale = static_cast<float>(a);
   p.block_scale = static_cast<float>(b);
@@ -257,9 +264,10 @@ PyObject* verify(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     const Args a{v};
     const Tensor target = a.at(0, "target");
     if (target.dim() != 3 || target.size(1) < 1) throw Refused("target must be [N, T + 1, V]");
-    on_cuda(target, "target");
     const int64_t N = target.size(0), T = target.size(1) - 1, V = target.size(2);
-    if (N > INT32_MAX || T > INT32_MAX || V > INT32_MAX) throw Refused("target is too large");
+    const int32_t seqs = size32(N, "the number of sequences"), drafts = size32(T, "the number of drafts"),
+                  vocab = size32(V, "the vocabulary");
+    on_cuda(target, "target");
     const auto dev = target.get_device();
     const float* const tp = static_cast<float*>(fit(target, "target", target.sizes(), at::kFloat, dev));
     const float* const dp = static_cast<float*>(fit(a.maybe(1, "draft"), "draft", {N, T, V}, at::kFloat, dev));
@@ -271,8 +279,7 @@ PyObject* verify(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     const c10::cuda::CUDAGuard on(dev);
     const auto ints = target.options().dtype(at::kInt).requires_grad(false);
     const Tensor tokens = at::empty({N, T + 1}, ints), accepted = at::empty({N}, ints);
-    const kda_status r = g_entry.verify(static_cast<int32_t>(N), static_cast<int32_t>(T), static_cast<int32_t>(V), tp, dp, xp,
-                                        np, up, ep, static_cast<int32_t*>(tokens.data_ptr()),
+    const kda_status r = g_entry.verify(seqs, drafts, vocab, tp, dp, xp, np, up, ep, static_cast<int32_t*>(tokens.data_ptr()),
                                         static_cast<int32_t*>(accepted.data_ptr()), status, stream_of(target));
     return r == KDA_OK ? Py_BuildValue("(NN)", wrap(tokens), wrap(accepted)) : PyLong_FromLong(r);
   });
@@ -282,25 +289,28 @@ struct Paged {
   kda_paged_problem p;
   void *k, *v;
 };
-Paged paged(const Args& a, int i, int64_t S, int64_t Hq, int64_t Hkv, int64_t D, double scale, c10::DeviceIndex dev) {
+// `first`: the new tokens' tensor [S, heads, D], argument `name`; a[i]: k_pages.
+Paged paged(const Args& a, int i, const Tensor& first, const char* name, int64_t Hkv, double scale) {
+  const int64_t S = first.size(0), Hq = first.size(1), D = first.size(2);
   const Tensor kp = a.at(i, "k_pages"), vp = a.at(i + 1, "v_pages"), table = a.at(i + 2, "page_table"),
                lens = a.at(i + 3, "kv_lens"), cu = a.at(i + 4, "cu_seqlens");
   if (kp.dim() != 4 || table.dim() != 2)
     throw Refused("k_pages must be [pages, page_size, Hkv, D] and page_table [N, max_pages]");
   const int64_t pages = kp.size(0), size = kp.size(1), N = table.size(0), width = table.size(1);
-  if (size > INT32_MAX || N > INT32_MAX || width > INT32_MAX) throw Refused("page_table is too large");
   Paged r{};
+  r.p.num_seqs = size32(N, "the number of sequences");
+  r.p.num_heads = size32(Hq, "the number of heads");
+  r.p.num_kv_heads = size32(Hkv, "the number of key/value heads");
+  r.p.head_dim = size32(D, "head_dim");
+  r.p.page_size = size32(size, "page_size");
+  r.p.max_pages = size32(width, "the width of page_table,");
+  on_cuda(first, name);
+  const auto dev = first.get_device();
   r.k = fit(kp, "k_pages", {pages, size, Hkv, D}, at::kBFloat16, dev);
   r.v = fit(vp, "v_pages", {pages, size, Hkv, D}, at::kBFloat16, dev);
   r.p.total_tokens = S;
   r.p.num_pages = pages;
-  r.p.num_seqs = static_cast<int32_t>(N);
-  r.p.num_heads = static_cast<int32_t>(Hq);
-  r.p.num_kv_heads = static_cast<int32_t>(Hkv);
-  r.p.head_dim = static_cast<int32_t>(D);
   r.p.dtype = KDA_DTYPE_BF16;
-  r.p.page_size = static_cast<int32_t>(size);
-  r.p.max_pages = static_cast<int32_t>(width);
   r.p.scale = static_cast<float>(scale);
   r.p.cu_seqlens = static_cast<const int32_t*>(fit(cu, "cu_seqlens", {N + 1}, at::kInt, dev));
   r.p.page_table = static_cast<const int32_t*>(fit(table, "page_table", {N, width}, at::kInt, dev));
@@ -314,9 +324,8 @@ PyObject* append(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     const Args a{v};
     const Tensor k = a.at(0, "k");
     if (k.dim() != 3) throw Refused("k must be [S, Hkv, D] (got " + text(k.sizes()) + ")");
-    on_cuda(k, "k");
+    const Paged g = paged(a, 2, k, "k", k.size(1), 1.0);
     const auto dev = k.get_device();
-    const Paged g = paged(a, 2, k.size(0), k.size(1), k.size(1), k.size(2), 1.0, dev);
     void* const kp = fit(k, "k", k.sizes(), at::kBFloat16, dev);
     void* const vp = fit(a.at(1, "v"), "v", k.sizes(), at::kBFloat16, dev);
     int32_t* const status = word(a.maybe(7, "status"), dev);
@@ -334,10 +343,9 @@ PyObject* attention(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     const Tensor q = a.at(0, "q"), pages = a.at(1, "k_pages");
     if (q.dim() != 3 || pages.dim() != 4)
       throw Refused("q must be [S, Hq, D] and k_pages [pages, page_size, Hkv, D]");
-    on_cuda(q, "q");
-    const auto dev = q.get_device();
     const double scale = v[6] == Py_None ? 1.0 / std::sqrt(static_cast<double>(q.size(2))) : a.number(6);
-    const Paged g = paged(a, 1, q.size(0), q.size(1), pages.size(2), q.size(2), scale, dev);
+    const Paged g = paged(a, 1, q, "q", pages.size(2), scale);
+    const auto dev = q.get_device();
     void* const qp = fit(q, "q", q.sizes(), at::kBFloat16, dev);
     const c10::cuda::CUDAGuard on(dev);
     Tensor out = a.maybe(7, "out"), ws = a.maybe(8, "workspace");
