@@ -218,10 +218,8 @@ PyObject* norm_fwd(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     const float* const wn = static_cast<float*>(fit(w_pre, "w_pre", wide, at::kFloat, dev));
     const c10::cuda::CUDAGuard on(dev);
     Tensor ho = a.maybe(8, "h_out"), n = a.maybe(9, "n");
-    if (!ho.defined()) {
-      ho = like(y);
-      if (w_pre.defined()) n = like(y);
-    }
+    if (!ho.defined()) ho = like(y);
+    if (!n.defined() && w_pre.defined()) n = like(y);
     const kda_status r = g_entry.norm_fwd(&p, yp, zp, hp, wp, wn, fit(ho, "h_out", all, dt, dev), fit(n, "n", all, dt, dev),
                                           stream_of(y));
     return r == KDA_OK ? Py_BuildValue("(NN)", wrap(ho), wrap(n)) : PyLong_FromLong(r);

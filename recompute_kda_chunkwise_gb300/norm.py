@@ -19,7 +19,7 @@ def block_norm_fwd(y, *, z=None, h=None, w_post=None, w_pre=None, residual_scale
                    eps: float = 1e-5, out=None):
     """Forward. y, z, h: [..., width] in one dtype; w_post, w_pre: [width]
     fp32. Returns (h_out, n); n is None without w_pre. ``out`` may hold
-    (h_out, n) and h_out may be h."""
+    (h_out, n), either of them None, and h_out may be h."""
     h_out, n = (None, None) if out is None else out
     return done(bind().norm_fwd(y, z, h, w_post, w_pre, residual_scale, block_scale, eps, h_out, n), "kda_block_norm_fwd")
 
