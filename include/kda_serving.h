@@ -101,7 +101,7 @@ kda_status kda_block_norm_fwd(const kda_norm_problem* p,
  * w_post, w_pre are given (NULL otherwise). The weight gradients are summed
  * in a fixed order for given sizes. dh may be dh_out, dy may be y (each only
  * as the whole tensor). workspace: kda_block_norm_workspace_bytes(p) bytes,
- * 16-byte aligned (0 without weights: may be NULL then). */
+ * 16-byte aligned (0 without weights: not used then, and may be NULL). */
 size_t kda_block_norm_workspace_bytes(const kda_norm_problem* p, int32_t has_w_post, int32_t has_w_pre);
 kda_status kda_block_norm_bwd(const kda_norm_problem* p,
                               const void* y, const void* z, const void* h,

@@ -804,10 +804,11 @@ kda_status kda_block_norm_bwd(const kda_norm_problem* p, const void* y, const vo
   NORM_TRY(need("dy", dy, true));
   NORM_TRY(need("dz", dz, z != nullptr));
   NORM_TRY(need("dh", dh, h != nullptr));
-  NORM_TRY(need("workspace", workspace, w_post != nullptr || w_pre != nullptr));
+  const bool weights = w_post != nullptr || w_pre != nullptr;  // without them a workspace is not used
+  if (weights) NORM_TRY(need("workspace", workspace, true));
   NormArgs a{};
   a.y = y; a.z = z; a.h = h; a.wpost = w_post; a.wpre = w_pre; a.dho = dh_out; a.dn = dn;
-  a.dy = dy; a.dz = dz; a.dh = dh; a.part = (float*)workspace;
+  a.dy = dy; a.dz = dz; a.dh = dh; a.part = weights ? (float*)workspace : nullptr;
   a.rows = p->rows; a.width = p->width; a.a = p->residual_scale; a.b = p->block_scale; a.eps = p->eps;
   return launch_norm(p, a, true, dw_post, dw_pre, s);
 }

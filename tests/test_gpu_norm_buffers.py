@@ -1,4 +1,5 @@
-"""The block norm's optional buffers: each output may be given by itself."""
+"""The block norm's optional buffers: each output may be given by itself, and
+a workspace may be given to a call that needs none."""
 import pytest
 import torch
 
@@ -22,3 +23,12 @@ def test_each_output_may_be_given_by_itself():
     assert a is not None and b is None
     with pytest.raises((ValueError, RuntimeError)):
         norm.block_norm_fwd(x["y"], z=x["z"], out=(None, mine))  # n without w_pre
+
+
+def test_a_workspace_where_none_is_needed():
+    x, dho, _ = make(20, 64, torch.bfloat16, "zh", seed=2)
+    kw = dict(z=x["z"], h=x["h"], dh_out=dho)
+    a = norm.block_norm_bwd(x["y"], **kw)
+    ws = torch.full((4096,), 7, dtype=torch.uint8, device="cuda")
+    b = norm.block_norm_bwd(x["y"], **kw, workspace=ws)
+    assert bool((ws == 7).all()) and all(torch.equal(a[k], b[k]) for k in ("dy", "dz", "dh"))
