@@ -96,7 +96,10 @@ class Server:
     Between two calls a sequence has ``committed`` tokens in its states and
     cache, and pending ones, verified but not committed: the last step's accepted drafts and
     the token it drew. A step feeds pending tokens and drafts together and
-    commits the pending ones but the last; refused drafts leave no trace."""
+    commits the pending ones but the last; refused drafts leave no trace.
+
+    ``capacity`` is the number of tokens that a sequence's pages hold: max_len
+    in whole pages (None without attention blocks: states have no length)."""
 
     def __init__(self, model, sequences, max_len, page=16):
         self.m, self.n = model, sequences
@@ -109,11 +112,16 @@ class Server:
                              for _ in range(2)) if b.kind == "attn" else None for b in model.blocks]
         self.table = torch.arange(sequences * width, dtype=torch.int32, device=dev).view(sequences, width)
         self.committed = [0] * sequences
+        self.capacity = width * page if any(b.kind == "attn" for b in model.blocks) else None
 
     @torch.no_grad()
     def run(self, tokens, lengths, commit=None):
         """Probabilities [S, vocab] after each of the packed tokens. commit
-        None: a prefill (chunked delta rule, every token committed)."""
+        None: a prefill (chunked delta rule, every token committed). Raises
+        ValueError, with nothing changed, for a sequence that its pages do not hold."""
+        for i, (c, l) in enumerate(zip(self.committed, lengths)):
+            if self.capacity is not None and c + l > self.capacity:
+                raise ValueError(f"sequence {i} would have {c + l} tokens: its pages hold {self.capacity}")
         m, dev = self.m, self.table.device
         cu = torch.tensor([0] + lengths, dtype=torch.int32).cumsum(0).to(torch.int32).to(dev)
         lens = torch.tensor([c + l for c, l in zip(self.committed, lengths)], dtype=torch.int32, device=dev)
@@ -152,7 +160,14 @@ def lookup_drafts(tokens, most):
 def generate(server, prompts, steps, drafts=3, seed=0, greedy=False):
     """Continues each prompt (lists of tokens) by at least ``steps`` tokens, up
     to ``drafts`` drafted at a time. Returns the sequences and the number of
-    model calls after the prefill."""
+    model calls after the prefill. A sequence that is done goes on as long as
+    others are not and its pages hold more."""
+    # places that are left of each sequence's pages
+    room = [None if server.capacity is None else server.capacity - c for c in server.committed]
+    for i, (p, r) in enumerate(zip(prompts, room)):  # the last token that is drawn is not fed
+        if r is not None and len(p) + steps - 1 > r:
+            raise ValueError(f"prompt {i} has {len(p)} tokens: {steps} more tokens need {len(p) + steps - 1} places and "
+                             f"its pages hold {r}")
     dev, vocab = server.table.device, server.m.embed.shape[0]
     gen = torch.Generator(device=dev)
     gen.manual_seed(seed)
@@ -177,16 +192,23 @@ def generate(server, prompts, steps, drafts=3, seed=0, greedy=False):
         out[i] += pending[i]
     calls = 0
     while min(len(o) - l for o, l in zip(out, lengths)) < steps:
-        drafted = [lookup_drafts(o, drafts) for o in out]
-        feed = [p + d for p, d in zip(pending, drafted)]
+        # len(out) counts the pending tokens: what is left of the pages is for drafts, and a sequence whose pending
+        # tokens do not fit (it has more than it was asked for) rests
+        resting = [r is not None and len(o) > r for o, r in zip(out, room)]
+        drafted = [[] if rests else lookup_drafts(o, drafts if r is None else min(drafts, r - len(o)))
+                   for o, r, rests in zip(out, room, resting)]
+        feed = [[] if r else p + d for p, d, r in zip(pending, drafted, resting)]
         sizes = [len(f) for f in feed]
         # everything before the last pending token was verified in an earlier call
-        probs = server.run(torch.tensor([t for f in feed for t in f], device=dev), sizes, [len(p) - 1 for p in pending])
+        probs = server.run(torch.tensor([t for f in feed for t in f], device=dev), sizes,
+                           [0 if r else len(p) - 1 for p, r in zip(pending, resting)])
         T = max(len(d) for d in drafted)
         target = torch.zeros(N, T + 1, vocab, device=dev)
         drafted_t = torch.zeros(N, T, dtype=torch.int32)
         at = 0
         for i in range(N):
+            if resting[i]:
+                continue
             first_row = at + len(pending[i]) - 1
             target[i, : len(drafted[i]) + 1] = probs[first_row: at + sizes[i]]
             drafted_t[i, : len(drafted[i])] = torch.tensor(drafted[i], dtype=torch.int32)
@@ -194,6 +216,8 @@ def generate(server, prompts, steps, drafts=3, seed=0, greedy=False):
         counts = torch.tensor([len(d) for d in drafted], dtype=torch.int32, device=dev)
         tokens, accepted = draw(target, drafted_t.to(dev), counts)
         for i in range(N):
+            if resting[i]:
+                continue
             fresh = tokens[i][: accepted[i] + 1]
             out[i] += fresh
             pending[i] = pending[i][-1:] + fresh
