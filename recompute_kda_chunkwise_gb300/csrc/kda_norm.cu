@@ -15,7 +15,7 @@
 // Bound: HBM; each tensor is read or written once. A row stays at hand between
 // its reductions. A group of G threads takes a row; a thread holds NV 16-byte
 // vectors of it. Forward and backward together, bf16: head norms of 128 with a
-// gate take 253 us, 94% of the measured copy rate; 8192 rows of 4096 with the
+// gate take 254 us, 93% of the measured copy rate; 8192 rows of 4096 with the
 // next norm 162 us, 79%. There a row is spread over a CTA and its reductions
 // are barriers: between them the SM waits for the slowest warp, and the weight
 // gradients' registers leave room for one CTA.

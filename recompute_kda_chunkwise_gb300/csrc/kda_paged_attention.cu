@@ -9,7 +9,12 @@
 // fills the tensor cores' 128 rows. Keys come in tiles of 128: S = Q K^T and
 // O += P V are 128 x 128 x D and 128 x D x 128 products with fp32 sums in
 // TMEM; P goes back to TMEM as bf16, over those of its own scores that have
-// been read, and is the A operand of the second product from there.
+// been read, and is the A operand of the second product from there. bf16
+// because the product takes both operands in one type and V is held in bf16:
+// against float64 the output's error goes from 0.0017 of its size (bf16
+// outputs of fp32 arithmetic) to 0.0023. P as a sum of two bf16 parts would
+// keep 0.0017 and double the second product. The row's sum adds the
+// probabilities before they are rounded, in fp32.
 //
 // Two streams. Even and odd key tiles of a segment go to two warpgroups, each
 // with its own S, running maximum, sum and O: while one forms its
@@ -42,11 +47,12 @@
 // measured copy rate; about 13 us of it is the start, the cuts and the joins.
 // Chunks by the tensor cores, in principle: a 128 x 128 tile is 1024 cycles of
 // theirs and 512 of exponentials. Chunks of up to 2048 tokens over 8192 keys
-// take 720 us, 57% of the measured bf16 rate, a tile every 1655 cycles: each
-// stream's scores, probabilities (1725 cycles of latency for a thread's 128)
-// and products (1585) wait for one another, and two streams hide half of that.
-// Without the loads that stays as it is; without the exponentials it is 1555,
-// which is what the one issuing warp takes.
+// take 722 us with their append, 57% of the measured bf16 rate, a tile every
+// 1655 cycles: each stream's scores, probabilities (1725 cycles of latency for
+// a thread's 128) and products (1585) wait for one another, and two streams
+// hide half of that. Without the loads that stays as it is; without the
+// exponentials it is 1555. The look at V rows that not every row of a tile
+// sees is 0.5% of it.
 #include <math.h>
 
 #include "kda_device.cuh"

@@ -9,11 +9,11 @@
 // of two, and the state stays in registers from the load to the store.
 //
 // Bound: HBM. One token moves 2 * 4 D^2 bytes of state per sequence and head
-// and needs 7 D^2 flops. 128 x 96 states of 128 with one token each take 247
-// us, 97% of the measured copy rate. Several tokens a state are bound by the
-// latency from barrier to barrier of a token (about 2000 cycles with 16 warps
-// an SM): 48 x 16 states of 128 with up to six tokens take 33 us (GDN-2; KDA
-// 31), 2.3 times what their bytes take.
+// and needs 7 D^2 flops. 128 x 96 states of 128 with one token each take 246
+// us, 97% of the measured copy rate (GDN-2: 262). Several tokens a state are
+// bound by the latency from barrier to barrier of a token (about 2000 cycles
+// with 16 warps an SM): 48 x 16 states of 128 with up to six tokens take 35 us
+// (GDN-2; KDA 32), 2.4 times what their bytes take.
 //
 // Split: a value column of the state depends on no other, so a CTA takes 32
 // columns (128 bytes of each state row: whole lines) of one (sequence, head)

@@ -10,7 +10,7 @@
 // Bound: HBM for a batch (one row of p and e, and of q after a refusal: 8 to
 // 12 bytes per vocabulary entry; the other rows are never read), latency for
 // one sequence. 256 sequences of up to 5 drafts over 131072 entries take 53 us,
-// 89% of the measured copy rate; one sequence takes 6. A cluster of CTAs shares
+// 89% of the measured copy rate; one sequence takes 5. A cluster of CTAs shares
 // a sequence: each finds the accepted count itself (a few gathered
 // probabilities), scans its part of the row, and reads the others' best through
 // distributed shared memory. So one launch does it, without scratch memory or
