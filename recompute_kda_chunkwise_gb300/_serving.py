@@ -1,5 +1,6 @@
-"""What the bindings in ``decode`` and ``norm`` share: the ctypes declarations of
-include/kda_serving.h and the compiled host side. As in ``kda``: argument
+"""What the bindings in ``decode``, ``norm``, ``rotary``, ``attention`` and ``grads``
+share: the ctypes declarations of include/kda_serving.h and include/kda_blocks.h
+and the compiled host side. As in ``kda``: argument
 marshalling only, no CPU path."""
 from __future__ import annotations
 
@@ -26,6 +27,21 @@ class PagedProblem(ctypes.Structure):
                 ("scale", _f32), ("cu_seqlens", _vp), ("page_table", _vp), ("kv_lens", _vp)]
 
 
+class RotaryProblem(ctypes.Structure):
+    """Mirror of ``kda_rotary_problem``."""
+    _fields_ = [("total_tokens", _i64), ("q_stride", _i64), ("k_stride", _i64), ("num_seqs", _i32), ("num_heads", _i32),
+                ("num_kv_heads", _i32), ("head_dim", _i32), ("rotary_dim", _i32), ("dtype", _i32), ("interleaved", _i32),
+                ("inverse", _i32), ("magnitude", _f32), ("reserved", _f32), ("freqs", _vp), ("positions", _vp),
+                ("cu_seqlens", _vp)]
+
+
+class AttentionProblem(ctypes.Structure):
+    """Mirror of ``kda_attention_problem``."""
+    _fields_ = [("total_tokens", _i64), ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64), ("num_seqs", _i32),
+                ("num_heads", _i32), ("num_kv_heads", _i32), ("head_dim", _i32), ("dtype", _i32), ("scale", _f32),
+                ("cu_seqlens", _vp)]
+
+
 _lib = None
 
 
@@ -34,7 +50,7 @@ def library():
     global _lib
     if _lib is None:
         lib = _kda.load_library()
-        P, N, G = (ctypes.POINTER(t) for t in (_kda.KdaProblem, NormProblem, PagedProblem))
+        P, N, G, R, A = (ctypes.POINTER(t) for t in (_kda.KdaProblem, NormProblem, PagedProblem, RotaryProblem, AttentionProblem))
         for name, res, args in (
                 ("kda_step", ctypes.c_int, [P] + [_vp] * 8 + [_i64] + [_vp] * 5),
                 ("kda_gdn2_step", ctypes.c_int, [P] + [_vp] * 9 + [_i64] + [_vp] * 5),
@@ -44,7 +60,16 @@ def library():
                 ("kda_verify_drafts", ctypes.c_int, [_i32] * 3 + [_vp] * 10),
                 ("kda_paged_append", ctypes.c_int, [G] + [_vp] * 6),
                 ("kda_paged_attention_workspace_bytes", ctypes.c_size_t, [G]),
-                ("kda_paged_attention", ctypes.c_int, [G] + [_vp] * 6)):
+                ("kda_paged_attention", ctypes.c_int, [G] + [_vp] * 6),
+                ("kda_rotary", ctypes.c_int, [R] + [_vp] * 6),
+                ("kda_paged_append_rotary", ctypes.c_int, [G, R, _i64] + [_vp] * 8),
+                ("kda_attention_fwd_workspace_bytes", ctypes.c_size_t, [A]),
+                ("kda_attention_fwd", ctypes.c_int, [A] + [_vp] * 7),
+                ("kda_attention_bwd_workspace_bytes", ctypes.c_size_t, [A]),
+                ("kda_attention_bwd", ctypes.c_int, [A] + [_vp] * 11),
+                ("kda_grad_norm_workspace_bytes", ctypes.c_size_t, [_i32]),
+                ("kda_grad_norm", ctypes.c_int, [_i32] + [_vp] * 6),
+                ("kda_clip_grads", ctypes.c_int, [_i32] + [_vp] * 5 + [ctypes.c_double] + [_vp] * 3)):
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = res, args
         _lib = lib
@@ -71,7 +96,10 @@ def bind():
         loader.exec_module(m)
         m.init(*(ctypes.cast(getattr(lib, n), _vp).value for n in (
             "kda_step", "kda_gdn2_step", "kda_block_norm_fwd", "kda_block_norm_workspace_bytes", "kda_block_norm_bwd",
-            "kda_verify_drafts", "kda_paged_append", "kda_paged_attention_workspace_bytes", "kda_paged_attention")))
+            "kda_verify_drafts", "kda_paged_append", "kda_paged_attention_workspace_bytes", "kda_paged_attention",
+            "kda_rotary", "kda_paged_append_rotary", "kda_attention_fwd_workspace_bytes", "kda_attention_fwd",
+            "kda_attention_bwd_workspace_bytes", "kda_attention_bwd", "kda_grad_norm_workspace_bytes", "kda_grad_norm",
+            "kda_clip_grads")))
         _bind = m
     return _bind
 

@@ -1,6 +1,7 @@
-// kda_bind.cpp -- the host side of the serving operators' Python binding
-// (decode.py, norm.py): checks of the tensors, outputs, and the call of the C
-// entry point (kda_serving.h) on the current stream.
+// kda_bind.cpp -- the host side of the Python binding of the operators around
+// the delta rule (decode.py, norm.py, rotary.py, attention.py, grads.py): checks
+// of the tensors, outputs, and the call of the C entry point (kda_serving.h,
+// kda_blocks.h) on the current stream.
 //
 // These calls take a few microseconds on the GPU. Checking a dozen tensors,
 // allocating the outputs and marshalling the arguments in Python took 15 to 27
@@ -18,13 +19,15 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <array>
 #include <cmath>
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
-#include "kda_serving.h"
+#include "kda_blocks.h"
 
 namespace {
 
@@ -40,6 +43,15 @@ struct Entry {
   decltype(&kda_paged_append) append;
   decltype(&kda_paged_attention_workspace_bytes) attention_bytes;
   decltype(&kda_paged_attention) attention;
+  decltype(&kda_rotary) rotary;
+  decltype(&kda_paged_append_rotary) append_rotary;
+  decltype(&kda_attention_fwd_workspace_bytes) packed_fwd_bytes;
+  decltype(&kda_attention_fwd) packed_fwd;
+  decltype(&kda_attention_bwd_workspace_bytes) packed_bwd_bytes;
+  decltype(&kda_attention_bwd) packed_bwd;
+  decltype(&kda_grad_norm_workspace_bytes) norm_of_grads_bytes;
+  decltype(&kda_grad_norm) norm_of_grads;
+  decltype(&kda_clip_grads) clip;
 } g_entry;
 
 struct Refused : std::runtime_error {
@@ -51,6 +63,7 @@ const char* name_of(at::ScalarType t) {
     case at::kBFloat16: return "torch.bfloat16";
     case at::kFloat: return "torch.float32";
     case at::kInt: return "torch.int32";
+    case at::kLong: return "torch.int64";
     case at::kByte: return "torch.uint8";
     default: return "another dtype";
   }
@@ -356,6 +369,272 @@ PyObject* attention(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
   });
 }
 
+// A tensor [S, heads, D] whose tokens lie a stride apart, heads and channels
+// side by side: a slice of a fused projection fits as it is.
+struct Rows {
+  void* p;
+  int64_t stride;
+};
+Rows rows_of(const Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType dtype, c10::DeviceIndex dev) {
+  if (!t.defined()) return {nullptr, 0};
+  const bool shaped = t.dim() == 3 && t.sizes() == shape;
+  if (!shaped || t.scalar_type() != dtype || !t.is_cuda() || t.get_device() != dev ||
+      (t.numel() > 0 && ((t.size(2) > 1 && t.stride(2) != 1) || (t.size(1) > 1 && t.stride(1) != t.size(2)))))
+    throw Refused(std::string(name) + " must be a " + name_of(dtype) + " CUDA tensor of shape " + text(shape) +
+                  ", contiguous within a token, on the first tensor's device (got " + name_of(t.scalar_type()) + " " +
+                  text(t.sizes()) + (t.is_cuda() ? "" : " on the CPU") + (shaped ? ", strided " + text(t.strides()) + ")" : ")"));
+  return {t.data_ptr(), t.size(0) > 1 ? t.stride(0) : t.size(1) * t.size(2)};
+}
+
+// freqs interleaved magnitude
+kda_rotary_problem turn(const Args& a, int i, c10::DeviceIndex dev) {
+  kda_rotary_problem p{};
+  const Tensor freqs = a.at(i, "frequencies");
+  if (freqs.dim() != 1) throw Refused("frequencies must be [rotary_dim / 2]");
+  p.rotary_dim = size32(2 * freqs.size(0), "rotary_dim");
+  p.freqs = static_cast<const int64_t*>(fit(freqs, "frequencies", freqs.sizes(), at::kLong, dev));
+  p.interleaved = a.number(i + 1) != 0;
+  p.magnitude = static_cast<float>(a.number(i + 2));
+  return p;
+}
+
+// freqs interleaved magnitude q k|None inverse positions|None cu_seqlens|None q_out|None k_out|None status|None
+PyObject* rotary(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
+  return guarded(nargs, 11, [&]() -> PyObject* {
+    const Args a{v};
+    const Tensor q = a.at(3, "q"), k = a.maybe(4, "k"), pos = a.maybe(6, "positions"), cu = a.maybe(7, "cu_seqlens");
+    if (q.dim() != 3 || (k.defined() && k.dim() != 3)) throw Refused("q and k must be [S, heads, D] (q: " + text(q.sizes()) + ")");
+    const int32_t code = activation(q, "q must be [S, heads, D]");
+    on_cuda(q, "q");
+    const auto dev = q.get_device();
+    const auto dt = q.scalar_type();
+    if (pos.defined() == cu.defined()) throw Refused("one of positions and cu_seqlens has to be given");
+    kda_rotary_problem p = turn(a, 0, dev);
+    const std::array<int64_t, 3> qs{q.size(0), q.size(1), q.size(2)}, ks{q.size(0), k.defined() ? k.size(1) : 0, q.size(2)};
+    p.total_tokens = qs[0];
+    p.num_heads = size32(qs[1], "the number of heads");
+    p.num_kv_heads = size32(ks[1], "the number of key/value heads");
+    p.head_dim = size32(qs[2], "head_dim");
+    p.dtype = code;
+    p.inverse = a.number(5) != 0;
+    if (k.defined() && ks[1] == 0) throw Refused("k has no heads");
+    const Rows qr = rows_of(q, "q", qs, dt, dev), kr = rows_of(k, "k", ks, dt, dev);
+    p.q_stride = qr.stride;
+    p.k_stride = kr.stride;
+    p.positions = static_cast<const int32_t*>(fit(pos, "positions", {qs[0]}, at::kInt, dev));
+    if (cu.defined()) {
+      p.num_seqs = size32(cu.numel() - 1, "the number of sequences of cu_seqlens,");
+      p.cu_seqlens = static_cast<const int32_t*>(fit(cu, "cu_seqlens", {cu.numel()}, at::kInt, dev));
+    }
+    int32_t* const status = word(a.maybe(10, "status"), dev);
+    const c10::cuda::CUDAGuard on(dev);
+    Tensor qo = a.maybe(8, "q_out"), ko = a.maybe(9, "k_out");
+    if (!k.defined() && ko.defined()) throw Refused("k_out without k");
+    if (!qo.defined()) qo = at::empty(qs, q.options().requires_grad(false));
+    if (k.defined() && !ko.defined()) ko = at::empty(ks, q.options().requires_grad(false));
+    const kda_status r = g_entry.rotary(&p, qr.p, kr.p, fit(qo, "q_out", qs, dt, dev), fit(ko, "k_out", ks, dt, dev), status,
+                                        stream_of(q));
+    return r == KDA_OK ? Py_BuildValue("(NN)", wrap(qo), wrap(ko)) : PyLong_FromLong(r);
+  });
+}
+
+// freqs interleaved magnitude q|None k v k_pages v_pages page_table kv_lens cu_seqlens q_out|None status|None
+PyObject* append_rotary(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
+  return guarded(nargs, 13, [&]() -> PyObject* {
+    const Args a{v};
+    const Tensor q = a.maybe(3, "q"), k = a.at(4, "k");
+    if (k.dim() != 3 || (q.defined() && q.dim() != 3)) throw Refused("q and k must be [S, heads, D] (k: " + text(k.sizes()) + ")");
+    on_cuda(k, "k");
+    const auto dev = k.get_device();
+    kda_rotary_problem p = turn(a, 0, dev);
+    const Paged g = paged(a, 6, q.defined() ? q : k, q.defined() ? "q" : "k", k.size(1), 1.0);
+    const std::array<int64_t, 3> ks{k.size(0), k.size(1), k.size(2)}, qs{ks[0], q.defined() ? q.size(1) : 0, ks[2]};
+    const Rows qr = rows_of(q, "q", qs, at::kBFloat16, dev), kr = rows_of(k, "k", ks, at::kBFloat16, dev),
+               vr = rows_of(a.at(5, "v"), "v", ks, at::kBFloat16, dev);
+    p.q_stride = qr.stride;
+    p.k_stride = kr.stride;
+    int32_t* const status = word(a.maybe(12, "status"), dev);
+    const c10::cuda::CUDAGuard on(dev);
+    Tensor qo = a.maybe(11, "q_out");
+    if (!q.defined() && qo.defined()) throw Refused("q_out without q");
+    if (q.defined() && !qo.defined()) qo = at::empty(qs, q.options().requires_grad(false));
+    const kda_status r = g_entry.append_rotary(&g.p, &p, vr.stride, qr.p, kr.p, vr.p, fit(qo, "q_out", qs, at::kBFloat16, dev),
+                                               g.k, g.v, status, stream_of(k));
+    return r == KDA_OK ? wrap(qo) : PyLong_FromLong(r);
+  });
+}
+
+struct Packed {
+  kda_attention_problem p;
+  void *q, *k, *v;
+  std::array<int64_t, 3> qs, ks;
+};
+Packed packed(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& cu, PyObject* scale, double given) {
+  if (q.dim() != 3 || k.dim() != 3)
+    throw Refused("q must be [S, Hq, D] and k, v [S, Hkv, D] (got " + text(q.sizes()) + ", " + text(k.sizes()) + ")");
+  on_cuda(q, "q");
+  const auto dev = q.get_device();
+  Packed r{};
+  r.qs = {q.size(0), q.size(1), q.size(2)};
+  r.ks = {q.size(0), k.size(1), q.size(2)};
+  r.p.total_tokens = r.qs[0];
+  r.p.num_seqs = size32(cu.numel() - 1, "the number of sequences of cu_seqlens,");
+  r.p.num_heads = size32(r.qs[1], "the number of heads");
+  r.p.num_kv_heads = size32(r.ks[1], "the number of key/value heads");
+  r.p.head_dim = size32(r.qs[2], "head_dim");
+  r.p.dtype = KDA_DTYPE_BF16;
+  r.p.scale = static_cast<float>(scale == Py_None ? 1.0 / std::sqrt(static_cast<double>(r.qs[2])) : given);
+  const Rows qr = rows_of(q, "q", r.qs, at::kBFloat16, dev), kr = rows_of(k, "k", r.ks, at::kBFloat16, dev),
+             vr = rows_of(v, "v", r.ks, at::kBFloat16, dev);
+  r.q = qr.p;
+  r.k = kr.p;
+  r.v = vr.p;
+  r.p.q_stride = qr.stride;
+  r.p.k_stride = kr.stride;
+  r.p.v_stride = vr.stride;
+  r.p.cu_seqlens = static_cast<const int32_t*>(fit(cu, "cu_seqlens", {cu.numel()}, at::kInt, dev));
+  return r;
+}
+
+// q k v cu_seqlens scale|None out|None workspace|None
+PyObject* packed_fwd(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
+  return guarded(nargs, 7, [&]() -> PyObject* {
+    const Args a{v};
+    const Tensor q = a.at(0, "q");
+    const Packed g = packed(q, a.at(1, "k"), a.at(2, "v"), a.at(3, "cu_seqlens"), v[4], v[4] == Py_None ? 0 : a.number(4));
+    const auto dev = q.get_device();
+    const c10::cuda::CUDAGuard on(dev);
+    Tensor out = a.maybe(5, "out"), ws = a.maybe(6, "workspace");
+    if (!out.defined()) out = at::empty(g.qs, q.options().requires_grad(false));
+    void* const op = fit(out, "out", g.qs, at::kBFloat16, dev);
+    const Tensor lse = at::empty({g.qs[1], g.qs[0]}, q.options().dtype(at::kFloat).requires_grad(false));
+    void* const wsp = buffer(ws, g_entry.packed_fwd_bytes(&g.p), q);
+    const kda_status r = g_entry.packed_fwd(&g.p, g.q, g.k, g.v, op, static_cast<float*>(lse.data_ptr()), wsp, stream_of(q));
+    return r == KDA_OK ? Py_BuildValue("(NN)", wrap(out), wrap(lse)) : PyLong_FromLong(r);
+  });
+}
+
+// q k v o lse d_o cu_seqlens scale|None workspace|None
+PyObject* packed_bwd(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
+  return guarded(nargs, 9, [&]() -> PyObject* {
+    const Args a{v};
+    const Tensor q = a.at(0, "q");
+    const Packed g = packed(q, a.at(1, "k"), a.at(2, "v"), a.at(6, "cu_seqlens"), v[7], v[7] == Py_None ? 0 : a.number(7));
+    const auto dev = q.get_device();
+    void* const op = fit(a.at(3, "o"), "o", g.qs, at::kBFloat16, dev);
+    const float* const lp = static_cast<float*>(fit(a.at(4, "lse"), "lse", {g.qs[1], g.qs[0]}, at::kFloat, dev));
+    void* const gp = fit(a.at(5, "d_o"), "d_o", g.qs, at::kBFloat16, dev);
+    const c10::cuda::CUDAGuard on(dev);
+    Tensor ws = a.maybe(8, "workspace");
+    void* const wsp = buffer(ws, g_entry.packed_bwd_bytes(&g.p), q);
+    const auto opts = q.options().requires_grad(false);
+    const Tensor dq = at::empty(g.qs, opts), dk = at::empty(g.ks, opts), dv = at::empty(g.ks, opts);
+    const kda_status r = g_entry.packed_bwd(&g.p, g.q, g.k, g.v, op, lp, gp, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), wsp,
+                                            stream_of(q));
+    return r == KDA_OK ? Py_BuildValue("(NNN)", wrap(dq), wrap(dk), wrap(dv)) : PyLong_FromLong(r);
+  });
+}
+
+// Tensors of a list or tuple as the gradient operators take them.
+struct Grads {
+  std::vector<Tensor> t;
+  std::vector<const void*> p;
+  std::vector<int64_t> n;
+  std::vector<int32_t> dtype;
+};
+Grads grads_of(PyObject* list, const char* name) {
+  if (!PyList_Check(list) && !PyTuple_Check(list)) throw Refused(std::string(name) + " must be a list or tuple of tensors");
+  const Py_ssize_t num = PySequence_Fast_GET_SIZE(list);
+  PyObject* const* const items = PySequence_Fast_ITEMS(list);
+  Grads g;
+  g.n.reserve(num);
+  g.t.reserve(num);
+  g.p.reserve(num);
+  g.dtype.reserve(num);
+  for (Py_ssize_t i = 0; i < num; ++i) {
+    const std::string which = std::string(name) + "[" + std::to_string(i) + "]";
+    if (!THPVariable_Check(items[i])) throw Refused(which + " must be a tensor");
+    const Tensor& t = THPVariable_Unpack(items[i]);
+    if (!t.is_cuda() || (i > 0 && t.get_device() != g.t[0].get_device()) || t.layout() != at::kStrided ||
+        !t.is_non_overlapping_and_dense())
+      throw Refused(which + " must be a dense CUDA tensor on the first one's device (got " + text(t.sizes()) +
+                    (t.is_cuda() ? ")" : " on the CPU)"));
+    g.dtype.push_back(activation(t, (which + " must be").c_str()));
+    g.p.push_back(t.numel() ? t.data_ptr() : nullptr);
+    g.n.push_back(t.numel());
+    g.t.push_back(t);
+  }
+  return g;
+}
+
+// An output may be its own gradient's memory and nothing else of the call's.
+void no_overlap(const Grads& g, const Grads& o) {
+  struct Range {
+    uintptr_t at, end;
+    bool out;
+    size_t i;
+  };
+  std::vector<Range> r;
+  for (size_t i = 0; i < g.t.size(); ++i) {
+    if (g.n[i] == 0) continue;
+    const auto add = [&](const Grads& x, bool out) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(x.p[i]);
+      r.push_back({at, at + x.t[i].nbytes(), out, i});
+    };
+    add(o, true);
+    if (g.p[i] != o.p[i]) add(g, false);
+  }
+  std::sort(r.begin(), r.end(), [](const Range& x, const Range& y) { return x.at < y.at; });
+  uintptr_t end = 0, out_end = 0;  // of what came before
+  for (const Range& x : r) {
+    if (x.at < (x.out ? end : out_end))
+      throw Refused((x.out ? "out[" : "grads[") + std::to_string(x.i) + "] overlaps another tensor of the call");
+    end = std::max(end, x.end);
+    if (x.out) out_end = std::max(out_end, x.end);
+  }
+}
+
+// grads workspace|None
+PyObject* norm_of_grads(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
+  return guarded(nargs, 2, [&]() -> PyObject* {
+    const Args a{v};
+    const Grads g = grads_of(v[0], "grads");
+    const auto dev = g.t.empty() ? c10::cuda::current_device() : g.t[0].get_device();
+    const c10::cuda::CUDAGuard on(dev);
+    const Tensor norm = at::empty({}, at::TensorOptions().dtype(at::kFloat).device(c10::Device(at::kCUDA, dev)));
+    const int32_t num = size32(static_cast<int64_t>(g.t.size()), "the number of tensors");
+    Tensor ws = a.maybe(1, "workspace");
+    void* const wsp = buffer(ws, g_entry.norm_of_grads_bytes(num), norm);
+    const kda_status r = g_entry.norm_of_grads(num, g.p.data(), g.n.data(), g.dtype.data(), static_cast<float*>(norm.data_ptr()),
+                                               wsp, stream_of(norm));
+    return r == KDA_OK ? wrap(norm) : PyLong_FromLong(r);
+  });
+}
+
+// grads max_norm out|None workspace|None
+PyObject* clip(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
+  return guarded(nargs, 4, [&]() -> PyObject* {
+    const Args a{v};
+    const Grads g = grads_of(v[0], "grads");
+    const Grads o = grads_of(v[2] == Py_None ? v[0] : v[2], v[2] == Py_None ? "grads" : "out");
+    if (o.t.size() != g.t.size()) throw Refused("out must have as many tensors as grads");
+    for (size_t i = 0; i < g.t.size(); ++i)
+      if (o.t[i].sizes() != g.t[i].sizes() || o.t[i].strides() != g.t[i].strides() ||
+          o.t[i].get_device() != g.t[i].get_device() || (g.n[i] > 0 && o.p[i] == g.p[i] && o.dtype[i] != g.dtype[i]))
+        throw Refused("out[" + std::to_string(i) + "] must have the shape, strides and device of grads[" + std::to_string(i) + "]");
+    no_overlap(g, o);
+    const auto dev = g.t.empty() ? c10::cuda::current_device() : g.t[0].get_device();
+    const c10::cuda::CUDAGuard on(dev);
+    const Tensor norm = at::empty({}, at::TensorOptions().dtype(at::kFloat).device(c10::Device(at::kCUDA, dev)));
+    const int32_t num = size32(static_cast<int64_t>(g.t.size()), "the number of tensors");
+    Tensor ws = a.maybe(3, "workspace");
+    void* const wsp = buffer(ws, g_entry.norm_of_grads_bytes(num), norm);
+    const kda_status r = g_entry.clip(num, g.p.data(), g.n.data(), g.dtype.data(), const_cast<void* const*>(o.p.data()),
+                                      o.dtype.data(), a.number(1), static_cast<float*>(norm.data_ptr()), wsp, stream_of(norm));
+    return r == KDA_OK ? wrap(norm) : PyLong_FromLong(r);
+  });
+}
+
 // addresses of the entry points, in the order of Entry
 PyObject* init(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
   constexpr Py_ssize_t n = sizeof(Entry) / sizeof(void*);
@@ -370,8 +649,10 @@ PyObject* init(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
 }
 
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {METHOD(init),   METHOD(step),   METHOD(norm_fwd),  METHOD(norm_bwd),
-                         METHOD(verify), METHOD(append), METHOD(attention), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {METHOD(init),          METHOD(step),       METHOD(norm_fwd),   METHOD(norm_bwd),
+                         METHOD(verify),        METHOD(append),     METHOD(attention),  METHOD(rotary),
+                         METHOD(append_rotary), METHOD(packed_fwd), METHOD(packed_bwd), METHOD(norm_of_grads),
+                         METHOD(clip),          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,158 @@
+// kda_packed.cuh -- what the kernels of causal attention over packed sequences
+// share: their arguments, the list of row tiles, waits, and tensor maps.
+#pragma once
+
+#include "kda_attention.cuh"
+#include "kda_blocks.h"
+#include "kda_device.cuh"
+
+namespace kda {
+
+constexpr int kPackedMaxSeqs = 65536;
+constexpr int kPackedMaxCtas = 152;  // one per SM
+
+struct PackedArgs {
+  const int32_t* cu;
+  int* status;
+  const int* list;     // count, then from list + 4 on {first token, length, weight, 0} of each tile; null: one sequence
+  int64_t S;
+  int N, Hq, Hkv, D;
+  float scale;
+  __nv_bfloat16 *o, *dq, *dk, *dv;   // contiguous
+  const __nv_bfloat16 *o_in, *d_o;
+  float* lse;          // [Hq][S]
+  float* delta;        // [Hq][S]
+  float* part;         // gradients of k and v by parts of the head group: [2][split][S][Hkv][D]
+  int split;
+};
+
+// A tile of `rows` rows of a sequence. Weight w counts the tiles up to it: it
+// is tile w - 1 from the sequence's start (or, for work that goes to the
+// sequence's end, w tiles from there).
+struct Tile {
+  int lo, L, w;
+};
+
+// Tiles of the call, heaviest first, so that the last ones to be handed out are
+// short. 0: lengths that do not fit (recorded).
+__device__ __forceinline__ int tiles_of(const PackedArgs& a, int rows) {
+  if (a.list) return a.list[0];
+  if (a.cu[0] != 0 || a.cu[1] != a.S) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) set_status(a.status, KDA_ERR_DEVICE_CHECK);
+    return 0;
+  }
+  return static_cast<int>((a.S + rows - 1) / rows);
+}
+__device__ __forceinline__ Tile tile_of(const PackedArgs& a, int tiles, int e) {
+  if (!a.list) return {0, static_cast<int>(a.S), tiles - e};
+  const int4 t = reinterpret_cast<const int4*>(a.list + 4)[e];
+  return {t.x, t.y, t.z};
+}
+// Item i of this CTA (there and back over the CTAs, so that none gets the
+// heavier of every round), or past the end.
+__device__ __forceinline__ int64_t item_of(int64_t i) {
+  const int64_t g = gridDim.x;
+  return i * g + (i & 1 ? g - 1 - blockIdx.x : blockIdx.x);
+}
+
+namespace tc {
+
+// Bounded wait for a phase; false when it ran out (the CTA's abort flag is then
+// set) or another role gave up.
+__device__ __forceinline__ bool wait_or(int* abort_, uint64_t* bar, uint32_t parity, int* status) {
+  const uint32_t at = smem_addr(bar);
+  for (int it = 0; it < (1 << 22); ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((it & 15) == 15 && *const_cast<volatile int*>(abort_)) return false;
+  }
+  *const_cast<volatile int*>(abort_) = 1;
+  set_status(status, KDA_ERR_TIMEOUT);
+  return false;
+}
+// The same by a whole warp, with one answer; lanes may wait for barriers of their own.
+__device__ __forceinline__ bool wait_all(int* abort_, uint64_t* bar, uint32_t parity, int* status) {
+  return __all_sync(~0u, wait_or(abort_, bar, parity, status));
+}
+// Waits, at most so long, without giving up.
+__device__ __forceinline__ void settle_for(uint64_t* bar, uint32_t parity) {
+  const uint32_t at = smem_addr(bar);
+  for (int it = 0; it < (1 << 20); ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (ok) return;
+  }
+}
+
+// A ring's position: slot, and the parity of its turn.
+struct Ring {
+  int slot = 0;
+  uint32_t turn = 0;
+  __device__ __forceinline__ void next(int slots) {
+    if (++slot == slots) {
+      slot = 0;
+      ++turn;
+    }
+  }
+};
+
+// 128 rows of one head, from token `tok` on (rows past the tensor are zeros):
+// a block of 128 x 128 swizzled bytes for each 64 channels.
+template <int D>
+__device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* map, int head, int tok, uint64_t* bar) {
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * 16384, map, c * 64, head, tok, bar);
+}
+
+// Zeros in the rows of such a tile from `from` on, by threads 0 .. 127 of `row`.
+template <int D>
+__device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(tile + sw128_chunk(row, c, 128)) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+}  // namespace tc
+
+// [S][heads][D] bf16 as (channel, head, token), boxes of 64 channels of 128 tokens of one head.
+inline bool rows_map(CUtensorMap* m, const void* base, int64_t S, int heads, int D, int64_t stride) {
+  const EncodeFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)S};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t boxes[3] = {64, 1, 128}, ones[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, boxes, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// SMs of the current device for a kernel's grid, with its shared memory allowed.
+template <typename K>
+cudaError_t packed_sms(PerDevice& kept, K kernel, size_t smem, int64_t* sms) {
+  return kept.get(sms, [&](int dev, int64_t* n) {
+    const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    int count = 0;
+    const cudaError_t got = cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev);
+    *n = count;
+    return set != cudaSuccess ? set : got;
+  });
+}
+
+struct PackedInputs {
+  const void *q, *k, *v;
+  int64_t qs, ks, vs;
+};
+cudaError_t launch_packed_fwd(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                              cudaStream_t s);
+cudaError_t launch_packed_bwd(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                              const CUtensorMap& d_o, cudaStream_t s);
+
+}  // namespace kda

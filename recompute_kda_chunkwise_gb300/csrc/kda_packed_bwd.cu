@@ -1,0 +1,751 @@
+// kda_packed_bwd.cu -- backward of causal attention over packed sequences
+// (kda_attention_bwd of kda_blocks.h) on the tcgen05 tensor cores.
+//
+//   P = exp(scale q k - lse)      delta = sum(d_o o)
+//   dv = P^T d_o      dS = P (d_o v^T - delta)      dk = scale dS^T q      dq = scale dS k
+//
+// Two passes, one over queries for each tile of keys (dk, dv: 4 products) and
+// one over keys for each tile of queries (dq: 3 products), 7 products where 5
+// would do. A single pass would add every tile's part of dq to memory in fp32:
+// in the order in which CTAs come (other bits every time), or in turns, with
+// CTAs waiting for one another. Here each sum is one CTA's, in TMEM.
+//
+// dk, dv. Keys are the rows (TMEM lanes) of S^T = K Q^T and dP^T = V d_o^T, so
+// that P^T and dS^T, written back over the scores as bf16, are A operands of
+// dv += P^T d_o and dk += dS^T Q straight from TMEM: neither goes through
+// shared memory, whose bandwidth bounds products of two operands there. While
+// the warps form P^T the tensor cores run dS^T's product and the next dP^T, and
+// the other way round: the order is dv(t), S(t+1), dk(t), dP(t+1).
+// A key/value head's keys go over all query heads of its group in one item, or
+// over a part of them where there are few items: the parts are then added up,
+// in order, by another kernel.
+//
+// dq. Queries are the rows; dS is dq's A operand in TMEM. dP has two buffers,
+// so that the next tile's scores and dP are formed while dS is.
+#include <math.h>
+
+#include "kda_packed.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 128;
+constexpr int kMathWarps = 8;               // two warpgroups, each half of a tile's columns
+constexpr int kMmaWarp = 0, kLoadWarp = 1, kMathWarp = 4;
+constexpr int kThreads = 32 * (kMathWarp + kMathWarps);
+constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);
+
+// D (+)= A B, A: bf16 in TMEM at `a`, its columns 0 .. 63 there and 64 .. 127
+// at a + 64 (each warpgroup's half over its own scores), B: 128 rows of D in shared memory.
+template <int D>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t tile, uint32_t acc) {
+  constexpr uint32_t id = idesc(kRows, D, false, true) | kBf16;
+#pragma unroll
+  for (int k = 0; k < kRows / 16; ++k)
+    mma_ta(d, a + 64 * (k >> 2) + 8 * (k & 3), desc_mnmajor(tile, kRows * 128, k), id, k > 0 ? 1u : acc);
+}
+// D = A B^T, both 128 rows of D in shared memory.
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t id = idesc(kRows, kRows) | kBf16;
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) mma(d, desc_kmajor(a, kRows, 0, k), desc_kmajor(b, kRows, 0, k), id, k > 0);
+}
+
+// ---- delta[h][s] = sum over channels of d_o o: eight lanes a row ----
+template <int D>
+__global__ void __launch_bounds__(256) kda_packed_delta_kernel(const __grid_constant__ PackedArgs a) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 3;
+  const int sub = threadIdx.x & 7;
+  float sum = 0.f;
+  if (i < a.S * a.Hq) {
+    const uint4* const x = reinterpret_cast<const uint4*>(a.o_in + i * D);
+    const uint4* const y = reinterpret_cast<const uint4*>(a.d_o + i * D);
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      const uint4 u = x[sub + 8 * c], v = y[sub + 8 * c];
+      const uint32_t us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 p = unpack_bf16(us[e]), q = unpack_bf16(vs[e]);
+        sum = fmaf(p.x, q.x, sum);
+        sum = fmaf(p.y, q.y, sum);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  if (sub == 0 && i < a.S * a.Hq) a.delta[(i % a.Hq) * a.S + i / a.Hq] = sum;
+}
+
+// ---- dk and dv ----
+template <int D>
+struct KvCfg {
+  static constexpr int kTile = kRows * D * 2;
+  static constexpr int kQ = 3, kDo = 2;  // slots of queries, of d_o
+  static constexpr int kBytes = (2 + kQ + kDo) * kTile;
+};
+struct KvShared {
+  float row[2][2][kRows];  // lse (base 2) and delta of a step's queries
+  uint64_t kv_full, kv_empty;
+  uint64_t q_full[3], q_empty[3], do_full[2], do_empty[2];
+  uint64_t s_full, dp_full, p_ready, ds_ready, done, acc_free, drain;
+  uint32_t tmem;
+  int abort_;
+};
+struct KvItem {
+  int lo, L, j, nt, hk, head0, heads, part;  // key tile j of nt; query heads head0 .. + heads
+  __device__ __forceinline__ int steps() const { return heads * (nt - j); }
+};
+__device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t i, KvItem& it) {
+  const int64_t x = item_of(i);
+  const int per = a.Hkv * a.split;
+  if (x >= static_cast<int64_t>(tiles) * per) return false;
+  const Tile t = tile_of(a, tiles, static_cast<int>(x / per));
+  const int r = static_cast<int>(x % per);
+  it.lo = t.lo;
+  it.L = t.L;
+  it.nt = (t.L + kRows - 1) / kRows;
+  it.j = it.nt - t.w;
+  it.hk = r / a.split;
+  it.part = r % a.split;
+  it.heads = a.Hq / a.Hkv / a.split;
+  it.head0 = it.hk * (a.Hq / a.Hkv) + it.part * it.heads;
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    kda_packed_dkv_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ CUtensorMap qmap,
+                          const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                          const __grid_constant__ CUtensorMap domap, const float sc) {
+  using C = KvCfg<D>;
+  constexpr int kTile = C::kTile;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* const kt = smem;
+  uint8_t* const vt = smem + kTile;
+  uint8_t* const qt = smem + 2 * kTile;
+  uint8_t* const dot = qt + C::kQ * kTile;
+  KvShared* const sh = reinterpret_cast<KvShared*>(smem + C::kBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int* const ab = &sh->abort_;
+
+  const int tiles = tiles_of(a, kRows);
+  if (tiles == 0) return;
+  if (smem_addr(smem) & 1023) {
+    if (tid == 0) set_status(a.status, KDA_ERR_DEVICE_CHECK);
+    return;
+  }
+  if (tid == 0) {
+    mbar_init(&sh->kv_full, 1);
+    mbar_init(&sh->kv_empty, 1);
+    for (int i = 0; i < C::kQ; ++i) {
+      mbar_init(&sh->q_full[i], 1);
+      mbar_init(&sh->q_empty[i], 1);
+    }
+    for (int i = 0; i < C::kDo; ++i) {
+      mbar_init(&sh->do_full[i], 1);
+      mbar_init(&sh->do_empty[i], 1);
+    }
+    mbar_init(&sh->s_full, 1);
+    mbar_init(&sh->dp_full, 1);
+    mbar_init(&sh->p_ready, kMathWarps);
+    mbar_init(&sh->ds_ready, kMathWarps);
+    mbar_init(&sh->done, 1);
+    mbar_init(&sh->acc_free, kMathWarps);
+    mbar_init(&sh->drain, 1);
+    sh->abort_ = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) tmem_alloc(&sh->tmem, 512);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = sh->tmem;
+  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
+  KvItem it;
+
+  if (warp == kLoadWarp) {
+    Ring rq, rd;
+    bool ok = true;
+    uint32_t items = 0;
+    int64_t steps = 0;
+    for (int64_t i = 0; ok && item_at(a, tiles, i, it); ++i) {
+      if (items > 0) ok = wait_all(ab, &sh->kv_empty, (items - 1) & 1, a.status);
+      if (!ok) break;
+      if (elect()) {
+        mbar_expect_tx(&sh->kv_full, 2 * kTile);
+        load_rows<D>(kt, &kmap, it.hk, it.lo + it.j * kRows, &sh->kv_full);
+        load_rows<D>(vt, &vmap, it.hk, it.lo + it.j * kRows, &sh->kv_full);
+      }
+      ++items;
+      for (int h = 0; ok && h < it.heads; ++h) {
+        for (int m = it.j; m < it.nt; ++m) {
+          if (rq.turn > 0) ok = wait_all(ab, &sh->q_empty[rq.slot], (rq.turn - 1) & 1, a.status);
+          if (!ok) break;
+          if (elect()) {
+            mbar_expect_tx(&sh->q_full[rq.slot], kTile);
+            load_rows<D>(qt + rq.slot * kTile, &qmap, it.head0 + h, it.lo + m * kRows, &sh->q_full[rq.slot]);
+          }
+          __syncwarp();
+          // counted below from here on: this step's query copy is in flight
+          ++steps;
+          if (rd.turn > 0) ok = wait_all(ab, &sh->do_empty[rd.slot], (rd.turn - 1) & 1, a.status);
+          if (!ok) break;
+          if (elect()) {
+            mbar_expect_tx(&sh->do_full[rd.slot], kTile);
+            load_rows<D>(dot + rd.slot * kTile, &domap, it.head0 + h, it.lo + m * kRows, &sh->do_full[rd.slot]);
+          }
+          rq.next(C::kQ);
+          rd.next(C::kDo);
+        }
+      }
+    }
+    // after an abort: the copies in flight land before the CTA ends (a copy that
+    // was not issued only costs its wait)
+    if (!ok) {
+      for (int64_t p = steps > C::kQ ? steps - C::kQ : 0; p < steps; ++p)
+        settle_for(&sh->q_full[p % C::kQ], static_cast<uint32_t>((p / C::kQ) & 1));
+      for (int64_t p = steps > C::kDo ? steps - C::kDo : 0; p < steps; ++p)
+        settle_for(&sh->do_full[p % C::kDo], static_cast<uint32_t>((p / C::kDo) & 1));
+      if (items > 0) settle_for(&sh->kv_full, (items - 1) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    const uint32_t k_at = smem_addr(kt), v_at = smem_addr(vt), q_at = smem_addr(qt), do_at = smem_addr(dot);
+    Ring rq, rd;  // of step t
+    uint32_t items = 0, turn = 0;
+    bool ok = true;
+    for (int64_t i = 0; ok && item_at(a, tiles, i, it); ++i) {
+      const int steps = it.steps();
+      // K and V, the first Q and d_o
+      {
+        uint64_t* bar = &sh->kv_full;
+        uint32_t par = items;
+        if (lane == 1) bar = &sh->q_full[rq.slot], par = rq.turn;
+        if (lane == 2) bar = &sh->do_full[rd.slot], par = rd.turn;
+        ok = wait_all(ab, bar, par & 1, a.status);
+      }
+      if (!ok) break;
+      fence_after_sync();
+      if (elect()) {
+        mma_scores<D>(t_s, k_at, q_at + rq.slot * kTile);
+        mma_commit(&sh->s_full);
+        mma_scores<D>(t_dp, v_at, do_at + rd.slot * kTile);
+        mma_commit(&sh->dp_full);
+        if (steps == 1) mma_commit(&sh->kv_empty);
+      }
+      for (int t = 0; t < steps; ++t) {
+        const bool more = t + 1 < steps;
+        Ring nq = rq, nd = rd;
+        nq.next(C::kQ);
+        nd.next(C::kDo);
+        {  // P(t), the next Q, and at an item's start the accumulators
+          uint64_t* bar = &sh->p_ready;
+          uint32_t par = turn;
+          if (lane == 1 && more) bar = &sh->q_full[nq.slot], par = nq.turn;
+          if (lane == 2 && t == 0 && items > 0) bar = &sh->acc_free, par = items - 1;
+          ok = wait_all(ab, bar, par & 1, a.status);
+        }
+        if (!ok) break;
+        fence_after_sync();
+        if (elect()) {
+          mma_rows<D>(t_dv, t_s, do_at + rd.slot * kTile, t > 0);
+          mma_commit(&sh->do_empty[rd.slot]);
+          if (more) {
+            mma_scores<D>(t_s, k_at, q_at + nq.slot * kTile);
+            mma_commit(&sh->s_full);
+          }
+        }
+        {  // dS(t), the next d_o
+          uint64_t* bar = &sh->ds_ready;
+          uint32_t par = turn;
+          if (lane == 1 && more) bar = &sh->do_full[nd.slot], par = nd.turn;
+          ok = wait_all(ab, bar, par & 1, a.status);
+        }
+        ++turn;
+        if (!ok) break;
+        fence_after_sync();
+        if (elect()) {
+          mma_rows<D>(t_dk, t_dp, q_at + rq.slot * kTile, t > 0);
+          mma_commit(&sh->q_empty[rq.slot]);
+          if (more) {
+            mma_scores<D>(t_dp, v_at, do_at + nd.slot * kTile);
+            mma_commit(&sh->dp_full);
+            if (t + 2 == steps) mma_commit(&sh->kv_empty);
+          } else {
+            mma_commit(&sh->done);
+          }
+        }
+        rq = nq;
+        rd = nd;
+      }
+      ++items;
+    }
+    if (elect()) mma_commit(&sh->drain);
+    settle_for(&sh->drain, 0);
+    __syncwarp();
+  } else if (warp >= kMathWarp) {
+    const int wg = (warp - kMathWarp) >> 2, row = tid & 127, mt = tid - 32 * kMathWarp;
+    const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;
+    const uint32_t my_s = t_s + lane_base + 64 * wg, my_dp = t_dp + lane_base + 64 * wg;
+    uint32_t turn = 0, items = 0;
+    Ring rq, rd;
+    for (int64_t i = 0; item_at(a, tiles, i, it); ++i, ++items) {
+      const int steps = it.steps();
+      const float* const src = mt < kRows ? a.lse : a.delta;
+      // lse or delta of query row mt % 128 of a step; 0 past the sequence
+      auto fetch = [&](int h, int m) {
+        const int at = m * kRows + row;
+        return at < it.L ? src[static_cast<int64_t>(it.head0 + h) * a.S + it.lo + at] : 0.f;
+      };
+      float ahead = fetch(0, it.j);
+      int h = 0, m = it.j;
+      for (int t = 0; t < steps; ++t, ++turn) {
+        float* const mine = sh->row[turn & 1][mt < kRows ? 0 : 1];
+        mine[row] = mt < kRows ? ahead * 1.4426950408889634f : ahead;
+        named_bar_sync(1, 32 * kMathWarps);
+        const int past = it.L - m * kRows;       // query rows of the tile from here on are another sequence's
+        const bool diagonal = m == it.j, tail = past < kRows;
+        if (++m == it.nt) {
+          m = it.j;
+          ++h;
+        }
+        if (t + 1 < steps) ahead = fetch(h, m);
+        const float4* const lse4 = reinterpret_cast<const float4*>(sh->row[turn & 1][0] + 64 * wg);
+        const float4* const del4 = reinterpret_cast<const float4*>(sh->row[turn & 1][1] + 64 * wg);
+        // columns (queries) that see this thread's key
+        uint32_t see[2] = {~0u, ~0u};
+        if (diagonal || tail) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int c0 = 64 * wg + 32 * c, lo = diagonal ? row - c0 : 0, hi = past - c0;
+            see[c] = lo >= 32 ? 0u : lo > 0 ? ~0u << lo : ~0u;
+            see[c] &= hi >= 32 ? ~0u : hi > 0 ? ~(~0u << hi) : 0u;
+          }
+        }
+        const bool all = !(diagonal || tail);
+        wait_all(ab, &sh->s_full, turn & 1, a.status);
+        if (tail) {  // those rows' Q and d_o to zero, once the scores' products have read them
+          wait_all(ab, &sh->dp_full, turn & 1, a.status);
+          if (row >= past) zero_row<D>(mt < kRows ? qt + rq.slot * kTile : dot + rd.slot * kTile, row);
+          fence_async_smem();
+        }
+        fence_after_sync();
+        float p[64];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t x[32];
+          tmem_ask(my_s + 32 * c, x);
+          tmem_got(x);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 l = lse4[(32 * c + e) / 4];
+            p[32 * c + e] = ex2(fmaf(__uint_as_float(x[e]), sc, -l.x));
+            p[32 * c + e + 1] = ex2(fmaf(__uint_as_float(x[e + 1]), sc, -l.y));
+            p[32 * c + e + 2] = ex2(fmaf(__uint_as_float(x[e + 2]), sc, -l.z));
+            p[32 * c + e + 3] = ex2(fmaf(__uint_as_float(x[e + 3]), sc, -l.w));
+          }
+          if (!all) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(see[c] >> e & 1)) p[32 * c + e] = 0.f;
+          }
+          uint32_t y[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] = pack_bf16(p[32 * c + 2 * e], p[32 * c + 2 * e + 1]);
+          tmem_st(my_s + 16 * c, y);
+        }
+        tmem_st_wait();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->p_ready);
+        wait_all(ab, &sh->dp_full, turn & 1, a.status);
+        fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t x[32];
+          tmem_ask(my_dp + 32 * c, x);
+          tmem_got(x);
+          float g[32];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 d = del4[(32 * c + e) / 4];
+            g[e] = p[32 * c + e] * (__uint_as_float(x[e]) - d.x);
+            g[e + 1] = p[32 * c + e + 1] * (__uint_as_float(x[e + 1]) - d.y);
+            g[e + 2] = p[32 * c + e + 2] * (__uint_as_float(x[e + 2]) - d.z);
+            g[e + 3] = p[32 * c + e + 3] * (__uint_as_float(x[e + 3]) - d.w);
+          }
+          if (!all) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(see[c] >> e & 1)) g[e] = 0.f;
+          }
+          uint32_t y[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] = pack_bf16(g[2 * e], g[2 * e + 1]);
+          tmem_st(my_dp + 16 * c, y);
+        }
+        tmem_st_wait();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->ds_ready);
+        rq.next(C::kQ);
+        rd.next(C::kDo);
+      }
+      const bool fine = wait_all(ab, &sh->done, items & 1, a.status);
+      fence_after_sync();
+      // this warpgroup's half of the channels of dv and of dk
+      const int at = it.j * kRows + row;
+      const bool used = fine && at < it.L;
+      const int64_t dst = (static_cast<int64_t>(it.lo + at) * a.Hkv + it.hk) * D + wg * (D / 2);
+      const int64_t all_rows = a.S * a.Hkv * D;
+#pragma unroll 1
+      for (int g = 0; g < 2; ++g) {
+        const float f = g ? a.scale : 1.f;
+        const uint32_t acc = (g ? t_dk : t_dv) + lane_base + wg * (D / 2);
+#pragma unroll 1
+        for (int c = 0; c < D / 2; c += 32) {
+          uint32_t x[32];
+          tmem_ask(acc + c, x);
+          tmem_got(x);
+          if (!used) continue;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+          if (a.split > 1) {
+            float* const o = a.part + (g * a.split + it.part) * all_rows + dst + c;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(o + e) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          } else {
+            __nv_bfloat16* const o = (g ? a.dk : a.dv) + dst + c;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              auto two = [&](int k) { return pack_bf16(__uint_as_float(x[e + k]), __uint_as_float(x[e + k + 1])); };
+              *reinterpret_cast<uint4*>(o + e) = make_uint4(two(0), two(2), two(4), two(6));
+            }
+          }
+        }
+      }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->acc_free);
+    }
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Sums of the parts of dk and dv, in order.
+__global__ void __launch_bounds__(256) kda_packed_parts_kernel(const __grid_constant__ PackedArgs a) {
+  const int64_t all = a.S * a.Hkv * a.D;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= 2 * all || tiles_of(a, kRows) == 0) return;
+  const int g = i >= all;
+  const int64_t at = i - g * all;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = 0; p < a.split; ++p) {
+    const float4 x = *reinterpret_cast<const float4*>(a.part + (g * a.split + p) * all + at);
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+  }
+  *reinterpret_cast<uint2*>((g ? a.dk : a.dv) + at) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+}
+
+// ---- dq ----
+template <int D>
+struct QCfg {
+  static constexpr int kTile = kRows * D * 2;
+  static constexpr int kSlots = D == 128 ? 5 : 8;  // of K and V in turn
+  static constexpr int kBytes = (2 + kSlots) * kTile;
+};
+struct QShared {
+  uint64_t full[8], empty[8];
+  uint64_t q_full, q_empty;
+  // dP and dS by buffer: their next phases can be over before every role has seen the last ones
+  uint64_t s_full, s_read, dp_full[2], ds_ready[2], done, acc_free, drain;
+  uint32_t tmem;
+  int abort_;
+};
+struct QItem {
+  int lo, L, m, head, hk;  // query tile m: key tiles 0 .. m
+};
+__device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t i, QItem& it) {
+  const int64_t x = item_of(i);
+  if (x >= static_cast<int64_t>(tiles) * a.Hq) return false;
+  const Tile t = tile_of(a, tiles, static_cast<int>(x / a.Hq));
+  it.lo = t.lo;
+  it.L = t.L;
+  it.m = t.w - 1;
+  it.head = static_cast<int>(x % a.Hq);
+  it.hk = it.head / (a.Hq / a.Hkv);
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    kda_packed_dq_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ CUtensorMap qmap,
+                         const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                         const __grid_constant__ CUtensorMap domap, const float sc) {
+  using C = QCfg<D>;
+  constexpr int kTile = C::kTile, kSlots = C::kSlots;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* const ring = smem + 2 * kTile;  // behind the tiles of q and d_o
+  QShared* const sh = reinterpret_cast<QShared*>(smem + C::kBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int* const ab = &sh->abort_;
+
+  const int tiles = tiles_of(a, kRows);
+  if (tiles == 0) return;
+  if (smem_addr(smem) & 1023) {
+    if (tid == 0) set_status(a.status, KDA_ERR_DEVICE_CHECK);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], 1);
+    }
+    mbar_init(&sh->q_full, 1);
+    mbar_init(&sh->q_empty, 1);
+    mbar_init(&sh->s_full, 1);
+    mbar_init(&sh->s_read, kMathWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->dp_full[i], 1);
+      mbar_init(&sh->ds_ready[i], kMathWarps);
+    }
+    mbar_init(&sh->done, 1);
+    mbar_init(&sh->acc_free, kMathWarps);
+    mbar_init(&sh->drain, 1);
+    sh->abort_ = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) tmem_alloc(&sh->tmem, 512);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = sh->tmem;
+  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dq = tmem + 384;  // dP at t_dp and t_dp + 128 in turn
+  QItem it;
+
+  if (warp == kLoadWarp) {
+    Ring r;
+    bool ok = true;
+    uint32_t items = 0;
+    int64_t copies = 0;
+    for (int64_t i = 0; ok && item_at(a, tiles, i, it); ++i) {
+      if (items > 0) ok = wait_all(ab, &sh->q_empty, (items - 1) & 1, a.status);
+      if (!ok) break;
+      if (elect()) {
+        mbar_expect_tx(&sh->q_full, 2 * kTile);
+        load_rows<D>(smem, &qmap, it.head, it.lo + it.m * kRows, &sh->q_full);
+        load_rows<D>(smem + kTile, &domap, it.head, it.lo + it.m * kRows, &sh->q_full);
+      }
+      ++items;
+      for (int j = 0; j <= it.m; ++j) {
+        for (int v = 0; v < 2; ++v) {
+          if (r.turn > 0) ok = ok && wait_all(ab, &sh->empty[r.slot], (r.turn - 1) & 1, a.status);
+          if (!ok) break;
+          if (elect()) {
+            mbar_expect_tx(&sh->full[r.slot], kTile);
+            load_rows<D>(ring + r.slot * kTile, v ? &vmap : &kmap, it.hk, it.lo + j * kRows, &sh->full[r.slot]);
+          }
+          ++copies;
+          r.next(kSlots);
+        }
+      }
+    }
+    if (!ok) {
+      for (int64_t p = copies > kSlots ? copies - kSlots : 0; p < copies; ++p)
+        settle_for(&sh->full[p % kSlots], static_cast<uint32_t>((p / kSlots) & 1));
+      if (items > 0) settle_for(&sh->q_full, (items - 1) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    const uint32_t q_at = smem_addr(smem), do_at = q_at + kTile, ring_at = smem_addr(ring);
+    Ring rk, rv;  // K(j), V(j)
+    rv.next(kSlots);
+    uint32_t items = 0, turn = 0;
+    bool ok = true;
+    auto scores = [&](uint32_t n, const Ring& k, const Ring& v, bool last) {  // S and dP of the CTA's n-th tile
+      if (elect()) {
+        mma_scores<D>(t_s, q_at, ring_at + k.slot * kTile);
+        mma_commit(&sh->s_full);
+        mma_scores<D>(t_dp + 128 * (n & 1), do_at, ring_at + v.slot * kTile);
+        mma_commit(&sh->dp_full[n & 1]);
+        mma_commit(&sh->empty[v.slot]);
+        if (last) mma_commit(&sh->q_empty);
+      }
+    };
+    for (int64_t i = 0; ok && item_at(a, tiles, i, it); ++i) {
+      {
+        uint64_t* bar = &sh->q_full;
+        uint32_t par = items;
+        if (lane == 1) bar = &sh->full[rk.slot], par = rk.turn;
+        if (lane == 2) bar = &sh->full[rv.slot], par = rv.turn;
+        ok = wait_all(ab, bar, par & 1, a.status);
+      }
+      if (!ok) break;
+      fence_after_sync();
+      scores(turn, rk, rv, it.m == 0);
+      for (int j = 0; j <= it.m; ++j) {
+        const bool more = j < it.m;
+        Ring nk = rv, nv;
+        nk.next(kSlots);
+        nv = nk;
+        nv.next(kSlots);
+        {  // S(j) is read; the next K and V
+          uint64_t* bar = &sh->s_read;
+          uint32_t par = turn;
+          if (lane == 1 && more) bar = &sh->full[nk.slot], par = nk.turn;
+          if (lane == 2 && more) bar = &sh->full[nv.slot], par = nv.turn;
+          ok = wait_all(ab, bar, par & 1, a.status);
+        }
+        if (!ok) break;
+        fence_after_sync();
+        if (more) scores(turn + 1, nk, nv, j + 1 == it.m);
+        {  // dS(j), and at an item's start the accumulator
+          uint64_t* bar = &sh->ds_ready[turn & 1];
+          uint32_t par = turn >> 1;
+          if (lane == 1 && j == 0 && items > 0) bar = &sh->acc_free, par = items - 1;
+          ok = wait_all(ab, bar, par & 1, a.status);
+        }
+        const uint32_t t_ds = t_dp + 128 * (turn++ & 1);
+        if (!ok) break;
+        fence_after_sync();
+        if (elect()) {
+          mma_rows<D>(t_dq, t_ds, ring_at + rk.slot * kTile, j > 0);
+          mma_commit(&sh->empty[rk.slot]);
+          if (!more) mma_commit(&sh->done);
+        }
+        rk = nk;
+        rv = nv;
+      }
+      ++items;
+    }
+    if (elect()) mma_commit(&sh->drain);
+    settle_for(&sh->drain, 0);
+    __syncwarp();
+  } else if (warp >= kMathWarp) {
+    const int wg = (warp - kMathWarp) >> 2, row = tid & 127;
+    const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;
+    const uint32_t my_s = t_s + lane_base + 64 * wg;
+    uint32_t turn = 0, items = 0;
+    int64_t pos = 0;  // ring position of the item's K(0)
+    for (int64_t i = 0; item_at(a, tiles, i, it); ++i, ++items) {
+      const int at = it.m * kRows + row;
+      const bool used = at < it.L;
+      const int64_t stat = static_cast<int64_t>(it.head) * a.S + it.lo + at;
+      const float lse = used ? a.lse[stat] * 1.4426950408889634f : 0.f, delta = used ? a.delta[stat] : 0.f;
+      for (int j = 0; j <= it.m; ++j, ++turn) {
+        const uint32_t my_dp = t_dp + 128 * (turn & 1) + lane_base + 64 * wg;
+        const bool diagonal = j == it.m;
+        uint32_t see[2] = {~0u, ~0u};  // keys that this thread's query sees
+        if (diagonal) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int hi = (used ? row + 1 : 0) - (64 * wg + 32 * c);
+            see[c] = hi >= 32 ? ~0u : hi > 0 ? ~(~0u << hi) : 0u;
+          }
+        }
+        wait_all(ab, &sh->s_full, turn & 1, a.status);
+        fence_after_sync();
+        float p[64];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t x[32];
+          tmem_ask(my_s + 32 * c, x);
+          tmem_got(x);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) p[32 * c + e] = ex2(fmaf(__uint_as_float(x[e]), sc, -lse));
+          if (diagonal) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(see[c] >> e & 1)) p[32 * c + e] = 0.f;
+          }
+        }
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->s_read);
+        if (diagonal && it.L - j * kRows < kRows) {  // rows of K past the sequence to zero: S has read them
+          if (wg == 0 && at >= it.L) zero_row<D>(ring + (pos + 2 * j) % kSlots * kTile, row);
+          fence_async_smem();
+        }
+        wait_all(ab, &sh->dp_full[turn & 1], turn >> 1 & 1, a.status);
+        fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t x[32];
+          tmem_ask(my_dp + 32 * c, x);
+          tmem_got(x);
+          float g[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) g[e] = p[32 * c + e] * (__uint_as_float(x[e]) - delta);
+          if (diagonal) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(see[c] >> e & 1)) g[e] = 0.f;
+          }
+          uint32_t y[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] = pack_bf16(g[2 * e], g[2 * e + 1]);
+          tmem_st(my_dp + 16 * c, y);
+        }
+        tmem_st_wait();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->ds_ready[turn & 1]);
+      }
+      pos += 2 * (it.m + 1);
+      const bool fine = wait_all(ab, &sh->done, items & 1, a.status);
+      fence_after_sync();
+      __nv_bfloat16* const out = a.dq + (static_cast<int64_t>(it.lo + at) * a.Hq + it.head) * D + wg * (D / 2);
+#pragma unroll 1
+      for (int c = 0; c < D / 2; c += 32) {
+        uint32_t x[32];
+        tmem_ask(t_dq + lane_base + wg * (D / 2) + c, x);
+        tmem_got(x);
+        if (!used || !fine) continue;
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          auto two = [&](int k) {
+            return pack_bf16(__uint_as_float(x[e + k]) * a.scale, __uint_as_float(x[e + k + 1]) * a.scale);
+          };
+          *reinterpret_cast<uint4*>(out + c + e) = make_uint4(two(0), two(2), two(4), two(6));
+        }
+      }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->acc_free);
+    }
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                   const CUtensorMap& d_o, cudaStream_t s) {
+  const size_t smem_kv = KvCfg<D>::kBytes + sizeof(KvShared), smem_q = QCfg<D>::kBytes + sizeof(QShared);
+  static PerDevice kept_kv, kept_q;
+  int64_t sms = 0;
+  cudaError_t e = packed_sms(kept_kv, kda_packed_dkv_kernel<D>, smem_kv, &sms);
+  if (e == cudaSuccess) e = packed_sms(kept_q, kda_packed_dq_kernel<D>, smem_q, &sms);
+  if (e != cudaSuccess) return e;
+  if (sms > kPackedMaxCtas) sms = kPackedMaxCtas;
+  const float sc = a.scale * 1.4426950408889634f;
+  const int64_t rows = a.S * a.Hq, tiles = a.S / kRows + a.N;
+  kda_packed_delta_kernel<D><<<static_cast<unsigned>((rows * 8 + 255) / 256), 256, 0, s>>>(a);
+  const int64_t kv = tiles * a.Hkv * a.split, nq = tiles * a.Hq;
+  kda_packed_dkv_kernel<D><<<static_cast<unsigned>(kv < sms ? kv : sms), kThreads, smem_kv, s>>>(a, q, k, v, d_o, sc);
+  kda_packed_dq_kernel<D><<<static_cast<unsigned>(nq < sms ? nq : sms), kThreads, smem_q, s>>>(a, q, k, v, d_o, sc);
+  if (a.split > 1) kda_packed_parts_kernel<<<static_cast<unsigned>((2 * a.S * a.Hkv * a.D / 4 + 255) / 256), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_packed_bwd(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                              const CUtensorMap& d_o, cudaStream_t s) {
+  return a.D == 128 ? launch<128>(a, q, k, v, d_o, s) : launch<64>(a, q, k, v, d_o, s);
+}
+
+}  // namespace kda

@@ -1,0 +1,387 @@
+// kda_packed_fwd.cu -- forward of causal attention over packed sequences
+// (kda_attention_fwd of kda_blocks.h) on the tcgen05 tensor cores.
+//
+//   o = softmax(scale q K^T) V,   lse = log sum exp(scale q K^T)
+//
+// Tiles. An item is 256 tokens of one query head: two streams of 128 rows that
+// share every tile of 128 keys, K and V loaded once for both. S = Q K^T and
+// O += P V are 128 x 128 x D and 128 x D x 128 products with fp32 sums in
+// TMEM; P goes back to TMEM as bf16 over scores that have been read, and is the
+// A operand of the second product from there. While one stream's warpgroup
+// forms its probabilities (a thread owns a row) the tensor cores run the other's
+// products. A row's O is rescaled only when its maximum has grown by more than
+// 2^8, by a whole power of two: the factor is exact and the sum takes it out.
+// bf16 probabilities because both operands have one type; the row's sum adds
+// them in fp32 before they are rounded.
+//
+// Items are handed out heaviest first, a fixed share to each of one CTA per
+// SM. The next item's queries, keys and values are fetched, and its first
+// scores formed, while the last item's outputs are written.
+#include <math.h>
+
+#include "kda_packed.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 128;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kMmaWarp = 0, kLoadWarp = 1, kSoftmaxWarp = 4;  // warps 2 and 3 are idle
+constexpr int kThreads = 32 * (kSoftmaxWarp + kSoftmaxWarps);
+constexpr float kRescale = 8.f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kTile = kRows * D * 2;              // bytes of 128 rows
+  static constexpr int kSlots = D == 128 ? 5 : 8;          // of K and V in turn
+  static constexpr int kBytes = (2 + kSlots) * kTile;
+};
+
+struct Shared {
+  uint64_t full[8], empty[8];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_ready[2], o_done[2], o_free[2];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort_;
+};
+
+// What every role knows of an item.
+struct Item {
+  int lo, L, head, hk, row0;  // row0: first row of stream 0 in the sequence
+  int n[2];                   // key tiles of each stream
+};
+__device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t i, Item& it) {
+  const int64_t x = item_of(i);
+  if (x >= static_cast<int64_t>(tiles) * a.Hq) return false;
+  const Tile t = tile_of(a, tiles, static_cast<int>(x / a.Hq));
+  it.lo = t.lo;
+  it.L = t.L;
+  it.head = static_cast<int>(x % a.Hq);
+  it.hk = it.head / (a.Hq / a.Hkv);
+  it.row0 = (t.w - 1) * 2 * kRows;
+  it.n[0] = 2 * t.w - 1;
+  it.n[1] = it.row0 + kRows < t.L ? 2 * t.w : 0;
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    kda_packed_fwd_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ CUtensorMap qmap,
+                          const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                          const float sc) {
+  constexpr int kTile = Cfg<D>::kTile, kSlots = Cfg<D>::kSlots;
+  score_regs();
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* const ring = smem + 2 * kTile;  // behind the two query tiles
+  Shared* const sh = reinterpret_cast<Shared*>(smem + Cfg<D>::kBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int* const ab = &sh->abort_;
+
+  const int tiles = tiles_of(a, 2 * kRows);
+  if (tiles == 0) return;
+  if (smem_addr(smem) & 1023) {  // the swizzle needs it; no static shared memory comes before
+    if (tid == 0) set_status(a.status, KDA_ERR_DEVICE_CHECK);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], 1);
+    }
+    mbar_init(&sh->q_full, 1);
+    mbar_init(&sh->q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->s_full[i], 1);
+      mbar_init(&sh->p_ready[i], 4);
+      mbar_init(&sh->o_done[i], 1);
+      mbar_init(&sh->o_free[i], 4);
+    }
+    mbar_init(&sh->drain, 1);
+    sh->abort_ = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) tmem_alloc(&sh->tmem, 512);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = sh->tmem;
+  const uint32_t tmem_s = tmem, tmem_o = tmem + 256;  // S (P over it) of stream i at + 128 i, O at + 128 i
+  Item it;
+
+  if (warp == kLoadWarp) {
+    // ---- loads: Q, then K and V in turn ----
+    Ring r;
+    bool ok = true;
+    uint32_t items = 0;
+    int64_t copies = 0;
+    for (int64_t i = 0; ok && item_at(a, tiles, i, it); ++i) {
+      if (items > 0) ok = wait_all(ab, &sh->q_empty, (items - 1) & 1, a.status);
+      if (!ok) break;
+      const int streams = it.n[1] ? 2 : 1, nk = it.n[1] ? it.n[1] : it.n[0];
+      if (elect()) {
+        mbar_expect_tx(&sh->q_full, streams * kTile);
+        for (int s = 0; s < streams; ++s)
+          load_rows<D>(smem + s * kTile, &qmap, it.head, it.lo + it.row0 + s * kRows, &sh->q_full);
+      }
+      ++items;
+      for (int j = 0; j < nk; ++j) {
+        for (int v = 0; v < 2; ++v) {
+          if (r.turn > 0) ok = ok && wait_all(ab, &sh->empty[r.slot], (r.turn - 1) & 1, a.status);
+          if (!ok) break;
+          if (elect()) {
+            mbar_expect_tx(&sh->full[r.slot], kTile);
+            load_rows<D>(ring + r.slot * kTile, v ? &vmap : &kmap, it.hk, it.lo + j * kRows, &sh->full[r.slot]);
+          }
+          ++copies;
+          r.next(kSlots);
+        }
+      }
+    }
+    // after an abort: the copies in flight land before the CTA ends
+    if (!ok) {
+      for (int64_t p = copies > kSlots ? copies - kSlots : 0; p < copies; ++p)
+        settle_for(&sh->full[p % kSlots], static_cast<uint32_t>((p / kSlots) & 1));
+      if (items > 0) settle_for(&sh->q_full, (items - 1) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- products ----
+    constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);
+    constexpr uint32_t id_qk = idesc(kRows, kRows) | kBf16, id_pv = idesc(kRows, D, false, true) | kBf16;
+    const uint32_t q_at = smem_addr(smem), ring_at = smem_addr(ring);
+    Ring rk;  // the ring's position of K(j); V(j) is the next one
+    uint32_t items = 0, turn_p[2] = {0, 0}, used_o[2] = {0, 0};
+    bool ok = true;
+    auto qk = [&](int s, int slot) {
+      if (elect()) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma(tmem_s + 128 * s, desc_kmajor(q_at + s * kTile, kRows, 0, k), desc_kmajor(ring_at + slot * kTile, kRows, 0, k),
+              id_qk, k > 0);
+        mma_commit(&sh->s_full[s]);
+      }
+    };
+    for (int64_t i = 0; ok && item_at(a, tiles, i, it); ++i) {
+      const int nk = it.n[1] ? it.n[1] : it.n[0];
+      ok = wait_all(ab, lane == 0 ? &sh->q_full : &sh->full[rk.slot], (lane == 0 ? items : rk.turn) & 1, a.status);
+      ++items;
+      if (!ok) break;
+      fence_after_sync();
+      for (int s = 0; s < 2; ++s)
+        if (it.n[s]) qk(s, rk.slot);
+      if (elect()) {
+        mma_commit(&sh->empty[rk.slot]);
+        if (nk == 1) mma_commit(&sh->q_empty);
+      }
+      for (int j = 0; ok && j < nk; ++j) {
+        Ring rv = rk;
+        rv.next(kSlots);
+        rk = rv;
+        rk.next(kSlots);  // K(j + 1)
+        const bool more = j + 1 < nk;
+        for (int s = 0; ok && s < 2; ++s) {
+          if (j >= it.n[s]) continue;
+          // P, V, the next K, and at an item's start O, in one wait by a lane each
+          const bool first = j == 0 && used_o[s] > 0;
+          uint64_t* bar = &sh->p_ready[s];
+          uint32_t par = turn_p[s];
+          if (lane == 1) bar = &sh->full[rv.slot], par = rv.turn;
+          if (lane == 2 && more) bar = &sh->full[rk.slot], par = rk.turn;
+          if (lane == 3 && first) bar = &sh->o_free[s], par = used_o[s] - 1;
+          ok = wait_all(ab, bar, par & 1, a.status);
+          ++turn_p[s];
+          if (j == 0) ++used_o[s];
+          if (!ok) break;
+          fence_after_sync();
+          const uint32_t ts = tmem_s + 128 * s, to = tmem_o + 128 * s;
+          if (elect()) {
+#pragma unroll
+            for (int k = 0; k < kRows / 16; ++k)
+              mma_ta(to, ts + 8 * k, desc_mnmajor(ring_at + rv.slot * kTile, kRows * 128, k), id_pv, (j > 0 || k > 0) ? 1u : 0u);
+            if (j + 1 == it.n[s]) mma_commit(&sh->o_done[s]);
+          }
+          if (j + 1 < it.n[s]) qk(s, rk.slot);
+        }
+        if (ok && elect()) {
+          mma_commit(&sh->empty[rv.slot]);
+          if (more) mma_commit(&sh->empty[rk.slot]);
+          if (j + 2 == nk) mma_commit(&sh->q_empty);
+        }
+      }
+    }
+    // nothing of this warp may be in flight when TMEM is freed
+    if (elect()) mma_commit(&sh->drain);
+    settle_for(&sh->drain, 0);
+    __syncwarp();
+  } else if (warp >= kSoftmaxWarp) {
+    // ---- softmax: thread = row, warpgroup = stream ----
+    const int st = (warp - kSoftmaxWarp) >> 2, row = tid & 127;
+    const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
+    const uint32_t my_s = tmem_s + 128 * st + lane_base;
+    const uint32_t my_o = tmem_o + 128 * st + lane_base;
+    uint32_t turn_s = 0, turn_d = 0;
+    int64_t pos = 0;  // ring position of the item's K(0)
+    for (int64_t i = 0; item_at(a, tiles, i, it); ++i) {
+      const int nt = it.n[st], nk = it.n[1] ? it.n[1] : it.n[0];
+      const int at = it.row0 + st * kRows + row;  // row of the sequence
+      const bool used = at < it.L;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < nt; ++j) {
+        wait_all(ab, &sh->s_full[st], turn_s++ & 1, a.status);
+        fence_after_sync();
+        if (j + 1 == nt) {  // the tile on the diagonal: -inf into S first, off the common path
+          const int open = used ? row + 1 : 0;
+#pragma unroll 1
+          for (int c0 = 0; c0 < kRows; c0 += 32) {
+            uint32_t y[32];
+            tmem_ask(my_s + c0, y);
+            tmem_got(y);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c0 + c >= open) y[c] = 0xff800000u;
+            tmem_st(my_s + c0, y);
+          }
+          tmem_st_wait();
+          const int past = it.L - j * kRows;  // rows of the tile from here on are another sequence's
+          if (past < kRows) {
+            const int64_t vpos = pos + 2 * j + 1;
+            const int slot = static_cast<int>(vpos % kSlots);
+            if (wait_all(ab, &sh->full[slot], static_cast<uint32_t>((vpos / kSlots) & 1), a.status) && row >= past)
+              zero_row<D>(ring + slot * kTile, row);
+            fence_async_smem();
+          }
+        }
+        // One pass over the row, 32 scores at a time with the next 32 on their way.
+        const uint64_t sc2 = pack2(__float_as_uint(sc), __float_as_uint(sc));
+        uint64_t sum[4] = {0, 0, 0, 0};
+        uint32_t x[32];
+        auto highest = [&]() {
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 32; c += 2)
+            top[c / 2 & 3] = fmaxf(fmaxf(top[c / 2 & 3], __uint_as_float(x[c])), __uint_as_float(x[c + 1]));
+          return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+        };
+        score_ask(my_s);
+        score_got(x);
+        float mn = highest();
+#pragma unroll 1
+        for (int h = 0; h < 4; ++h) {
+          const bool grow = mn > m + kRescale;  // m = -inf: any finite maximum
+          if (__any_sync(~0u, grow)) {
+            // by a whole number of octaves: the factor is exact, for P too
+            const float k = ceilf(mn - m);
+            const float f = !grow ? 1.f : k < 126.f ? __uint_as_float((127u - static_cast<uint32_t>(k)) << 23) : 0.f;
+            if (grow) m = m == -INFINITY ? mn : m + k;
+            l *= f;
+            const uint64_t f2 = pack2(__float_as_uint(f), __float_as_uint(f));
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sum[c] = fma2(sum[c], f2, 0);
+            tmem_st_wait();
+            uint32_t y[16];
+#pragma unroll 1
+            for (int c = 0; c < 16 * h; c += 16) {
+              tmem_ask(my_s + c, y);
+              tmem_got(y);
+#pragma unroll
+              for (int q = 0; q < 16; ++q)
+                y[q] = pack_bf16(__uint_as_float(y[q] << 16) * f, __uint_as_float(y[q] & 0xffff0000u) * f);
+              tmem_st(my_s + c, y);
+            }
+            if (j > 0) {  // the stream's O exists, and is complete: S of this tile was issued after it
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                tmem_ask(my_o + c, y);
+                tmem_got(y);
+#pragma unroll
+                for (int q = 0; q < 16; ++q) y[q] = __float_as_uint(__uint_as_float(y[q]) * f);
+                tmem_st(my_o + c, y);
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          const uint64_t ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
+          uint64_t t[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) t[c] = fma2(pack2(x[2 * c], x[2 * c + 1]), sc2, ref2);
+          score_ask(my_s + (32 * (h + 1) & 96));  // after the last: not used
+          uint32_t p[16];
+          auto exps = [&](int c) {
+            const float2 e = unpack2(t[c]);
+            const float e0 = ex2(e.x), e1 = ex2(e.y);
+            sum[c & 3] = add2(sum[c & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
+            p[c] = pack_bf16(e0, e1);
+          };
+#pragma unroll
+          for (int c = 0; c < 8; ++c) exps(c);
+          score_got(x);
+          mn = highest();
+#pragma unroll
+          for (int c = 8; c < 16; ++c) exps(c);
+          tmem_st(my_s + 16 * h, p);
+        }
+        const float2 all = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+        l += all.x + all.y;
+        tmem_st_wait();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->p_ready[st]);
+      }
+      pos += 2 * nk;
+      if (nt == 0) continue;
+      const bool fine = wait_all(ab, &sh->o_done[st], turn_d++ & 1, a.status);
+      fence_after_sync();
+      // every row sees its own key: l is 0 or NaN only where the scores are not finite
+      const float inv = 1.f / l;
+      const int64_t tok = static_cast<int64_t>(it.lo) + at;
+      __nv_bfloat16* const out = a.o + (tok * a.Hq + it.head) * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t x[32];
+        tmem_ask(my_o + c, x);
+        tmem_got(x);
+        if (used && fine) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            auto two = [&](int e) {
+              return pack_bf16(__uint_as_float(x[k + e]) * inv, __uint_as_float(x[k + e + 1]) * inv);
+            };
+            *reinterpret_cast<uint4*>(out + c + k) = make_uint4(two(0), two(2), two(4), two(6));
+          }
+        }
+      }
+      if (used && fine)
+        a.lse[static_cast<int64_t>(it.head) * a.S + tok] = (m + log2f(l)) * 0.6931471805599453f;
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->o_free[st]);
+    }
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+  const size_t smem = Cfg<D>::kBytes + sizeof(Shared);
+  static PerDevice kept;
+  int64_t sms = 0;
+  const cudaError_t e = packed_sms(kept, kda_packed_fwd_kernel<D>, smem, &sms);
+  if (e != cudaSuccess) return e;
+  const int64_t most = (a.S / (2 * kRows) + a.N) * a.Hq;  // items
+  int64_t ctas = sms < kPackedMaxCtas ? sms : kPackedMaxCtas;
+  if (ctas > most) ctas = most;
+  kda_packed_fwd_kernel<D><<<static_cast<unsigned>(ctas), kThreads, smem, s>>>(a, q, k, v, a.scale * 1.4426950408889634f);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_packed_fwd(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                              cudaStream_t s) {
+  return a.D == 128 ? launch<128>(a, q, k, v, s) : launch<64>(a, q, k, v, s);
+}
+
+}  // namespace kda

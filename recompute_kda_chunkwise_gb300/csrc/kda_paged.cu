@@ -47,6 +47,29 @@ __global__ void __launch_bounds__(128) kda_paged_append_kernel(const PagedArgs a
   }
 }
 
+kda_status tensor(const char* name, const void* p) {
+  if (!p) return set_error(KDA_ERR_INVALID_ARG, "%s is NULL", name);
+  if ((uintptr_t)p & 15u) return set_error(KDA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+  return KDA_OK;
+}
+
+PagedArgs args_of(const kda_paged_problem* p) {
+  PagedArgs a{};
+  a.cu = p->cu_seqlens; a.table = p->page_table; a.lens = p->kv_lens;
+  a.S = p->total_tokens; a.pages = p->num_pages;
+  a.N = p->num_seqs; a.Hq = p->num_heads; a.Hkv = p->num_kv_heads; a.D = p->head_dim;
+  a.page = p->page_size; a.width = p->max_pages; a.scale = p->scale;
+  return a;
+}
+
+#define PAGED_TRY(x)               \
+  do {                             \
+    const kda_status st_ = (x);    \
+    if (st_ != KDA_OK) return st_; \
+  } while (0)
+
+}  // namespace
+
 kda_status validate_paged(const kda_paged_problem* p, bool ptrs) {
   if (!p) return set_error(KDA_ERR_INVALID_ARG, "problem is NULL");
   if (p->dtype != KDA_DTYPE_BF16) return set_error(KDA_ERR_UNSUPPORTED, "dtype %d is not supported (bf16)", p->dtype);
@@ -76,28 +99,6 @@ kda_status validate_paged(const kda_paged_problem* p, bool ptrs) {
   return KDA_OK;
 }
 
-kda_status tensor(const char* name, const void* p) {
-  if (!p) return set_error(KDA_ERR_INVALID_ARG, "%s is NULL", name);
-  if ((uintptr_t)p & 15u) return set_error(KDA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
-  return KDA_OK;
-}
-
-PagedArgs args_of(const kda_paged_problem* p) {
-  PagedArgs a{};
-  a.cu = p->cu_seqlens; a.table = p->page_table; a.lens = p->kv_lens;
-  a.S = p->total_tokens; a.pages = p->num_pages;
-  a.N = p->num_seqs; a.Hq = p->num_heads; a.Hkv = p->num_kv_heads; a.D = p->head_dim;
-  a.page = p->page_size; a.width = p->max_pages; a.scale = p->scale;
-  return a;
-}
-
-#define PAGED_TRY(x)               \
-  do {                             \
-    const kda_status st_ = (x);    \
-    if (st_ != KDA_OK) return st_; \
-  } while (0)
-
-}  // namespace
 }  // namespace kda
 
 extern "C" {

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "kda_internal.cuh"
+#include "kda_serving.h"
 
 namespace kda {
 
@@ -18,6 +19,9 @@ struct PagedArgs {
   int N, Hq, Hkv, D, page, width;
   float scale;
 };
+
+// Host-side checks of a problem; ptrs: of its device arrays too.
+kda_status validate_paged(const kda_paged_problem* p, bool ptrs);
 
 size_t paged_attention_scratch_bytes(const PagedArgs& a);
 kda_status launch_paged_attention(const PagedArgs& a, cudaStream_t s);

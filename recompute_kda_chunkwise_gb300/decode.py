@@ -51,6 +51,17 @@ def paged_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, *, sta
     done(bind().append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, status), "kda_paged_append")
 
 
+def paged_append_rotary(rope, q, k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, *, out=None, status=None):
+    """``paged_append`` with rotary positions (kda_paged_append_rotary): the new
+    tokens' k is rotated by its position in the cache on the way there, v is
+    written as it is, and the rotated q [S, Hq, D] is returned (None where q
+    is; ``out`` may hold it, and may be q). rope: a ``rotary.Rotary``. q, k and
+    v may be slices of a fused projection. Tokens that paged_append skips are
+    skipped: their rows of the result are not written."""
+    return done(bind().append_rotary(rope.turns, rope.interleaved, rope.magnitude, q, k, v, k_pages, v_pages, page_table,
+                                     kv_lens, cu_seqlens, out, status), "kda_paged_append_rotary")
+
+
 def paged_attention(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens, *, scale=None, out=None, workspace=None):
     """Causal attention of the new tokens q [S, Hq, D] over the paged cache
     (kda_paged_attention), whose kv_lens [N] positions end with them. scale:
