@@ -54,6 +54,35 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
   for (int k = 0; k < D / 16; ++k) mma(d, desc_kmajor(a, kRows, 0, k), desc_kmajor(b, kRows, 0, k), id, k > 0);
 }
 
+// 64 consecutive columns of the thread's TMEM lane.
+__device__ __forceinline__ void load64(uint32_t at, uint32_t (&x)[2][32]) {
+  tmem_ask(at, x[0]);
+  tmem_ask(at + 32, x[1]);
+  tmem_got(x[0]);
+  tmem_got(x[1]);
+}
+// Exponentials (base 2) of a pair, in place.
+__device__ __forceinline__ void ex2_pair(uint64_t t, uint32_t& lo, uint32_t& hi) {
+  const float2 e = unpack2(t);
+  lo = __float_as_uint(ex2(e.x));
+  hi = __float_as_uint(ex2(e.y));
+}
+// Zero where a column is not seen.
+__device__ __forceinline__ void hide(uint32_t (&x)[2][32], const uint32_t (&see)[2]) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!(see[c] >> e & 1)) x[c][e] = 0u;
+}
+// Rounded to bf16, two to a column, 16 columns for each 32.
+__device__ __forceinline__ void store_bf16(uint32_t at, const uint32_t (&x)[32]) {
+  uint32_t y[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) y[e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+  tmem_st(at, y);
+}
+
 // ---- delta[h][s] = sum over channels of d_o o: eight lanes a row ----
 template <int D>
 __global__ void __launch_bounds__(256) kda_packed_delta_kernel(const __grid_constant__ PackedArgs a) {
@@ -88,7 +117,7 @@ struct KvCfg {
   static constexpr int kBytes = (2 + kQ + kDo) * kTile;
 };
 struct KvShared {
-  float row[2][2][kRows];  // lse (base 2) and delta of a step's queries
+  alignas(16) float row[2][2][kRows];  // -lse (base 2) and -delta of a step's queries
   uint64_t kv_full, kv_empty;
   uint64_t q_full[3], q_empty[3], do_full[2], do_empty[2];
   uint64_t s_full, dp_full, p_ready, ds_ready, done, acc_free, drain;
@@ -167,49 +196,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
   KvItem it;
 
-  if (warp == kLoadWarp) {
-    Ring rq, rd;
+  if (warp == kLoadWarp || warp == kLoadWarp + 1) {
+    // ---- loads: a warp for K, V and q, another for d_o ----
+    const bool second = warp != kLoadWarp;
+    uint64_t* const full = second ? sh->do_full : sh->q_full;
+    uint64_t* const empty = second ? sh->do_empty : sh->q_empty;
+    uint8_t* const at = second ? dot : qt;
+    const int slots = second ? C::kDo : C::kQ;
+    Ring r;
     bool ok = true;
     uint32_t items = 0;
-    int64_t steps = 0;
+    int64_t copies = 0;
     for (int64_t i = 0; ok && item_at(a, tiles, i, it); ++i) {
-      if (items > 0) ok = wait_all(ab, &sh->kv_empty, (items - 1) & 1, a.status);
-      if (!ok) break;
-      if (elect()) {
-        mbar_expect_tx(&sh->kv_full, 2 * kTile);
-        load_rows<D>(kt, &kmap, it.hk, it.lo + it.j * kRows, &sh->kv_full);
-        load_rows<D>(vt, &vmap, it.hk, it.lo + it.j * kRows, &sh->kv_full);
+      if (!second) {
+        if (items > 0) ok = wait_all(ab, &sh->kv_empty, (items - 1) & 1, a.status);
+        if (!ok) break;
+        if (elect()) {
+          mbar_expect_tx(&sh->kv_full, 2 * kTile);
+          load_rows<D>(kt, &kmap, it.hk, it.lo + it.j * kRows, &sh->kv_full);
+          load_rows<D>(vt, &vmap, it.hk, it.lo + it.j * kRows, &sh->kv_full);
+        }
+        ++items;
       }
-      ++items;
       for (int h = 0; ok && h < it.heads; ++h) {
         for (int m = it.j; m < it.nt; ++m) {
-          if (rq.turn > 0) ok = wait_all(ab, &sh->q_empty[rq.slot], (rq.turn - 1) & 1, a.status);
+          if (r.turn > 0) ok = wait_all(ab, &empty[r.slot], (r.turn - 1) & 1, a.status);
           if (!ok) break;
           if (elect()) {
-            mbar_expect_tx(&sh->q_full[rq.slot], kTile);
-            load_rows<D>(qt + rq.slot * kTile, &qmap, it.head0 + h, it.lo + m * kRows, &sh->q_full[rq.slot]);
+            mbar_expect_tx(&full[r.slot], kTile);
+            load_rows<D>(at + r.slot * kTile, second ? &domap : &qmap, it.head0 + h, it.lo + m * kRows, &full[r.slot]);
           }
-          __syncwarp();
-          // counted below from here on: this step's query copy is in flight
-          ++steps;
-          if (rd.turn > 0) ok = wait_all(ab, &sh->do_empty[rd.slot], (rd.turn - 1) & 1, a.status);
-          if (!ok) break;
-          if (elect()) {
-            mbar_expect_tx(&sh->do_full[rd.slot], kTile);
-            load_rows<D>(dot + rd.slot * kTile, &domap, it.head0 + h, it.lo + m * kRows, &sh->do_full[rd.slot]);
-          }
-          rq.next(C::kQ);
-          rd.next(C::kDo);
+          ++copies;
+          r.next(slots);
         }
       }
     }
-    // after an abort: the copies in flight land before the CTA ends (a copy that
-    // was not issued only costs its wait)
+    // after an abort: the copies in flight land before the CTA ends
     if (!ok) {
-      for (int64_t p = steps > C::kQ ? steps - C::kQ : 0; p < steps; ++p)
-        settle_for(&sh->q_full[p % C::kQ], static_cast<uint32_t>((p / C::kQ) & 1));
-      for (int64_t p = steps > C::kDo ? steps - C::kDo : 0; p < steps; ++p)
-        settle_for(&sh->do_full[p % C::kDo], static_cast<uint32_t>((p / C::kDo) & 1));
+      for (int64_t p = copies > slots ? copies - slots : 0; p < copies; ++p)
+        settle_for(&full[p % slots], static_cast<uint32_t>((p / slots) & 1));
       if (items > 0) settle_for(&sh->kv_full, (items - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
@@ -290,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wg = (warp - kMathWarp) >> 2, row = tid & 127, mt = tid - 32 * kMathWarp;
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;
     const uint32_t my_s = t_s + lane_base + 64 * wg, my_dp = t_dp + lane_base + 64 * wg;
+    const uint64_t sc2 = twice2(sc);
     uint32_t turn = 0, items = 0;
     Ring rq, rd;
     for (int64_t i = 0; item_at(a, tiles, i, it); ++i, ++items) {
@@ -304,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int h = 0, m = it.j;
       for (int t = 0; t < steps; ++t, ++turn) {
         float* const mine = sh->row[turn & 1][mt < kRows ? 0 : 1];
-        mine[row] = mt < kRows ? ahead * 1.4426950408889634f : ahead;
+        mine[row] = mt < kRows ? ahead * -1.4426950408889634f : -ahead;
         named_bar_sync(1, 32 * kMathWarps);
         const int past = it.L - m * kRows;       // query rows of the tile from here on are another sequence's
         const bool diagonal = m == it.j, tail = past < kRows;
@@ -313,8 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++h;
         }
         if (t + 1 < steps) ahead = fetch(h, m);
-        const float4* const lse4 = reinterpret_cast<const float4*>(sh->row[turn & 1][0] + 64 * wg);
-        const float4* const del4 = reinterpret_cast<const float4*>(sh->row[turn & 1][1] + 64 * wg);
+        const ulonglong2* const lse2 = reinterpret_cast<const ulonglong2*>(sh->row[turn & 1][0] + 64 * wg);
+        const ulonglong2* const del2 = reinterpret_cast<const ulonglong2*>(sh->row[turn & 1][1] + 64 * wg);
         // columns (queries) that see this thread's key
         uint32_t see[2] = {~0u, ~0u};
         if (diagonal || tail) {
@@ -333,60 +359,49 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_smem();
         }
         fence_after_sync();
-        float p[64];
+        uint32_t p[2][32], x[2][32];
+        load64(my_s, p);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t x[32];
-          tmem_ask(my_s + 32 * c, x);
-          tmem_got(x);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float4 l = lse4[(32 * c + e) / 4];
-            p[32 * c + e] = ex2(fmaf(__uint_as_float(x[e]), sc, -l.x));
-            p[32 * c + e + 1] = ex2(fmaf(__uint_as_float(x[e + 1]), sc, -l.y));
-            p[32 * c + e + 2] = ex2(fmaf(__uint_as_float(x[e + 2]), sc, -l.z));
-            p[32 * c + e + 3] = ex2(fmaf(__uint_as_float(x[e + 3]), sc, -l.w));
+            const ulonglong2 l = lse2[(32 * c + e) / 4];
+            ex2_pair(fma2(pack2(p[c][e], p[c][e + 1]), sc2, l.x), p[c][e], p[c][e + 1]);
+            ex2_pair(fma2(pack2(p[c][e + 2], p[c][e + 3]), sc2, l.y), p[c][e + 2], p[c][e + 3]);
           }
-          if (!all) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(see[c] >> e & 1)) p[32 * c + e] = 0.f;
-          }
-          uint32_t y[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = pack_bf16(p[32 * c + 2 * e], p[32 * c + 2 * e + 1]);
-          tmem_st(my_s + 16 * c, y);
+          if (c == 0 && all) store_bf16(my_s, p[0]);
         }
+        if (!all) {
+          hide(p, see);
+          store_bf16(my_s, p[0]);
+        }
+        store_bf16(my_s + 16, p[1]);
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->p_ready);
         wait_all(ab, &sh->dp_full, turn & 1, a.status);
         fence_after_sync();
+        load64(my_dp, x);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t x[32];
-          tmem_ask(my_dp + 32 * c, x);
-          tmem_got(x);
-          float g[32];
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float4 d = del4[(32 * c + e) / 4];
-            g[e] = p[32 * c + e] * (__uint_as_float(x[e]) - d.x);
-            g[e + 1] = p[32 * c + e + 1] * (__uint_as_float(x[e + 1]) - d.y);
-            g[e + 2] = p[32 * c + e + 2] * (__uint_as_float(x[e + 2]) - d.z);
-            g[e + 3] = p[32 * c + e + 3] * (__uint_as_float(x[e + 3]) - d.w);
+            const ulonglong2 d = del2[(32 * c + e) / 4];
+            const float2 g = unpack2(mul2(pack2(p[c][e], p[c][e + 1]), add2(pack2(x[c][e], x[c][e + 1]), d.x)));
+            const float2 h = unpack2(mul2(pack2(p[c][e + 2], p[c][e + 3]), add2(pack2(x[c][e + 2], x[c][e + 3]), d.y)));
+            x[c][e] = __float_as_uint(g.x);
+            x[c][e + 1] = __float_as_uint(g.y);
+            x[c][e + 2] = __float_as_uint(h.x);
+            x[c][e + 3] = __float_as_uint(h.y);
           }
-          if (!all) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(see[c] >> e & 1)) g[e] = 0.f;
-          }
-          uint32_t y[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = pack_bf16(g[2 * e], g[2 * e + 1]);
-          tmem_st(my_dp + 16 * c, y);
+          if (c == 0 && all) store_bf16(my_dp, x[0]);
         }
+        if (!all) {
+          hide(x, see);
+          store_bf16(my_dp, x[0]);
+        }
+        store_bf16(my_dp + 16, x[1]);
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
@@ -455,11 +470,11 @@ __global__ void __launch_bounds__(256) kda_packed_parts_kernel(const __grid_cons
 template <int D>
 struct QCfg {
   static constexpr int kTile = kRows * D * 2;
-  static constexpr int kSlots = D == 128 ? 5 : 8;  // of K and V in turn
-  static constexpr int kBytes = (2 + kSlots) * kTile;
+  static constexpr int kK = D == 128 ? 3 : 5, kV = D == 128 ? 2 : 4;  // slots: a tile of K is held for longer
+  static constexpr int kBytes = (2 + kK + kV) * kTile;
 };
 struct QShared {
-  uint64_t full[8], empty[8];
+  uint64_t k_full[5], k_empty[5], v_full[4], v_empty[4];
   uint64_t q_full, q_empty;
   // dP and dS by buffer: their next phases can be over before every role has seen the last ones
   uint64_t s_full, s_read, dp_full[2], ds_ready[2], done, acc_free, drain;
@@ -487,9 +502,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const __grid_constant__ CUtensorMap domap, const float sc) {
   using C = QCfg<D>;
-  constexpr int kTile = C::kTile, kSlots = C::kSlots;
+  constexpr int kTile = C::kTile;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* const ring = smem + 2 * kTile;  // behind the tiles of q and d_o
+  uint8_t* const kt = smem + 2 * kTile;  // behind the tiles of q and d_o
+  uint8_t* const vt = kt + C::kK * kTile;
   QShared* const sh = reinterpret_cast<QShared*>(smem + C::kBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* const ab = &sh->abort_;
@@ -501,9 +517,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&sh->full[i], 1);
-      mbar_init(&sh->empty[i], 1);
+    for (int i = 0; i < C::kK; ++i) {
+      mbar_init(&sh->k_full[i], 1);
+      mbar_init(&sh->k_empty[i], 1);
+    }
+    for (int i = 0; i < C::kV; ++i) {
+      mbar_init(&sh->v_full[i], 1);
+      mbar_init(&sh->v_empty[i], 1);
     }
     mbar_init(&sh->q_full, 1);
     mbar_init(&sh->q_empty, 1);
@@ -527,51 +547,56 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t t_s = tmem, t_dp = tmem + 128, t_dq = tmem + 384;  // dP at t_dp and t_dp + 128 in turn
   QItem it;
 
-  if (warp == kLoadWarp) {
+  if (warp == kLoadWarp || warp == kLoadWarp + 1) {
+    // ---- loads: a warp for q, d_o and K, another for V: neither waits for the other's slots ----
+    const bool v = warp != kLoadWarp;
+    uint64_t* const full = v ? sh->v_full : sh->k_full;
+    uint64_t* const empty = v ? sh->v_empty : sh->k_empty;
+    uint8_t* const at = v ? vt : kt;
+    const int slots = v ? C::kV : C::kK;
     Ring r;
     bool ok = true;
     uint32_t items = 0;
     int64_t copies = 0;
     for (int64_t i = 0; ok && item_at(a, tiles, i, it); ++i) {
-      if (items > 0) ok = wait_all(ab, &sh->q_empty, (items - 1) & 1, a.status);
-      if (!ok) break;
-      if (elect()) {
-        mbar_expect_tx(&sh->q_full, 2 * kTile);
-        load_rows<D>(smem, &qmap, it.head, it.lo + it.m * kRows, &sh->q_full);
-        load_rows<D>(smem + kTile, &domap, it.head, it.lo + it.m * kRows, &sh->q_full);
-      }
-      ++items;
-      for (int j = 0; j <= it.m; ++j) {
-        for (int v = 0; v < 2; ++v) {
-          if (r.turn > 0) ok = ok && wait_all(ab, &sh->empty[r.slot], (r.turn - 1) & 1, a.status);
-          if (!ok) break;
-          if (elect()) {
-            mbar_expect_tx(&sh->full[r.slot], kTile);
-            load_rows<D>(ring + r.slot * kTile, v ? &vmap : &kmap, it.hk, it.lo + j * kRows, &sh->full[r.slot]);
-          }
-          ++copies;
-          r.next(kSlots);
+      if (!v) {
+        if (items > 0) ok = wait_all(ab, &sh->q_empty, (items - 1) & 1, a.status);
+        if (!ok) break;
+        if (elect()) {
+          mbar_expect_tx(&sh->q_full, 2 * kTile);
+          load_rows<D>(smem, &qmap, it.head, it.lo + it.m * kRows, &sh->q_full);
+          load_rows<D>(smem + kTile, &domap, it.head, it.lo + it.m * kRows, &sh->q_full);
         }
+        ++items;
+      }
+      for (int j = 0; j <= it.m; ++j) {
+        if (r.turn > 0) ok = ok && wait_all(ab, &empty[r.slot], (r.turn - 1) & 1, a.status);
+        if (!ok) break;
+        if (elect()) {
+          mbar_expect_tx(&full[r.slot], kTile);
+          load_rows<D>(at + r.slot * kTile, v ? &vmap : &kmap, it.hk, it.lo + j * kRows, &full[r.slot]);
+        }
+        ++copies;
+        r.next(slots);
       }
     }
     if (!ok) {
-      for (int64_t p = copies > kSlots ? copies - kSlots : 0; p < copies; ++p)
-        settle_for(&sh->full[p % kSlots], static_cast<uint32_t>((p / kSlots) & 1));
+      for (int64_t p = copies > slots ? copies - slots : 0; p < copies; ++p)
+        settle_for(&full[p % slots], static_cast<uint32_t>((p / slots) & 1));
       if (items > 0) settle_for(&sh->q_full, (items - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
-    const uint32_t q_at = smem_addr(smem), do_at = q_at + kTile, ring_at = smem_addr(ring);
+    const uint32_t q_at = smem_addr(smem), do_at = q_at + kTile, k_at = smem_addr(kt), v_at = smem_addr(vt);
     Ring rk, rv;  // K(j), V(j)
-    rv.next(kSlots);
     uint32_t items = 0, turn = 0;
     bool ok = true;
     auto scores = [&](uint32_t n, const Ring& k, const Ring& v, bool last) {  // S and dP of the CTA's n-th tile
       if (elect()) {
-        mma_scores<D>(t_s, q_at, ring_at + k.slot * kTile);
+        mma_scores<D>(t_s, q_at, k_at + k.slot * kTile);
         mma_commit(&sh->s_full);
-        mma_scores<D>(t_dp + 128 * (n & 1), do_at, ring_at + v.slot * kTile);
+        mma_scores<D>(t_dp + 128 * (n & 1), do_at, v_at + v.slot * kTile);
         mma_commit(&sh->dp_full[n & 1]);
-        mma_commit(&sh->empty[v.slot]);
+        mma_commit(&sh->v_empty[v.slot]);
         if (last) mma_commit(&sh->q_empty);
       }
     };
@@ -579,8 +604,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         uint64_t* bar = &sh->q_full;
         uint32_t par = items;
-        if (lane == 1) bar = &sh->full[rk.slot], par = rk.turn;
-        if (lane == 2) bar = &sh->full[rv.slot], par = rv.turn;
+        if (lane == 1) bar = &sh->k_full[rk.slot], par = rk.turn;
+        if (lane == 2) bar = &sh->v_full[rv.slot], par = rv.turn;
         ok = wait_all(ab, bar, par & 1, a.status);
       }
       if (!ok) break;
@@ -588,15 +613,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       scores(turn, rk, rv, it.m == 0);
       for (int j = 0; j <= it.m; ++j) {
         const bool more = j < it.m;
-        Ring nk = rv, nv;
-        nk.next(kSlots);
-        nv = nk;
-        nv.next(kSlots);
+        Ring nk = rk, nv = rv;
+        nk.next(C::kK);
+        nv.next(C::kV);
         {  // S(j) is read; the next K and V
           uint64_t* bar = &sh->s_read;
           uint32_t par = turn;
-          if (lane == 1 && more) bar = &sh->full[nk.slot], par = nk.turn;
-          if (lane == 2 && more) bar = &sh->full[nv.slot], par = nv.turn;
+          if (lane == 1 && more) bar = &sh->k_full[nk.slot], par = nk.turn;
+          if (lane == 2 && more) bar = &sh->v_full[nv.slot], par = nv.turn;
           ok = wait_all(ab, bar, par & 1, a.status);
         }
         if (!ok) break;
@@ -612,8 +636,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         fence_after_sync();
         if (elect()) {
-          mma_rows<D>(t_dq, t_ds, ring_at + rk.slot * kTile, j > 0);
-          mma_commit(&sh->empty[rk.slot]);
+          mma_rows<D>(t_dq, t_ds, k_at + rk.slot * kTile, j > 0);
+          mma_commit(&sh->k_empty[rk.slot]);
           if (!more) mma_commit(&sh->done);
         }
         rk = nk;
@@ -628,13 +652,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wg = (warp - kMathWarp) >> 2, row = tid & 127;
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;
     const uint32_t my_s = t_s + lane_base + 64 * wg;
+    const uint64_t sc2 = twice2(sc);
     uint32_t turn = 0, items = 0;
-    int64_t pos = 0;  // ring position of the item's K(0)
+    Ring rk;
     for (int64_t i = 0; item_at(a, tiles, i, it); ++i, ++items) {
       const int at = it.m * kRows + row;
       const bool used = at < it.L;
       const int64_t stat = static_cast<int64_t>(it.head) * a.S + it.lo + at;
-      const float lse = used ? a.lse[stat] * 1.4426950408889634f : 0.f, delta = used ? a.delta[stat] : 0.f;
+      const uint64_t lse2 = twice2(used ? a.lse[stat] * -1.4426950408889634f : 0.f), delta2 = twice2(used ? -a.delta[stat] : 0.f);
       for (int j = 0; j <= it.m; ++j, ++turn) {
         const uint32_t my_dp = t_dp + 128 * (turn & 1) + lane_base + 64 * wg;
         const bool diagonal = j == it.m;
@@ -648,53 +673,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         wait_all(ab, &sh->s_full, turn & 1, a.status);
         fence_after_sync();
-        float p[64];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t x[32];
-          tmem_ask(my_s + 32 * c, x);
-          tmem_got(x);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) p[32 * c + e] = ex2(fmaf(__uint_as_float(x[e]), sc, -lse));
-          if (diagonal) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(see[c] >> e & 1)) p[32 * c + e] = 0.f;
-          }
-        }
+        uint32_t p[2][32], x[2][32];
+        load64(my_s, p);
         fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->s_read);
+        if (lane == 0) mbar_arrive(&sh->s_read);  // the next scores may come: P stays in registers
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) ex2_pair(fma2(pack2(p[c][e], p[c][e + 1]), sc2, lse2), p[c][e], p[c][e + 1]);
+        if (diagonal) hide(p, see);
         if (diagonal && it.L - j * kRows < kRows) {  // rows of K past the sequence to zero: S has read them
-          if (wg == 0 && at >= it.L) zero_row<D>(ring + (pos + 2 * j) % kSlots * kTile, row);
+          if (wg == 0 && at >= it.L) zero_row<D>(kt + rk.slot * kTile, row);
           fence_async_smem();
         }
         wait_all(ab, &sh->dp_full[turn & 1], turn >> 1 & 1, a.status);
         fence_after_sync();
+        load64(my_dp, x);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t x[32];
-          tmem_ask(my_dp + 32 * c, x);
-          tmem_got(x);
-          float g[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) g[e] = p[32 * c + e] * (__uint_as_float(x[e]) - delta);
-          if (diagonal) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(see[c] >> e & 1)) g[e] = 0.f;
+          for (int e = 0; e < 32; e += 2) {
+            const float2 g = unpack2(mul2(pack2(p[c][e], p[c][e + 1]), add2(pack2(x[c][e], x[c][e + 1]), delta2)));
+            x[c][e] = __float_as_uint(g.x);
+            x[c][e + 1] = __float_as_uint(g.y);
           }
-          uint32_t y[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = pack_bf16(g[2 * e], g[2 * e + 1]);
-          tmem_st(my_dp + 16 * c, y);
+          if (c == 0 && !diagonal) store_bf16(my_dp, x[0]);
         }
+        if (diagonal) {
+          hide(x, see);
+          store_bf16(my_dp, x[0]);
+        }
+        store_bf16(my_dp + 16, x[1]);
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->ds_ready[turn & 1]);
+        rk.next(C::kK);
       }
-      pos += 2 * (it.m + 1);
       const bool fine = wait_all(ab, &sh->done, items & 1, a.status);
       fence_after_sync();
       __nv_bfloat16* const out = a.dq + (static_cast<int64_t>(it.lo + at) * a.Hq + it.head) * D + wg * (D / 2);
