@@ -6,17 +6,17 @@
 // Two launches over all tensors, however many: the tensors' addresses and
 // sizes are parameters of the launch (up to 1000 of them; above that, one
 // launch for every 1000), so there is no table to copy first and a captured
-// graph holds its own. The tensors are cut into chunks of 8192 elements, and
-// each CTA takes every grid-th chunk: the sum of squares of each CTA's chunks
+// graph holds its own. The tensors are cut into chunks of 16 KB, and each CTA
+// takes every grid-th chunk: the sum of squares of each CTA's chunks
 // goes to the workspace in fp64. The second launch's CTAs each add those sums
 // up, in the same order, and scale their chunks, last ones first, while part
 // of what was read last is still in L2.
 //
-// Range. 32 elements of a thread are squared and summed in fp32 where the
-// largest of them is between 2^-40 and 2^40 (their sum then neither overflows
-// nor loses what matters beside the largest), else in fp64; sums above 32
-// elements are fp64. One fp64 addition for 32 elements is a sixth of what the
-// SM's slow fp64 unit could do in the time that memory takes.
+// Range. A thread's 32 elements of a chunk (16 in fp32) are squared and summed in
+// fp32, and where that sum is outside 2^-70 .. 2^100 again in fp64: inside, it has
+// neither overflowed nor lost what matters beside its largest square. Sums above
+// that are fp64: one addition for 32 elements is a sixth of what the SM's slow
+// fp64 unit could do in the time that memory takes.
 //
 // Bound: HBM. The gradients are read twice where they do not fit L2.
 #include <math.h>
@@ -29,7 +29,10 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 32 * kThreads;  // elements
+constexpr int kChunkBytes = 64 * kThreads;  // of a gradient: four 16-byte vectors a thread
+constexpr int kCtasPerSm = 6;         // of the pass that only reads
+constexpr int kScaleCtas = 3;         // of the one that writes: 948 us of both for 0.74e9 elements, bf16 into fp32; two 915, but
+                                      // fp32 in place 1482 (three 1322), six 1103 and 1374
 constexpr int kMaxCtas = 1024;
 constexpr int kTable = 1000;           // tensors of a launch
 
@@ -66,60 +69,55 @@ __device__ __forceinline__ int tensor_of(const Table<N>& tb, int chunk) {
   return lo;
 }
 
-__device__ __forceinline__ void widen(uint4 u, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Vector i (16 bytes) of a tensor, zeros past its end.
+__device__ __forceinline__ uint4 load16(const Tensor& t, int64_t i, bool aligned) {
+  const int per = t.bf16_in ? 8 : 4;
+  const int64_t at = i * per;
+  if (aligned && at + per <= t.n) return reinterpret_cast<const uint4*>(t.g)[i];
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  for (int e = 0; e < 8; ++e) {
+    if (e >= per || at + e >= t.n) continue;
+    if (t.bf16_in)
+      w[e / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(t.g)[at + e]) << (16 * (e & 1));
+    else
+      w[e & 3] = static_cast<const uint32_t*>(t.g)[at + e];
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// Elements [at, at + 8) of a tensor, zeros past its end; `whole`: all eight are there and aligned.
-__device__ __forceinline__ void load8(const Tensor& t, int64_t at, bool whole, float (&x)[8]) {
-  if (t.bf16_in) {
-    const __nv_bfloat16* const p = static_cast<const __nv_bfloat16*>(t.g) + at;
-    if (whole) {
-      widen(*reinterpret_cast<const uint4*>(p), x);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = at + i < t.n ? ldf(p + i) : 0.f;
-    }
-  } else {
-    const float* const p = static_cast<const float*>(t.g) + at;
-    if (whole) {
-      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-      x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = at + i < t.n ? p[i] : 0.f;
-    }
-  }
-}
-__device__ __forceinline__ void store8(const Tensor& t, int64_t at, bool whole, const float (&x)[8]) {
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Eight (four) values to elements at .. of the output.
+template <int N>
+__device__ __forceinline__ void store(const Tensor& t, int64_t at, bool aligned, const float (&x)[N]) {
+  const bool whole = aligned && at + N <= t.n;
   if (t.bf16_out) {
     __nv_bfloat16* const p = static_cast<__nv_bfloat16*>(t.out) + at;
     if (whole) {
-      uint32_t w[4];
+      uint32_t w[N / 2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < N / 2; ++i) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t*>(&b);
       }
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (N == 8)
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2 % (N / 2)], w[3 % (N / 2)]);
+      else
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < N; ++i)
         if (at + i < t.n) stf(p + i, x[i]);
     }
   } else {
     float* const p = static_cast<float*>(t.out) + at;
     if (whole) {
-      *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+      for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < N; ++i)
         if (at + i < t.n) p[i] = x[i];
     }
   }
@@ -137,36 +135,48 @@ __device__ __forceinline__ double cta_sum(double x, double* s) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) kda_squares_kernel(const __grid_constant__ Table<N> tb, double* sums) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) kda_squares_kernel(const __grid_constant__ Table<N> tb, double* sums) {
   __shared__ double s[kThreads / 32];
   const int tid = static_cast<int>(threadIdx.x);
   double all = 0;
   for (int chunk = static_cast<int>(blockIdx.x); chunk < tb.first[tb.num]; chunk += static_cast<int>(gridDim.x)) {
     const int i = tensor_of(tb, chunk);
     const Tensor t = tb.t[i].get();
-    const int64_t at0 = static_cast<int64_t>(chunk - tb.first[i]) * kChunk + tid * 8;
+    const int64_t at = static_cast<int64_t>(chunk - tb.first[i]) * (4 * kThreads) + tid;
     const bool aligned = (reinterpret_cast<uintptr_t>(t.g) & 15) == 0;
-    float x[4][8];
+    uint4 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = load16(t, at + j * kThreads, aligned);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t any = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int64_t at = at0 + j * (8 * kThreads);
-      load8(t, at, aligned && at + 8 <= t.n, x[j]);
-    }
-    float top = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        top = fmaxf(top, fabsf(x[j][c]));
-        sum[c & 3] = fmaf(x[j][c], x[j][c], sum[c & 3]);
+      for (int e = 0; e < 4; ++e) {
+        any |= w[e];
+        if (t.bf16_in) {
+          sum[e] = fmaf(low(w[e]), low(w[e]), sum[e]);
+          sum[e] = fmaf(high(w[e]), high(w[e]), sum[e]);
+        } else {
+          sum[e] = fmaf(__uint_as_float(w[e]), __uint_as_float(w[e]), sum[e]);
+        }
       }
-    if (top == 0.f || (top > 0x1p-40f && top < 0x1p40f)) {  // a NaN is in the sum
-      all += static_cast<double>((sum[0] + sum[1]) + (sum[2] + sum[3]));
-    } else {
+    }
+    const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    if (total > 0x1p-70f && total < 0x1p100f) {
+      all += static_cast<double>(total);
+    } else if (any & 0x7fff7fffu) {  // out of fp32's range, or not finite; zeros of either sign add nothing
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        const uint4 y = j == 0 ? x[0] : j == 1 ? x[1] : j == 2 ? x[2] : x[3];
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int c = 0; c < 8; ++c) all = fma(static_cast<double>(x[j][c]), static_cast<double>(x[j][c]), all);
+        for (int e = 0; e < 4; ++e) {
+          const double u = t.bf16_in ? low(w[e]) : __uint_as_float(w[e]), v = t.bf16_in ? high(w[e]) : 0.f;
+          all = fma(u, u, fma(v, v, all));
+        }
+      }
     }
   }
   all = cta_sum(all, s);
@@ -190,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) kda_norm_of_sums_kernel(const double
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) kda_scale_kernel(const __grid_constant__ Table<N> tb, const double* sums, int num,
+__global__ void __launch_bounds__(kThreads, kScaleCtas) kda_scale_kernel(const __grid_constant__ Table<N> tb, const double* sums, int num,
                                                              double most, float* norm) {
   __shared__ double s[kThreads / 32];
   const int tid = static_cast<int>(threadIdx.x);
@@ -208,26 +218,48 @@ __global__ void __launch_bounds__(kThreads) kda_scale_kernel(const __grid_consta
     const int i = tensor_of(tb, chunk);
     const Tensor t = tb.t[i].get();
     if (!clip && t.out == t.g) continue;
-    const int64_t at0 = static_cast<int64_t>(chunk - tb.first[i]) * kChunk + tid * 8;
+    const int64_t at = static_cast<int64_t>(chunk - tb.first[i]) * (4 * kThreads);  // 16-byte vectors of the gradient
     const bool aligned = ((reinterpret_cast<uintptr_t>(t.g) | reinterpret_cast<uintptr_t>(t.out)) & 15) == 0;
-    float x[4][8];
+    if (t.bf16_in && !t.bf16_out && aligned && (at + 4 * kThreads) * 8 <= t.n) {
+      // bf16 into fp32: four elements at a time, so that a warp's stores are whole lines
+      uint2 x[8];
+      const uint2* const src = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(t.g) + at * 8) + tid;
+      float4* const dst = reinterpret_cast<float4*>(static_cast<float*>(t.out) + at * 8) + tid;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t at = at0 + j * (8 * kThreads);
-      load8(t, at, aligned && at + 8 <= t.n, x[j]);
+      for (int j = 0; j < 8; ++j) x[j] = src[j * kThreads];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        dst[j * kThreads] = make_float4(low(x[j].x) * f1 * f2, high(x[j].x) * f1 * f2, low(x[j].y) * f1 * f2,
+                                        high(x[j].y) * f1 * f2);
+      continue;
     }
+    uint4 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = load16(t, at + tid + j * kThreads, aligned);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+      const int64_t to = at + tid + j * kThreads;
+      if (t.bf16_in) {
+        float y[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[j][e] = x[j][e] * f1 * f2;
-      const int64_t at = at0 + j * (8 * kThreads);
-      store8(t, at, aligned && at + 8 <= t.n, x[j]);
+        for (int e = 0; e < 4; ++e) {
+          y[2 * e] = low(w[e]) * f1 * f2;
+          y[2 * e + 1] = high(w[e]) * f1 * f2;
+        }
+        store(t, to * 8, aligned, y);
+      } else {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = __uint_as_float(w[e]) * f1 * f2;
+        store(t, to * 4, aligned, y);
+      }
     }
   }
 }
 
-int grid_of(int64_t chunks, int64_t sms) {
-  const int64_t most = sms * 4 < kMaxCtas ? sms * 4 : kMaxCtas;
+int grid_of(int64_t chunks, int64_t sms, int per_sm) {
+  const int64_t most = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
   return static_cast<int>(chunks < 1 ? 1 : chunks < most ? chunks : most);
 }
 
@@ -242,7 +274,8 @@ void fill(Table<N>& tb, int i0, int num, const void* const* g, const int64_t* si
     const uint64_t in = dtypes[j] == KDA_DTYPE_BF16, out = outs && out_dtypes[j] == KDA_DTYPE_BF16;
     tb.t[i] = {g[j], outs ? outs[j] : nullptr, 4 * static_cast<uint64_t>(sizes[j]) + 2 * out + in};
     tb.first[i] = static_cast<int32_t>(chunks);
-    chunks += (sizes[j] + kChunk - 1) / kChunk;
+    const int64_t per = kChunkBytes / (in ? 2 : 4);
+    chunks += (sizes[j] + per - 1) / per;
   }
   tb.first[num] = static_cast<int32_t>(chunks);
 }
@@ -268,7 +301,7 @@ kda_status run(const Call& c) {
   int sums = 0;
   for (int i0 = 0; i0 == 0 || i0 < c.num; i0 += N) {
     fill(tb, i0, c.num - i0 < N ? c.num - i0 : N, c.g, c.sizes, c.dtypes, nullptr, nullptr);
-    const int grid = grid_of(tb.first[tb.num], c.sms);
+    const int grid = grid_of(tb.first[tb.num], c.sms, kCtasPerSm);
     kda_squares_kernel<N><<<grid, kThreads, 0, c.s>>>(tb, c.sums + sums);
     sums += grid;
   }
@@ -277,7 +310,7 @@ kda_status run(const Call& c) {
   } else {
     for (int i0 = c.num <= N ? 0 : (c.num - 1) / N * N; i0 >= 0; i0 -= N) {  // last ones first
       fill(tb, i0, c.num - i0 < N ? c.num - i0 : N, c.g, c.sizes, c.dtypes, c.outs, c.out_dtypes);
-      kda_scale_kernel<N><<<grid_of(tb.first[tb.num], c.sms), kThreads, 0, c.s>>>(tb, c.sums, sums, c.most,
+      kda_scale_kernel<N><<<grid_of(tb.first[tb.num], c.sms, kScaleCtas), kThreads, 0, c.s>>>(tb, c.sums, sums, c.most,
                                                                                   i0 == 0 ? c.norm : nullptr);
     }
   }

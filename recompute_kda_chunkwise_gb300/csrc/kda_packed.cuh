@@ -19,7 +19,8 @@ struct PackedArgs {
   int N, Hq, Hkv, D;
   float scale;
   __nv_bfloat16 *o, *dq, *dk, *dv;   // contiguous
-  const __nv_bfloat16 *o_in, *d_o;
+  const __nv_bfloat16 *q, *o_in, *d_o;
+  int64_t qs;          // elements from a token of q to the next
   float* lse;          // [Hq][S]
   float* delta;        // [Hq][S]
   float* part;         // gradients of k and v by parts of the head group: [2][split][S][Hkv][D]
@@ -111,6 +112,38 @@ template <int D>
 __device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* map, int head, int tok, uint64_t* bar) {
 #pragma unroll
   for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * 16384, map, c * 64, head, tok, bar);
+}
+
+// Matrix descriptors of such tiles, in two words: the lower is an address plus
+// constants that never carry, so that a step costs the issuing thread one
+// addition. (It shares its scheduler with two warps of arithmetic: descriptors
+// formed anew for each product took it longer than the product.)
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(const void* tile) { return (smem_addr(tile) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(const void* tile) { return (smem_addr(tile) >> 4) | ((128u * 128u >> 4) << 16); }
+__device__ __forceinline__ uint64_t desc_at(uint32_t lo, uint32_t bytes) { return pack2(lo + (bytes >> 4), kDescHi); }
+__host__ __device__ constexpr uint32_t k_step(int k) { return (k >> 2) * 128 * 128 + (k & 3) * 32; }
+constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // of an instruction: bf16 A and B
+
+// D = A B^T: A 128 rows of D in shared memory, or (_ta) as bf16 in TMEM, B 128
+// rows of D in shared memory (desc_k).
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) mma(d, desc_at(a, k_step(k)), desc_at(b, k_step(k)), idesc(128, 128) | kBf16, k > 0);
+}
+template <int D>
+__device__ __forceinline__ void mma_scores_ta(uint32_t d, uint32_t a, uint32_t b) {
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) mma_ta(d, a + 8 * k, desc_at(b, k_step(k)), idesc(128, 128) | kBf16, k > 0);
+}
+// D (+)= A B: A 128 columns of bf16 in TMEM, the second half of them `second`
+// columns behind the first, B 128 rows of D in shared memory (desc_mn).
+template <int D, int second>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    mma_ta(d, a + second * (k >> 2) + 8 * (k & 3), desc_at(b, k * 2048), idesc(128, D, false, true) | kBf16, k > 0 ? 1u : acc);
 }
 
 // Zeros in the rows of such a tile from `from` on, by threads 0 .. 127 of `row`.

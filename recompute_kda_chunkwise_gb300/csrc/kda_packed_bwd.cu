@@ -35,24 +35,6 @@ constexpr int kRows = 128;
 constexpr int kMathWarps = 8;               // two warpgroups, each half of a tile's columns
 constexpr int kMmaWarp = 0, kLoadWarp = 1, kMathWarp = 4;
 constexpr int kThreads = 32 * (kMathWarp + kMathWarps);
-constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);
-
-// D (+)= A B, A: bf16 in TMEM at `a`, its columns 0 .. 63 there and 64 .. 127
-// at a + 64 (each warpgroup's half over its own scores), B: 128 rows of D in shared memory.
-template <int D>
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t tile, uint32_t acc) {
-  constexpr uint32_t id = idesc(kRows, D, false, true) | kBf16;
-#pragma unroll
-  for (int k = 0; k < kRows / 16; ++k)
-    mma_ta(d, a + 64 * (k >> 2) + 8 * (k & 3), desc_mnmajor(tile, kRows * 128, k), id, k > 0 ? 1u : acc);
-}
-// D = A B^T, both 128 rows of D in shared memory.
-template <int D>
-__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
-  constexpr uint32_t id = idesc(kRows, kRows) | kBf16;
-#pragma unroll
-  for (int k = 0; k < D / 16; ++k) mma(d, desc_kmajor(a, kRows, 0, k), desc_kmajor(b, kRows, 0, k), id, k > 0);
-}
 
 // 64 consecutive columns of the thread's TMEM lane.
 __device__ __forceinline__ void load64(uint32_t at, uint32_t (&x)[2][32]) {
@@ -238,7 +220,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (items > 0) settle_for(&sh->kv_full, (items - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
-    const uint32_t k_at = smem_addr(kt), v_at = smem_addr(vt), q_at = smem_addr(qt), do_at = smem_addr(dot);
+    const uint32_t k_at = desc_k(kt), v_at = desc_k(vt), q_at = desc_k(qt), do_at = desc_k(dot);
+    const uint32_t q_mn = desc_mn(qt), do_mn = desc_mn(dot);
+    constexpr uint32_t kStep = kTile >> 4;  // from a slot's descriptor to the next
     Ring rq, rd;  // of step t
     uint32_t items = 0, turn = 0;
     bool ok = true;
@@ -255,9 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       fence_after_sync();
       if (elect()) {
-        mma_scores<D>(t_s, k_at, q_at + rq.slot * kTile);
+        mma_scores<D>(t_s, k_at, q_at + rq.slot * kStep);
         mma_commit(&sh->s_full);
-        mma_scores<D>(t_dp, v_at, do_at + rd.slot * kTile);
+        mma_scores<D>(t_dp, v_at, do_at + rd.slot * kStep);
         mma_commit(&sh->dp_full);
         if (steps == 1) mma_commit(&sh->kv_empty);
       }
@@ -276,10 +260,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         fence_after_sync();
         if (elect()) {
-          mma_rows<D>(t_dv, t_s, do_at + rd.slot * kTile, t > 0);
+          mma_rows<D, 64>(t_dv, t_s, do_mn + rd.slot * kStep, t > 0);
           mma_commit(&sh->do_empty[rd.slot]);
           if (more) {
-            mma_scores<D>(t_s, k_at, q_at + nq.slot * kTile);
+            mma_scores<D>(t_s, k_at, q_at + nq.slot * kStep);
             mma_commit(&sh->s_full);
           }
         }
@@ -293,10 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         fence_after_sync();
         if (elect()) {
-          mma_rows<D>(t_dk, t_dp, q_at + rq.slot * kTile, t > 0);
+          mma_rows<D, 64>(t_dk, t_dp, q_mn + rq.slot * kStep, t > 0);
           mma_commit(&sh->q_empty[rq.slot]);
           if (more) {
-            mma_scores<D>(t_dp, v_at, do_at + nd.slot * kTile);
+            mma_scores<D>(t_dp, v_at, do_at + nd.slot * kStep);
             mma_commit(&sh->dp_full);
             if (t + 2 == steps) mma_commit(&sh->kv_empty);
           } else {
@@ -466,7 +450,7 @@ __global__ void __launch_bounds__(256) kda_packed_parts_kernel(const __grid_cons
   *reinterpret_cast<uint2*>((g ? a.dk : a.dv) + at) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
 }
 
-// ---- dq ----
+// ---- dq, and a better delta for the other pass ----
 template <int D>
 struct QCfg {
   static constexpr int kTile = kRows * D * 2;
@@ -474,6 +458,7 @@ struct QCfg {
   static constexpr int kBytes = (2 + kK + kV) * kTile;
 };
 struct QShared {
+  float sum[2][kRows];  // per row, of each warpgroup's half
   uint64_t k_full[5], k_empty[5], v_full[4], v_empty[4];
   uint64_t q_full, q_empty;
   // dP and dS by buffer: their next phases can be over before every role has seen the last ones
@@ -586,15 +571,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (items > 0) settle_for(&sh->q_full, (items - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
-    const uint32_t q_at = smem_addr(smem), do_at = q_at + kTile, k_at = smem_addr(kt), v_at = smem_addr(vt);
+    const uint32_t q_at = desc_k(smem), do_at = desc_k(smem + kTile), k_at = desc_k(kt), v_at = desc_k(vt), k_mn = desc_mn(kt);
+    constexpr uint32_t kStep = kTile >> 4;  // from a slot's descriptor to the next
     Ring rk, rv;  // K(j), V(j)
     uint32_t items = 0, turn = 0;
     bool ok = true;
     auto scores = [&](uint32_t n, const Ring& k, const Ring& v, bool last) {  // S and dP of the CTA's n-th tile
       if (elect()) {
-        mma_scores<D>(t_s, q_at, k_at + k.slot * kTile);
+        mma_scores<D>(t_s, q_at, k_at + k.slot * kStep);
         mma_commit(&sh->s_full);
-        mma_scores<D>(t_dp + 128 * (n & 1), do_at, v_at + v.slot * kTile);
+        mma_scores<D>(t_dp + 128 * (n & 1), do_at, v_at + v.slot * kStep);
         mma_commit(&sh->dp_full[n & 1]);
         mma_commit(&sh->v_empty[v.slot]);
         if (last) mma_commit(&sh->q_empty);
@@ -636,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         fence_after_sync();
         if (elect()) {
-          mma_rows<D>(t_dq, t_ds, k_at + rk.slot * kTile, j > 0);
+          mma_rows<D, 64>(t_dq, t_ds, k_mn + rk.slot * kStep, j > 0);
           mma_commit(&sh->k_empty[rk.slot]);
           if (!more) mma_commit(&sh->done);
         }
@@ -655,11 +641,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t sc2 = twice2(sc);
     uint32_t turn = 0, items = 0;
     Ring rk;
+    // a row's sum over both warpgroups' halves
+    auto both = [&](float x) {
+      sh->sum[wg][row] = x;
+      named_bar_sync(1, 32 * kMathWarps);
+      x = sh->sum[0][row] + sh->sum[1][row];
+      named_bar_sync(1, 32 * kMathWarps);
+      return x;
+    };
     for (int64_t i = 0; item_at(a, tiles, i, it); ++i, ++items) {
       const int at = it.m * kRows + row;
       const bool used = at < it.L;
       const int64_t stat = static_cast<int64_t>(it.head) * a.S + it.lo + at;
-      const uint64_t lse2 = twice2(used ? a.lse[stat] * -1.4426950408889634f : 0.f), delta2 = twice2(used ? -a.delta[stat] : 0.f);
+      const uint64_t lse2 = twice2(used ? a.lse[stat] * -1.4426950408889634f : 0.f);
+      float delta = used ? a.delta[stat] : 0.f;
+      // What a row's dS sums to, over all keys: zero but for the rounding of the o
+      // that delta was formed from.
+      uint64_t rest2[2] = {0, 0};
       for (int j = 0; j <= it.m; ++j, ++turn) {
         const uint32_t my_dp = t_dp + 128 * (turn & 1) + lane_base + 64 * wg;
         const bool diagonal = j == it.m;
@@ -690,6 +688,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_all(ab, &sh->dp_full[turn & 1], turn >> 1 & 1, a.status);
         fence_after_sync();
         load64(my_dp, x);
+        if (it.m == 0) {  // all keys in one tile: delta as the sum that it is, free of o's rounding
+          hide(x, see);
+          uint64_t sum = 0;
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) sum = fma2(pack2(p[c][e], p[c][e + 1]), pack2(x[c][e], x[c][e + 1]), sum);
+          const float2 s = unpack2(sum);
+          delta = both(s.x + s.y);
+        }
+        const uint64_t delta2 = twice2(-delta);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -705,11 +714,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           store_bf16(my_dp, x[0]);
         }
         store_bf16(my_dp + 16, x[1]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) rest2[c] = add2(rest2[c], pack2(x[c][e], x[c][e + 1]));
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->ds_ready[turn & 1]);
         rk.next(C::kK);
+      }
+      {
+        const float2 s = unpack2(add2(rest2[0], rest2[1]));
+        const float rest = both(s.x + s.y);
+        if (used && wg == 0) a.delta[stat] = delta + rest;
       }
       const bool fine = wait_all(ab, &sh->done, items & 1, a.status);
       fence_after_sync();
@@ -748,11 +766,10 @@ cudaError_t launch(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap&
   if (e != cudaSuccess) return e;
   if (sms > kPackedMaxCtas) sms = kPackedMaxCtas;
   const float sc = a.scale * 1.4426950408889634f;
-  const int64_t rows = a.S * a.Hq, tiles = a.S / kRows + a.N;
-  kda_packed_delta_kernel<D><<<static_cast<unsigned>((rows * 8 + 255) / 256), 256, 0, s>>>(a);
-  const int64_t kv = tiles * a.Hkv * a.split, nq = tiles * a.Hq;
-  kda_packed_dkv_kernel<D><<<static_cast<unsigned>(kv < sms ? kv : sms), kThreads, smem_kv, s>>>(a, q, k, v, d_o, sc);
+  const int64_t tiles = a.S / kRows + a.N, kv = tiles * a.Hkv * a.split, nq = tiles * a.Hq;
+  kda_packed_delta_kernel<D><<<static_cast<unsigned>((a.S * a.Hq * 8 + 255) / 256), 256, 0, s>>>(a);
   kda_packed_dq_kernel<D><<<static_cast<unsigned>(nq < sms ? nq : sms), kThreads, smem_q, s>>>(a, q, k, v, d_o, sc);
+  kda_packed_dkv_kernel<D><<<static_cast<unsigned>(kv < sms ? kv : sms), kThreads, smem_kv, s>>>(a, q, k, v, d_o, sc);
   if (a.split > 1) kda_packed_parts_kernel<<<static_cast<unsigned>((2 * a.S * a.Hkv * a.D / 4 + 255) / 256), 256, 0, s>>>(a);
   return cudaGetLastError();
 }

@@ -148,18 +148,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ---- products ----
-    constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);
-    constexpr uint32_t id_qk = idesc(kRows, kRows) | kBf16, id_pv = idesc(kRows, D, false, true) | kBf16;
-    const uint32_t q_at = smem_addr(smem), ring_at = smem_addr(ring);
+    const uint32_t q_at = desc_k(smem), k_at = desc_k(ring), v_at = desc_mn(ring);
+    constexpr uint32_t kStep = kTile >> 4;  // from a slot's descriptor to the next
     Ring rk;  // the ring's position of K(j); V(j) is the next one
     uint32_t items = 0, turn_p[2] = {0, 0}, used_o[2] = {0, 0};
     bool ok = true;
     auto qk = [&](int s, int slot) {
       if (elect()) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma(tmem_s + 128 * s, desc_kmajor(q_at + s * kTile, kRows, 0, k), desc_kmajor(ring_at + slot * kTile, kRows, 0, k),
-              id_qk, k > 0);
+        mma_scores<D>(tmem_s + 128 * s, q_at + s * kStep, k_at + slot * kStep);
         mma_commit(&sh->s_full[s]);
       }
     };
@@ -197,9 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_after_sync();
           const uint32_t ts = tmem_s + 128 * s, to = tmem_o + 128 * s;
           if (elect()) {
-#pragma unroll
-            for (int k = 0; k < kRows / 16; ++k)
-              mma_ta(to, ts + 8 * k, desc_mnmajor(ring_at + rv.slot * kTile, kRows * 128, k), id_pv, (j > 0 || k > 0) ? 1u : 0u);
+            mma_rows<D, 32>(to, ts, v_at + rv.slot * kStep, j > 0);
             if (j + 1 == it.n[s]) mma_commit(&sh->o_done[s]);
           }
           if (j + 1 < it.n[s]) qk(s, rk.slot);

@@ -10,14 +10,22 @@
 // nearest quarter turn, whose rest is exact in fp32 to 2^-34 of a turn.
 //
 // Bound: HBM, each element read and written once. 72 heads of 128 of 8192
-// tokens, bf16: 151 MB each way.
+// tokens in bf16 (151 MB each way), rotated and, for the gradient, rotated back:
+// 105 us, 86% of the measured copy rate; in fp32 40 heads, 6.0 TB/s. Interleaved
+// pairs, whose items are half as long: 54 us a pass, 84%. Pairs that no vector
+// divides (21 of 128 channels) go element by element: 160 us.
 //
 // Split. A CTA takes a tile of tokens with all their heads. A token's sines
 // and cosines are formed once, in shared memory, for all of its heads (each
 // costs some 40 instructions: formed anew for every head they would take as
 // long as the memory). Its threads take 16-byte vectors, both ends of eight
-// (fp32: four) pairs each; the first loads are under way while the angles are
-// formed, which is what a call for one token waits for.
+// (fp32: four) pairs each; the first loads are under way while the tile's
+// positions are looked up and its angles formed, and each later one while the
+// vectors before it are worked on. bf16 is bound by instructions as much as by
+// memory: a thread keeps its place in the heads and its sines in registers, steps
+// through heads without a division, and works on words of two values (171 us
+// before). Five CTAs an SM hold that; pairs and single elements do better with
+// eight.
 #include <math.h>
 
 #include "kda_blocks.h"
@@ -28,9 +36,12 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTile = 32;          // tokens of a CTA, at most
+constexpr int kMaxTile = 32;          // tokens of a CTA, at most: one warp looks them up
+constexpr int64_t kMaxStride = 1 << 25;  // elements from a token to the next
+static_assert(kMaxStride * kMaxTile <= 1 << 30, "");
 constexpr int kTableBytes = 32768;    // sines and cosines of a tile
-constexpr int kBatch = 2;             // items of a thread whose loads are in flight together
+constexpr int kTileVectors = 2048;    // 16-byte vectors of a CTA, about
+constexpr int kMinCtas = 608;
 
 struct RotaryArgs {
   const void *q, *k, *v;   // v: paged form only
@@ -59,10 +70,33 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int N, int64_t t, 
   return base;
 }
 
-template <typename T>
-struct alignas(16) Vec {
-  T x[16 / sizeof(T)];
-};
+// A 16-byte vector's pairs, turned in words: two bf16 values or one fp32 value each.
+__device__ __forceinline__ uint32_t round2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ void turn_pair(float& a, float& b, float2 w) {
+  const float x = a;
+  a = fmaf(x, w.x, -b * w.y);
+  b = fmaf(x, w.y, b * w.x);
+}
+// a and b hold the first and second channels of the pairs of `w`.
+template <bool BF16>
+__device__ __forceinline__ void turn_halves(uint32_t& a, uint32_t& b, const float2* w) {
+  if (BF16) {
+    float a0 = __uint_as_float(a << 16), a1 = __uint_as_float(a & 0xffff0000u);
+    float b0 = __uint_as_float(b << 16), b1 = __uint_as_float(b & 0xffff0000u);
+    turn_pair(a0, b0, w[0]);
+    turn_pair(a1, b1, w[1]);
+    a = round2(a0, a1);
+    b = round2(b0, b1);
+  } else {
+    float x = __uint_as_float(a), y = __uint_as_float(b);
+    turn_pair(x, y, w[0]);
+    a = __float_as_uint(x);
+    b = __float_as_uint(y);
+  }
+}
 
 // How a head's channels are cut into items of work.
 enum Layout {
@@ -72,92 +106,181 @@ enum Layout {
 };
 
 template <typename T, int LAYOUT, bool PAGED>
-__global__ void __launch_bounds__(kThreads) kda_rotary_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(kThreads, LAYOUT == kHalf || sizeof(T) == 4 ? 5 : 8) kda_rotary_kernel(const RotaryArgs a) {
   constexpr int V = 16 / sizeof(T);
+  constexpr bool kBf16 = sizeof(T) == 2;
+  // Items of a thread that are loaded together, while as many more are worked on.
+  constexpr int kBatch = LAYOUT == kSingle ? 4 : 1;
   extern __shared__ float2 turn[];  // [tile][R / 2]: magnitude * (cos, sin)
   __shared__ int32_t s_pos[kMaxTile];
-  __shared__ int64_t s_row[kMaxTile];  // row of k_out (paged: of the pages); negative: the token is skipped
+  __shared__ int64_t s_row[kMaxTile];  // paged: elements before the token's row of the pages; negative: the token is skipped
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tile;
   const int nt = static_cast<int>(a.S - t0 < a.tile ? a.S - t0 : a.tile);
   const int half = a.R / 2;
   const int per_head = LAYOUT == kHalf ? half / V + (a.D - a.R) / V : LAYOUT == kPairs ? a.D / V : half + a.D - a.R;
-  const int turned = (a.Hq + a.Hk) * per_head;
-  const int per_token = turned + (PAGED ? a.Hk * (a.D / V) : 0);
-  const int total = nt * per_token;
+  const int turned = a.Hq + a.Hk, heads = turned + (PAGED ? a.Hk : 0);  // the paged form's values are copied beside them
 
-  struct Item {
-    const T* src;
-    T* dst;
-    int t, c;      // token of the tile; first pair of the item, -1: passes
-    int other;     // elements from an item's a to its b
+  // A thread keeps its place within the heads, and goes over the tokens' heads
+  // `slots` at a time; places past one for each thread (long heads that are cut
+  // into single elements) are taken in another round.
+  const int slots = per_head < kThreads ? kThreads / per_head : 1;
+  const int first = per_head < kThreads ? tid / per_head : 0;
+  const int step_t = slots / heads, step_h = slots % heads;
+  struct At {
+    int t, h;
   };
-  // `row`: whether destinations are wanted (they need s_row)
-  auto item_of = [&](int e, bool row) {
-    Item it;
-    it.t = e / per_token;
-    int r = e - it.t * per_token;
-    const int64_t tok = t0 + it.t;
-    it.other = half;
-    it.dst = nullptr;
-    if (PAGED && r >= turned) {  // a vector of values
-      r = (r - turned) * V;
-      it.src = static_cast<const T*>(a.v) + tok * a.vs + r;
-      if (row) it.dst = static_cast<T*>(a.vo) + s_row[it.t] * (static_cast<int64_t>(a.Hk) * a.D) + r;
-      it.c = -1;
-      return it;
+  auto advance = [&](At& x) {
+    x.t += step_t;
+    x.h += step_h;
+    if (x.h >= heads) {
+      x.h -= heads;
+      ++x.t;
     }
-    int head = r / per_head, c = r - head * per_head, off;
+  };
+  int c = per_head < kThreads ? tid - first * per_head : tid;
+  int off, pair;  // the place's first channel; its first pair, -1: it passes
+  auto place = [&]() {
     if (LAYOUT == kHalf) {
       const bool pass = c >= half / V;
       off = pass ? a.R + (c - half / V) * V : c * V;
-      it.c = pass ? -1 : off;
+      pair = pass ? -1 : off;
     } else if (LAYOUT == kPairs) {
       off = c * V;
-      it.c = off < a.R ? off / 2 : -1;
+      pair = off < a.R ? off / 2 : -1;
     } else {
       off = c < half ? c : half + c;
-      it.c = c < half ? c : -1;
+      pair = c < half ? c : -1;
     }
-    if (head < a.Hq) {
-      it.src = static_cast<const T*>(a.q) + tok * a.qs + head * a.D + off;
-      it.dst = static_cast<T*>(a.qo) + (tok * a.Hq + head) * a.D + off;
-    } else {
-      head -= a.Hq;
-      it.src = static_cast<const T*>(a.k) + tok * a.ks + head * a.D + off;
-      if (row) it.dst = static_cast<T*>(a.ko) + (s_row[it.t] * a.Hk + head) * a.D + off;
-    }
-    return it;
   };
-  Vec<T> va[kBatch], vb[kBatch];
-  auto load = [&](int base) {
+  // within a CTA's tile offsets fit 32 bits (kMaxStride)
+  const T* const q = static_cast<const T*>(a.q) + t0 * a.qs;
+  const T* const k = static_cast<const T*>(a.k) + t0 * a.ks;
+  const T* const v = static_cast<const T*>(a.v) + t0 * a.vs;
+  T* const qo = static_cast<T*>(a.qo) + t0 * a.Hq * a.D;
+  T* const ko = static_cast<T*>(a.ko) + (PAGED ? 0 : t0 * a.Hk * a.D);
+  T* const vo = static_cast<T*>(a.vo);
+  const int qs = static_cast<int>(a.qs), ks = static_cast<int>(a.ks), vs = static_cast<int>(a.vs);
+  auto source = [&](const At& x) {
+    if (x.h < a.Hq) return q + (x.t * qs + x.h * a.D + off);
+    if (!PAGED || x.h < turned) return k + (x.t * ks + (x.h - a.Hq) * a.D + off);
+    return v + (x.t * vs + (x.h - turned) * a.D + off);
+  };
+  auto target = [&](const At& x) {
+    if (x.h < a.Hq) return qo + ((x.t * a.Hq + x.h) * a.D + off);
+    const int h = x.h - (!PAGED || x.h < turned ? a.Hq : turned);
+    if (!PAGED) return ko + ((x.t * a.Hk + h) * a.D + off);
+    return (x.h < turned ? ko : vo) + s_row[x.t] + (h * a.D + off);
+  };
+  struct Batch {
+    uint4 a[kBatch], b[kBatch];
+  };
+  auto load = [&](Batch& r, At& x) {  // from x on, which moves past them
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int e = base + u * kThreads;
-      if (e < total) {
-        const Item it = item_of(e, false);
-        if (LAYOUT == kSingle && !(PAGED && e % per_token >= turned)) {
-          va[u].x[0] = *it.src;
-          if (it.c >= 0) vb[u].x[0] = it.src[it.other];
+      if (x.t < nt) {
+        const T* const src = source(x);
+        if (LAYOUT == kSingle) {
+          r.a[u].x = kBf16 ? *reinterpret_cast<const uint16_t*>(src) : *reinterpret_cast<const uint32_t*>(src);
+          if (pair >= 0)
+            r.b[u].x = kBf16 ? *reinterpret_cast<const uint16_t*>(src + half) : *reinterpret_cast<const uint32_t*>(src + half);
         } else {
-          va[u] = *reinterpret_cast<const Vec<T>*>(it.src);
-          if (LAYOUT == kHalf && it.c >= 0) vb[u] = *reinterpret_cast<const Vec<T>*>(it.src + it.other);
+          r.a[u] = *reinterpret_cast<const uint4*>(src);
+          if (LAYOUT == kHalf && pair >= 0) r.b[u] = *reinterpret_cast<const uint4*>(src + half);
         }
       }
+      advance(x);
     }
   };
-  load(tid);
+  // Sines and cosines of this place's pairs for token `held`: read from shared
+  // memory once a token, since lanes 64 bytes apart fall on few banks.
+  constexpr int kPairsOf = LAYOUT == kHalf ? V : LAYOUT == kPairs ? V / 2 : 1;
+  float2 w[LAYOUT == kSingle ? 2 : kPairsOf] = {};
+  int held = -1;
+  auto finish = [&](Batch& r, At& x) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (x.t < nt && s_row[x.t] >= 0) {
+        T* const dst = target(x);
+        const bool turns = pair >= 0 && (!PAGED || x.h < turned);
+        if (turns && x.t != held) {
+          held = x.t;
+          const float2* const from = turn + x.t * half + pair;
+#pragma unroll
+          for (int j = 0; j < kPairsOf; ++j)
+            if (LAYOUT != kPairs || pair + j < half) w[j] = from[j];
+        }
+        if constexpr (LAYOUT == kSingle) {
+          if (turns) turn_halves<kBf16>(r.a[u].x, r.b[u].x, w);  // bf16: the upper halves are not used
+          if (kBf16) {
+            *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(r.a[u].x);
+            if (pair >= 0) *reinterpret_cast<uint16_t*>(dst + half) = static_cast<uint16_t>(r.b[u].x);
+          } else {
+            *reinterpret_cast<uint32_t*>(dst) = r.a[u].x;
+            if (pair >= 0) *reinterpret_cast<uint32_t*>(dst + half) = r.b[u].x;
+          }
+        } else if constexpr (LAYOUT == kHalf) {
+          constexpr int e = kBf16 ? 2 : 1;
+          if (turns) {
+            turn_halves<kBf16>(r.a[u].x, r.b[u].x, w);
+            turn_halves<kBf16>(r.a[u].y, r.b[u].y, w + e);
+            turn_halves<kBf16>(r.a[u].z, r.b[u].z, w + 2 * e);
+            turn_halves<kBf16>(r.a[u].w, r.b[u].w, w + 3 * e);
+          }
+          *reinterpret_cast<uint4*>(dst) = r.a[u];
+          if (pair >= 0) *reinterpret_cast<uint4*>(dst + half) = r.b[u];
+        } else {
+          if (turns) {
+            uint32_t* const words[4] = {&r.a[u].x, &r.a[u].y, &r.a[u].z, &r.a[u].w};
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+              if (pair + j >= half) continue;  // a vector may reach past the channels that turn
+              if (kBf16) {
+                float x0 = __uint_as_float(*words[j] << 16), x1 = __uint_as_float(*words[j] & 0xffff0000u);
+                turn_pair(x0, x1, w[j]);
+                *words[j] = round2(x0, x1);
+              } else {
+                float x0 = __uint_as_float(*words[(2 * j) & 3]), x1 = __uint_as_float(*words[(2 * j + 1) & 3]);
+                turn_pair(x0, x1, w[j]);
+                *words[(2 * j) & 3] = __float_as_uint(x0);
+                *words[(2 * j + 1) & 3] = __float_as_uint(x1);
+              }
+            }
+          }
+          *reinterpret_cast<uint4*>(dst) = r.a[u];
+        }
+      }
+      advance(x);
+    }
+  };
+  const At none{nt, 0};
+  const At begin = first < slots ? At{first / heads, first % heads} : none;
+  Batch even, odd;
+  At next = begin, done = begin;
+  place();
+  load(even, next);
 
-  for (int t = warp; t < nt; t += kThreads / 32) {
-    const int64_t tok = t0 + t;
-    int64_t row = tok;
+  if (warp == 0) {  // a lane for each token of the tile
+    const bool here = lane < nt;
+    const int64_t tok = t0 + lane;
+    int64_t row = 0;
     int pos = 0;
     if (!PAGED && a.positions) {
-      pos = a.positions[tok];
+      if (here) pos = a.positions[tok];
     } else {
-      const int n = sequence_of(a.cu, a.N, tok, lane);
+      // the first token's sequence, by the whole warp; tokens past its end look among those behind it
+      int n = sequence_of(a.cu, a.N, t0, lane);
+      if (here && n < a.N && a.cu[n + 1] <= tok) {
+        int lo = n + 1, hi = a.N;  // sequences lo .. end at or before tok, as far as it goes
+        while (lo < hi) {
+          const int mid = (lo + hi) / 2;
+          if (a.cu[mid + 1] <= tok) lo = mid + 1;
+          else hi = mid;
+        }
+        n = lo;
+      }
       // where cu_seqlens decreases, sequence n need not hold the token
-      bool ok = n < a.N && tok >= a.cu[n] && tok < a.cu[n + 1];
+      bool ok = here && n < a.N && tok >= a.cu[n] && tok < a.cu[n + 1];
       if (ok) {
         if (PAGED) {
           const int64_t p = static_cast<int64_t>(a.lens[n]) - (a.cu[n + 1] - tok);
@@ -165,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) kda_rotary_kernel(const RotaryArgs a
           if (ok) {
             const int64_t page = a.table[static_cast<int64_t>(n) * a.width + p / a.page];
             ok = page >= 0 && page < a.pages;
-            row = page * a.page + p % a.page;
+            row = (page * a.page + p % a.page) * a.Hk * a.D;
             pos = static_cast<int>(p);
           }
         } else {
@@ -174,13 +297,11 @@ __global__ void __launch_bounds__(kThreads) kda_rotary_kernel(const RotaryArgs a
       }
       if (!ok) {
         row = -1;
-        if (lane == 0) set_status(a.status, KDA_ERR_DEVICE_CHECK);
+        if (here) set_status(a.status, KDA_ERR_DEVICE_CHECK);
       }
     }
-    if (lane == 0) {
-      s_pos[t] = pos;
-      s_row[t] = row;
-    }
+    s_pos[lane] = pos;
+    s_row[lane] = row;
   }
   __syncthreads();
   for (int i = tid; i < nt * half; i += kThreads) {
@@ -192,60 +313,27 @@ __global__ void __launch_bounds__(kThreads) kda_rotary_kernel(const RotaryArgs a
     float sn, cs;
     sincospif(rest, &sn, &cs);
     const bool swap = quarter & 1;
-    float c = swap ? sn : cs, s = swap ? cs : sn;
-    if ((quarter + 1) & 2) c = -c;
-    if (quarter & 2) s = -s;
-    if (a.inverse) s = -s;
-    turn[i] = make_float2(a.mag * c, a.mag * s);
+    float x0 = swap ? sn : cs, x1 = swap ? cs : sn;
+    if ((quarter + 1) & 2) x0 = -x0;
+    if (quarter & 2) x1 = -x1;
+    if (a.inverse) x1 = -x1;
+    turn[i] = make_float2(a.mag * x0, a.mag * x1);
   }
   __syncthreads();
 
-  for (int base = tid; base < total; base += kBatch * kThreads) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int e = base + u * kThreads;
-      if (e >= total) continue;
-      const Item it = item_of(e, true);
-      if (s_row[it.t] < 0) continue;
-      const float2* const w = turn + it.t * half + it.c;
-      if (LAYOUT == kSingle) {
-        if (PAGED && e % per_token >= turned) {
-          *reinterpret_cast<Vec<T>*>(it.dst) = va[u];
-        } else if (it.c >= 0) {
-          const float x = ldf(&va[u].x[0]), y = ldf(&vb[u].x[0]);
-          const float2 r = *w;
-          stf(it.dst, fmaf(x, r.x, -y * r.y));
-          stf(it.dst + it.other, fmaf(x, r.y, y * r.x));
-        } else {
-          *it.dst = va[u].x[0];
-        }
-        continue;
-      }
-      if (it.c >= 0) {
-        if (LAYOUT == kHalf) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float x = ldf(&va[u].x[j]), y = ldf(&vb[u].x[j]);
-            const float2 r = w[j];
-            stf(&va[u].x[j], fmaf(x, r.x, -y * r.y));
-            stf(&vb[u].x[j], fmaf(x, r.y, y * r.x));
-          }
-          *reinterpret_cast<Vec<T>*>(it.dst + it.other) = vb[u];
-        } else {
-#pragma unroll
-          for (int j = 0; j < V; j += 2) {
-            if (it.c + j / 2 < half) {  // a vector may reach past the channels that turn
-              const float x = ldf(&va[u].x[j]), y = ldf(&va[u].x[j + 1]);
-              const float2 r = w[j / 2];
-              stf(&va[u].x[j], fmaf(x, r.x, -y * r.y));
-              stf(&va[u].x[j + 1], fmaf(x, r.y, y * r.x));
-            }
-          }
-        }
-      }
-      *reinterpret_cast<Vec<T>*>(it.dst) = va[u];
+  for (;;) {
+    while (done.t < nt) {
+      load(odd, next);
+      finish(even, done);
+      load(even, next);
+      finish(odd, done);
     }
-    load(base + kBatch * kThreads);
+    c += kThreads;
+    if (per_head < kThreads || c >= per_head) break;
+    place();
+    held = -1;
+    next = done = begin;
+    load(even, next);
   }
 }
 
@@ -253,11 +341,11 @@ template <typename T, bool PAGED>
 cudaError_t launch(RotaryArgs a, bool pairs, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const int layout = pairs ? kPairs : a.R / 2 % V == 0 ? kHalf : kSingle;
-  // Tokens of a CTA: enough for two rounds of its threads, but no fewer CTAs
-  // than two an SM; the table of a tile within its bytes.
-  const int64_t vectors = static_cast<int64_t>(a.Hq + a.Hk) * a.D / V;
-  int64_t tile = (2 * kBatch * kThreads + vectors - 1) / vectors;
-  if (tile > a.S / 304) tile = a.S / 304;
+  // Tokens of a CTA: enough for a few rounds of its threads, but no fewer CTAs
+  // than four an SM; the table of a tile within its bytes.
+  const int64_t vectors = static_cast<int64_t>(a.Hq + a.Hk * (PAGED ? 2 : 1)) * a.D / V;
+  int64_t tile = (kTileVectors + vectors - 1) / vectors;
+  if (tile > a.S / kMinCtas) tile = a.S / kMinCtas;
   if (tile > kTableBytes / (a.R / 2 * 8)) tile = kTableBytes / (a.R / 2 * 8);
   a.tile = static_cast<int>(tile < 1 ? 1 : tile > kMaxTile ? kMaxTile : tile);
   const unsigned grid = static_cast<unsigned>((a.S + a.tile - 1) / a.tile);
@@ -277,9 +365,9 @@ kda_status tensor(const char* name, const void* p, unsigned align = 15u) {
   return KDA_OK;
 }
 kda_status stride(const char* name, int64_t n, int64_t wide, int elt) {
-  if (n < wide || n * elt % 16 != 0 || n > ((int64_t)1 << 40))
-    return set_error(KDA_ERR_INVALID_ARG, "%s %lld must be at least %lld and a multiple of 16 bytes", name, (long long)n,
-                     (long long)wide);
+  if (n < wide || n * elt % 16 != 0 || n > kMaxStride)
+    return set_error(KDA_ERR_INVALID_ARG, "%s %lld must be at least %lld, at most %lld and a multiple of 16 bytes", name,
+                     (long long)n, (long long)wide, (long long)kMaxStride);
   return KDA_OK;
 }
 
