@@ -137,13 +137,15 @@ __device__ __forceinline__ void mma_scores_ta(uint32_t d, uint32_t a, uint32_t b
 #pragma unroll
   for (int k = 0; k < D / 16; ++k) mma_ta(d, a + 8 * k, desc_at(b, k_step(k)), idesc(128, 128) | kBf16, k > 0);
 }
-// D (+)= A B: A 128 columns of bf16 in TMEM, the second half of them `second`
-// columns behind the first, B 128 rows of D in shared memory (desc_mn).
-template <int D, int second>
+// D (+)= A B: A 128 columns of bf16 in TMEM, packed over the first half of each
+// run of `run` fp32 columns (128: all in one place), B 128 rows of D in shared
+// memory (desc_mn).
+template <int D, int run>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
+  constexpr int each = run / 16;  // steps of a run
 #pragma unroll
   for (int k = 0; k < 8; ++k)
-    mma_ta(d, a + second * (k >> 2) + 8 * (k & 3), desc_at(b, k * 2048), idesc(128, D, false, true) | kBf16, k > 0 ? 1u : acc);
+    mma_ta(d, a + run * (k / each) + 8 * (k % each), desc_at(b, k * 2048), idesc(128, D, false, true) | kBf16, k > 0 ? 1u : acc);
 }
 
 // Zeros in the rows of such a tile from `from` on, by threads 0 .. 127 of `row`.

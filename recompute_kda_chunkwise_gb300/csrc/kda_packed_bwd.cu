@@ -32,16 +32,18 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128;
-constexpr int kMathWarps = 8;               // two warpgroups, each half of a tile's columns
+constexpr int kGroups = 4, kMathWarps = 4 * kGroups;  // warpgroups, each a part of a tile's columns
+constexpr int kCols = kRows / kGroups, kParts = kCols / 32;
 constexpr int kMmaWarp = 0, kLoadWarp = 1, kMathWarp = 4;
 constexpr int kThreads = 32 * (kMathWarp + kMathWarps);
 
-// 64 consecutive columns of the thread's TMEM lane.
-__device__ __forceinline__ void load64(uint32_t at, uint32_t (&x)[2][32]) {
-  tmem_ask(at, x[0]);
-  tmem_ask(at + 32, x[1]);
-  tmem_got(x[0]);
-  tmem_got(x[1]);
+typedef uint32_t Scores[kParts][32];  // a thread's columns of a tile
+
+__device__ __forceinline__ void load_scores(uint32_t at, Scores& x) {
+#pragma unroll
+  for (int c = 0; c < kParts; ++c) tmem_ask(at + 32 * c, x[c]);
+#pragma unroll
+  for (int c = 0; c < kParts; ++c) tmem_got(x[c]);
 }
 // Exponentials (base 2) of a pair, in place.
 __device__ __forceinline__ void ex2_pair(uint64_t t, uint32_t& lo, uint32_t& hi) {
@@ -50,19 +52,43 @@ __device__ __forceinline__ void ex2_pair(uint64_t t, uint32_t& lo, uint32_t& hi)
   hi = __float_as_uint(ex2(e.y));
 }
 // Zero where a column is not seen.
-__device__ __forceinline__ void hide(uint32_t (&x)[2][32], const uint32_t (&see)[2]) {
+__device__ __forceinline__ void hide(Scores& x, const uint32_t (&see)[kParts]) {
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
+  for (int c = 0; c < kParts; ++c)
 #pragma unroll
     for (int e = 0; e < 32; ++e)
       if (!(see[c] >> e & 1)) x[c][e] = 0u;
 }
-// Rounded to bf16, two to a column, 16 columns for each 32.
-__device__ __forceinline__ void store_bf16(uint32_t at, const uint32_t (&x)[32]) {
-  uint32_t y[16];
+// Rounded to bf16, two to a column, over the first half of the columns.
+__device__ __forceinline__ void store_bf16(uint32_t at, const Scores& x) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) y[e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-  tmem_st(at, y);
+  for (int c = 0; c < kParts; ++c) {
+    uint32_t y[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[e] = pack_bf16(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1]));
+    tmem_st(at + 16 * c, y);
+  }
+}
+// `f` times a row's sums (n fp32 columns of TMEM) to fp32 or bf16 memory.
+template <int N, typename T>
+__device__ __forceinline__ void write_row(uint32_t at, float f, T* dst, bool used) {
+  constexpr int step = N < 32 ? N : 32;
+#pragma unroll 1
+  for (int c = 0; c < N; c += step) {
+    uint32_t x[step];
+    tmem_ask(at + c, x);
+    tmem_got(x);
+    if (!used) continue;
+#pragma unroll
+    for (int e = 0; e < step; e += 16 / sizeof(T)) {
+      auto v = [&](int k) { return __uint_as_float(x[e + k]) * f; };
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4*>(dst + c + e) = make_float4(v(0), v(1), v(2), v(3));
+      else
+        *reinterpret_cast<uint4*>(dst + c + e) =
+            make_uint4(pack_bf16(v(0), v(1)), pack_bf16(v(2), v(3)), pack_bf16(v(4), v(5)), pack_bf16(v(6), v(7)));
+    }
+  }
 }
 
 // ---- delta[h][s] = sum over channels of d_o o: eight lanes a row ----
@@ -260,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         fence_after_sync();
         if (elect()) {
-          mma_rows<D, 64>(t_dv, t_s, do_mn + rd.slot * kStep, t > 0);
+          mma_rows<D, kCols>(t_dv, t_s, do_mn + rd.slot * kStep, t > 0);
           mma_commit(&sh->do_empty[rd.slot]);
           if (more) {
             mma_scores<D>(t_s, k_at, q_at + nq.slot * kStep);
@@ -277,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         fence_after_sync();
         if (elect()) {
-          mma_rows<D, 64>(t_dk, t_dp, q_mn + rq.slot * kStep, t > 0);
+          mma_rows<D, kCols>(t_dk, t_dp, q_mn + rq.slot * kStep, t > 0);
           mma_commit(&sh->q_empty[rq.slot]);
           if (more) {
             mma_scores<D>(t_dp, v_at, do_at + nd.slot * kStep);
@@ -298,23 +324,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kMathWarp) {
     const int wg = (warp - kMathWarp) >> 2, row = tid & 127, mt = tid - 32 * kMathWarp;
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;
-    const uint32_t my_s = t_s + lane_base + 64 * wg, my_dp = t_dp + lane_base + 64 * wg;
+    const uint32_t my_s = t_s + lane_base + kCols * wg, my_dp = t_dp + lane_base + kCols * wg;
     const uint64_t sc2 = twice2(sc);
     uint32_t turn = 0, items = 0;
     Ring rq, rd;
     for (int64_t i = 0; item_at(a, tiles, i, it); ++i, ++items) {
       const int steps = it.steps();
+      const bool rows = mt < 2 * kRows;  // the first two warpgroups fetch lse and delta
       const float* const src = mt < kRows ? a.lse : a.delta;
       // lse or delta of query row mt % 128 of a step; 0 past the sequence
       auto fetch = [&](int h, int m) {
         const int at = m * kRows + row;
-        return at < it.L ? src[static_cast<int64_t>(it.head0 + h) * a.S + it.lo + at] : 0.f;
+        return rows && at < it.L ? src[static_cast<int64_t>(it.head0 + h) * a.S + it.lo + at] : 0.f;
       };
       float ahead = fetch(0, it.j);
       int h = 0, m = it.j;
       for (int t = 0; t < steps; ++t, ++turn) {
-        float* const mine = sh->row[turn & 1][mt < kRows ? 0 : 1];
-        mine[row] = mt < kRows ? ahead * -1.4426950408889634f : -ahead;
+        if (rows) sh->row[turn & 1][mt < kRows ? 0 : 1][row] = mt < kRows ? ahead * -1.4426950408889634f : -ahead;
         named_bar_sync(1, 32 * kMathWarps);
         const int past = it.L - m * kRows;       // query rows of the tile from here on are another sequence's
         const bool diagonal = m == it.j, tail = past < kRows;
@@ -323,14 +349,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++h;
         }
         if (t + 1 < steps) ahead = fetch(h, m);
-        const ulonglong2* const lse2 = reinterpret_cast<const ulonglong2*>(sh->row[turn & 1][0] + 64 * wg);
-        const ulonglong2* const del2 = reinterpret_cast<const ulonglong2*>(sh->row[turn & 1][1] + 64 * wg);
+        const ulonglong2* const lse2 = reinterpret_cast<const ulonglong2*>(sh->row[turn & 1][0] + kCols * wg);
+        const ulonglong2* const del2 = reinterpret_cast<const ulonglong2*>(sh->row[turn & 1][1] + kCols * wg);
         // columns (queries) that see this thread's key
-        uint32_t see[2] = {~0u, ~0u};
+        uint32_t see[kParts];
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) see[c] = ~0u;
         if (diagonal || tail) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int c0 = 64 * wg + 32 * c, lo = diagonal ? row - c0 : 0, hi = past - c0;
+          for (int c = 0; c < kParts; ++c) {
+            const int c0 = kCols * wg + 32 * c, lo = diagonal ? row - c0 : 0, hi = past - c0;
             see[c] = lo >= 32 ? 0u : lo > 0 ? ~0u << lo : ~0u;
             see[c] &= hi >= 32 ? ~0u : hi > 0 ? ~(~0u << hi) : 0u;
           }
@@ -339,36 +367,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_all(ab, &sh->s_full, turn & 1, a.status);
         if (tail) {  // those rows' Q and d_o to zero, once the scores' products have read them
           wait_all(ab, &sh->dp_full, turn & 1, a.status);
-          if (row >= past) zero_row<D>(mt < kRows ? qt + rq.slot * kTile : dot + rd.slot * kTile, row);
+          if (rows && row >= past) zero_row<D>(mt < kRows ? qt + rq.slot * kTile : dot + rd.slot * kTile, row);
           fence_async_smem();
         }
         fence_after_sync();
-        uint32_t p[2][32], x[2][32];
-        load64(my_s, p);
+        Scores p, x;
+        load_scores(my_s, p);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < kParts; ++c)
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const ulonglong2 l = lse2[(32 * c + e) / 4];
             ex2_pair(fma2(pack2(p[c][e], p[c][e + 1]), sc2, l.x), p[c][e], p[c][e + 1]);
             ex2_pair(fma2(pack2(p[c][e + 2], p[c][e + 3]), sc2, l.y), p[c][e + 2], p[c][e + 3]);
           }
-          if (c == 0 && all) store_bf16(my_s, p[0]);
-        }
-        if (!all) {
-          hide(p, see);
-          store_bf16(my_s, p[0]);
-        }
-        store_bf16(my_s + 16, p[1]);
+        if (!all) hide(p, see);
+        store_bf16(my_s, p);
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->p_ready);
         wait_all(ab, &sh->dp_full, turn & 1, a.status);
         fence_after_sync();
-        load64(my_dp, x);
+        load_scores(my_dp, x);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < kParts; ++c)
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const ulonglong2 d = del2[(32 * c + e) / 4];
@@ -379,13 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             x[c][e + 2] = __float_as_uint(h.x);
             x[c][e + 3] = __float_as_uint(h.y);
           }
-          if (c == 0 && all) store_bf16(my_dp, x[0]);
-        }
-        if (!all) {
-          hide(x, see);
-          store_bf16(my_dp, x[0]);
-        }
-        store_bf16(my_dp + 16, x[1]);
+        if (!all) hide(x, see);
+        store_bf16(my_dp, x);
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
@@ -395,36 +413,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool fine = wait_all(ab, &sh->done, items & 1, a.status);
       fence_after_sync();
-      // this warpgroup's half of the channels of dv and of dk
+      // this warpgroup's part of the channels of dv and of dk
+      constexpr int kCh = D / kGroups;
       const int at = it.j * kRows + row;
       const bool used = fine && at < it.L;
-      const int64_t dst = (static_cast<int64_t>(it.lo + at) * a.Hkv + it.hk) * D + wg * (D / 2);
-      const int64_t all_rows = a.S * a.Hkv * D;
-#pragma unroll 1
-      for (int g = 0; g < 2; ++g) {
-        const float f = g ? a.scale : 1.f;
-        const uint32_t acc = (g ? t_dk : t_dv) + lane_base + wg * (D / 2);
-#pragma unroll 1
-        for (int c = 0; c < D / 2; c += 32) {
-          uint32_t x[32];
-          tmem_ask(acc + c, x);
-          tmem_got(x);
-          if (!used) continue;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-          if (a.split > 1) {
-            float* const o = a.part + (g * a.split + it.part) * all_rows + dst + c;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(o + e) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-          } else {
-            __nv_bfloat16* const o = (g ? a.dk : a.dv) + dst + c;
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              auto two = [&](int k) { return pack_bf16(__uint_as_float(x[e + k]), __uint_as_float(x[e + k + 1])); };
-              *reinterpret_cast<uint4*>(o + e) = make_uint4(two(0), two(2), two(4), two(6));
-            }
-          }
-        }
+      const int64_t dst = (static_cast<int64_t>(it.lo + at) * a.Hkv + it.hk) * D + wg * kCh;
+      const uint32_t acc = lane_base + wg * kCh;
+      if (a.split > 1) {
+        const int64_t all_rows = a.S * a.Hkv * D;
+        write_row<kCh>(t_dv + acc, 1.f, a.part + it.part * all_rows + dst, used);
+        write_row<kCh>(t_dk + acc, a.scale, a.part + (a.split + it.part) * all_rows + dst, used);
+      } else {
+        write_row<kCh>(t_dv + acc, 1.f, a.dv + dst, used);
+        write_row<kCh>(t_dk + acc, a.scale, a.dk + dst, used);
       }
       fence_before_sync();
       __syncwarp();
@@ -458,7 +459,7 @@ struct QCfg {
   static constexpr int kBytes = (2 + kK + kV) * kTile;
 };
 struct QShared {
-  float sum[2][kRows];  // per row, of each warpgroup's half
+  float sum[kGroups][kRows];  // per row, of each warpgroup's columns
   uint64_t k_full[5], k_empty[5], v_full[4], v_empty[4];
   uint64_t q_full, q_empty;
   // dP and dS by buffer: their next phases can be over before every role has seen the last ones
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         fence_after_sync();
         if (elect()) {
-          mma_rows<D, 64>(t_dq, t_ds, k_mn + rk.slot * kStep, j > 0);
+          mma_rows<D, kCols>(t_dq, t_ds, k_mn + rk.slot * kStep, j > 0);
           mma_commit(&sh->k_empty[rk.slot]);
           if (!more) mma_commit(&sh->done);
         }
@@ -637,15 +638,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kMathWarp) {
     const int wg = (warp - kMathWarp) >> 2, row = tid & 127;
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;
-    const uint32_t my_s = t_s + lane_base + 64 * wg;
+    const uint32_t my_s = t_s + lane_base + kCols * wg;
     const uint64_t sc2 = twice2(sc);
     uint32_t turn = 0, items = 0;
     Ring rk;
-    // a row's sum over both warpgroups' halves
-    auto both = [&](float x) {
+    // a row's sum over all warpgroups' columns
+    auto together = [&](float x) {
       sh->sum[wg][row] = x;
       named_bar_sync(1, 32 * kMathWarps);
-      x = sh->sum[0][row] + sh->sum[1][row];
+      x = sh->sum[0][row];
+#pragma unroll
+      for (int i = 1; i < kGroups; ++i) x += sh->sum[i][row];
       named_bar_sync(1, 32 * kMathWarps);
       return x;
     };
@@ -659,25 +662,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       // that delta was formed from.
       uint64_t rest2[2] = {0, 0};
       for (int j = 0; j <= it.m; ++j, ++turn) {
-        const uint32_t my_dp = t_dp + 128 * (turn & 1) + lane_base + 64 * wg;
+        const uint32_t my_dp = t_dp + 128 * (turn & 1) + lane_base + kCols * wg;
         const bool diagonal = j == it.m;
-        uint32_t see[2] = {~0u, ~0u};  // keys that this thread's query sees
+        uint32_t see[kParts];  // keys that this thread's query sees
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) see[c] = ~0u;
         if (diagonal) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int hi = (used ? row + 1 : 0) - (64 * wg + 32 * c);
+          for (int c = 0; c < kParts; ++c) {
+            const int hi = (used ? row + 1 : 0) - (kCols * wg + 32 * c);
             see[c] = hi >= 32 ? ~0u : hi > 0 ? ~(~0u << hi) : 0u;
           }
         }
         wait_all(ab, &sh->s_full, turn & 1, a.status);
         fence_after_sync();
-        uint32_t p[2][32], x[2][32];
-        load64(my_s, p);
+        Scores p, x;
+        load_scores(my_s, p);
         fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->s_read);  // the next scores may come: P stays in registers
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < kParts; ++c)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) ex2_pair(fma2(pack2(p[c][e], p[c][e + 1]), sc2, lse2), p[c][e], p[c][e + 1]);
         if (diagonal) hide(p, see);
@@ -687,37 +692,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         wait_all(ab, &sh->dp_full[turn & 1], turn >> 1 & 1, a.status);
         fence_after_sync();
-        load64(my_dp, x);
+        load_scores(my_dp, x);
         if (it.m == 0) {  // all keys in one tile: delta as the sum that it is, free of o's rounding
           hide(x, see);
           uint64_t sum = 0;
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < kParts; ++c)
 #pragma unroll
             for (int e = 0; e < 32; e += 2) sum = fma2(pack2(p[c][e], p[c][e + 1]), pack2(x[c][e], x[c][e + 1]), sum);
           const float2 s = unpack2(sum);
-          delta = both(s.x + s.y);
+          delta = together(s.x + s.y);
         }
         const uint64_t delta2 = twice2(-delta);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < kParts; ++c) {
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const float2 g = unpack2(mul2(pack2(p[c][e], p[c][e + 1]), add2(pack2(x[c][e], x[c][e + 1]), delta2)));
             x[c][e] = __float_as_uint(g.x);
             x[c][e + 1] = __float_as_uint(g.y);
           }
-          if (c == 0 && !diagonal) store_bf16(my_dp, x[0]);
         }
-        if (diagonal) {
-          hide(x, see);
-          store_bf16(my_dp, x[0]);
-        }
-        store_bf16(my_dp + 16, x[1]);
+        if (diagonal) hide(x, see);
+        store_bf16(my_dp, x);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < kParts; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) rest2[c] = add2(rest2[c], pack2(x[c][e], x[c][e + 1]));
+          for (int e = 0; e < 32; e += 2) rest2[e / 2 & 1] = add2(rest2[e / 2 & 1], pack2(x[c][e], x[c][e + 1]));
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
@@ -726,26 +727,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       {
         const float2 s = unpack2(add2(rest2[0], rest2[1]));
-        const float rest = both(s.x + s.y);
+        const float rest = together(s.x + s.y);
         if (used && wg == 0) a.delta[stat] = delta + rest;
       }
       const bool fine = wait_all(ab, &sh->done, items & 1, a.status);
       fence_after_sync();
-      __nv_bfloat16* const out = a.dq + (static_cast<int64_t>(it.lo + at) * a.Hq + it.head) * D + wg * (D / 2);
-#pragma unroll 1
-      for (int c = 0; c < D / 2; c += 32) {
-        uint32_t x[32];
-        tmem_ask(t_dq + lane_base + wg * (D / 2) + c, x);
-        tmem_got(x);
-        if (!used || !fine) continue;
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          auto two = [&](int k) {
-            return pack_bf16(__uint_as_float(x[e + k]) * a.scale, __uint_as_float(x[e + k + 1]) * a.scale);
-          };
-          *reinterpret_cast<uint4*>(out + c + e) = make_uint4(two(0), two(2), two(4), two(6));
-        }
-      }
+      constexpr int kCh = D / kGroups;
+      write_row<kCh>(t_dq + lane_base + wg * kCh, a.scale,
+                     a.dq + (static_cast<int64_t>(it.lo + at) * a.Hq + it.head) * D + wg * kCh, used && fine);
       fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->acc_free);

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_after_sync();
           const uint32_t ts = tmem_s + 128 * s, to = tmem_o + 128 * s;
           if (elect()) {
-            mma_rows<D, 32>(to, ts, v_at + rv.slot * kStep, j > 0);
+            mma_rows<D, 128>(to, ts, v_at + rv.slot * kStep, j > 0);
             if (j + 1 == it.n[s]) mma_commit(&sh->o_done[s]);
           }
           if (j + 1 < it.n[s]) qk(s, rk.slot);
