@@ -3,11 +3,12 @@ weights: the package's operators together, as a program uses them.
 
     python -m recompute_kda_chunkwise_gb300.hybrid
 
-trains a stack of delta-rule blocks for a few steps (``kda`` and ``block_norm``
-with gradients), then serves a stack with attention blocks between them:
-prefill (``kda_fwd`` to a pool of states, ``paged_append`` and
-``paged_attention``), and decoding with drafted tokens (``kda_step``, the paged
-cache, ``verify_drafts``). Projections are plain matrix products.
+trains a stack of delta-rule blocks with an attention block between them for a
+few steps (``kda``, ``rotary``, ``attention`` and ``block_norm`` with gradients,
+clipped by their global norm), then serves one: prefill (``kda_fwd`` to a pool of
+states, ``paged_append_rotary`` and ``paged_attention``), and decoding with
+drafted tokens (``kda_step``, the paged cache, ``verify_drafts``). Projections are
+plain matrix products.
 """
 from __future__ import annotations
 
@@ -15,7 +16,10 @@ import torch
 
 from . import decode
 from . import kda as K
+from .attention import attention
+from .grads import clip_grads
 from .norm import block_norm, block_norm_fwd
+from .rotary import Rotary, rotary
 
 EPS = 1e-5
 
@@ -50,14 +54,21 @@ class Block(torch.nn.Module):
         q, k, v, g, z = (t.reshape(S, H, D).contiguous() for t in (n @ self.proj).split(H * D, 1))
         return q, k, v, g, z, n @ self.beta
 
+    def attention_inputs(self, n):
+        """q, k, v: slices of the fused projection, as rotary and attention take them."""
+        S, D = n.shape[0], self.head_dim
+        return tuple(t.view(S, -1, D) for t in (n @ self.proj).split([self.heads * D, self.kv_heads * D, self.kv_heads * D], 1))
+
 
 class Stack(torch.nn.Module):
     """Blocks joined by block_norm: h += post-norm of a block's output, and the
-    next block reads the pre-norm of h."""
+    next block reads the pre-norm of h. rope: a ``rotary.Rotary`` for the
+    attention blocks' positions (None: they see none)."""
 
     def __init__(self, vocab=512, dim=256, heads=2, head_dim=128, kinds=("delta", "delta"), kv_heads=1, seed=0,
-                 device="cuda"):
+                 device="cuda", rope=None):
         super().__init__()
+        self.rope = rope
         gen = torch.Generator(device=device)
         gen.manual_seed(seed)
         self.blocks = torch.nn.ModuleList(Block(dim, heads, head_dim, k, kv_heads, gen, device) for k in kinds)
@@ -70,20 +81,30 @@ class Stack(torch.nn.Module):
         return h, n
 
     def forward(self, tokens, cu_seqlens):
-        """Logits [S, vocab] of packed sequences; every block a delta rule."""
+        """Logits [S, vocab] of packed sequences."""
         h, n = self.start(tokens)
         for b in self.blocks:
-            q, k, v, g, z, beta = b.delta_inputs(n)
-            o = K.kda(q, k, v, g, beta, b.A_log, b.dt_bias, cu_seqlens)
-            o = block_norm(o, z=z, w_post=b.out_norm, eps=EPS)
+            if b.kind == "delta":
+                q, k, v, g, z, beta = b.delta_inputs(n)
+                o = K.kda(q, k, v, g, beta, b.A_log, b.dt_bias, cu_seqlens)
+                o = block_norm(o, z=z, w_post=b.out_norm, eps=EPS)
+            else:
+                q, k, v = b.attention_inputs(n)
+                if self.rope is not None:
+                    q, k = rotary(self.rope, q, k, cu_seqlens=cu_seqlens)
+                o = attention(q, k, v, cu_seqlens)
             h, n = block_norm(o.flatten(1) @ b.out, h=h, w_post=b.post, w_pre=b.pre, block_scale=0.5, eps=EPS)
         return n @ self.embed.T
 
 
-def train_step(model, tokens, cu_seqlens, targets, lr=1e-3):
-    """One step of gradient descent; returns the loss."""
+def train_step(model, tokens, cu_seqlens, targets, lr=1e-3, max_norm=None):
+    """One step of gradient descent; returns the loss. max_norm: clips the
+    gradients to this global norm (None: as they are)."""
     loss = torch.nn.functional.cross_entropy(model(tokens, cu_seqlens).float(), targets)
     grads = torch.autograd.grad(loss, list(model.parameters()))
+    if max_norm is not None:
+        grads = [g if g.is_contiguous() else g.contiguous() for g in grads]
+        clip_grads(grads, max_norm)
     with torch.no_grad():
         for p, g in zip(model.parameters(), grads):
             p -= lr * g.to(p.dtype)
@@ -138,11 +159,13 @@ class Server:
                     o = decode.kda_step(q, k, v, g, beta, b.A_log, b.dt_bias, cu, self.states[i], commit=commit_t)
                 o, _ = block_norm_fwd(o, z=z, w_post=b.out_norm, eps=EPS)
             else:
-                S, D = n.shape[0], b.head_dim
-                q, k, v = (t.reshape(S, -1, D).contiguous()
-                           for t in (n @ b.proj).split([b.heads * D, b.kv_heads * D, b.kv_heads * D], 1))
+                q, k, v = b.attention_inputs(n)
                 kp, vp = self.caches[i]
-                decode.paged_append(k, v, kp, vp, self.table, lens, cu)
+                if m.rope is not None:
+                    q = decode.paged_append_rotary(m.rope, q, k, v, kp, vp, self.table, lens, cu)
+                else:
+                    q = q.contiguous()
+                    decode.paged_append(k.contiguous(), v.contiguous(), kp, vp, self.table, lens, cu)
                 o = decode.paged_attention(q, kp, vp, self.table, lens, cu)
             h, n = block_norm_fwd(o.flatten(1) @ b.out, h=h, w_post=b.post, w_pre=b.pre, block_scale=0.5, eps=EPS)
         self.committed = [c + k for c, k in zip(self.committed, kept)]
@@ -227,12 +250,13 @@ def generate(server, prompts, steps, drafts=3, seed=0, greedy=False):
 
 def main():
     torch.manual_seed(0)
-    model = Stack()
+    rope = Rotary(128)
+    model = Stack(kinds=("delta", "attn", "delta"), rope=rope)
     tokens = torch.randint(0, 512, (600,), device="cuda")
     cu = torch.tensor([0, 250, 600], dtype=torch.int32, device="cuda")
     for i in range(3):
-        print(f"training step {i}: loss {train_step(model, tokens, cu, tokens.roll(-1)).item():.4f}")
-    model = Stack(kinds=("delta", "delta", "attn", "delta"), heads=4, kv_heads=2)
+        print(f"training step {i}: loss {train_step(model, tokens, cu, tokens.roll(-1), lr=0.3, max_norm=1.0).item():.4f}")
+    model = Stack(kinds=("delta", "delta", "attn", "delta"), heads=4, kv_heads=2, rope=rope)
     prompts = [[5, 6, 7, 8] * 12, [1, 2, 3] * 7, list(range(40))]
     out, calls = generate(Server(model, 3, 256), prompts, steps=24, greedy=True)
     new = [o[len(p):] for o, p in zip(out, prompts)]
