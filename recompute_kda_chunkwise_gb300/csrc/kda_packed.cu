@@ -140,6 +140,7 @@ kda_status begin(const kda_attention_problem* p, int rows, void* workspace, Pack
   *a = PackedArgs{};
   a->cu = p->cu_seqlens;
   a->status = static_cast<int*>(workspace);
+  a->tickets = a->status + 4;
   a->S = p->total_tokens;
   a->N = p->num_seqs;
   a->Hq = p->num_heads;
@@ -147,7 +148,7 @@ kda_status begin(const kda_attention_problem* p, int rows, void* workspace, Pack
   a->D = p->head_dim;
   a->scale = p->scale;
   a->split = 1;
-  cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int), s);
+  cudaError_t e = cudaMemsetAsync(workspace, 0, 32, s);  // the status word, and the tickets
   if (e == cudaSuccess && a->N > 1 && a->S > 0) {
     int* const list = reinterpret_cast<int*>(static_cast<char*>(workspace) + kHeaderBytes);
     kda_packed_list_kernel<<<1, 1024, 0, s>>>(a->cu, a->N, a->S, rows, list, a->status);

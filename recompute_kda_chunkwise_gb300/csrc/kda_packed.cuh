@@ -14,6 +14,7 @@ constexpr int kPackedMaxCtas = 152;  // one per SM
 struct PackedArgs {
   const int32_t* cu;
   int* status;
+  int* tickets;        // items handed out, by kernel (zeroed before the call's first)
   const int* list;     // count, then from list + 4 on {first token, length, weight, 0} of each tile; null: one sequence
   int64_t S;
   int N, Hq, Hkv, D;
@@ -49,13 +50,6 @@ __device__ __forceinline__ Tile tile_of(const PackedArgs& a, int tiles, int e) {
   const int4 t = reinterpret_cast<const int4*>(a.list + 4)[e];
   return {t.x, t.y, t.z};
 }
-// Item i of this CTA (there and back over the CTAs, so that none gets the
-// heavier of every round), or past the end.
-__device__ __forceinline__ int64_t item_of(int64_t i) {
-  const int64_t g = gridDim.x;
-  return i * g + (i & 1 ? g - 1 - blockIdx.x : blockIdx.x);
-}
-
 namespace tc {
 
 // Bounded wait for a phase; false when it ran out (the CTA's abort flag is then
@@ -80,8 +74,8 @@ __device__ __forceinline__ bool wait_or(int* abort_, uint64_t* bar, uint32_t par
 __device__ __forceinline__ bool wait_all(int* abort_, uint64_t* bar, uint32_t parity, int* status) {
   return __all_sync(~0u, wait_or(abort_, bar, parity, status));
 }
-// Waits, at most so long, without giving up.
-__device__ __forceinline__ void settle_for(uint64_t* bar, uint32_t parity) {
+// Waits, at most so long, without giving up; whether the phase is over.
+__device__ __forceinline__ bool settle_for(uint64_t* bar, uint32_t parity) {
   const uint32_t at = smem_addr(bar);
   for (int it = 0; it < (1 << 20); ++it) {
     uint32_t ok;
@@ -90,8 +84,64 @@ __device__ __forceinline__ void settle_for(uint64_t* bar, uint32_t parity) {
         : "=r"(ok)
         : "r"(at), "r"(parity)
         : "memory");
-    if (ok) return;
+    if (ok) return true;
   }
+  return false;
+}
+
+// Hands items to the CTA's warps. The first is the CTA's own number, every
+// further one the next that no CTA has taken, heaviest first: the order decides
+// when an item is worked on, not what comes out. One warp fetches a number when
+// it has issued the copies of the item before (earlier, and an item would be
+// taken long before its turn), and passes it on through two slots. These waits look at no
+// abort flag, so that every warp sees the same items whatever happens; after an
+// abort the fetching warp passes on the end.
+struct Handout {
+  uint64_t full[2], empty[2];
+  int64_t item[2];
+};
+constexpr int64_t kNoItem = INT64_MAX;
+__device__ __forceinline__ void handout_init(Handout* h, int warps) {
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&h->full[i], 1);
+    mbar_init(&h->empty[i], warps);
+  }
+}
+__device__ __forceinline__ void settle_long(uint64_t* bar, uint32_t parity) {
+  for (int i = 0; i < 64; ++i)
+    if (settle_for(bar, parity)) return;
+}
+// The CTA's n-th item, by one of the warps that are passed it.
+__device__ __forceinline__ int64_t handout_take(Handout* h, uint32_t n) {
+  if (n == 0) return blockIdx.x;
+  const int slot = (n - 1) & 1;
+  settle_long(&h->full[slot], (n - 1) >> 1 & 1);
+  const int64_t x = *const_cast<volatile int64_t*>(&h->item[slot]);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&h->empty[slot]);
+  return x;
+}
+// Passes on item n > 0, by the fetching warp.
+__device__ __forceinline__ void handout_give(Handout* h, uint32_t n, int64_t x) {
+  const int slot = (n - 1) & 1;
+  if (n > 2) settle_long(&h->empty[slot], (((n - 1) >> 1) - 1) & 1);
+  if ((threadIdx.x & 31) == 0) {
+    *const_cast<volatile int64_t*>(&h->item[slot]) = x;
+    mbar_arrive(&h->full[slot]);
+  }
+  __syncwarp();
+}
+
+// The next item, fetched and passed on as number n.
+__device__ __forceinline__ int64_t handout_next(Handout* h, uint32_t n, int* ticket, bool ok) {
+  int64_t x = kNoItem;
+  if (ok) {
+    int i = 0;
+    if ((threadIdx.x & 31) == 0) i = atomicAdd(ticket, 1);
+    x = static_cast<int64_t>(gridDim.x) + __shfl_sync(~0u, i, 0);
+  }
+  handout_give(h, n, x);
+  return x;
 }
 
 // A ring's position: slot, and the parity of its turn.

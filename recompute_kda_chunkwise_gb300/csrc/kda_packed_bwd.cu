@@ -32,18 +32,30 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128;
-constexpr int kGroups = 4, kMathWarps = 4 * kGroups;  // warpgroups, each a part of a tile's columns
-constexpr int kCols = kRows / kGroups, kParts = kCols / 32;
+// Warpgroups of arithmetic, each a part of a tile's columns: two threads a row,
+// or four. Four hide more of one another's latencies; with heads of 128 the
+// products take most of the time, and dq's warps, which also form sums over
+// rows, do better in two. Forward and backward of 8192 tokens, 64 heads: of 64,
+// 4: 1978 us in the backward, 2: 2262; of 128 dk and dv alike (1296 to 1302), dq
+// 1130 and 1087.
+template <int G>
+struct Math {
+  static constexpr int kGroups = G, kWarps = 4 * G, kThreads = 32 * (4 + kWarps);
+  static constexpr int kCols = 128 / G, kParts = kCols / 32;
+};
+template <int D>
+using KvMath = Math<4>;
+template <int D>
+using QMath = Math<D == 128 ? 2 : 4>;
 constexpr int kMmaWarp = 0, kLoadWarp = 1, kMathWarp = 4;
-constexpr int kThreads = 32 * (kMathWarp + kMathWarps);
 
-typedef uint32_t Scores[kParts][32];  // a thread's columns of a tile
-
-__device__ __forceinline__ void load_scores(uint32_t at, Scores& x) {
+// P x 32 columns of a tile, a thread's.
+template <int P>
+__device__ __forceinline__ void load_scores(uint32_t at, uint32_t (&x)[P][32]) {
 #pragma unroll
-  for (int c = 0; c < kParts; ++c) tmem_ask(at + 32 * c, x[c]);
+  for (int c = 0; c < P; ++c) tmem_ask(at + 32 * c, x[c]);
 #pragma unroll
-  for (int c = 0; c < kParts; ++c) tmem_got(x[c]);
+  for (int c = 0; c < P; ++c) tmem_got(x[c]);
 }
 // Exponentials (base 2) of a pair, in place.
 __device__ __forceinline__ void ex2_pair(uint64_t t, uint32_t& lo, uint32_t& hi) {
@@ -52,17 +64,19 @@ __device__ __forceinline__ void ex2_pair(uint64_t t, uint32_t& lo, uint32_t& hi)
   hi = __float_as_uint(ex2(e.y));
 }
 // Zero where a column is not seen.
-__device__ __forceinline__ void hide(Scores& x, const uint32_t (&see)[kParts]) {
+template <int P>
+__device__ __forceinline__ void hide(uint32_t (&x)[P][32], const uint32_t (&see)[P]) {
 #pragma unroll
-  for (int c = 0; c < kParts; ++c)
+  for (int c = 0; c < P; ++c)
 #pragma unroll
     for (int e = 0; e < 32; ++e)
       if (!(see[c] >> e & 1)) x[c][e] = 0u;
 }
 // Rounded to bf16, two to a column, over the first half of the columns.
-__device__ __forceinline__ void store_bf16(uint32_t at, const Scores& x) {
+template <int P>
+__device__ __forceinline__ void store_bf16(uint32_t at, const uint32_t (&x)[P][32]) {
 #pragma unroll
-  for (int c = 0; c < kParts; ++c) {
+  for (int c = 0; c < P; ++c) {
     uint32_t y[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) y[e] = pack_bf16(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1]));
@@ -125,6 +139,7 @@ struct KvCfg {
   static constexpr int kBytes = (2 + kQ + kDo) * kTile;
 };
 struct KvShared {
+  Handout items;
   alignas(16) float row[2][2][kRows];  // -lse (base 2) and -delta of a step's queries
   uint64_t kv_full, kv_empty;
   uint64_t q_full[3], q_empty[3], do_full[2], do_empty[2];
@@ -136,8 +151,7 @@ struct KvItem {
   int lo, L, j, nt, hk, head0, heads, part;  // key tile j of nt; query heads head0 .. + heads
   __device__ __forceinline__ int steps() const { return heads * (nt - j); }
 };
-__device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t i, KvItem& it) {
-  const int64_t x = item_of(i);
+__device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t x, KvItem& it) {
   const int per = a.Hkv * a.split;
   if (x >= static_cast<int64_t>(tiles) * per) return false;
   const Tile t = tile_of(a, tiles, static_cast<int>(x / per));
@@ -154,11 +168,12 @@ __device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
     kda_packed_dkv_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ CUtensorMap qmap,
                           const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                           const __grid_constant__ CUtensorMap domap, const float sc) {
   using C = KvCfg<D>;
+  constexpr int kMathWarps = KvMath<D>::kWarps, kGroups = KvMath<D>::kGroups, kCols = KvMath<D>::kCols, kParts = KvMath<D>::kParts;
   constexpr int kTile = C::kTile;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const kt = smem;
@@ -176,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if (tid == 0) {
+    handout_init(&sh->items, 2 + kMathWarps);
     mbar_init(&sh->kv_full, 1);
     mbar_init(&sh->kv_empty, 1);
     for (int i = 0; i < C::kQ; ++i) {
@@ -214,17 +230,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring r;
     bool ok = true;
     uint32_t items = 0;
-    int64_t copies = 0;
-    for (int64_t i = 0; ok && item_at(a, tiles, i, it); ++i) {
+    int64_t copies = 0, x = blockIdx.x;
+    bool kv = false;  // copies of K and V are in flight, or have been
+    for (; item_at(a, tiles, x, it); ++items) {
       if (!second) {
-        if (items > 0) ok = wait_all(ab, &sh->kv_empty, (items - 1) & 1, a.status);
-        if (!ok) break;
-        if (elect()) {
+        if (items > 0) ok = ok && wait_all(ab, &sh->kv_empty, (items - 1) & 1, a.status);
+        kv = ok;
+        if (ok && elect()) {
           mbar_expect_tx(&sh->kv_full, 2 * kTile);
           load_rows<D>(kt, &kmap, it.hk, it.lo + it.j * kRows, &sh->kv_full);
           load_rows<D>(vt, &vmap, it.hk, it.lo + it.j * kRows, &sh->kv_full);
         }
-        ++items;
       }
       for (int h = 0; ok && h < it.heads; ++h) {
         for (int m = it.j; m < it.nt; ++m) {
@@ -238,12 +254,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           r.next(slots);
         }
       }
+      x = second ? handout_take(&sh->items, items + 1) : handout_next(&sh->items, items + 1, &a.tickets[1], ok);
     }
     // after an abort: the copies in flight land before the CTA ends
     if (!ok) {
       for (int64_t p = copies > slots ? copies - slots : 0; p < copies; ++p)
         settle_for(&full[p % slots], static_cast<uint32_t>((p / slots) & 1));
-      if (items > 0) settle_for(&sh->kv_full, (items - 1) & 1);
+      if (kv) settle_for(&sh->kv_full, (items - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
     const uint32_t k_at = desc_k(kt), v_at = desc_k(vt), q_at = desc_k(qt), do_at = desc_k(dot);
@@ -252,8 +269,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring rq, rd;  // of step t
     uint32_t items = 0, turn = 0;
     bool ok = true;
-    for (int64_t i = 0; ok && item_at(a, tiles, i, it); ++i) {
+    for (; item_at(a, tiles, handout_take(&sh->items, items), it); ++items) {
       const int steps = it.steps();
+      if (!ok) continue;
       // K and V, the first Q and d_o
       {
         uint64_t* bar = &sh->kv_full;
@@ -262,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 2) bar = &sh->do_full[rd.slot], par = rd.turn;
         ok = wait_all(ab, bar, par & 1, a.status);
       }
-      if (!ok) break;
+      if (!ok) continue;
       fence_after_sync();
       if (elect()) {
         mma_scores<D>(t_s, k_at, q_at + rq.slot * kStep);
@@ -316,7 +334,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         rq = nq;
         rd = nd;
       }
-      ++items;
     }
     if (elect()) mma_commit(&sh->drain);
     settle_for(&sh->drain, 0);
@@ -328,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t sc2 = twice2(sc);
     uint32_t turn = 0, items = 0;
     Ring rq, rd;
-    for (int64_t i = 0; item_at(a, tiles, i, it); ++i, ++items) {
+    for (; item_at(a, tiles, handout_take(&sh->items, items), it); ++items) {
       const int steps = it.steps();
       const bool rows = mt < 2 * kRows;  // the first two warpgroups fetch lse and delta
       const float* const src = mt < kRows ? a.lse : a.delta;
@@ -371,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_smem();
         }
         fence_after_sync();
-        Scores p, x;
+        uint32_t p[kParts][32], x[kParts][32];
         load_scores(my_s, p);
 #pragma unroll
         for (int c = 0; c < kParts; ++c)
@@ -459,7 +476,8 @@ struct QCfg {
   static constexpr int kBytes = (2 + kK + kV) * kTile;
 };
 struct QShared {
-  float sum[kGroups][kRows];  // per row, of each warpgroup's columns
+  Handout items;
+  float sum[4][kRows];  // per row, of each warpgroup's columns
   uint64_t k_full[5], k_empty[5], v_full[4], v_empty[4];
   uint64_t q_full, q_empty;
   // dP and dS by buffer: their next phases can be over before every role has seen the last ones
@@ -470,8 +488,7 @@ struct QShared {
 struct QItem {
   int lo, L, m, head, hk;  // query tile m: key tiles 0 .. m
 };
-__device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t i, QItem& it) {
-  const int64_t x = item_of(i);
+__device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t x, QItem& it) {
   if (x >= static_cast<int64_t>(tiles) * a.Hq) return false;
   const Tile t = tile_of(a, tiles, static_cast<int>(x / a.Hq));
   it.lo = t.lo;
@@ -483,11 +500,12 @@ __device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(QMath<D>::kThreads, 1)
     kda_packed_dq_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const __grid_constant__ CUtensorMap domap, const float sc) {
   using C = QCfg<D>;
+  constexpr int kMathWarps = QMath<D>::kWarps, kGroups = QMath<D>::kGroups, kCols = QMath<D>::kCols, kParts = QMath<D>::kParts;
   constexpr int kTile = C::kTile;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const kt = smem + 2 * kTile;  // behind the tiles of q and d_o
@@ -503,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if (tid == 0) {
+    handout_init(&sh->items, 2 + kMathWarps);
     for (int i = 0; i < C::kK; ++i) {
       mbar_init(&sh->k_full[i], 1);
       mbar_init(&sh->k_empty[i], 1);
@@ -543,17 +562,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring r;
     bool ok = true;
     uint32_t items = 0;
-    int64_t copies = 0;
-    for (int64_t i = 0; ok && item_at(a, tiles, i, it); ++i) {
+    int64_t copies = 0, x = blockIdx.x;
+    bool rows = false;  // copies of q and d_o are in flight, or have been
+    for (; item_at(a, tiles, x, it); ++items) {
       if (!v) {
-        if (items > 0) ok = wait_all(ab, &sh->q_empty, (items - 1) & 1, a.status);
-        if (!ok) break;
-        if (elect()) {
+        if (items > 0) ok = ok && wait_all(ab, &sh->q_empty, (items - 1) & 1, a.status);
+        rows = ok;
+        if (ok && elect()) {
           mbar_expect_tx(&sh->q_full, 2 * kTile);
           load_rows<D>(smem, &qmap, it.head, it.lo + it.m * kRows, &sh->q_full);
           load_rows<D>(smem + kTile, &domap, it.head, it.lo + it.m * kRows, &sh->q_full);
         }
-        ++items;
       }
       for (int j = 0; j <= it.m; ++j) {
         if (r.turn > 0) ok = ok && wait_all(ab, &empty[r.slot], (r.turn - 1) & 1, a.status);
@@ -565,11 +584,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++copies;
         r.next(slots);
       }
+      x = v ? handout_take(&sh->items, items + 1) : handout_next(&sh->items, items + 1, &a.tickets[0], ok);
     }
     if (!ok) {
       for (int64_t p = copies > slots ? copies - slots : 0; p < copies; ++p)
         settle_for(&full[p % slots], static_cast<uint32_t>((p / slots) & 1));
-      if (items > 0) settle_for(&sh->q_full, (items - 1) & 1);
+      if (rows) settle_for(&sh->q_full, (items - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
     const uint32_t q_at = desc_k(smem), do_at = desc_k(smem + kTile), k_at = desc_k(kt), v_at = desc_k(vt), k_mn = desc_mn(kt);
@@ -587,7 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (last) mma_commit(&sh->q_empty);
       }
     };
-    for (int64_t i = 0; ok && item_at(a, tiles, i, it); ++i) {
+    for (; item_at(a, tiles, handout_take(&sh->items, items), it); ++items) {
+      if (!ok) continue;
       {
         uint64_t* bar = &sh->q_full;
         uint32_t par = items;
@@ -595,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 2) bar = &sh->v_full[rv.slot], par = rv.turn;
         ok = wait_all(ab, bar, par & 1, a.status);
       }
-      if (!ok) break;
+      if (!ok) continue;
       fence_after_sync();
       scores(turn, rk, rv, it.m == 0);
       for (int j = 0; j <= it.m; ++j) {
@@ -630,7 +651,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         rk = nk;
         rv = nv;
       }
-      ++items;
     }
     if (elect()) mma_commit(&sh->drain);
     settle_for(&sh->drain, 0);
@@ -652,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_bar_sync(1, 32 * kMathWarps);
       return x;
     };
-    for (int64_t i = 0; item_at(a, tiles, i, it); ++i, ++items) {
+    for (; item_at(a, tiles, handout_take(&sh->items, items), it); ++items) {
       const int at = it.m * kRows + row;
       const bool used = at < it.L;
       const int64_t stat = static_cast<int64_t>(it.head) * a.S + it.lo + at;
@@ -676,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         wait_all(ab, &sh->s_full, turn & 1, a.status);
         fence_after_sync();
-        Scores p, x;
+        uint32_t p[kParts][32], x[kParts][32];
         load_scores(my_s, p);
         fence_before_sync();
         __syncwarp();
@@ -757,8 +777,8 @@ cudaError_t launch(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap&
   const float sc = a.scale * 1.4426950408889634f;
   const int64_t tiles = a.S / kRows + a.N, kv = tiles * a.Hkv * a.split, nq = tiles * a.Hq;
   kda_packed_delta_kernel<D><<<static_cast<unsigned>((a.S * a.Hq * 8 + 255) / 256), 256, 0, s>>>(a);
-  kda_packed_dq_kernel<D><<<static_cast<unsigned>(nq < sms ? nq : sms), kThreads, smem_q, s>>>(a, q, k, v, d_o, sc);
-  kda_packed_dkv_kernel<D><<<static_cast<unsigned>(kv < sms ? kv : sms), kThreads, smem_kv, s>>>(a, q, k, v, d_o, sc);
+  kda_packed_dq_kernel<D><<<static_cast<unsigned>(nq < sms ? nq : sms), QMath<D>::kThreads, smem_q, s>>>(a, q, k, v, d_o, sc);
+  kda_packed_dkv_kernel<D><<<static_cast<unsigned>(kv < sms ? kv : sms), KvMath<D>::kThreads, smem_kv, s>>>(a, q, k, v, d_o, sc);
   if (a.split > 1) kda_packed_parts_kernel<<<static_cast<unsigned>((2 * a.S * a.Hkv * a.D / 4 + 255) / 256), 256, 0, s>>>(a);
   return cudaGetLastError();
 }

@@ -14,8 +14,7 @@
 // bf16 probabilities because both operands have one type; the row's sum adds
 // them in fp32 before they are rounded.
 //
-// Items are handed out heaviest first, a fixed share to each of one CTA per
-// SM. The next item's queries, keys and values are fetched, and its first
+// Items are handed out heaviest first to one CTA per SM. The next item's queries, keys and values are fetched, and its first
 // scores formed, while the last item's outputs are written.
 #include <math.h>
 
@@ -40,6 +39,7 @@ struct Cfg {
 };
 
 struct Shared {
+  Handout items;
   uint64_t full[8], empty[8];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_ready[2], o_done[2], o_free[2];
@@ -53,8 +53,7 @@ struct Item {
   int lo, L, head, hk, row0;  // row0: first row of stream 0 in the sequence
   int n[2];                   // key tiles of each stream
 };
-__device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t i, Item& it) {
-  const int64_t x = item_of(i);
+__device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t x, Item& it) {
   if (x >= static_cast<int64_t>(tiles) * a.Hq) return false;
   const Tile t = tile_of(a, tiles, static_cast<int>(x / a.Hq));
   it.lo = t.lo;
@@ -91,6 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh->full[i], 1);
       mbar_init(&sh->empty[i], 1);
     }
+    handout_init(&sh->items, 1 + kSoftmaxWarps);
     mbar_init(&sh->q_full, 1);
     mbar_init(&sh->q_empty, 1);
     for (int i = 0; i < 2; ++i) {
@@ -117,9 +117,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t items = 0;
     int64_t copies = 0;
-    for (int64_t i = 0; ok && item_at(a, tiles, i, it); ++i) {
-      if (items > 0) ok = wait_all(ab, &sh->q_empty, (items - 1) & 1, a.status);
-      if (!ok) break;
+    for (int64_t x = blockIdx.x; item_at(a, tiles, x, it);) {
+      if (items > 0) ok = ok && wait_all(ab, &sh->q_empty, (items - 1) & 1, a.status);
+      if (!ok) {
+        handout_give(&sh->items, items + 1, kNoItem);
+        break;
+      }
       const int streams = it.n[1] ? 2 : 1, nk = it.n[1] ? it.n[1] : it.n[0];
       if (elect()) {
         mbar_expect_tx(&sh->q_full, streams * kTile);
@@ -139,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           r.next(kSlots);
         }
       }
+      x = handout_next(&sh->items, items, &a.tickets[0], ok);
     }
     // after an abort: the copies in flight land before the CTA ends
     if (!ok) {
@@ -159,11 +163,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(&sh->s_full[s]);
       }
     };
-    for (int64_t i = 0; ok && item_at(a, tiles, i, it); ++i) {
+    while (item_at(a, tiles, handout_take(&sh->items, items), it)) {
       const int nk = it.n[1] ? it.n[1] : it.n[0];
-      ok = wait_all(ab, lane == 0 ? &sh->q_full : &sh->full[rk.slot], (lane == 0 ? items : rk.turn) & 1, a.status);
       ++items;
-      if (!ok) break;
+      if (!ok) continue;
+      ok = wait_all(ab, lane == 0 ? &sh->q_full : &sh->full[rk.slot], (lane == 0 ? items - 1 : rk.turn) & 1, a.status);
+      if (!ok) continue;
       fence_after_sync();
       for (int s = 0; s < 2; ++s)
         if (it.n[s]) qk(s, rk.slot);
@@ -215,9 +220,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
     const uint32_t my_s = tmem_s + 128 * st + lane_base;
     const uint32_t my_o = tmem_o + 128 * st + lane_base;
-    uint32_t turn_s = 0, turn_d = 0;
+    uint32_t turn_s = 0, turn_d = 0, items = 0;
     int64_t pos = 0;  // ring position of the item's K(0)
-    for (int64_t i = 0; item_at(a, tiles, i, it); ++i) {
+    while (item_at(a, tiles, handout_take(&sh->items, items++), it)) {
       const int nt = it.n[st], nk = it.n[1] ? it.n[1] : it.n[0];
       const int at = it.row0 + st * kRows + row;  // row of the sequence
       const bool used = at < it.L;
