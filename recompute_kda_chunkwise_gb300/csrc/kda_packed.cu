@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(1024) kda_packed_list_kernel(const int32_t* cu
   int4* const out = reinterpret_cast<int4*>(list + 4);
   for (int n = warp; n < N; n += 32) {
     const int lo = cu[n], L = cu[n + 1] - lo, tiles = (L + rows - 1) / rows;
-    for (int w = 1 + lane; w <= tiles; w += 32) out[atomicAdd(&count[bucket(w)], 1)] = make_int4(lo, L, w, 0);
+    for (int w = 1 + lane; w <= tiles; w += 32) out[atomicAdd(&count[bucket(w)], 1)] = make_int4(lo, L, w, n);
   }
 }
 
@@ -91,6 +91,8 @@ int split_of(const kda_attention_problem* p) {
   return split;
 }
 size_t delta_bytes(const kda_attention_problem* p) { return up(sizeof(float) * p->total_tokens * p->num_heads); }
+int64_t stat_tiles(const kda_attention_problem* p) { return p->total_tokens / 128 + p->num_seqs + 1; }
+size_t stat_bytes(const kda_attention_problem* p) { return static_cast<size_t>(1024) * stat_tiles(p) * p->num_heads; }
 size_t part_bytes(const kda_attention_problem* p) {
   const int split = split_of(p);
   return split == 1 ? 0 : sizeof(float) * 2 * split * p->total_tokens * p->num_kv_heads * p->head_dim;
@@ -202,7 +204,7 @@ kda_status kda_attention_fwd(const kda_attention_problem* p, const void* q, cons
 
 size_t kda_attention_bwd_workspace_bytes(const kda_attention_problem* p) {
   using namespace kda;
-  return validate(p, false) == KDA_OK ? kHeaderBytes + list_bytes(p, 128) + delta_bytes(p) + part_bytes(p) : 0;
+  return validate(p, false) == KDA_OK ? kHeaderBytes + list_bytes(p, 128) + delta_bytes(p) + stat_bytes(p) + part_bytes(p) : 0;
 }
 
 kda_status kda_attention_bwd(const kda_attention_problem* p, const void* q, const void* k, const void* v, const void* o,
@@ -234,7 +236,9 @@ kda_status kda_attention_bwd(const kda_attention_problem* p, const void* q, cons
   a.lse = const_cast<float*>(lse);
   char* at = static_cast<char*>(workspace) + kHeaderBytes + list_bytes(p, 128);
   a.delta = reinterpret_cast<float*>(at);
-  a.part = reinterpret_cast<float*>(at + delta_bytes(p));
+  a.stats = reinterpret_cast<float*>(at + delta_bytes(p));
+  a.stat_tiles = stat_tiles(p);
+  a.part = reinterpret_cast<float*>(at + delta_bytes(p) + stat_bytes(p));
   a.split = split_of(p);
   const cudaError_t e = launch_packed_bwd(a, m.q, m.k, m.v, m.d_o, s);
   return e == cudaSuccess ? KDA_OK : set_error(KDA_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));

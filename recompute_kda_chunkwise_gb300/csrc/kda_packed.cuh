@@ -15,7 +15,7 @@ struct PackedArgs {
   const int32_t* cu;
   int* status;
   int* tickets;        // items handed out, by kernel (zeroed before the call's first)
-  const int* list;     // count, then from list + 4 on {first token, length, weight, 0} of each tile; null: one sequence
+  const int* list;     // count, then from list + 4 on {first token, length, weight, sequence} of each tile; null: one sequence
   int64_t S;
   int N, Hq, Hkv, D;
   float scale;
@@ -24,6 +24,8 @@ struct PackedArgs {
   int64_t qs;          // elements from a token of q to the next
   float* lse;          // [Hq][S]
   float* delta;        // [Hq][S]
+  float* stats;        // [Hq][stat_tiles][2][128]: -lse in base 2 and -delta of each tile's rows, zero past its sequence
+  int64_t stat_tiles;
   float* part;         // gradients of k and v by parts of the head group: [2][split][S][Hkv][D]
   int split;
 };
@@ -32,7 +34,9 @@ struct PackedArgs {
 // is tile w - 1 from the sequence's start (or, for work that goes to the
 // sequence's end, w tiles from there).
 struct Tile {
-  int lo, L, w;
+  int lo, L, w, n;
+  // place of tile m of the sequence among all sequences' tiles of 128 rows
+  __device__ __forceinline__ int64_t slot(int m) const { return static_cast<int64_t>(lo) / 128 + n + m; }
 };
 
 // Tiles of the call, heaviest first, so that the last ones to be handed out are
@@ -46,9 +50,9 @@ __device__ __forceinline__ int tiles_of(const PackedArgs& a, int rows) {
   return static_cast<int>((a.S + rows - 1) / rows);
 }
 __device__ __forceinline__ Tile tile_of(const PackedArgs& a, int tiles, int e) {
-  if (!a.list) return {0, static_cast<int>(a.S), tiles - e};
+  if (!a.list) return {0, static_cast<int>(a.S), tiles - e, 0};
   const int4 t = reinterpret_cast<const int4*>(a.list + 4)[e];
-  return {t.x, t.y, t.z};
+  return {t.x, t.y, t.z, t.w};
 }
 namespace tc {
 

@@ -15,7 +15,8 @@
 // dv += P^T d_o and dk += dS^T Q straight from TMEM: neither goes through
 // shared memory, whose bandwidth bounds products of two operands there. While
 // the warps form P^T the tensor cores run dS^T's product and the next dP^T, and
-// the other way round: the order is dv(t), S(t+1), dk(t), dP(t+1).
+// the other way round: the order is dv(t), S(t+1), dk(t), dP(t+1). With heads of
+// 64 P^T and dS^T have columns of their own and the next scores go first.
 // A key/value head's keys go over all query heads of its group in one item, or
 // over a part of them where there are few items: the parts are then added up,
 // in order, by another kernel.
@@ -135,19 +136,25 @@ __global__ void __launch_bounds__(256) kda_packed_delta_kernel(const __grid_cons
 template <int D>
 struct KvCfg {
   static constexpr int kTile = kRows * D * 2;
-  static constexpr int kQ = 3, kDo = 2;  // slots of queries, of d_o
+  static constexpr int kQ = D == 128 ? 3 : 5, kDo = D == 128 ? 2 : 4;  // slots of queries, of d_o
   static constexpr int kBytes = (2 + kQ + kDo) * kTile;
+  // Columns of TMEM: S, dP, dv, dk. Heads of 64 leave room for P and dS beside
+  // the scores, so that the next scores need not wait for the products with them.
+  static constexpr bool kOwn = D == 64;
+  static constexpr int kDv = 256, kDk = 256 + D, kP = kOwn ? 384 : 0, kDs = kOwn ? 448 : 128;
 };
+template <int D>
 struct KvShared {
+  alignas(16) float row[KvCfg<D>::kDo][2][kRows];  // -lse (base 2) and -delta of a step's queries, with its d_o
   Handout items;
-  alignas(16) float row[2][2][kRows];  // -lse (base 2) and -delta of a step's queries
   uint64_t kv_full, kv_empty;
-  uint64_t q_full[3], q_empty[3], do_full[2], do_empty[2];
-  uint64_t s_full, dp_full, p_ready, ds_ready, done, acc_free, drain;
+  uint64_t q_full[5], q_empty[5], do_full[4], do_empty[4];
+  uint64_t s_full, dp_full, p_ready, ds_ready, p_free, ds_free, done, acc_free, drain;
   uint32_t tmem;
   int abort_;
 };
 struct KvItem {
+  int64_t slot0;  // of the sequence's first tile in the statistics
   int lo, L, j, nt, hk, head0, heads, part;  // key tile j of nt; query heads head0 .. + heads
   __device__ __forceinline__ int steps() const { return heads * (nt - j); }
 };
@@ -158,6 +165,7 @@ __device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t 
   const int r = static_cast<int>(x % per);
   it.lo = t.lo;
   it.L = t.L;
+  it.slot0 = t.slot(0);
   it.nt = (t.L + kRows - 1) / kRows;
   it.j = it.nt - t.w;
   it.hk = r / a.split;
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
   uint8_t* const vt = smem + kTile;
   uint8_t* const qt = smem + 2 * kTile;
   uint8_t* const dot = qt + C::kQ * kTile;
-  KvShared* const sh = reinterpret_cast<KvShared*>(smem + C::kBytes);
+  KvShared<D>* const sh = reinterpret_cast<KvShared<D>*>(smem + C::kBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* const ab = &sh->abort_;
 
@@ -200,12 +208,14 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
     }
     for (int i = 0; i < C::kDo; ++i) {
       mbar_init(&sh->do_full[i], 1);
-      mbar_init(&sh->do_empty[i], 1);
+      mbar_init(&sh->do_empty[i], 1 + kMathWarps);  // the products with d_o, and the rows' lse and delta
     }
     mbar_init(&sh->s_full, 1);
     mbar_init(&sh->dp_full, 1);
     mbar_init(&sh->p_ready, kMathWarps);
     mbar_init(&sh->ds_ready, kMathWarps);
+    mbar_init(&sh->p_free, 1);
+    mbar_init(&sh->ds_free, 1);
     mbar_init(&sh->done, 1);
     mbar_init(&sh->acc_free, kMathWarps);
     mbar_init(&sh->drain, 1);
@@ -217,7 +227,7 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = sh->tmem;
-  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
+  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + C::kDv, t_dk = tmem + C::kDk, t_p = tmem + C::kP, t_ds = tmem + C::kDs;
   KvItem it;
 
   if (warp == kLoadWarp || warp == kLoadWarp + 1) {
@@ -247,8 +257,11 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
           if (r.turn > 0) ok = wait_all(ab, &empty[r.slot], (r.turn - 1) & 1, a.status);
           if (!ok) break;
           if (elect()) {
-            mbar_expect_tx(&full[r.slot], kTile);
+            mbar_expect_tx(&full[r.slot], kTile + (second ? sizeof(sh->row[0]) : 0));
             load_rows<D>(at + r.slot * kTile, second ? &domap : &qmap, it.head0 + h, it.lo + m * kRows, &full[r.slot]);
+            if (second)
+              bulk_load(smem_addr(sh->row[r.slot]), a.stats + ((it.head0 + h) * a.stat_tiles + it.slot0 + m) * 256,
+                        sizeof(sh->row[0]), &full[r.slot]);
           }
           ++copies;
           r.next(slots);
@@ -304,12 +317,16 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
         if (!ok) break;
         fence_after_sync();
         if (elect()) {
-          mma_rows<D, kCols>(t_dv, t_s, do_mn + rd.slot * kStep, t > 0);
-          mma_commit(&sh->do_empty[rd.slot]);
-          if (more) {
+          auto next = [&]() {
+            if (!more) return;
             mma_scores<D>(t_s, k_at, q_at + nq.slot * kStep);
             mma_commit(&sh->s_full);
-          }
+          };
+          if (C::kOwn) next();
+          mma_rows<D, C::kOwn ? 128 : kCols>(t_dv, t_p, do_mn + rd.slot * kStep, t > 0);
+          mma_commit(&sh->do_empty[rd.slot]);
+          if (C::kOwn) mma_commit(&sh->p_free);
+          if (!C::kOwn) next();
         }
         {  // dS(t), the next d_o
           uint64_t* bar = &sh->ds_ready;
@@ -321,15 +338,18 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
         if (!ok) break;
         fence_after_sync();
         if (elect()) {
-          mma_rows<D, kCols>(t_dk, t_dp, q_mn + rq.slot * kStep, t > 0);
-          mma_commit(&sh->q_empty[rq.slot]);
-          if (more) {
+          auto next = [&]() {
+            if (!more) return;
             mma_scores<D>(t_dp, v_at, do_at + nd.slot * kStep);
             mma_commit(&sh->dp_full);
             if (t + 2 == steps) mma_commit(&sh->kv_empty);
-          } else {
-            mma_commit(&sh->done);
-          }
+          };
+          if (C::kOwn) next();
+          mma_rows<D, C::kOwn ? 128 : kCols>(t_dk, t_ds, q_mn + rq.slot * kStep, t > 0);
+          mma_commit(&sh->q_empty[rq.slot]);
+          if (C::kOwn) mma_commit(&sh->ds_free);
+          if (!C::kOwn) next();
+          if (!more) mma_commit(&sh->done);
         }
         rq = nq;
         rd = nd;
@@ -347,27 +367,13 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
     Ring rq, rd;
     for (; item_at(a, tiles, handout_take(&sh->items, items), it); ++items) {
       const int steps = it.steps();
-      const bool rows = mt < 2 * kRows;  // the first two warpgroups fetch lse and delta
-      const float* const src = mt < kRows ? a.lse : a.delta;
-      // lse or delta of query row mt % 128 of a step; 0 past the sequence
-      auto fetch = [&](int h, int m) {
-        const int at = m * kRows + row;
-        return rows && at < it.L ? src[static_cast<int64_t>(it.head0 + h) * a.S + it.lo + at] : 0.f;
-      };
-      float ahead = fetch(0, it.j);
-      int h = 0, m = it.j;
+      int m = it.j;
       for (int t = 0; t < steps; ++t, ++turn) {
-        if (rows) sh->row[turn & 1][mt < kRows ? 0 : 1][row] = mt < kRows ? ahead * -1.4426950408889634f : -ahead;
-        named_bar_sync(1, 32 * kMathWarps);
         const int past = it.L - m * kRows;       // query rows of the tile from here on are another sequence's
         const bool diagonal = m == it.j, tail = past < kRows;
-        if (++m == it.nt) {
-          m = it.j;
-          ++h;
-        }
-        if (t + 1 < steps) ahead = fetch(h, m);
-        const ulonglong2* const lse2 = reinterpret_cast<const ulonglong2*>(sh->row[turn & 1][0] + kCols * wg);
-        const ulonglong2* const del2 = reinterpret_cast<const ulonglong2*>(sh->row[turn & 1][1] + kCols * wg);
+        if (++m == it.nt) m = it.j;
+        const ulonglong2* const lse2 = reinterpret_cast<const ulonglong2*>(sh->row[rd.slot][0] + kCols * wg);
+        const ulonglong2* const del2 = reinterpret_cast<const ulonglong2*>(sh->row[rd.slot][1] + kCols * wg);
         // columns (queries) that see this thread's key
         uint32_t see[kParts];
 #pragma unroll
@@ -381,10 +387,11 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
           }
         }
         const bool all = !(diagonal || tail);
+        wait_all(ab, &sh->do_full[rd.slot], rd.turn & 1, a.status);  // lse and delta
         wait_all(ab, &sh->s_full, turn & 1, a.status);
         if (tail) {  // those rows' Q and d_o to zero, once the scores' products have read them
           wait_all(ab, &sh->dp_full, turn & 1, a.status);
-          if (rows && row >= past) zero_row<D>(mt < kRows ? qt + rq.slot * kTile : dot + rd.slot * kTile, row);
+          if (mt < 2 * kRows && row >= past) zero_row<D>(mt < kRows ? qt + rq.slot * kTile : dot + rd.slot * kTile, row);
           fence_async_smem();
         }
         fence_after_sync();
@@ -399,7 +406,8 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
             ex2_pair(fma2(pack2(p[c][e + 2], p[c][e + 3]), sc2, l.y), p[c][e + 2], p[c][e + 3]);
           }
         if (!all) hide(p, see);
-        store_bf16(my_s, p);
+        if (C::kOwn && turn > 0) wait_all(ab, &sh->p_free, (turn - 1) & 1, a.status);
+        store_bf16(C::kOwn ? t_p + lane_base + kCols / 2 * wg : my_s, p);
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
@@ -420,11 +428,15 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
             x[c][e + 3] = __float_as_uint(h.y);
           }
         if (!all) hide(x, see);
-        store_bf16(my_dp, x);
+        if (C::kOwn && turn > 0) wait_all(ab, &sh->ds_free, (turn - 1) & 1, a.status);
+        store_bf16(C::kOwn ? t_ds + lane_base + kCols / 2 * wg : my_dp, x);
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->ds_ready);
+        if (lane == 0) {
+          mbar_arrive(&sh->ds_ready);
+          mbar_arrive(&sh->do_empty[rd.slot]);
+        }
         rq.next(C::kQ);
         rd.next(C::kDo);
       }
@@ -486,6 +498,7 @@ struct QShared {
   int abort_;
 };
 struct QItem {
+  int64_t slot;  // in the statistics
   int lo, L, m, head, hk;  // query tile m: key tiles 0 .. m
 };
 __device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t x, QItem& it) {
@@ -494,6 +507,7 @@ __device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t 
   it.lo = t.lo;
   it.L = t.L;
   it.m = t.w - 1;
+  it.slot = t.slot(it.m);
   it.head = static_cast<int>(x % a.Hq);
   it.hk = it.head / (a.Hq / a.Hkv);
   return true;
@@ -748,7 +762,11 @@ __global__ void __launch_bounds__(QMath<D>::kThreads, 1)
       {
         const float2 s = unpack2(add2(rest2[0], rest2[1]));
         const float rest = together(s.x + s.y);
-        if (used && wg == 0) a.delta[stat] = delta + rest;
+        if (wg == 0) {
+          float* const to = a.stats + (it.head * a.stat_tiles + it.slot) * 256 + row;
+          to[0] = unpack2(lse2).x;
+          to[kRows] = used ? -(delta + rest) : 0.f;
+        }
       }
       const bool fine = wait_all(ab, &sh->done, items & 1, a.status);
       fence_after_sync();
@@ -767,7 +785,7 @@ __global__ void __launch_bounds__(QMath<D>::kThreads, 1)
 template <int D>
 cudaError_t launch(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                    const CUtensorMap& d_o, cudaStream_t s) {
-  const size_t smem_kv = KvCfg<D>::kBytes + sizeof(KvShared), smem_q = QCfg<D>::kBytes + sizeof(QShared);
+  const size_t smem_kv = KvCfg<D>::kBytes + sizeof(KvShared<D>), smem_q = QCfg<D>::kBytes + sizeof(QShared);
   static PerDevice kept_kv, kept_q;
   int64_t sms = 0;
   cudaError_t e = packed_sms(kept_kv, kda_packed_dkv_kernel<D>, smem_kv, &sms);
