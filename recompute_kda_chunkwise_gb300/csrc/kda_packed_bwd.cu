@@ -15,8 +15,7 @@
 // dv += P^T d_o and dk += dS^T Q straight from TMEM: neither goes through
 // shared memory, whose bandwidth bounds products of two operands there. While
 // the warps form P^T the tensor cores run dS^T's product and the next dP^T, and
-// the other way round: the order is dv(t), S(t+1), dk(t), dP(t+1). With heads of
-// 64 P^T and dS^T have columns of their own and the next scores go first.
+// the other way round: the order is dv(t), S(t+1), dk(t), dP(t+1).
 // A key/value head's keys go over all query heads of its group in one item, or
 // over a part of them where there are few items: the parts are then added up,
 // in order, by another kernel.
@@ -138,10 +137,6 @@ struct KvCfg {
   static constexpr int kTile = kRows * D * 2;
   static constexpr int kQ = D == 128 ? 3 : 5, kDo = D == 128 ? 2 : 4;  // slots of queries, of d_o
   static constexpr int kBytes = (2 + kQ + kDo) * kTile;
-  // Columns of TMEM: S, dP, dv, dk. Heads of 64 leave room for P and dS beside
-  // the scores, so that the next scores need not wait for the products with them.
-  static constexpr bool kOwn = D == 64;
-  static constexpr int kDv = 256, kDk = 256 + D, kP = kOwn ? 384 : 0, kDs = kOwn ? 448 : 128;
 };
 template <int D>
 struct KvShared {
@@ -149,7 +144,7 @@ struct KvShared {
   Handout items;
   uint64_t kv_full, kv_empty;
   uint64_t q_full[5], q_empty[5], do_full[4], do_empty[4];
-  uint64_t s_full, dp_full, p_ready, ds_ready, p_free, ds_free, done, acc_free, drain;
+  uint64_t s_full, dp_full, p_ready, ds_ready, done, acc_free, drain;
   uint32_t tmem;
   int abort_;
 };
@@ -214,8 +209,6 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
     mbar_init(&sh->dp_full, 1);
     mbar_init(&sh->p_ready, kMathWarps);
     mbar_init(&sh->ds_ready, kMathWarps);
-    mbar_init(&sh->p_free, 1);
-    mbar_init(&sh->ds_free, 1);
     mbar_init(&sh->done, 1);
     mbar_init(&sh->acc_free, kMathWarps);
     mbar_init(&sh->drain, 1);
@@ -227,7 +220,7 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = sh->tmem;
-  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + C::kDv, t_dk = tmem + C::kDk, t_p = tmem + C::kP, t_ds = tmem + C::kDs;
+  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
   KvItem it;
 
   if (warp == kLoadWarp || warp == kLoadWarp + 1) {
@@ -317,16 +310,12 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
         if (!ok) break;
         fence_after_sync();
         if (elect()) {
-          auto next = [&]() {
-            if (!more) return;
+          mma_rows<D, kCols>(t_dv, t_s, do_mn + rd.slot * kStep, t > 0);
+          mma_commit(&sh->do_empty[rd.slot]);
+          if (more) {
             mma_scores<D>(t_s, k_at, q_at + nq.slot * kStep);
             mma_commit(&sh->s_full);
-          };
-          if (C::kOwn) next();
-          mma_rows<D, C::kOwn ? 128 : kCols>(t_dv, t_p, do_mn + rd.slot * kStep, t > 0);
-          mma_commit(&sh->do_empty[rd.slot]);
-          if (C::kOwn) mma_commit(&sh->p_free);
-          if (!C::kOwn) next();
+          }
         }
         {  // dS(t), the next d_o
           uint64_t* bar = &sh->ds_ready;
@@ -338,18 +327,15 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
         if (!ok) break;
         fence_after_sync();
         if (elect()) {
-          auto next = [&]() {
-            if (!more) return;
+          mma_rows<D, kCols>(t_dk, t_dp, q_mn + rq.slot * kStep, t > 0);
+          mma_commit(&sh->q_empty[rq.slot]);
+          if (more) {
             mma_scores<D>(t_dp, v_at, do_at + nd.slot * kStep);
             mma_commit(&sh->dp_full);
             if (t + 2 == steps) mma_commit(&sh->kv_empty);
-          };
-          if (C::kOwn) next();
-          mma_rows<D, C::kOwn ? 128 : kCols>(t_dk, t_ds, q_mn + rq.slot * kStep, t > 0);
-          mma_commit(&sh->q_empty[rq.slot]);
-          if (C::kOwn) mma_commit(&sh->ds_free);
-          if (!C::kOwn) next();
-          if (!more) mma_commit(&sh->done);
+          } else {
+            mma_commit(&sh->done);
+          }
         }
         rq = nq;
         rd = nd;
@@ -406,8 +392,7 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
             ex2_pair(fma2(pack2(p[c][e + 2], p[c][e + 3]), sc2, l.y), p[c][e + 2], p[c][e + 3]);
           }
         if (!all) hide(p, see);
-        if (C::kOwn && turn > 0) wait_all(ab, &sh->p_free, (turn - 1) & 1, a.status);
-        store_bf16(C::kOwn ? t_p + lane_base + kCols / 2 * wg : my_s, p);
+        store_bf16(my_s, p);
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
@@ -428,8 +413,7 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
             x[c][e + 3] = __float_as_uint(h.y);
           }
         if (!all) hide(x, see);
-        if (C::kOwn && turn > 0) wait_all(ab, &sh->ds_free, (turn - 1) & 1, a.status);
-        store_bf16(C::kOwn ? t_ds + lane_base + kCols / 2 * wg : my_dp, x);
+        store_bf16(my_dp, x);
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
