@@ -552,14 +552,16 @@ Grads grads_of(PyObject* list, const char* name) {
   g.p.reserve(num);
   g.dtype.reserve(num);
   for (Py_ssize_t i = 0; i < num; ++i) {
-    const std::string which = std::string(name) + "[" + std::to_string(i) + "]";
-    if (!THPVariable_Check(items[i])) throw Refused(which + " must be a tensor");
+    const auto which = [&]() { return std::string(name) + "[" + std::to_string(i) + "]"; };
+    if (!THPVariable_Check(items[i])) throw Refused(which() + " must be a tensor");
     const Tensor& t = THPVariable_Unpack(items[i]);
-    if (!t.is_cuda() || (i > 0 && t.get_device() != g.t[0].get_device()) || t.layout() != at::kStrided ||
-        !t.is_non_overlapping_and_dense())
-      throw Refused(which + " must be a dense CUDA tensor on the first one's device (got " + text(t.sizes()) +
+    const bool dense = t.layout() == at::kStrided && (t.is_contiguous() || t.is_non_overlapping_and_dense());
+    if (!t.is_cuda() || (i > 0 && t.get_device() != g.t[0].get_device()) || !dense)
+      throw Refused(which() + " must be a dense CUDA tensor on the first one's device (got " + text(t.sizes()) +
                     (t.is_cuda() ? ")" : " on the CPU)"));
-    g.dtype.push_back(activation(t, (which + " must be").c_str()));
+    const auto dt = t.scalar_type();
+    g.dtype.push_back(dt == at::kBFloat16 ? KDA_DTYPE_BF16
+                                          : dt == at::kFloat ? KDA_DTYPE_F32 : activation(t, (which() + " must be").c_str()));
     g.p.push_back(t.numel() ? t.data_ptr() : nullptr);
     g.n.push_back(t.numel());
     g.t.push_back(t);
@@ -575,6 +577,7 @@ void no_overlap(const Grads& g, const Grads& o) {
     size_t i;
   };
   std::vector<Range> r;
+  r.reserve(2 * g.t.size());
   for (size_t i = 0; i < g.t.size(); ++i) {
     if (g.n[i] == 0) continue;
     const auto add = [&](const Grads& x, bool out) {
@@ -616,9 +619,10 @@ PyObject* clip(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
   return guarded(nargs, 4, [&]() -> PyObject* {
     const Args a{v};
     const Grads g = grads_of(v[0], "grads");
-    const Grads o = grads_of(v[2] == Py_None ? v[0] : v[2], v[2] == Py_None ? "grads" : "out");
+    const Grads other = v[2] == Py_None ? Grads() : grads_of(v[2], "out");
+    const Grads& o = v[2] == Py_None ? g : other;
     if (o.t.size() != g.t.size()) throw Refused("out must have as many tensors as grads");
-    for (size_t i = 0; i < g.t.size(); ++i)
+    for (size_t i = 0; &o != &g && i < g.t.size(); ++i)
       if (o.t[i].sizes() != g.t[i].sizes() || o.t[i].strides() != g.t[i].strides() ||
           o.t[i].get_device() != g.t[i].get_device() || (g.n[i] > 0 && o.p[i] == g.p[i] && o.dtype[i] != g.dtype[i]))
         throw Refused("out[" + std::to_string(i) + "] must have the shape, strides and device of grads[" + std::to_string(i) + "]");

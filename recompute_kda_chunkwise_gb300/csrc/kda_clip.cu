@@ -138,6 +138,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) kda_squares_kernel(const __grid_constant__ Table<N> tb, double* sums) {
   __shared__ double s[kThreads / 32];
   const int tid = static_cast<int>(threadIdx.x);
+  before_kernel();
   double all = 0;
   for (int chunk = static_cast<int>(blockIdx.x); chunk < tb.first[tb.num]; chunk += static_cast<int>(gridDim.x)) {
     const int i = tensor_of(tb, chunk);
@@ -195,6 +196,7 @@ __device__ __forceinline__ double norm_of(const double* sums, int num, double* s
 
 __global__ void __launch_bounds__(kThreads) kda_norm_of_sums_kernel(const double* sums, int num, float* norm) {
   __shared__ double s[kThreads / 32];
+  after_kernel();
   const double n = norm_of(sums, num, s);
   if (threadIdx.x == 0) *norm = static_cast<float>(n);
 }
@@ -204,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, kScaleCtas) kda_scale_kernel(const _
                                                              double most, float* norm) {
   __shared__ double s[kThreads / 32];
   const int tid = static_cast<int>(threadIdx.x);
+  after_kernel();
   const double n = norm_of(sums, num, s);
   if (norm && blockIdx.x == 0 && tid == 0) *norm = static_cast<float>(n);
   // what the caller sees as not finite (fp32) clips nothing
@@ -305,16 +308,14 @@ kda_status run(const Call& c) {
     kda_squares_kernel<N><<<grid, kThreads, 0, c.s>>>(tb, c.sums + sums);
     sums += grid;
   }
-  if (!c.outs) {
-    kda_norm_of_sums_kernel<<<1, kThreads, 0, c.s>>>(c.sums, sums, c.norm);
-  } else {
-    for (int i0 = c.num <= N ? 0 : (c.num - 1) / N * N; i0 >= 0; i0 -= N) {  // last ones first
-      fill(tb, i0, c.num - i0 < N ? c.num - i0 : N, c.g, c.sizes, c.dtypes, c.outs, c.out_dtypes);
-      kda_scale_kernel<N><<<grid_of(tb.first[tb.num], c.sms, kScaleCtas), kThreads, 0, c.s>>>(tb, c.sums, sums, c.most,
-                                                                                  i0 == 0 ? c.norm : nullptr);
-    }
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && !c.outs)
+    e = launch_after(kda_norm_of_sums_kernel, 1, kThreads, 0, c.s, static_cast<const double*>(c.sums), sums, c.norm);
+  for (int i0 = c.num <= N ? 0 : (c.num - 1) / N * N; e == cudaSuccess && c.outs && i0 >= 0; i0 -= N) {  // last ones first
+    fill(tb, i0, c.num - i0 < N ? c.num - i0 : N, c.g, c.sizes, c.dtypes, c.outs, c.out_dtypes);
+    e = launch_after(kda_scale_kernel<N>, grid_of(tb.first[tb.num], c.sms, kScaleCtas), kThreads, 0, c.s, tb,
+                     static_cast<const double*>(c.sums), sums, c.most, i0 == 0 ? c.norm : nullptr);
   }
-  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? KDA_OK : set_error(KDA_ERR_CUDA, "gradient norm launch failed: %s", cudaGetErrorString(e));
 }
 

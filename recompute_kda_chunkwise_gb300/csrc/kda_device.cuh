@@ -1,4 +1,5 @@
-// kda_device.cuh -- what launches keep about the devices they go to.
+// kda_device.cuh -- what launches keep about the devices they go to, and
+// launches that overlap the end of the kernel before them.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -34,5 +35,25 @@ class PerDevice {
   static constexpr int kDevices = 64;  // beyond these it is found on every call
   std::atomic<int64_t> kept_[kDevices] = {};
 };
+
+// A launch may begin while the kernel before it in the call still runs: what it
+// reads of that kernel's results comes behind after_kernel(). The kernel before
+// allows it with before_kernel().
+__device__ __forceinline__ void after_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void before_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename K, typename... A>
+cudaError_t launch_after(K kernel, int64_t grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(static_cast<unsigned>(grid));
+  c.blockDim = dim3(static_cast<unsigned>(threads));
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
 
 }  // namespace kda

@@ -18,6 +18,8 @@ __global__ void __launch_bounds__(1024) kda_packed_list_kernel(const int32_t* cu
                                                                int* status) {
   __shared__ int count[kBuckets], sums[32], s_most;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  before_kernel();
+  if (tid < kClearBytes / 4) status[tid] = 0;
   int bad = 0, most = 0;
   for (int n = tid; n < N; n += 1024) {
     const int lo = cu[n], hi = cu[n + 1];
@@ -150,8 +152,21 @@ kda_status begin(const kda_attention_problem* p, int rows, void* workspace, Pack
   a->D = p->head_dim;
   a->scale = p->scale;
   a->split = 1;
-  cudaError_t e = cudaMemsetAsync(workspace, 0, 32, s);  // the status word, and the tickets
-  if (e == cudaSuccess && a->N > 1 && a->S > 0) {
+  // The header is cleared by the call's first kernel: the list's; without a list,
+  // the backward's sums; or the forward's where it hands out nothing.
+  static PerDevice kept;
+  int64_t sms = 0;
+  cudaError_t e = kept.get(&sms, [](int dev, int64_t* n) {
+    int count = 0;
+    const cudaError_t got = cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev);
+    *n = count;
+    return got;
+  });
+  if (e != cudaSuccess) return set_error(KDA_ERR_CUDA, "attention set-up failed: %s", cudaGetErrorString(e));
+  a->fresh = rows == 256 && a->N == 1 && a->S > 0 && (a->S + 255) / 256 * a->Hq <= (sms < kPackedMaxCtas ? sms : kPackedMaxCtas);
+  if (a->S == 0 || (a->N == 1 && rows == 256 && !a->fresh)) {
+    e = cudaMemsetAsync(workspace, 0, kClearBytes, s);
+  } else if (a->N > 1) {
     int* const list = reinterpret_cast<int*>(static_cast<char*>(workspace) + kHeaderBytes);
     kda_packed_list_kernel<<<1, 1024, 0, s>>>(a->cu, a->N, a->S, rows, list, a->status);
     e = cudaGetLastError();

@@ -28,7 +28,9 @@ struct PackedArgs {
   int64_t stat_tiles;
   float* part;         // gradients of k and v by parts of the head group: [2][split][S][Hkv][D]
   int split;
+  int fresh;           // forward of one short sequence: the kernel itself clears the header
 };
+constexpr int kClearBytes = 32;  // of the workspace's header: the status word, and the tickets
 
 // A tile of `rows` rows of a sequence. Weight w counts the tiles up to it: it
 // is tile w - 1 from the sequence's start (or, for work that goes to the
@@ -136,10 +138,10 @@ __device__ __forceinline__ void handout_give(Handout* h, uint32_t n, int64_t x) 
   __syncwarp();
 }
 
-// The next item, fetched and passed on as number n.
-__device__ __forceinline__ int64_t handout_next(Handout* h, uint32_t n, int* ticket, bool ok) {
+// The next of the call's items, fetched and passed on as number n.
+__device__ __forceinline__ int64_t handout_next(Handout* h, uint32_t n, int* ticket, bool ok, int64_t items) {
   int64_t x = kNoItem;
-  if (ok) {
+  if (ok && items > gridDim.x) {
     int i = 0;
     if ((threadIdx.x & 31) == 0) i = atomicAdd(ticket, 1);
     x = static_cast<int64_t>(gridDim.x) + __shfl_sync(~0u, i, 0);

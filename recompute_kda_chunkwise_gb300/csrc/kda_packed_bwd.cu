@@ -110,6 +110,8 @@ template <int D>
 __global__ void __launch_bounds__(256) kda_packed_delta_kernel(const __grid_constant__ PackedArgs a) {
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 3;
   const int sub = threadIdx.x & 7;
+  before_kernel();
+  if (!a.list && i < kClearBytes / 4 && sub == 0) a.status[i] = 0;
   float sum = 0.f;
   if (i < a.S * a.Hq) {
     const uint4* const x = reinterpret_cast<const uint4*>(a.o_in + i * D);
@@ -187,8 +189,6 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* const ab = &sh->abort_;
 
-  const int tiles = tiles_of(a, kRows);
-  if (tiles == 0) return;
   if (smem_addr(smem) & 1023) {
     if (tid == 0) set_status(a.status, KDA_ERR_DEVICE_CHECK);
     return;
@@ -219,6 +219,9 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
+  before_kernel();
+  after_kernel();
+  const int tiles = tiles_of(a, kRows);  // 0: no warp has work
   const uint32_t tmem = sh->tmem;
   const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
   KvItem it;
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
           r.next(slots);
         }
       }
-      x = second ? handout_take(&sh->items, items + 1) : handout_next(&sh->items, items + 1, &a.tickets[1], ok);
+      x = second ? handout_take(&sh->items, items + 1) : handout_next(&sh->items, items + 1, &a.tickets[1], ok, static_cast<int64_t>(tiles) * a.Hkv * a.split);
     }
     // after an abort: the copies in flight land before the CTA ends
     if (!ok) {
@@ -512,8 +515,6 @@ __global__ void __launch_bounds__(QMath<D>::kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* const ab = &sh->abort_;
 
-  const int tiles = tiles_of(a, kRows);
-  if (tiles == 0) return;
   if (smem_addr(smem) & 1023) {
     if (tid == 0) set_status(a.status, KDA_ERR_DEVICE_CHECK);
     return;
@@ -546,6 +547,9 @@ __global__ void __launch_bounds__(QMath<D>::kThreads, 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
+  before_kernel();
+  after_kernel();
+  const int tiles = tiles_of(a, kRows);  // 0: no warp has work
   const uint32_t tmem = sh->tmem;
   const uint32_t t_s = tmem, t_dp = tmem + 128, t_dq = tmem + 384;  // dP at t_dp and t_dp + 128 in turn
   QItem it;
@@ -582,7 +586,7 @@ __global__ void __launch_bounds__(QMath<D>::kThreads, 1)
         ++copies;
         r.next(slots);
       }
-      x = v ? handout_take(&sh->items, items + 1) : handout_next(&sh->items, items + 1, &a.tickets[0], ok);
+      x = v ? handout_take(&sh->items, items + 1) : handout_next(&sh->items, items + 1, &a.tickets[0], ok, static_cast<int64_t>(tiles) * a.Hq);
     }
     if (!ok) {
       for (int64_t p = copies > slots ? copies - slots : 0; p < copies; ++p)
@@ -779,10 +783,16 @@ cudaError_t launch(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap&
   const float sc = a.scale * 1.4426950408889634f;
   const int64_t tiles = a.S / kRows + a.N, kv = tiles * a.Hkv * a.split, nq = tiles * a.Hq;
   kda_packed_delta_kernel<D><<<static_cast<unsigned>((a.S * a.Hq * 8 + 255) / 256), 256, 0, s>>>(a);
-  kda_packed_dq_kernel<D><<<static_cast<unsigned>(nq < sms ? nq : sms), QMath<D>::kThreads, smem_q, s>>>(a, q, k, v, d_o, sc);
-  kda_packed_dkv_kernel<D><<<static_cast<unsigned>(kv < sms ? kv : sms), KvMath<D>::kThreads, smem_kv, s>>>(a, q, k, v, d_o, sc);
-  if (a.split > 1) kda_packed_parts_kernel<<<static_cast<unsigned>((2 * a.S * a.Hkv * a.D / 4 + 255) / 256), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e == cudaSuccess)
+    e = launch_after(kda_packed_dq_kernel<D>, nq < sms ? nq : sms, QMath<D>::kThreads, smem_q, s, a, q, k, v, d_o, sc);
+  if (e == cudaSuccess)
+    e = launch_after(kda_packed_dkv_kernel<D>, kv < sms ? kv : sms, KvMath<D>::kThreads, smem_kv, s, a, q, k, v, d_o, sc);
+  if (e == cudaSuccess && a.split > 1) {
+    kda_packed_parts_kernel<<<static_cast<unsigned>((2 * a.S * a.Hkv * a.D / 4 + 255) / 256), 256, 0, s>>>(a);
+    e = cudaGetLastError();
+  }
+  return e;
 }
 
 }  // namespace

@@ -79,8 +79,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* const ab = &sh->abort_;
 
-  const int tiles = tiles_of(a, 2 * kRows);
-  if (tiles == 0) return;
   if (smem_addr(smem) & 1023) {  // the swizzle needs it; no static shared memory comes before
     if (tid == 0) set_status(a.status, KDA_ERR_DEVICE_CHECK);
     return;
@@ -107,6 +105,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
+  after_kernel();
+  if (a.fresh && blockIdx.x == 0 && tid < kClearBytes / 4) a.status[tid] = 0;
+  if (a.fresh) __syncthreads();
+  const int tiles = tiles_of(a, 2 * kRows);  // 0: no warp has work
   const uint32_t tmem = sh->tmem;
   const uint32_t tmem_s = tmem, tmem_o = tmem + 256;  // S (P over it) of stream i at + 128 i, O at + 128 i
   Item it;
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           r.next(kSlots);
         }
       }
-      x = handout_next(&sh->items, items, &a.tickets[0], ok);
+      x = handout_next(&sh->items, items, &a.tickets[0], ok, static_cast<int64_t>(tiles) * a.Hq);
     }
     // after an abort: the copies in flight land before the CTA ends
     if (!ok) {
@@ -372,8 +374,7 @@ cudaError_t launch(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap&
   const int64_t most = (a.S / (2 * kRows) + a.N) * a.Hq;  // items
   int64_t ctas = sms < kPackedMaxCtas ? sms : kPackedMaxCtas;
   if (ctas > most) ctas = most;
-  kda_packed_fwd_kernel<D><<<static_cast<unsigned>(ctas), kThreads, smem, s>>>(a, q, k, v, a.scale * 1.4426950408889634f);
-  return cudaGetLastError();
+  return launch_after(kda_packed_fwd_kernel<D>, ctas, kThreads, smem, s, a, q, k, v, a.scale * 1.4426950408889634f);
 }
 
 }  // namespace
