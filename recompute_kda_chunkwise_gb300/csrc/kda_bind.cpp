@@ -635,7 +635,10 @@ PyObject* clip(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     void* const wsp = buffer(ws, g_entry.norm_of_grads_bytes(num), norm);
     const kda_status r = g_entry.clip(num, g.p.data(), g.n.data(), g.dtype.data(), const_cast<void* const*>(o.p.data()),
                                       o.dtype.data(), a.number(1), static_cast<float*>(norm.data_ptr()), wsp, stream_of(norm));
-    return r == KDA_OK ? wrap(norm) : PyLong_FromLong(r);
+    if (r != KDA_OK) return PyLong_FromLong(r);
+    for (const Tensor& x : o.t)  // written behind autograd's back: a graph that saved one has to notice
+      if (!x.is_inference()) x.unsafeGetTensorImpl()->bump_version();
+    return wrap(norm);
   });
 }
 

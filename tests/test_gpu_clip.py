@@ -150,3 +150,38 @@ def test_the_same_bits_every_time_and_captured():
         graph.replay()
     s.synchronize()
     assert torch.equal(n, want) and all(torch.equal(a, b) for a, b in zip(got, out))
+
+
+def test_a_graph_that_saved_a_clipped_tensor_notices():
+    from recompute_kda_chunkwise_gb300 import grads as G
+    w, x = torch.ones(8, device="cuda", requires_grad=True), torch.full((8,), 3.0, device="cuda")
+    y = (w * x).sum()
+    G.clip_grads([x], 1.0)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward()
+    with torch.inference_mode():
+        z = torch.full((4,), 2.0, device="cuda")
+        assert G.clip_grads([z], 1.0).item() == 4.0 and z.tolist() == [0.5] * 4
+
+
+def test_workspace_of_the_caller_shared_by_two_graphs():
+    from recompute_kda_chunkwise_gb300 import grads as G
+    ws = torch.empty(8192, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="workspace"):
+        G.grad_norm([torch.ones(3, device="cuda")], workspace=ws[:100])
+    a, b = make([(50_000,), (9,)], 1), make([(123,), (40_000,), (7, 7)], 2)
+    want = [G.grad_norm(a).item(), G.grad_norm(b).item()]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        graphs, norms = [], []
+        for ts in (a, b):
+            G.grad_norm(ts, workspace=ws)
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=s):
+                norms.append(G.grad_norm(ts, workspace=ws))
+        for _ in range(3):
+            for g in graphs:
+                g.replay()
+    s.synchronize()
+    assert [n.item() for n in norms] == want

@@ -176,3 +176,92 @@ def test_captured_with_other_work_on_another_stream():
     s.synchronize()
     for a, n in zip((o, lse, *g), ("o", "lse", "dq", "dk", "dv")):
         assert torch.equal(a, want[n]), n
+
+
+def test_more_tiles_than_buckets_in_the_list():
+    """A sequence of more than 1024 tiles beside a short one: tiles are sorted by buckets of lengths. A few
+    rows of the long one against float64; the short one as alone."""
+    from recompute_kda_chunkwise_gb300 import attention as A
+    lens, D = (140_000, 70), 64
+    q, k, v, d_o, cu = inputs(lens, 1, 1, D, seed=37)
+    got = run(q, k, v, d_o, cu)
+    ref, bar = R.attention(*(t[140_000:] for t in (q, k, v)), [0, 70], 0.125, d_o[140_000:])
+    R.check_all({n: t[140_000:] if n != "lse" else t[:, 140_000:] for n, t in got.items()}, ref, bar)
+    x, y, z, w = (t[:140_000, 0].double() for t in (q, k, v, d_o))
+    for r in (0, 1, 127, 128, 65_535, 131_071, 139_999):
+        s = (y[:r + 1] @ x[r]) * 0.125
+        p = torch.softmax(s, 0)
+        o, dp = p @ z[:r + 1], z[:r + 1] @ w[r]
+        delta = w[r] @ o
+        ds = p * (dp - delta)
+        fine = R.BF + R.FINE
+        R.check(got["o"][r, 0], R.d(o), R.d(fine * (p @ z[:r + 1].abs())), f"o {r}")
+        e = fine * ds.abs() + p * (fine * (w[r].abs() * o.abs()).sum() + R.FINE * (z[:r + 1].abs() @ w[r].abs()))
+        R.check(got["dq"][r, 0], R.d(0.125 * (ds @ y[:r + 1])), R.d(0.125 * (e @ y[:r + 1].abs())), f"dq {r}")
+    # the last keys are seen by the last queries only
+    lo = 140_000 - 40
+    p = torch.exp(x[lo:] @ y[lo:].T * 0.125 - got["lse"][0, lo:140_000].double()[:, None]).tril()
+    R.check(got["dv"][lo:140_000, 0], R.d(p.T @ w[lo:]), R.d((R.BF + R.FINE) * (p.T @ w[lo:].abs())), "dv")
+
+
+def test_refusals():
+    from recompute_kda_chunkwise_gb300 import attention as A
+    from recompute_kda_chunkwise_gb300.kda import KdaError
+    q, k, v, d_o, cu = inputs((40,), 4, 2, 64)
+    with pytest.raises(ValueError, match="bfloat16"):
+        A.attention_fwd(q.float(), k, v, cu)
+    with pytest.raises(ValueError, match="v must be"):
+        A.attention_fwd(q, k, v[:, :1], cu)
+    with pytest.raises(ValueError, match="k must be"):
+        A.attention_fwd(q, k[:30], v, cu)
+    with pytest.raises(ValueError, match="cu_seqlens"):
+        A.attention_fwd(q, k, v, cu.long())
+    with pytest.raises(ValueError, match="workspace"):
+        A.attention_bwd(q, k, v, q, torch.zeros(4, 40, device="cuda"), d_o, cu, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="lse"):
+        A.attention_bwd(q, k, v, q, torch.zeros(40, 4, device="cuda"), d_o, cu)
+    with pytest.raises(ValueError, match="d_o"):
+        A.attention_bwd(q, k, v, q, torch.zeros(4, 40, device="cuda"), d_o.transpose(0, 1).contiguous().transpose(0, 1), cu)
+    for bad, what in ((dict(scale=0.0), "scale"), (dict(scale=-0.1), "scale")):
+        with pytest.raises(KdaError, match=what):
+            A.attention_fwd(q, k, v, cu, **bad)
+    with pytest.raises(KdaError, match="multiple"):
+        A.attention_fwd(q[:, :3], k, v, cu)
+    with pytest.raises(KdaError, match="k_stride"):
+        A.attention_fwd(q, k[:1].expand(40, 2, 64), v, cu)
+    with pytest.raises(KdaError, match="head_dim"):
+        A.attention_fwd(q[..., :32].contiguous(), k[..., :32].contiguous(), v[..., :32].contiguous(), cu)
+
+
+def test_two_streams_at_once_and_a_workspace_of_two_graphs():
+    from recompute_kda_chunkwise_gb300 import attention as A
+    cases = [inputs((900,), 8, 2, 128, seed=41), inputs((500, 31, 77), 8, 8, 64, seed=43)]
+    want = [run(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [None, None]
+    for _ in range(5):
+        for i, (s, (q, k, v, d_o, cu)) in enumerate(zip(streams, cases)):
+            with torch.cuda.stream(s):
+                o, lse = A.attention_fwd(q, k, v, cu)
+                got[i] = (o, lse, *A.attention_bwd(q, k, v, o, lse, d_o, cu))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(a, w[n]) for a, n in zip(g, ("o", "lse", "dq", "dk", "dv")))
+    ws = torch.empty(max(A.attention_workspace_bytes(c[0], c[1], c[4], backward=True) for c in cases), dtype=torch.uint8, device="cuda")
+    ws.fill_(255)  # nothing of it is read before it is written
+    s, graphs, got = streams[0], [], []
+    with torch.cuda.stream(s):
+        for q, k, v, d_o, cu in cases:
+            o, lse = A.attention_fwd(q, k, v, cu, workspace=ws)
+            A.attention_bwd(q, k, v, o, lse, d_o, cu, workspace=ws)
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=s):
+                o, lse = A.attention_fwd(q, k, v, cu, workspace=ws)
+                got.append((o, lse, *A.attention_bwd(q, k, v, o, lse, d_o, cu, workspace=ws)))
+        for _ in range(2):
+            for g in graphs:
+                g.replay()
+    s.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(a, w[n]) for a, n in zip(g, ("o", "lse", "dq", "dk", "dv")))

@@ -196,3 +196,33 @@ def test_captured_on_another_stream():
         graph.replay()
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_refusals():
+    from recompute_kda_chunkwise_gb300 import rotary
+    from recompute_kda_chunkwise_gb300.kda import KdaError
+    rope = make(64, "half", None)
+    x, cu = rand(gen(1), 10, 2, 64), torch.tensor([0, 10], dtype=I32, device="cuda")
+    pos = torch.arange(10, dtype=I32, device="cuda")
+    with pytest.raises(ValueError, match="one of positions"):
+        rotary.rotary_fwd(rope, x)
+    with pytest.raises(ValueError, match="one of positions"):
+        rotary.rotary_fwd(rope, x, positions=pos, cu_seqlens=cu)
+    with pytest.raises(ValueError, match="positions"):
+        rotary.rotary_fwd(rope, x, positions=pos.long())
+    with pytest.raises(ValueError, match="contiguous within a token"):
+        rotary.rotary_fwd(rope, x.transpose(0, 1).contiguous().transpose(0, 1), positions=pos)
+    with pytest.raises(ValueError, match="k must be"):
+        rotary.rotary_fwd(rope, x, x[:5], positions=pos)
+    with pytest.raises(ValueError, match="q_out"):
+        rotary.rotary_fwd(rope, x, positions=pos, out=(x[:, :1], None))
+    with pytest.raises(ValueError, match="k_out"):
+        rotary.rotary_fwd(rope, x, positions=pos, out=(None, x))
+    with pytest.raises(KdaError, match="rotary_dim"):
+        rotary.rotary_fwd(make(66, "half", None), x, positions=pos)
+    with pytest.raises(KdaError, match="aligned"):
+        rotary.rotary_fwd(rope, torch.zeros(10 * 128 + 4, dtype=BF, device="cuda")[4:].view(10, 2, 64), positions=pos)
+    with pytest.raises(KdaError, match="stride"):
+        rotary.rotary_fwd(rope, torch.zeros(10, 132, dtype=BF, device="cuda")[:, :128].view(10, 2, 64), positions=pos)
+    none = rotary.rotary_fwd(rope, x[:0], x[:0], cu_seqlens=cu * 0)
+    assert none[0].shape == (0, 2, 64) and none[1].shape == (0, 2, 64)
