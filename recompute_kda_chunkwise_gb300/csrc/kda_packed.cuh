@@ -80,6 +80,34 @@ __device__ __forceinline__ bool wait_or(int* abort_, uint64_t* bar, uint32_t par
 __device__ __forceinline__ bool wait_all(int* abort_, uint64_t* bar, uint32_t parity, int* status) {
   return __all_sync(~0u, wait_or(abort_, bar, parity, status));
 }
+// Waits of the one thread that issues the products, for up to three barriers at
+// once (given twice where there are fewer): its instructions between two products
+// are time in which the tensor cores run dry, since it is held up by the products
+// themselves until few of them are left.
+__device__ __forceinline__ bool poll3(uint32_t a0, uint32_t p0, uint32_t a1, uint32_t p1, uint32_t a2, uint32_t p2) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p, q, r;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 r, [%5], %6;\n"
+      "and.pred p, p, q;\nand.pred p, p, r;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(a0), "r"(p0 & 1), "r"(a1), "r"(p1 & 1), "r"(a2), "r"(p2 & 1)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait3(int* abort_, int* status, uint32_t a0, uint32_t p0, uint32_t a1, uint32_t p1,
+                                      uint32_t a2, uint32_t p2) {
+  for (int it = 0; it < (1 << 22); ++it) {
+    if (poll3(a0, p0, a1, p1, a2, p2)) return true;
+    if ((it & 15) == 15 && *const_cast<volatile int*>(abort_)) return false;
+  }
+  *const_cast<volatile int*>(abort_) = 1;
+  set_status(status, KDA_ERR_TIMEOUT);
+  return false;
+}
+
 // Waits, at most so long, without giving up; whether the phase is over.
 __device__ __forceinline__ bool settle_for(uint64_t* bar, uint32_t parity) {
   const uint32_t at = smem_addr(bar);
@@ -125,6 +153,15 @@ __device__ __forceinline__ int64_t handout_take(Handout* h, uint32_t n) {
   const int64_t x = *const_cast<volatile int64_t*>(&h->item[slot]);
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(&h->empty[slot]);
+  return x;
+}
+// The same by a single thread that stands for its warp.
+__device__ __forceinline__ int64_t handout_take_alone(Handout* h, uint32_t n) {
+  if (n == 0) return blockIdx.x;
+  const int slot = (n - 1) & 1;
+  settle_long(&h->full[slot], (n - 1) >> 1 & 1);
+  const int64_t x = *const_cast<volatile int64_t*>(&h->item[slot]);
+  mbar_arrive(&h->empty[slot]);
   return x;
 }
 // Passes on item n > 0, by the fetching warp.

@@ -46,7 +46,7 @@ struct Math {
 template <int D>
 using KvMath = Math<4>;
 template <int D>
-using QMath = Math<D == 128 ? 2 : 4>;
+using QMath = Math<4>;
 constexpr int kMmaWarp = 0, kLoadWarp = 1, kMathWarp = 4;
 
 // P x 32 columns of a tile, a thread's.
@@ -272,64 +272,49 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
       if (kv) settle_for(&sh->kv_full, (items - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
-    const uint32_t k_at = desc_k(kt), v_at = desc_k(vt), q_at = desc_k(qt), do_at = desc_k(dot);
-    const uint32_t q_mn = desc_mn(qt), do_mn = desc_mn(dot);
-    constexpr uint32_t kStep = kTile >> 4;  // from a slot's descriptor to the next
-    Ring rq, rd;  // of step t
-    uint32_t items = 0, turn = 0;
-    bool ok = true;
-    for (; item_at(a, tiles, handout_take(&sh->items, items), it); ++items) {
-      const int steps = it.steps();
-      if (!ok) continue;
-      // K and V, the first Q and d_o
-      {
-        uint64_t* bar = &sh->kv_full;
-        uint32_t par = items;
-        if (lane == 1) bar = &sh->q_full[rq.slot], par = rq.turn;
-        if (lane == 2) bar = &sh->do_full[rd.slot], par = rd.turn;
-        ok = wait_all(ab, bar, par & 1, a.status);
-      }
-      if (!ok) continue;
-      fence_after_sync();
-      if (elect()) {
+    // ---- products, issued by one thread ----
+    if (elect()) {
+      const uint32_t k_at = desc_k(kt), v_at = desc_k(vt), q_at = desc_k(qt), do_at = desc_k(dot);
+      const uint32_t q_mn = desc_mn(qt), do_mn = desc_mn(dot);
+      constexpr uint32_t kStep = kTile >> 4;  // from a slot's descriptor to the next
+      const uint32_t q_full = smem_addr(sh->q_full), do_full = smem_addr(sh->do_full), p_ready = smem_addr(&sh->p_ready),
+                     ds_ready = smem_addr(&sh->ds_ready), acc_free = smem_addr(&sh->acc_free);
+      Ring rq, rd;  // of step t
+      uint32_t items = 0, turn = 0;
+      bool ok = true;
+      for (; item_at(a, tiles, handout_take_alone(&sh->items, items), it); ++items) {
+        const int steps = it.steps();
+        // K and V, the first Q and d_o
+        ok = ok && wait3(ab, a.status, smem_addr(&sh->kv_full), items, q_full + 8 * rq.slot, rq.turn, do_full + 8 * rd.slot, rd.turn);
+        if (!ok) continue;
+        fence_after_sync();
         mma_scores<D>(t_s, k_at, q_at + rq.slot * kStep);
         mma_commit(&sh->s_full);
         mma_scores<D>(t_dp, v_at, do_at + rd.slot * kStep);
         mma_commit(&sh->dp_full);
         if (steps == 1) mma_commit(&sh->kv_empty);
-      }
-      for (int t = 0; t < steps; ++t) {
-        const bool more = t + 1 < steps;
-        Ring nq = rq, nd = rd;
-        nq.next(C::kQ);
-        nd.next(C::kDo);
-        {  // P(t), the next Q, and at an item's start the accumulators
-          uint64_t* bar = &sh->p_ready;
-          uint32_t par = turn;
-          if (lane == 1 && more) bar = &sh->q_full[nq.slot], par = nq.turn;
-          if (lane == 2 && t == 0 && items > 0) bar = &sh->acc_free, par = items - 1;
-          ok = wait_all(ab, bar, par & 1, a.status);
-        }
-        if (!ok) break;
-        fence_after_sync();
-        if (elect()) {
+        for (int t = 0; t < steps; ++t, ++turn) {
+          const bool more = t + 1 < steps;
+          Ring nq = rq, nd = rd;
+          nq.next(C::kQ);
+          nd.next(C::kDo);
+          // P(t), the next Q, and at an item's start the accumulators
+          const uint32_t nq_full = more ? q_full + 8 * nq.slot : p_ready, nq_turn = more ? nq.turn : turn;
+          const bool first = t == 0 && items > 0;
+          ok = wait3(ab, a.status, p_ready, turn, nq_full, nq_turn, first ? acc_free : p_ready, first ? items - 1 : turn);
+          if (!ok) break;
+          fence_after_sync();
           mma_rows<D, kCols>(t_dv, t_s, do_mn + rd.slot * kStep, t > 0);
           mma_commit(&sh->do_empty[rd.slot]);
           if (more) {
             mma_scores<D>(t_s, k_at, q_at + nq.slot * kStep);
             mma_commit(&sh->s_full);
           }
-        }
-        {  // dS(t), the next d_o
-          uint64_t* bar = &sh->ds_ready;
-          uint32_t par = turn;
-          if (lane == 1 && more) bar = &sh->do_full[nd.slot], par = nd.turn;
-          ok = wait_all(ab, bar, par & 1, a.status);
-        }
-        ++turn;
-        if (!ok) break;
-        fence_after_sync();
-        if (elect()) {
+          // dS(t), the next d_o
+          const uint32_t nd_full = more ? do_full + 8 * nd.slot : ds_ready, nd_turn = more ? nd.turn : turn;
+          ok = wait3(ab, a.status, ds_ready, turn, nd_full, nd_turn, ds_ready, turn);
+          if (!ok) break;
+          fence_after_sync();
           mma_rows<D, kCols>(t_dk, t_dp, q_mn + rq.slot * kStep, t > 0);
           mma_commit(&sh->q_empty[rq.slot]);
           if (more) {
@@ -339,13 +324,13 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
           } else {
             mma_commit(&sh->done);
           }
+          rq = nq;
+          rd = nd;
         }
-        rq = nq;
-        rd = nd;
       }
+      mma_commit(&sh->drain);
+      settle_for(&sh->drain, 0);
     }
-    if (elect()) mma_commit(&sh->drain);
-    settle_for(&sh->drain, 0);
     __syncwarp();
   } else if (warp >= kMathWarp) {
     const int wg = (warp - kMathWarp) >> 2, row = tid & 127, mt = tid - 32 * kMathWarp;
@@ -473,13 +458,14 @@ struct QCfg {
   static constexpr int kTile = kRows * D * 2;
   static constexpr int kK = D == 128 ? 3 : 5, kV = D == 128 ? 2 : 4;  // slots: a tile of K is held for longer
   static constexpr int kBytes = (2 + kK + kV) * kTile;
+  static constexpr bool kAhead = D == 128;  // scores are read a tile ahead
 };
 struct QShared {
   Handout items;
   float sum[4][kRows];  // per row, of each warpgroup's columns
   uint64_t k_full[5], k_empty[5], v_full[4], v_empty[4];
   uint64_t q_full, q_empty;
-  // dP and dS by buffer: their next phases can be over before every role has seen the last ones
+  // dP and dS by buffer: an item's last dS can be there before the one before it is seen
   uint64_t s_full, s_read, dp_full[2], ds_ready[2], done, acc_free, drain;
   uint32_t tmem;
   int abort_;
@@ -594,68 +580,59 @@ __global__ void __launch_bounds__(QMath<D>::kThreads, 1)
       if (rows) settle_for(&sh->q_full, (items - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
-    const uint32_t q_at = desc_k(smem), do_at = desc_k(smem + kTile), k_at = desc_k(kt), v_at = desc_k(vt), k_mn = desc_mn(kt);
-    constexpr uint32_t kStep = kTile >> 4;  // from a slot's descriptor to the next
-    Ring rk, rv;  // K(j), V(j)
-    uint32_t items = 0, turn = 0;
-    bool ok = true;
-    auto scores = [&](uint32_t n, const Ring& k, const Ring& v, bool last) {  // S and dP of the CTA's n-th tile
-      if (elect()) {
-        mma_scores<D>(t_s, q_at, k_at + k.slot * kStep);
+    // ---- products, issued by one thread ----
+    if (elect()) {
+      const uint32_t q_at = desc_k(smem), do_at = desc_k(smem + kTile), k_at = desc_k(kt), v_at = desc_k(vt), k_mn = desc_mn(kt);
+      constexpr uint32_t kStep = kTile >> 4;  // from a slot's descriptor to the next
+      const uint32_t k_full = smem_addr(sh->k_full), v_full = smem_addr(sh->v_full), ds_full = smem_addr(sh->ds_ready),
+                     s_read = smem_addr(&sh->s_read), acc_free = smem_addr(&sh->acc_free);
+      Ring rk, ks, vs;  // K(j); K and V of the next scores
+      uint32_t items = 0, turn = 0;
+      bool ok = true;
+      auto scores = [&](uint32_t n, bool last) {  // S and dP of the CTA's n-th tile
+        mma_scores<D>(t_s, q_at, k_at + ks.slot * kStep);
         mma_commit(&sh->s_full);
-        mma_scores<D>(t_dp + 128 * (n & 1), do_at, v_at + v.slot * kStep);
+        mma_scores<D>(t_dp + 128 * (n & 1), do_at, v_at + vs.slot * kStep);
         mma_commit(&sh->dp_full[n & 1]);
-        mma_commit(&sh->v_empty[v.slot]);
+        mma_commit(&sh->v_empty[vs.slot]);
         if (last) mma_commit(&sh->q_empty);
-      }
-    };
-    for (; item_at(a, tiles, handout_take(&sh->items, items), it); ++items) {
-      if (!ok) continue;
-      {
-        uint64_t* bar = &sh->q_full;
-        uint32_t par = items;
-        if (lane == 1) bar = &sh->k_full[rk.slot], par = rk.turn;
-        if (lane == 2) bar = &sh->v_full[rv.slot], par = rv.turn;
-        ok = wait_all(ab, bar, par & 1, a.status);
-      }
-      if (!ok) continue;
-      fence_after_sync();
-      scores(turn, rk, rv, it.m == 0);
-      for (int j = 0; j <= it.m; ++j) {
-        const bool more = j < it.m;
-        Ring nk = rk, nv = rv;
-        nk.next(C::kK);
-        nv.next(C::kV);
-        {  // S(j) is read; the next K and V
-          uint64_t* bar = &sh->s_read;
-          uint32_t par = turn;
-          if (lane == 1 && more) bar = &sh->k_full[nk.slot], par = nk.turn;
-          if (lane == 2 && more) bar = &sh->v_full[nv.slot], par = nv.turn;
-          ok = wait_all(ab, bar, par & 1, a.status);
-        }
-        if (!ok) break;
+        ks.next(C::kK);
+        vs.next(C::kV);
+      };
+      for (; item_at(a, tiles, handout_take_alone(&sh->items, items), it); ++items) {
+        ok = ok && wait3(ab, a.status, smem_addr(&sh->q_full), items, k_full + 8 * ks.slot, ks.turn, v_full + 8 * vs.slot, vs.turn);
+        if (!ok) continue;
         fence_after_sync();
-        if (more) scores(turn + 1, nk, nv, j + 1 == it.m);
-        {  // dS(j), and at an item's start the accumulator
-          uint64_t* bar = &sh->ds_ready[turn & 1];
-          uint32_t par = turn >> 1;
-          if (lane == 1 && j == 0 && items > 0) bar = &sh->acc_free, par = items - 1;
-          ok = wait_all(ab, bar, par & 1, a.status);
-        }
-        const uint32_t t_ds = t_dp + 128 * (turn++ & 1);
-        if (!ok) break;
-        fence_after_sync();
-        if (elect()) {
-          mma_rows<D, kCols>(t_dq, t_ds, k_mn + rk.slot * kStep, j > 0);
+        scores(turn, it.m == 0);
+        // S has one buffer: the next scores can be formed once every warp has read the
+        // last. Where they are read a tile ahead, dq(j), S(j + 2) and dP(j + 2) are one
+        // batch behind one wait; else S(j + 1) and dP(j + 1) come before dq(j).
+        auto next = [&](uint32_t bar, uint32_t par, uint32_t n, bool last) {
+          ok = wait3(ab, a.status, bar, par, k_full + 8 * ks.slot, ks.turn, v_full + 8 * vs.slot, vs.turn);
+          if (!ok) return;
+          fence_after_sync();
+          scores(n, last);
+        };
+        if (C::kAhead && it.m > 0) next(s_read, items, turn + 1, it.m == 1);
+        for (int j = 0; ok && j <= it.m; ++j, ++turn) {
+          if (!C::kAhead && j < it.m) next(s_read, turn, turn + 1, j + 1 == it.m);
+          const bool more = C::kAhead && j + 2 <= it.m;
+          const uint32_t ds = ds_full + 8 * (turn & 1), par = turn >> 1;
+          ok = ok && wait3(ab, a.status, ds, par, more ? k_full + 8 * ks.slot : ds, more ? ks.turn : par,
+                           more ? v_full + 8 * vs.slot : ds, more ? vs.turn : par);
+          if (j == 0 && items > 0) ok = ok && wait3(ab, a.status, acc_free, items - 1, acc_free, items - 1, acc_free, items - 1);
+          if (!ok) break;
+          fence_after_sync();
+          mma_rows<D, kCols>(t_dq, t_dp + 128 * (turn & 1), k_mn + rk.slot * kStep, j > 0);
           mma_commit(&sh->k_empty[rk.slot]);
-          if (!more) mma_commit(&sh->done);
+          if (j == it.m) mma_commit(&sh->done);
+          rk.next(C::kK);
+          if (more) scores(turn + 2, j + 2 == it.m);
         }
-        rk = nk;
-        rv = nv;
       }
+      mma_commit(&sh->drain);
+      settle_for(&sh->drain, 0);
     }
-    if (elect()) mma_commit(&sh->drain);
-    settle_for(&sh->drain, 0);
     __syncwarp();
   } else if (warp >= kMathWarp) {
     const int wg = (warp - kMathWarp) >> 2, row = tid & 127;
@@ -683,6 +660,21 @@ __global__ void __launch_bounds__(QMath<D>::kThreads, 1)
       // What a row's dS sums to, over all keys: zero but for the rounding of the o
       // that delta was formed from.
       uint64_t rest2[2] = {0, 0};
+      uint32_t p[kParts][32], x[kParts][32];  // scores, then probabilities; dP, then dS
+      auto read_scores = [&](uint32_t n) {
+        wait_all(ab, &sh->s_full, n & 1, a.status);
+        fence_after_sync();
+        load_scores(my_s, p);
+      };
+      auto scores_read = [&]() {
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->s_read);
+      };
+      if (C::kAhead) {
+        read_scores(turn);
+        scores_read();
+      }
       for (int j = 0; j <= it.m; ++j, ++turn) {
         const uint32_t my_dp = t_dp + 128 * (turn & 1) + lane_base + kCols * wg;
         const bool diagonal = j == it.m;
@@ -696,13 +688,10 @@ __global__ void __launch_bounds__(QMath<D>::kThreads, 1)
             see[c] = hi >= 32 ? ~0u : hi > 0 ? ~(~0u << hi) : 0u;
           }
         }
-        wait_all(ab, &sh->s_full, turn & 1, a.status);
-        fence_after_sync();
-        uint32_t p[kParts][32], x[kParts][32];
-        load_scores(my_s, p);
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->s_read);  // the next scores may come: P stays in registers
+        if (!C::kAhead) {
+          read_scores(turn);
+          scores_read();
+        }
 #pragma unroll
         for (int c = 0; c < kParts; ++c)
 #pragma unroll
@@ -741,6 +730,9 @@ __global__ void __launch_bounds__(QMath<D>::kThreads, 1)
         for (int c = 0; c < kParts; ++c)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) rest2[e / 2 & 1] = add2(rest2[e / 2 & 1], pack2(x[c][e], x[c][e + 1]));
+        // One arrival then stands for dS and for the next scores, and the issuing thread
+        // has one wait a tile. (Heads of 64, whose products are half as long, lose by it.)
+        if (C::kAhead && !diagonal) read_scores(turn + 1);
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();

@@ -153,68 +153,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (items > 0) settle_for(&sh->q_full, (items - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
-    // ---- products ----
-    const uint32_t q_at = desc_k(smem), k_at = desc_k(ring), v_at = desc_mn(ring);
-    constexpr uint32_t kStep = kTile >> 4;  // from a slot's descriptor to the next
-    Ring rk;  // the ring's position of K(j); V(j) is the next one
-    uint32_t items = 0, turn_p[2] = {0, 0}, used_o[2] = {0, 0};
-    bool ok = true;
-    auto qk = [&](int s, int slot) {
-      if (elect()) {
+    // ---- products, issued by one thread ----
+    if (elect()) {
+      const uint32_t q_at = desc_k(smem), k_at = desc_k(ring), v_at = desc_mn(ring);
+      constexpr uint32_t kStep = kTile >> 4;  // from a slot's descriptor to the next
+      const uint32_t full = smem_addr(sh->full), p_ready = smem_addr(sh->p_ready);
+      Ring rk;  // the ring's position of K(j); V(j) is the next one
+      uint32_t items = 0, turn_p[2] = {0, 0}, used_o[2] = {0, 0};
+      bool ok = true;
+      auto qk = [&](int s, int slot) {
         mma_scores<D>(tmem_s + 128 * s, q_at + s * kStep, k_at + slot * kStep);
         mma_commit(&sh->s_full[s]);
-      }
-    };
-    while (item_at(a, tiles, handout_take(&sh->items, items), it)) {
-      const int nk = it.n[1] ? it.n[1] : it.n[0];
-      ++items;
-      if (!ok) continue;
-      ok = wait_all(ab, lane == 0 ? &sh->q_full : &sh->full[rk.slot], (lane == 0 ? items - 1 : rk.turn) & 1, a.status);
-      if (!ok) continue;
-      fence_after_sync();
-      for (int s = 0; s < 2; ++s)
-        if (it.n[s]) qk(s, rk.slot);
-      if (elect()) {
+      };
+      while (item_at(a, tiles, handout_take_alone(&sh->items, items), it)) {
+        const int nk = it.n[1] ? it.n[1] : it.n[0];
+        ++items;
+        if (!ok) continue;
+        const uint32_t first = full + 8 * rk.slot;
+        ok = wait3(ab, a.status, smem_addr(&sh->q_full), items - 1, first, rk.turn, first, rk.turn);
+        if (!ok) continue;
+        fence_after_sync();
+        qk(0, rk.slot);
+        if (it.n[1]) qk(1, rk.slot);
         mma_commit(&sh->empty[rk.slot]);
         if (nk == 1) mma_commit(&sh->q_empty);
-      }
-      for (int j = 0; ok && j < nk; ++j) {
-        Ring rv = rk;
-        rv.next(kSlots);
-        rk = rv;
-        rk.next(kSlots);  // K(j + 1)
-        const bool more = j + 1 < nk;
-        for (int s = 0; ok && s < 2; ++s) {
-          if (j >= it.n[s]) continue;
-          // P, V, the next K, and at an item's start O, in one wait by a lane each
-          const bool first = j == 0 && used_o[s] > 0;
-          uint64_t* bar = &sh->p_ready[s];
-          uint32_t par = turn_p[s];
-          if (lane == 1) bar = &sh->full[rv.slot], par = rv.turn;
-          if (lane == 2 && more) bar = &sh->full[rk.slot], par = rk.turn;
-          if (lane == 3 && first) bar = &sh->o_free[s], par = used_o[s] - 1;
-          ok = wait_all(ab, bar, par & 1, a.status);
-          ++turn_p[s];
-          if (j == 0) ++used_o[s];
-          if (!ok) break;
-          fence_after_sync();
-          const uint32_t ts = tmem_s + 128 * s, to = tmem_o + 128 * s;
-          if (elect()) {
-            mma_rows<D, 128>(to, ts, v_at + rv.slot * kStep, j > 0);
+        for (int j = 0; ok && j < nk; ++j) {
+          Ring rv = rk;
+          rv.next(kSlots);
+          rk = rv;
+          rk.next(kSlots);  // K(j + 1)
+          const bool more = j + 1 < nk;
+          const uint32_t v_full = full + 8 * rv.slot, k_full = more ? full + 8 * rk.slot : v_full, k_turn = more ? rk.turn : rv.turn;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (!ok || j >= it.n[s]) continue;
+            // P, V, the next K, and at an item's start O
+            ok = wait3(ab, a.status, p_ready + 8 * s, turn_p[s]++, v_full, rv.turn, k_full, k_turn);
+            if (j == 0 && used_o[s]++ > 0) {
+              const uint32_t o_free = smem_addr(&sh->o_free[s]), turn = used_o[s] - 2;
+              ok = ok && wait3(ab, a.status, o_free, turn, o_free, turn, o_free, turn);
+            }
+            if (!ok) continue;
+            fence_after_sync();
+            mma_rows<D, 128>(tmem_o + 128 * s, tmem_s + 128 * s, v_at + rv.slot * kStep, j > 0);
             if (j + 1 == it.n[s]) mma_commit(&sh->o_done[s]);
+            if (j + 1 < it.n[s]) qk(s, rk.slot);
           }
-          if (j + 1 < it.n[s]) qk(s, rk.slot);
-        }
-        if (ok && elect()) {
-          mma_commit(&sh->empty[rv.slot]);
-          if (more) mma_commit(&sh->empty[rk.slot]);
-          if (j + 2 == nk) mma_commit(&sh->q_empty);
+          if (ok) {
+            mma_commit(&sh->empty[rv.slot]);
+            if (more) mma_commit(&sh->empty[rk.slot]);
+            if (j + 2 == nk) mma_commit(&sh->q_empty);
+          }
         }
       }
+      // nothing of this thread may be in flight when TMEM is freed
+      mma_commit(&sh->drain);
+      settle_for(&sh->drain, 0);
     }
-    // nothing of this warp may be in flight when TMEM is freed
-    if (elect()) mma_commit(&sh->drain);
-    settle_for(&sh->drain, 0);
     __syncwarp();
   } else if (warp >= kSoftmaxWarp) {
     // ---- softmax: thread = row, warpgroup = stream ----
