@@ -1,13 +1,13 @@
-"""Times the cases of perf/operators.py on the GPU.
+"""Times the cases of perf/operators.py or perf/more_operators.py on the GPU.
 
-    python perf/timing.py [--plain] [--only NAME,NAME] [--repeats 7] [--once]
+    python perf/timing.py [--more] [--plain] [--only NAME,NAME] [--repeats 7] [--once]
 
 For each case: microseconds of a pass (CUDA events around passes that follow one
 another, the median of the repeats), the same from a CUDA graph of one pass over
 each input set (the device's time: no host between the launches), the host's time
 for issuing a pass, and the rates of the first from the case's own bytes and
-operations. Passes take turns on input sets that together exceed L2. --plain times
-the plain forms; --once makes two passes of each case and no timing (to profile).
+operations. Passes take turns on input sets that together exceed L2. --more takes the
+cases of perf/more_operators.py; --plain times the plain forms; --once makes two passes of each case and no timing (to profile).
 """
 import argparse
 import importlib.util
@@ -23,8 +23,8 @@ sys.path.insert(0, ROOT)
 L2 = 129 << 20
 
 
-def load():
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+def load(name):
+    spec = importlib.util.spec_from_file_location(name, os.path.join(ROOT, "perf", name + ".py"))
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     return module
@@ -81,12 +81,13 @@ def measure(ops, case, repeats):
 
 def main():
     p = argparse.ArgumentParser()
+    p.add_argument("--more", action="store_true")
     p.add_argument("--plain", action="store_true")
     p.add_argument("--only", default="")
     p.add_argument("--repeats", type=int, default=7)
     p.add_argument("--once", action="store_true")
     a = p.parse_args()
-    ops = load()
+    ops = load("more_operators" if a.more else "operators")
     ops.own = not a.plain
     only = a.only.split(",") if a.only else None
     cases = [c for c in ops.listed() if not only or c["name"] in only]

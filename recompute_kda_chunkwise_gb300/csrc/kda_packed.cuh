@@ -58,32 +58,28 @@ __device__ __forceinline__ Tile tile_of(const PackedArgs& a, int tiles, int e) {
 }
 namespace tc {
 
-// Bounded wait for a phase; false when it ran out (the CTA's abort flag is then
-// set) or another role gave up.
-__device__ __forceinline__ bool wait_or(int* abort_, uint64_t* bar, uint32_t parity, int* status) {
-  const uint32_t at = smem_addr(bar);
-  for (int it = 0; it < (1 << 22); ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(at), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((it & 15) == 15 && *const_cast<volatile int*>(abort_)) return false;
-  }
-  *const_cast<volatile int*>(abort_) = 1;
-  set_status(status, KDA_ERR_TIMEOUT);
-  return false;
+// Whether a phase, or up to three of them, are over.
+__device__ __forceinline__ bool poll(uint32_t a, uint32_t p) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(a), "r"(p & 1)
+      : "memory");
+  return ok != 0;
 }
-// The same by a whole warp, with one answer; lanes may wait for barriers of their own.
-__device__ __forceinline__ bool wait_all(int* abort_, uint64_t* bar, uint32_t parity, int* status) {
-  return __all_sync(~0u, wait_or(abort_, bar, parity, status));
+__device__ __forceinline__ bool poll2(uint32_t a0, uint32_t p0, uint32_t a1, uint32_t p1) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p, q;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n"
+      "and.pred p, p, q;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(a0), "r"(p0 & 1), "r"(a1), "r"(p1 & 1)
+      : "memory");
+  return ok != 0;
 }
-// Waits of the one thread that issues the products, for up to three barriers at
-// once (given twice where there are fewer): its instructions between two products
-// are time in which the tensor cores run dry, since it is held up by the products
-// themselves until few of them are left.
 __device__ __forceinline__ bool poll3(uint32_t a0, uint32_t p0, uint32_t a1, uint32_t p1, uint32_t a2, uint32_t p2) {
   uint32_t ok;
   asm volatile(
@@ -97,29 +93,47 @@ __device__ __forceinline__ bool poll3(uint32_t a0, uint32_t p0, uint32_t a1, uin
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool wait3(int* abort_, int* status, uint32_t a0, uint32_t p0, uint32_t a1, uint32_t p1,
-                                      uint32_t a2, uint32_t p2) {
+
+// Bounded wait: false when it ran out (the CTA's abort flag is then set) or another
+// role gave up. After an abort every role still walks through its items, but issues
+// no copy and no product any more. `over`: whether what is waited for has happened.
+// `all`: by a whole warp, whose lanes then decide alike.
+template <bool all, typename F>
+__device__ __forceinline__ bool wait_for(int* abort_, int* status, const F& over) {
   for (int it = 0; it < (1 << 22); ++it) {
-    if (poll3(a0, p0, a1, p1, a2, p2)) return true;
-    if ((it & 15) == 15 && *const_cast<volatile int*>(abort_)) return false;
+    if (all ? __all_sync(~0u, over()) : over()) return true;
+    if ((it & 15) == 15) {
+      const bool gone = *const_cast<volatile int*>(abort_) != 0;
+      if (all ? __any_sync(~0u, gone) : gone) return false;
+    }
   }
   *const_cast<volatile int*>(abort_) = 1;
   set_status(status, KDA_ERR_TIMEOUT);
   return false;
 }
+// By a whole warp, for one phase or for two.
+__device__ __forceinline__ bool wait_all(int* abort_, uint64_t* bar, uint32_t parity, int* status) {
+  const uint32_t at = smem_addr(bar);
+  return wait_for<true>(abort_, status, [&]() { return poll(at, parity); });
+}
+__device__ __forceinline__ bool wait_both(int* abort_, uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, int* status) {
+  const uint32_t a0 = smem_addr(b0), a1 = smem_addr(b1);
+  return wait_for<true>(abort_, status, [&]() { return poll2(a0, p0, a1, p1); });
+}
+// By the one thread that issues the products, for up to three phases at once (given
+// twice where there are fewer): its instructions between two products are time in
+// which the tensor cores run dry, since it is held up by the products themselves
+// until few of them are left.
+__device__ __forceinline__ bool wait3(int* abort_, int* status, uint32_t a0, uint32_t p0, uint32_t a1, uint32_t p1,
+                                      uint32_t a2, uint32_t p2) {
+  return wait_for<false>(abort_, status, [&]() { return poll3(a0, p0, a1, p1, a2, p2); });
+}
 
 // Waits, at most so long, without giving up; whether the phase is over.
 __device__ __forceinline__ bool settle_for(uint64_t* bar, uint32_t parity) {
   const uint32_t at = smem_addr(bar);
-  for (int it = 0; it < (1 << 20); ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(at), "r"(parity)
-        : "memory");
-    if (ok) return true;
-  }
+  for (int it = 0; it < (1 << 20); ++it)
+    if (poll(at, parity)) return true;
   return false;
 }
 

@@ -21,7 +21,26 @@
 // in order, by another kernel.
 //
 // dq. Queries are the rows; dS is dq's A operand in TMEM. dP has two buffers,
-// so that the next tile's scores and dP are formed while dS is.
+// so that the next tile's scores and dP are formed while dS is. delta comes from
+// the forward's o, which was rounded to bf16; but a row's dS sums to zero, so what
+// this pass finds it to sum to is delta's error, and the other pass gets delta
+// without it. Rows whose keys all lie in one tile sum their delta up themselves.
+// (Gradients of 77 tokens: 0.0026 of their size off float64 before, 0.0023 with
+// it, 0.0017 if nothing but the outputs were rounded.) dS and P are rounded to
+// bf16 because the products' operands have one type; as sums of two parts each
+// they would cost 40% more products.
+//
+// Bound: the tensor cores in principle, 512 cycles a product of 128 x 128 x 128: 3584
+// a tile for both passes; counters show them active 77% (dk, dv) and 67% (dq) of
+// the time. What is left is latency: from a warpgroup's arrival to the product that
+// waited for it (300 to 400 cycles) and from there to the scores. 8192 tokens, 64
+// query heads on 8 of 128: 2296 us (40 for delta, 1040 dq, 1205 dk and dv), 1197
+// TFLOP/s counted as five products; 32768 tokens, 16 heads on 2: 1222. Heads of 64:
+// 1755 us, 783 TFLOP/s, bound by the arithmetic between the products. Without
+// loads, or without exponentials, neither pass is more than 3% faster. What brought
+// it there, in us: a ring each for K and V 2995 -> 2505; descriptors of one addition
+// 2452; lse and delta in the ring with d_o instead of a barrier a step 2414; one
+// issuing thread with joint waits, dq's scores read a tile ahead 2296.
 #include <math.h>
 
 #include "kda_packed.cuh"
@@ -32,22 +51,13 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128;
-// Warpgroups of arithmetic, each a part of a tile's columns: two threads a row,
-// or four. Four hide more of one another's latencies; with heads of 128 the
-// products take most of the time, and dq's warps, which also form sums over
-// rows, do better in two. Forward and backward of 8192 tokens, 64 heads: of 64,
-// 4: 1978 us in the backward, 2: 2262; of 128 dk and dv alike (1296 to 1302), dq
-// 1130 and 1087.
-template <int G>
-struct Math {
-  static constexpr int kGroups = G, kWarps = 4 * G, kThreads = 32 * (4 + kWarps);
-  static constexpr int kCols = 128 / G, kParts = kCols / 32;
-};
-template <int D>
-using KvMath = Math<4>;
-template <int D>
-using QMath = Math<4>;
+// Warpgroups of arithmetic, each a part of a tile's columns: four threads a row.
+// With two, heads of 64 take 1909 us instead of 1832 (8192 tokens, 64 heads); heads of
+// 128 are alike (2362 and 2339).
+constexpr int kGroups = 4, kMathWarps = 4 * kGroups;
+constexpr int kCols = kRows / kGroups, kParts = kCols / 32;
 constexpr int kMmaWarp = 0, kLoadWarp = 1, kMathWarp = 4;
+constexpr int kThreads = 32 * (kMathWarp + kMathWarps);
 
 // P x 32 columns of a tile, a thread's.
 template <int P>
@@ -173,12 +183,11 @@ __device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t 
 }
 
 template <int D>
-__global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     kda_packed_dkv_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ CUtensorMap qmap,
                           const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                           const __grid_constant__ CUtensorMap domap, const float sc) {
   using C = KvCfg<D>;
-  constexpr int kMathWarps = KvMath<D>::kWarps, kGroups = KvMath<D>::kGroups, kCols = KvMath<D>::kCols, kParts = KvMath<D>::kParts;
   constexpr int kTile = C::kTile;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const kt = smem;
@@ -361,8 +370,7 @@ __global__ void __launch_bounds__(KvMath<D>::kThreads, 1)
           }
         }
         const bool all = !(diagonal || tail);
-        wait_all(ab, &sh->do_full[rd.slot], rd.turn & 1, a.status);  // lse and delta
-        wait_all(ab, &sh->s_full, turn & 1, a.status);
+        wait_both(ab, &sh->do_full[rd.slot], rd.turn & 1, &sh->s_full, turn & 1, a.status);  // lse and delta; S
         if (tail) {  // those rows' Q and d_o to zero, once the scores' products have read them
           wait_all(ab, &sh->dp_full, turn & 1, a.status);
           if (mt < 2 * kRows && row >= past) zero_row<D>(mt < kRows ? qt + rq.slot * kTile : dot + rd.slot * kTile, row);
@@ -462,7 +470,7 @@ struct QCfg {
 };
 struct QShared {
   Handout items;
-  float sum[4][kRows];  // per row, of each warpgroup's columns
+  float sum[kGroups][kRows];  // per row, of each warpgroup's columns
   uint64_t k_full[5], k_empty[5], v_full[4], v_empty[4];
   uint64_t q_full, q_empty;
   // dP and dS by buffer: an item's last dS can be there before the one before it is seen
@@ -487,12 +495,11 @@ __device__ __forceinline__ bool item_at(const PackedArgs& a, int tiles, int64_t 
 }
 
 template <int D>
-__global__ void __launch_bounds__(QMath<D>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     kda_packed_dq_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const __grid_constant__ CUtensorMap domap, const float sc) {
   using C = QCfg<D>;
-  constexpr int kMathWarps = QMath<D>::kWarps, kGroups = QMath<D>::kGroups, kCols = QMath<D>::kCols, kParts = QMath<D>::kParts;
   constexpr int kTile = C::kTile;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const kt = smem + 2 * kTile;  // behind the tiles of q and d_o
@@ -777,9 +784,9 @@ cudaError_t launch(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap&
   kda_packed_delta_kernel<D><<<static_cast<unsigned>((a.S * a.Hq * 8 + 255) / 256), 256, 0, s>>>(a);
   e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = launch_after(kda_packed_dq_kernel<D>, nq < sms ? nq : sms, QMath<D>::kThreads, smem_q, s, a, q, k, v, d_o, sc);
+    e = launch_after(kda_packed_dq_kernel<D>, nq < sms ? nq : sms, kThreads, smem_q, s, a, q, k, v, d_o, sc);
   if (e == cudaSuccess)
-    e = launch_after(kda_packed_dkv_kernel<D>, kv < sms ? kv : sms, KvMath<D>::kThreads, smem_kv, s, a, q, k, v, d_o, sc);
+    e = launch_after(kda_packed_dkv_kernel<D>, kv < sms ? kv : sms, kThreads, smem_kv, s, a, q, k, v, d_o, sc);
   if (e == cudaSuccess && a.split > 1) {
     kda_packed_parts_kernel<<<static_cast<unsigned>((2 * a.S * a.Hkv * a.D / 4 + 255) / 256), 256, 0, s>>>(a);
     e = cudaGetLastError();
