@@ -272,7 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           r.next(slots);
         }
       }
-      x = second ? handout_take(&sh->items, items + 1) : handout_next(&sh->items, items + 1, &a.tickets[1], ok, static_cast<int64_t>(tiles) * a.Hkv * a.split);
+      x = second ? handout_take(&sh->items, items + 1)
+                 : handout_next(&sh->items, items + 1, &a.tickets[1], ok, static_cast<int64_t>(tiles) * a.Hkv * a.split);
     }
     // after an abort: the copies in flight land before the CTA ends
     if (!ok) {
@@ -294,7 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; item_at(a, tiles, handout_take_alone(&sh->items, items), it); ++items) {
         const int steps = it.steps();
         // K and V, the first Q and d_o
-        ok = ok && wait3(ab, a.status, smem_addr(&sh->kv_full), items, q_full + 8 * rq.slot, rq.turn, do_full + 8 * rd.slot, rd.turn);
+        ok = ok && wait3(ab, a.status, smem_addr(&sh->kv_full), items, q_full + 8 * rq.slot, rq.turn, do_full + 8 * rd.slot,
+                         rd.turn);
         if (!ok) continue;
         fence_after_sync();
         mma_scores<D>(t_s, k_at, q_at + rq.slot * kStep);
@@ -579,7 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++copies;
         r.next(slots);
       }
-      x = v ? handout_take(&sh->items, items + 1) : handout_next(&sh->items, items + 1, &a.tickets[0], ok, static_cast<int64_t>(tiles) * a.Hq);
+      x = v ? handout_take(&sh->items, items + 1)
+            : handout_next(&sh->items, items + 1, &a.tickets[0], ok, static_cast<int64_t>(tiles) * a.Hq);
     }
     if (!ok) {
       for (int64_t p = copies > slots ? copies - slots : 0; p < copies; ++p)
@@ -589,7 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ---- products, issued by one thread ----
     if (elect()) {
-      const uint32_t q_at = desc_k(smem), do_at = desc_k(smem + kTile), k_at = desc_k(kt), v_at = desc_k(vt), k_mn = desc_mn(kt);
+      const uint32_t q_at = desc_k(smem), do_at = desc_k(smem + kTile), k_at = desc_k(kt), v_at = desc_k(vt),
+                     k_mn = desc_mn(kt);
       constexpr uint32_t kStep = kTile >> 4;  // from a slot's descriptor to the next
       const uint32_t k_full = smem_addr(sh->k_full), v_full = smem_addr(sh->v_full), ds_full = smem_addr(sh->ds_ready),
                      s_read = smem_addr(&sh->s_read), acc_free = smem_addr(&sh->acc_free);
@@ -607,7 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         vs.next(C::kV);
       };
       for (; item_at(a, tiles, handout_take_alone(&sh->items, items), it); ++items) {
-        ok = ok && wait3(ab, a.status, smem_addr(&sh->q_full), items, k_full + 8 * ks.slot, ks.turn, v_full + 8 * vs.slot, vs.turn);
+        ok = ok && wait3(ab, a.status, smem_addr(&sh->q_full), items, k_full + 8 * ks.slot, ks.turn, v_full + 8 * vs.slot,
+                         vs.turn);
         if (!ok) continue;
         fence_after_sync();
         scores(turn, it.m == 0);
@@ -627,7 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t ds = ds_full + 8 * (turn & 1), par = turn >> 1;
           ok = ok && wait3(ab, a.status, ds, par, more ? k_full + 8 * ks.slot : ds, more ? ks.turn : par,
                            more ? v_full + 8 * vs.slot : ds, more ? vs.turn : par);
-          if (j == 0 && items > 0) ok = ok && wait3(ab, a.status, acc_free, items - 1, acc_free, items - 1, acc_free, items - 1);
+          if (j == 0 && items > 0)
+            ok = ok && wait3(ab, a.status, acc_free, items - 1, acc_free, items - 1, acc_free, items - 1);
           if (!ok) break;
           fence_after_sync();
           mma_rows<D, kCols>(t_dq, t_dp + 128 * (turn & 1), k_mn + rk.slot * kStep, j > 0);
@@ -711,8 +717,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_all(ab, &sh->dp_full[turn & 1], turn >> 1 & 1, a.status);
         fence_after_sync();
         load_scores(my_dp, x);
-        if (it.m == 0) {  // all keys in one tile: delta as the sum that it is, free of o's rounding
+        if (it.m == 0) {
+          // All keys in one tile: delta as the sum that it is, free of o's rounding. A
+          // sequence's first query sees one key, with probability 1 but for the rounding of
+          // lse: made exact, its dS is zero.
           hide(x, see);
+          if (at == 0 && wg == 0 && p[0][0] < 0x7f800000u) p[0][0] = __float_as_uint(1.f);
           uint64_t sum = 0;
 #pragma unroll
           for (int c = 0; c < kParts; ++c)

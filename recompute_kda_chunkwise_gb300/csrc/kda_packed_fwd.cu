@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           rk = rv;
           rk.next(kSlots);  // K(j + 1)
           const bool more = j + 1 < nk;
-          const uint32_t v_full = full + 8 * rv.slot, k_full = more ? full + 8 * rk.slot : v_full, k_turn = more ? rk.turn : rv.turn;
+          const uint32_t v_full = full + 8 * rv.slot, k_full = more ? full + 8 * rk.slot : v_full;
+          const uint32_t k_turn = more ? rk.turn : rv.turn;
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             if (!ok || j >= it.n[s]) continue;

@@ -131,6 +131,15 @@ def test_lengths_that_do_not_fit_leave_outputs_alone():
             assert K.query_device_status(ws) == 6, bad
 
 
+def test_a_single_key_has_no_gradient_through_its_probability():
+    """Sequences of one token: P is 1 and dS zero, whatever the scores are; dq and dk are zero exactly."""
+    for D, H in ((64, 3), (128, 2)):
+        q, k, v, d_o, cu = inputs((1, 1, 1, 1, 1), 2 * H, H, D, seed=D, std=3.0)
+        got = run(q, k, v, d_o, cu)
+        assert torch.equal(got["o"], v.repeat_interleave(2, 1))
+        assert (got["dq"] == 0).all() and (got["dk"] == 0).all()
+
+
 def test_no_tokens():
     q, k, v, d_o, cu = inputs((0, 0), 2, 1, 64)
     got = run(q, k, v, d_o, cu)
