@@ -97,28 +97,37 @@ __device__ __forceinline__ bool poll3(uint32_t a0, uint32_t p0, uint32_t a1, uin
 // Bounded wait: false when it ran out (the CTA's abort flag is then set) or another
 // role gave up. After an abort every role still walks through its items, but issues
 // no copy and no product any more. `over`: whether what is waited for has happened.
-// `all`: by a whole warp, whose lanes then decide alike.
-template <bool all, typename F>
+template <typename F>
 __device__ __forceinline__ bool wait_for(int* abort_, int* status, const F& over) {
   for (int it = 0; it < (1 << 22); ++it) {
-    if (all ? __all_sync(~0u, over()) : over()) return true;
-    if ((it & 15) == 15) {
-      const bool gone = *const_cast<volatile int*>(abort_) != 0;
-      if (all ? __any_sync(~0u, gone) : gone) return false;
-    }
+    if (over()) return true;
+    if ((it & 15) == 15 && *const_cast<volatile int*>(abort_)) return false;
   }
   *const_cast<volatile int*>(abort_) = 1;
   set_status(status, KDA_ERR_TIMEOUT);
   return false;
 }
-// By a whole warp, for one phase or for two.
+// By a whole warp, with one answer, for one phase or for two.
 __device__ __forceinline__ bool wait_all(int* abort_, uint64_t* bar, uint32_t parity, int* status) {
   const uint32_t at = smem_addr(bar);
-  return wait_for<true>(abort_, status, [&]() { return poll(at, parity); });
+  return __all_sync(~0u, wait_for(abort_, status, [&]() { return poll(at, parity); }));
+}
+// The same with a vote at every look. Measured either way: dq's arithmetic is faster
+// with it (heads of 64: 182 us against 187), that of dk and dv without (heads of 128:
+// 1214 against 1237).
+__device__ __forceinline__ bool wait_voting(int* abort_, uint64_t* bar, uint32_t parity, int* status) {
+  const uint32_t at = smem_addr(bar);
+  for (int it = 0; it < (1 << 22); ++it) {
+    if (__all_sync(~0u, poll(at, parity))) return true;
+    if ((it & 15) == 15 && __any_sync(~0u, *const_cast<volatile int*>(abort_))) return false;
+  }
+  *const_cast<volatile int*>(abort_) = 1;
+  set_status(status, KDA_ERR_TIMEOUT);
+  return false;
 }
 __device__ __forceinline__ bool wait_both(int* abort_, uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, int* status) {
   const uint32_t a0 = smem_addr(b0), a1 = smem_addr(b1);
-  return wait_for<true>(abort_, status, [&]() { return poll2(a0, p0, a1, p1); });
+  return __all_sync(~0u, wait_for(abort_, status, [&]() { return poll2(a0, p0, a1, p1); }));
 }
 // By the one thread that issues the products, for up to three phases at once (given
 // twice where there are fewer): its instructions between two products are time in
@@ -126,7 +135,7 @@ __device__ __forceinline__ bool wait_both(int* abort_, uint64_t* b0, uint32_t p0
 // until few of them are left.
 __device__ __forceinline__ bool wait3(int* abort_, int* status, uint32_t a0, uint32_t p0, uint32_t a1, uint32_t p1,
                                       uint32_t a2, uint32_t p2) {
-  return wait_for<false>(abort_, status, [&]() { return poll3(a0, p0, a1, p1, a2, p2); });
+  return wait_for(abort_, status, [&]() { return poll3(a0, p0, a1, p1, a2, p2); });
 }
 
 // Waits, at most so long, without giving up; whether the phase is over.

@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t rest2[2] = {0, 0};
       uint32_t p[kParts][32], x[kParts][32];  // scores, then probabilities; dP, then dS
       auto read_scores = [&](uint32_t n) {
-        wait_all(ab, &sh->s_full, n & 1, a.status);
+        wait_voting(ab, &sh->s_full, n & 1, a.status);
         fence_after_sync();
         load_scores(my_s, p);
       };
@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (wg == 0 && at >= it.L) zero_row<D>(kt + rk.slot * kTile, row);
           fence_async_smem();
         }
-        wait_all(ab, &sh->dp_full[turn & 1], turn >> 1 & 1, a.status);
+        wait_voting(ab, &sh->dp_full[turn & 1], turn >> 1 & 1, a.status);
         fence_after_sync();
         load_scores(my_dp, x);
         if (it.m == 0) {
@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           to[kRows] = used ? -(delta + rest) : 0.f;
         }
       }
-      const bool fine = wait_all(ab, &sh->done, items & 1, a.status);
+      const bool fine = wait_voting(ab, &sh->done, items & 1, a.status);
       fence_after_sync();
       constexpr int kCh = D / kGroups;
       write_row<kCh>(t_dq + lane_base + wg * kCh, a.scale,
