@@ -11,9 +11,10 @@
 //
 // Bound: HBM, each element read and written once. 72 heads of 128 of 8192
 // tokens in bf16 (151 MB each way), rotated and, for the gradient, rotated back:
-// 105 us, 86% of the measured copy rate; in fp32 40 heads, 6.0 TB/s. Interleaved
-// pairs, whose items are half as long: 54 us a pass, 84%. Pairs that no vector
-// divides (21 of 128 channels) go element by element: 160 us.
+// 104 us, 87% of the measured copy rate; in fp32 40 heads, 6.0 TB/s. Interleaved
+// pairs, whose items are half as long: 55 us a pass, 82%. Halves that no vector
+// divides go by what does, the channels behind them by vectors: 40 of 128 channels
+// (four at a time) 60 us, 44 (two) 65, 42 (one) 86; all of them one at a time 160.
 //
 // Split. A CTA takes a tile of tokens with all their heads. A token's sines
 // and cosines are formed once, in shared memory, for all of its heads (each
@@ -24,8 +25,8 @@
 // vectors before it are worked on. bf16 is bound by instructions as much as by
 // memory: a thread keeps its place in the heads and its sines in registers, steps
 // through heads without a division, and works on words of two values (171 us
-// before). Five CTAs an SM hold that; pairs and single elements do better with
-// eight.
+// before). Five CTAs an SM hold that, six half vectors (60 us; 64 with eight); pairs
+// and shorter items do better with eight (44 channels 65 us, 70 with six).
 #include <math.h>
 
 #include "kda_blocks.h"
@@ -98,19 +99,44 @@ __device__ __forceinline__ void turn_halves(uint32_t& a, uint32_t& b, const floa
   }
 }
 
-// How a head's channels are cut into items of work.
-enum Layout {
-  kHalf,    // pairs (i, i + R/2), both halves whole vectors: an item is a vector of either, or one that passes
-  kPairs,   // pairs (2i, 2i + 1): an item is a vector
-  kSingle,  // pairs (i, i + R/2) that no vector divides: an item is a pair, or an element that passes
-};
+// BYTES of a tensor in the lower words of a vector.
+template <int BYTES>
+__device__ __forceinline__ uint4 load_words(const void* p) {
+  uint4 r = make_uint4(0u, 0u, 0u, 0u);
+  if constexpr (BYTES == 16) {
+    r = *static_cast<const uint4*>(p);
+  } else if constexpr (BYTES == 8) {
+    const uint2 x = *static_cast<const uint2*>(p);
+    r.x = x.x;
+    r.y = x.y;
+  } else if constexpr (BYTES == 4) {
+    r.x = *static_cast<const uint32_t*>(p);
+  } else {
+    r.x = *static_cast<const uint16_t*>(p);
+  }
+  return r;
+}
+template <int BYTES>
+__device__ __forceinline__ void store_words(void* p, const uint4& r) {
+  if constexpr (BYTES == 16)
+    *static_cast<uint4*>(p) = r;
+  else if constexpr (BYTES == 8)
+    *static_cast<uint2*>(p) = make_uint2(r.x, r.y);
+  else if constexpr (BYTES == 4)
+    *static_cast<uint32_t*>(p) = r.x;
+  else
+    *static_cast<uint16_t*>(p) = static_cast<uint16_t>(r.x);
+}
 
-template <typename T, int LAYOUT, bool PAGED>
-__global__ void __launch_bounds__(kThreads, LAYOUT == kHalf || sizeof(T) == 4 ? 5 : 8) kda_rotary_kernel(const RotaryArgs a) {
-  constexpr int V = 16 / sizeof(T);
+// How a head's channels are cut into items of work. PAIRS, channels (2i, 2i + 1)
+// turn together: an item is a 16-byte vector. Else, channels (i, i + R/2): W, the
+// largest power of two up to a vector that divides R/2, elements of either half;
+// of the channels that pass, a vector, W elements only up to the first vector.
+template <typename T, int W, bool PAIRS, bool PAGED>
+__global__ void __launch_bounds__(kThreads, (W * sizeof(T) == 16 && !PAIRS) || sizeof(T) == 4 ? 5 : W * sizeof(T) == 8 ? 6 : 8)
+    kda_rotary_kernel(const RotaryArgs a) {
   constexpr bool kBf16 = sizeof(T) == 2;
-  // Items of a thread that are loaded together, while as many more are worked on.
-  constexpr int kBatch = LAYOUT == kSingle ? 4 : 1;
+  constexpr int kBytes = W * sizeof(T);
   extern __shared__ float2 turn[];  // [tile][R / 2]: magnitude * (cos, sin)
   __shared__ int32_t s_pos[kMaxTile];
   __shared__ int64_t s_row[kMaxTile];  // paged: elements before the token's row of the pages; negative: the token is skipped
@@ -118,12 +144,14 @@ __global__ void __launch_bounds__(kThreads, LAYOUT == kHalf || sizeof(T) == 4 ? 
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tile;
   const int nt = static_cast<int>(a.S - t0 < a.tile ? a.S - t0 : a.tile);
   const int half = a.R / 2;
-  const int per_head = LAYOUT == kHalf ? half / V + (a.D - a.R) / V : LAYOUT == kPairs ? a.D / V : half + a.D - a.R;
+  constexpr int V = 16 / sizeof(T);
+  const int lead = (V - a.R % V) % V / W;  // items between the channels that turn and the next vector's
+  const int per_head = PAIRS ? a.D / W : half / W + lead + (a.D - a.R - lead * W) / V;
   const int turned = a.Hq + a.Hk, heads = turned + (PAGED ? a.Hk : 0);  // the paged form's values are copied beside them
 
   // A thread keeps its place within the heads, and goes over the tokens' heads
   // `slots` at a time; places past one for each thread (long heads that are cut
-  // into single elements) are taken in another round.
+  // into short items) are taken in another round.
   const int slots = per_head < kThreads ? kThreads / per_head : 1;
   const int first = per_head < kThreads ? tid / per_head : 0;
   const int step_t = slots / heads, step_h = slots % heads;
@@ -140,17 +168,16 @@ __global__ void __launch_bounds__(kThreads, LAYOUT == kHalf || sizeof(T) == 4 ? 
   };
   int c = per_head < kThreads ? tid - first * per_head : tid;
   int off, pair;  // the place's first channel; its first pair, -1: it passes
+  bool wide = true;  // a vector
   auto place = [&]() {
-    if (LAYOUT == kHalf) {
-      const bool pass = c >= half / V;
-      off = pass ? a.R + (c - half / V) * V : c * V;
-      pair = pass ? -1 : off;
-    } else if (LAYOUT == kPairs) {
-      off = c * V;
+    if (PAIRS) {
+      off = c * W;
       pair = off < a.R ? off / 2 : -1;
     } else {
-      off = c < half ? c : half + c;
-      pair = c < half ? c : -1;
+      const int passing = c - half / W;
+      wide = W == V || passing >= lead;
+      off = passing < 0 ? c * W : a.R + (passing < lead ? passing * W : lead * W + (passing - lead) * V);
+      pair = passing < 0 ? off : -1;
     }
   };
   // within a CTA's tile offsets fit 32 bits (kMaxStride)
@@ -172,90 +199,68 @@ __global__ void __launch_bounds__(kThreads, LAYOUT == kHalf || sizeof(T) == 4 ? 
     if (!PAGED) return ko + ((x.t * a.Hk + h) * a.D + off);
     return (x.h < turned ? ko : vo) + s_row[x.t] + (h * a.D + off);
   };
-  struct Batch {
-    uint4 a[kBatch], b[kBatch];
+  struct Item {
+    uint4 a, b;
   };
-  auto load = [&](Batch& r, At& x) {  // from x on, which moves past them
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (x.t < nt) {
-        const T* const src = source(x);
-        if (LAYOUT == kSingle) {
-          r.a[u].x = kBf16 ? *reinterpret_cast<const uint16_t*>(src) : *reinterpret_cast<const uint32_t*>(src);
-          if (pair >= 0)
-            r.b[u].x = kBf16 ? *reinterpret_cast<const uint16_t*>(src + half) : *reinterpret_cast<const uint32_t*>(src + half);
-        } else {
-          r.a[u] = *reinterpret_cast<const uint4*>(src);
-          if (LAYOUT == kHalf && pair >= 0) r.b[u] = *reinterpret_cast<const uint4*>(src + half);
-        }
-      }
-      advance(x);
+  auto load = [&](Item& r, At& x) {  // x moves past it
+    if (x.t < nt) {
+      const T* const src = source(x);
+      r.a = wide ? load_words<16>(src) : load_words<kBytes>(src);
+      if (!PAIRS && pair >= 0) r.b = load_words<kBytes>(src + half);
     }
+    advance(x);
   };
   // Sines and cosines of this place's pairs for token `held`: read from shared
   // memory once a token, since lanes 64 bytes apart fall on few banks.
-  constexpr int kPairsOf = LAYOUT == kHalf ? V : LAYOUT == kPairs ? V / 2 : 1;
-  float2 w[LAYOUT == kSingle ? 2 : kPairsOf] = {};
+  constexpr int kPairsOf = PAIRS ? W / 2 : W;
+  float2 w[kPairsOf < 2 ? 2 : kPairsOf] = {};
   int held = -1;
-  auto finish = [&](Batch& r, At& x) {
+  auto finish = [&](Item& r, At& x) {
+    if (x.t < nt && s_row[x.t] >= 0) {
+      T* const dst = target(x);
+      const bool turns = pair >= 0 && (!PAGED || x.h < turned);
+      if (turns && x.t != held) {
+        held = x.t;
+        const float2* const from = turn + x.t * half + pair;
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (x.t < nt && s_row[x.t] >= 0) {
-        T* const dst = target(x);
-        const bool turns = pair >= 0 && (!PAGED || x.h < turned);
-        if (turns && x.t != held) {
-          held = x.t;
-          const float2* const from = turn + x.t * half + pair;
+        for (int j = 0; j < kPairsOf; ++j)
+          if (!PAIRS || pair + j < half) w[j] = from[j];
+      }
+      uint32_t* const words[4] = {&r.a.x, &r.a.y, &r.a.z, &r.a.w};
+      if constexpr (PAIRS) {
+        if (turns) {
 #pragma unroll
-          for (int j = 0; j < kPairsOf; ++j)
-            if (LAYOUT != kPairs || pair + j < half) w[j] = from[j];
-        }
-        if constexpr (LAYOUT == kSingle) {
-          if (turns) turn_halves<kBf16>(r.a[u].x, r.b[u].x, w);  // bf16: the upper halves are not used
-          if (kBf16) {
-            *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(r.a[u].x);
-            if (pair >= 0) *reinterpret_cast<uint16_t*>(dst + half) = static_cast<uint16_t>(r.b[u].x);
-          } else {
-            *reinterpret_cast<uint32_t*>(dst) = r.a[u].x;
-            if (pair >= 0) *reinterpret_cast<uint32_t*>(dst + half) = r.b[u].x;
-          }
-        } else if constexpr (LAYOUT == kHalf) {
-          constexpr int e = kBf16 ? 2 : 1;
-          if (turns) {
-            turn_halves<kBf16>(r.a[u].x, r.b[u].x, w);
-            turn_halves<kBf16>(r.a[u].y, r.b[u].y, w + e);
-            turn_halves<kBf16>(r.a[u].z, r.b[u].z, w + 2 * e);
-            turn_halves<kBf16>(r.a[u].w, r.b[u].w, w + 3 * e);
-          }
-          *reinterpret_cast<uint4*>(dst) = r.a[u];
-          if (pair >= 0) *reinterpret_cast<uint4*>(dst + half) = r.b[u];
-        } else {
-          if (turns) {
-            uint32_t* const words[4] = {&r.a[u].x, &r.a[u].y, &r.a[u].z, &r.a[u].w};
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) {
-              if (pair + j >= half) continue;  // a vector may reach past the channels that turn
-              if (kBf16) {
-                float x0 = __uint_as_float(*words[j] << 16), x1 = __uint_as_float(*words[j] & 0xffff0000u);
-                turn_pair(x0, x1, w[j]);
-                *words[j] = round2(x0, x1);
-              } else {
-                float x0 = __uint_as_float(*words[(2 * j) & 3]), x1 = __uint_as_float(*words[(2 * j + 1) & 3]);
-                turn_pair(x0, x1, w[j]);
-                *words[(2 * j) & 3] = __float_as_uint(x0);
-                *words[(2 * j + 1) & 3] = __float_as_uint(x1);
-              }
+          for (int j = 0; j < W / 2; ++j) {
+            if (pair + j >= half) continue;  // a vector may reach past the channels that turn
+            if (kBf16) {
+              float x0 = __uint_as_float(*words[j] << 16), x1 = __uint_as_float(*words[j] & 0xffff0000u);
+              turn_pair(x0, x1, w[j]);
+              *words[j] = round2(x0, x1);
+            } else {
+              float x0 = __uint_as_float(*words[(2 * j) & 3]), x1 = __uint_as_float(*words[(2 * j + 1) & 3]);
+              turn_pair(x0, x1, w[j]);
+              *words[(2 * j) & 3] = __float_as_uint(x0);
+              *words[(2 * j + 1) & 3] = __float_as_uint(x1);
             }
           }
-          *reinterpret_cast<uint4*>(dst) = r.a[u];
         }
+      } else {
+        uint32_t* const others[4] = {&r.b.x, &r.b.y, &r.b.z, &r.b.w};
+        constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4, e = kBf16 ? 2 : 1;  // a single bf16: the upper half is not used
+        if (turns) {
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) turn_halves<kBf16>(*words[j], *others[j], w + e * j);
+        }
+        if (pair >= 0) store_words<kBytes>(dst + half, r.b);
       }
-      advance(x);
+      if (wide) store_words<16>(dst, r.a);
+      else store_words<kBytes>(dst, r.a);
     }
+    advance(x);
   };
   const At none{nt, 0};
   const At begin = first < slots ? At{first / heads, first % heads} : none;
-  Batch even, odd;
+  Item even, odd;
   At next = begin, done = begin;
   place();
   load(even, next);
@@ -337,10 +342,15 @@ __global__ void __launch_bounds__(kThreads, LAYOUT == kHalf || sizeof(T) == 4 ? 
   }
 }
 
+template <typename T, int W, bool PAIRS, bool PAGED>
+cudaError_t launch_as(const RotaryArgs& a, unsigned grid, size_t smem, cudaStream_t s) {
+  kda_rotary_kernel<T, W, PAIRS, PAGED><<<grid, kThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T, bool PAGED>
 cudaError_t launch(RotaryArgs a, bool pairs, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  const int layout = pairs ? kPairs : a.R / 2 % V == 0 ? kHalf : kSingle;
   // Tokens of a CTA: enough for a few rounds of its threads, but no fewer CTAs
   // than four an SM; the table of a tile within its bytes.
   const int64_t vectors = static_cast<int64_t>(a.Hq + a.Hk * (PAGED ? 2 : 1)) * a.D / V;
@@ -350,13 +360,12 @@ cudaError_t launch(RotaryArgs a, bool pairs, cudaStream_t s) {
   a.tile = static_cast<int>(tile < 1 ? 1 : tile > kMaxTile ? kMaxTile : tile);
   const unsigned grid = static_cast<unsigned>((a.S + a.tile - 1) / a.tile);
   const size_t smem = static_cast<size_t>(a.tile) * (a.R / 2) * sizeof(float2);
-  if (layout == kPairs)
-    kda_rotary_kernel<T, kPairs, PAGED><<<grid, kThreads, smem, s>>>(a);
-  else if (layout == kHalf)
-    kda_rotary_kernel<T, kHalf, PAGED><<<grid, kThreads, smem, s>>>(a);
-  else
-    kda_rotary_kernel<T, kSingle, PAGED><<<grid, kThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  const int half = a.R / 2;
+  if (pairs) return launch_as<T, V, true, PAGED>(a, grid, smem, s);
+  if (half % V == 0) return launch_as<T, V, false, PAGED>(a, grid, smem, s);
+  if constexpr (V == 8)
+    if (half % 4 == 0) return launch_as<T, 4, false, PAGED>(a, grid, smem, s);
+  return half % 2 == 0 ? launch_as<T, 2, false, PAGED>(a, grid, smem, s) : launch_as<T, 1, false, PAGED>(a, grid, smem, s);
 }
 
 kda_status tensor(const char* name, const void* p, unsigned align = 15u) {

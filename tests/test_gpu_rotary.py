@@ -43,6 +43,34 @@ def test_forward_and_gradient(S, Hq, Hk, D, dim, dtype, layout, scaling):
                 assert torch.equal(y[..., dim:], x[..., dim:])
 
 
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("dim", [2, 4, 6, 8, 12, 20, 24, 26, 40, 44, 46, 60, 62, 64, 66, 68, 70, 72])
+def test_every_width_of_a_half(dim, dtype):
+    """Halves of 1 to 36 channels: single elements, words, half and whole vectors, and what passes behind them;
+    both outside place and over the inputs, and beside the paged append."""
+    from recompute_kda_chunkwise_gb300 import decode, rotary
+    g = gen(dim)
+    S, Hq, Hk, D, page = 77, 6, 2, 128 if dtype == BF else 72, 16
+    q, k, v = (rand(g, S, h, D, dtype=dtype) for h in (Hq, Hk, Hk))
+    rope = make(dim, "half", "ntk" if dim > 2 else None)
+    cu = torch.tensor([0, S], dtype=I32, device="cuda")
+    yq, yk = rotary.rotary_fwd(rope, q, k, cu_seqlens=cu)
+    for x, y in ((q, yq), (k, yk)):
+        ref, bar = R.turn(x, list(range(S)), rope.frequencies, 1.0, False)
+        R.check(y, ref, bar, "rotated")
+        assert torch.equal(y[..., dim:], x[..., dim:])
+    zq, zk = q.clone(), k.clone()
+    rotary.rotary_fwd(rope, zq, zk, cu_seqlens=cu, out=(zq, zk))
+    assert torch.equal(zq, yq) and torch.equal(zk, yk)
+    if dtype == BF:
+        kp, vp = (rand(g, 5, page, Hk, D) for _ in range(2))
+        table, lens = torch.arange(5, dtype=I32, device="cuda")[None], torch.tensor([S], dtype=I32, device="cuda")
+        tail = kp.view(-1, Hk, D)[S:].clone()
+        aq = decode.paged_append_rotary(rope, q, k, v, kp, vp, table, lens, cu)
+        assert torch.equal(aq, yq) and torch.equal(kp.view(-1, Hk, D)[:S], yk) and torch.equal(vp.view(-1, Hk, D)[:S], v)
+        assert torch.equal(kp.view(-1, Hk, D)[S:], tail)
+
+
 @pytest.mark.parametrize("layout,dim", [("half", 128), ("pairs", 128), ("half", 42)])
 def test_packed_slices_in_place_and_autograd(layout, dim):
     """Slices of a fused projection, positions from cu_seqlens, outputs over their inputs."""
