@@ -11,10 +11,10 @@
 //
 // Bound: HBM, each element read and written once. 72 heads of 128 of 8192
 // tokens in bf16 (151 MB each way), rotated and, for the gradient, rotated back:
-// 104 us, 87% of the measured copy rate; in fp32 40 heads, 6.0 TB/s. Interleaved
-// pairs, whose items are half as long: 55 us a pass, 82%. Halves that no vector
+// 101 us, 90% of the measured copy rate; in fp32 40 heads, 6.2 TB/s. Interleaved
+// pairs, whose items are half as long: 52 us a pass, 87%. Halves that no vector
 // divides go by what does, the channels behind them by vectors: 40 of 128 channels
-// (four at a time) 60 us, 44 (two) 65, 42 (one) 86; all of them one at a time 160.
+// (four at a time) 60 us, 44 (two) 67, 42 (one) 88; all of them one at a time 160.
 //
 // Split. A CTA takes a tile of tokens with all their heads. A token's sines
 // and cosines are formed once, in shared memory, for all of its heads (each
@@ -25,8 +25,9 @@
 // vectors before it are worked on. bf16 is bound by instructions as much as by
 // memory: a thread keeps its place in the heads and its sines in registers, steps
 // through heads without a division, and works on words of two values (171 us
-// before). Five CTAs an SM hold that, six half vectors (60 us; 64 with eight); pairs
-// and shorter items do better with eight (44 channels 65 us, 70 with six).
+// before). Ten CTAs of 128 threads an SM hold that (104 us with five of 256, pairs 55
+// instead of 52, one head of 64 a token 83 instead of 68; 103, 53 and 64 with 64
+// threads), twelve half vectors; pairs and shorter items do better with sixteen.
 #include <math.h>
 
 #include "kda_blocks.h"
@@ -36,12 +37,12 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxTile = 32;          // tokens of a CTA, at most: one warp looks them up
 constexpr int64_t kMaxStride = 1 << 25;  // elements from a token to the next
 static_assert(kMaxStride * kMaxTile <= 1 << 30, "");
 constexpr int kTableBytes = 32768;    // sines and cosines of a tile
-constexpr int kTileVectors = 2048;    // 16-byte vectors of a CTA, about
+constexpr int kTileVectors = 1024;    // 16-byte vectors of a CTA, about
 constexpr int kMinCtas = 608;
 
 struct RotaryArgs {
@@ -133,7 +134,7 @@ __device__ __forceinline__ void store_words(void* p, const uint4& r) {
 // largest power of two up to a vector that divides R/2, elements of either half;
 // of the channels that pass, a vector, W elements only up to the first vector.
 template <typename T, int W, bool PAIRS, bool PAGED>
-__global__ void __launch_bounds__(kThreads, (W * sizeof(T) == 16 && !PAIRS) || sizeof(T) == 4 ? 5 : W * sizeof(T) == 8 ? 6 : 8)
+__global__ void __launch_bounds__(kThreads, (W * sizeof(T) == 16 && !PAIRS) || sizeof(T) == 4 ? 10 : W * sizeof(T) == 8 ? 12 : 16)
     kda_rotary_kernel(const RotaryArgs a) {
   constexpr bool kBf16 = sizeof(T) == 2;
   constexpr int kBytes = W * sizeof(T);
