@@ -82,7 +82,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                           const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                           const float sc) {
   constexpr int kTile = Cfg<D>::kTile, kSlots = Cfg<D>::kSlots;
-  score_regs();
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const ring = smem + 2 * kTile;  // behind the two query tiles
   Shared* const sh = reinterpret_cast<Shared*>(smem + Cfg<D>::kBytes);
@@ -260,73 +259,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_async_smem();
           }
         }
-        // One pass over the row, 32 scores at a time with the next 32 on their way.
-        const uint64_t sc2 = pack2(__float_as_uint(sc), __float_as_uint(sc));
-        uint64_t sum[4] = {0, 0, 0, 0};
-        uint32_t x[32];
-        auto highest = [&]() {
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // The whole row in registers: its maximum first, then probabilities without a branch.
+        uint32_t x[4][32];
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto highest = [&](const uint32_t(&y)[32]) {
 #pragma unroll
           for (int c = 0; c < 32; c += 2)
-            top[c / 2 & 3] = fmaxf(fmaxf(top[c / 2 & 3], __uint_as_float(x[c])), __uint_as_float(x[c + 1]));
-          return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+            top[c / 2 & 3] = fmaxf(fmaxf(top[c / 2 & 3], __uint_as_float(y[c])), __uint_as_float(y[c + 1]));
         };
-        score_ask(my_s);
-        score_got(x);
-        float mn = highest();
-#pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
-          const bool grow = mn > m + kRescale;  // m = -inf: any finite maximum
-          if (__any_sync(~0u, grow)) {
-            // by a whole number of octaves: the factor is exact, for P too
-            const float k = ceilf(mn - m);
-            const float f = !grow ? 1.f : k < 126.f ? __uint_as_float((127u - static_cast<uint32_t>(k)) << 23) : 0.f;
-            if (grow) m = m == -INFINITY ? mn : m + k;
-            l *= f;
-            const uint64_t f2 = pack2(__float_as_uint(f), __float_as_uint(f));
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sum[c] = fma2(sum[c], f2, 0);
-            tmem_st_wait();
+        for (int h = 0; h < 4; ++h) tmem_ask(my_s + 32 * h, x[h]);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) tmem_got(x[h]);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) highest(x[h]);
+        const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+        const bool grow = mn > m + kRescale;  // m = -inf: any finite maximum
+        if (__any_sync(~0u, grow)) {
+          // by a whole number of octaves: the factor is exact
+          const float k = ceilf(mn - m);
+          const float f = !grow ? 1.f : k < 126.f ? __uint_as_float((127u - static_cast<uint32_t>(k)) << 23) : 0.f;
+          if (grow) m = m == -INFINITY ? mn : m + k;
+          l *= f;
+          if (j > 0) {  // the stream's O exists, and is complete: S of this tile was issued after it
             uint32_t y[16];
 #pragma unroll 1
-            for (int c = 0; c < 16 * h; c += 16) {
-              tmem_ask(my_s + c, y);
+            for (int c = 0; c < D; c += 16) {
+              tmem_ask(my_o + c, y);
               tmem_got(y);
 #pragma unroll
-              for (int q = 0; q < 16; ++q)
-                y[q] = pack_bf16(__uint_as_float(y[q] << 16) * f, __uint_as_float(y[q] & 0xffff0000u) * f);
-              tmem_st(my_s + c, y);
-            }
-            if (j > 0) {  // the stream's O exists, and is complete: S of this tile was issued after it
-#pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                tmem_ask(my_o + c, y);
-                tmem_got(y);
-#pragma unroll
-                for (int q = 0; q < 16; ++q) y[q] = __float_as_uint(__uint_as_float(y[q]) * f);
-                tmem_st(my_o + c, y);
-              }
+              for (int q = 0; q < 16; ++q) y[q] = __float_as_uint(__uint_as_float(y[q]) * f);
+              tmem_st(my_o + c, y);
             }
           }
-          const float ref = m == -INFINITY ? 0.f : m;
-          const uint64_t ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
-          uint64_t t[16];
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        const uint64_t sc2 = pack2(__float_as_uint(sc), __float_as_uint(sc));
+        const uint64_t ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
+        uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int c = 0; c < 16; ++c) t[c] = fma2(pack2(x[2 * c], x[2 * c + 1]), sc2, ref2);
-          score_ask(my_s + (32 * (h + 1) & 96));  // after the last: not used
+        for (int h = 0; h < 4; ++h) {
           uint32_t p[16];
-          auto exps = [&](int c) {
-            const float2 e = unpack2(t[c]);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float2 e = unpack2(fma2(pack2(x[h][2 * c], x[h][2 * c + 1]), sc2, ref2));
             const float e0 = ex2(e.x), e1 = ex2(e.y);
             sum[c & 3] = add2(sum[c & 3], pack2(__float_as_uint(e0), __float_as_uint(e1)));
             p[c] = pack_bf16(e0, e1);
-          };
-#pragma unroll
-          for (int c = 0; c < 8; ++c) exps(c);
-          score_got(x);
-          mn = highest();
-#pragma unroll
-          for (int c = 8; c < 16; ++c) exps(c);
+          }
           tmem_st(my_s + 16 * h, p);
         }
         const float2 all = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
