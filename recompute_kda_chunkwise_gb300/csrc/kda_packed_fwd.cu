@@ -46,13 +46,15 @@ struct Cfg {
   static constexpr int kTile = kRows * D * 2;              // bytes of 128 rows
   static constexpr int kSlots = D == 128 ? 5 : 8;          // of K and V in turn
   static constexpr int kBytes = (2 + kSlots) * kTile;
+  static constexpr int kScores = D == 128 ? 2 : 3;         // tiles of S in TMEM, besides the streams' O
 };
 
 struct Shared {
   Handout items;
   uint64_t full[8], empty[8];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_ready[2], o_done[2], o_free[2];
+  uint64_t s_full[2][2], p_ready[2][2];  // of a stream's even and odd tiles
+  uint64_t o_done[2], o_free[2];
   uint64_t drain;
   uint32_t tmem;
   int abort_;
@@ -81,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     kda_packed_fwd_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ CUtensorMap qmap,
                           const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                           const float sc) {
-  constexpr int kTile = Cfg<D>::kTile, kSlots = Cfg<D>::kSlots;
+  constexpr int kTile = Cfg<D>::kTile, kSlots = Cfg<D>::kSlots, kScores = Cfg<D>::kScores;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const ring = smem + 2 * kTile;  // behind the two query tiles
   Shared* const sh = reinterpret_cast<Shared*>(smem + Cfg<D>::kBytes);
@@ -101,8 +103,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh->q_full, 1);
     mbar_init(&sh->q_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh->s_full[i], 1);
-      mbar_init(&sh->p_ready[i], 4);
+      for (int odd = 0; odd < 2; ++odd) {
+        mbar_init(&sh->s_full[i][odd], 1);
+        mbar_init(&sh->p_ready[i][odd], 4);
+      }
       mbar_init(&sh->o_done[i], 1);
       mbar_init(&sh->o_free[i], 4);
     }
@@ -119,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (a.fresh) __syncthreads();
   const int tiles = tiles_of(a, 2 * kRows);  // 0: no warp has work
   const uint32_t tmem = sh->tmem;
-  const uint32_t tmem_s = tmem, tmem_o = tmem + 256;  // S (P over it) of stream i at + 128 i, O at + 128 i
+  const uint32_t tmem_s = tmem, tmem_o = tmem + 128 * kScores;  // tile i of S (P over it) at + 128 i, O of stream i at + D i
   Item it;
 
   if (warp == kLoadWarp) {
@@ -168,13 +172,78 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kStep = kTile >> 4;  // from a slot's descriptor to the next
       const uint32_t full = smem_addr(sh->full), p_ready = smem_addr(sh->p_ready);
       Ring rk;  // the ring's position of K(j); V(j) is the next one
-      uint32_t items = 0, turn_p[2] = {0, 0}, used_o[2] = {0, 0};
+      uint32_t items = 0, turn_p[2] = {0, 0}, used_o[2] = {0, 0}, pos = 0;
       bool ok = true;
+      if constexpr (kScores == 3) {
+        // Scores are issued three tiles ahead, in the place of the tile whose P has just been used. The order is
+        // stream 0, stream 1 of the first keys, of the second, ...; stream 0 has no part in the last.
+        while (item_at(a, tiles, handout_take_alone(&sh->items, items), it)) {
+          const bool two = it.n[1] > 0;
+          const int n0 = it.n[0], nk = two ? it.n[1] : n0;
+          ++items;
+          if (!ok) continue;
+          auto slot_k = [&](int j) { return pos + 2 * j & kSlots - 1; };
+          auto turn_k = [&](int j) { return (pos + 2 * j) / kSlots; };
+          auto scores = [&](int s, int j, uint32_t at) {
+            mma_scores<D>(at, q_at + s * kStep, k_at + slot_k(j) * kStep);
+            mma_commit(&sh->s_full[s][turn_p[s] + j & 1]);
+            if (s == two) {
+              mma_commit(&sh->empty[slot_k(j)]);
+              if (j + 1 == nk) mma_commit(&sh->q_empty);
+            }
+          };
+          auto first = [&](int s, int j, uint32_t at) {
+            const uint32_t k_full = full + 8 * slot_k(j);
+            ok = ok && wait3(ab, a.status, smem_addr(&sh->q_full), items - 1, k_full, turn_k(j), k_full, turn_k(j));
+            if (!ok) return;
+            fence_after_sync();
+            scores(s, j, at);
+          };
+          uint32_t at = tmem_s;
+          // O (+)= P V of stream s, tile j; then scores of (ns, nj) if `more`
+          auto outputs = [&](int s, int j, bool more, int ns, int nj) {
+            if (!ok) return;
+            const uint32_t slot = slot_k(j) + 1, v_full = full + 8 * slot, turn = turn_p[s] + j;
+            const uint32_t k_full = more ? full + 8 * slot_k(nj) : v_full, k_turn = more ? turn_k(nj) : turn_k(j);
+            ok = wait3(ab, a.status, p_ready + 16 * s + 8 * (turn & 1), turn >> 1, v_full, turn_k(j), k_full, k_turn);
+            if (j == 0 && used_o[s]++ > 0) {
+              const uint32_t o_free = smem_addr(&sh->o_free[s]), free = used_o[s] - 2;
+              ok = ok && wait3(ab, a.status, o_free, free, o_free, free, o_free, free);
+            }
+            if (!ok) return;
+            fence_after_sync();
+            mma_rows<D, 128>(tmem_o + D * s, at, v_at + slot * kStep, j > 0);
+            if (more) scores(ns, nj, at);
+            if (s == two) mma_commit(&sh->empty[slot]);
+            if (j + 1 == (s ? nk : n0)) mma_commit(&sh->o_done[s]);
+            at = at == tmem_s + 256 ? tmem_s : at + 128;
+          };
+          first(0, 0, tmem_s);
+          if (two) {
+            first(1, 0, tmem_s + 128);
+            if (n0 > 1) first(0, 1, tmem_s + 256);
+            else first(1, 1, tmem_s + 256);
+            for (int j = 0; j < n0; ++j) {
+              outputs(0, j, j + 1 < n0, 1, j + 1);
+              if (j + 2 == n0) outputs(1, j, true, 1, n0);
+              else outputs(1, j, j + 2 < n0, 0, j + 2);
+            }
+            outputs(1, n0, false, 0, 0);
+          } else {
+            if (n0 > 1) first(0, 1, tmem_s + 128);
+            if (n0 > 2) first(0, 2, tmem_s + 256);
+            for (int j = 0; j < n0; ++j) outputs(0, j, j + 3 < n0, 0, j + 3);
+          }
+          pos += 2 * nk;
+          turn_p[0] += n0;
+          turn_p[1] += it.n[1];
+        }
+      }
       auto qk = [&](int s, int slot) {
         mma_scores<D>(tmem_s + 128 * s, q_at + s * kStep, k_at + slot * kStep);
-        mma_commit(&sh->s_full[s]);
+        mma_commit(&sh->s_full[s][0]);
       };
-      while (item_at(a, tiles, handout_take_alone(&sh->items, items), it)) {
+      while (kScores == 2 && item_at(a, tiles, handout_take_alone(&sh->items, items), it)) {
         const int nk = it.n[1] ? it.n[1] : it.n[0];
         ++items;
         if (!ok) continue;
@@ -198,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int s = 0; s < 2; ++s) {
             if (!ok || j >= it.n[s]) continue;
             // P, V, the next K, and at an item's start O
-            ok = wait3(ab, a.status, p_ready + 8 * s, turn_p[s]++, v_full, rv.turn, k_full, k_turn);
+            ok = wait3(ab, a.status, p_ready + 16 * s, turn_p[s]++, v_full, rv.turn, k_full, k_turn);
             if (j == 0 && used_o[s]++ > 0) {
               const uint32_t o_free = smem_addr(&sh->o_free[s]), turn = used_o[s] - 2;
               ok = ok && wait3(ab, a.status, o_free, turn, o_free, turn, o_free, turn);
@@ -225,8 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- softmax: thread = row, warpgroup = stream ----
     const int st = (warp - kSoftmaxWarp) >> 2, row = tid & 127;
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
-    const uint32_t my_s = tmem_s + 128 * st + lane_base;
-    const uint32_t my_o = tmem_o + 128 * st + lane_base;
+    const uint32_t my_o = tmem_o + D * st + lane_base;
     uint32_t turn_s = 0, turn_d = 0, items = 0;
     int64_t pos = 0;  // ring position of the item's K(0)
     while (item_at(a, tiles, handout_take(&sh->items, items++), it)) {
@@ -235,7 +303,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool used = at < it.L;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nt; ++j) {
-        wait_all(ab, &sh->s_full[st], turn_s++ & 1, a.status);
+        const int number = it.n[1] == 0 ? j : 2 * j + (j < it.n[0] ? st : 0);  // of the tile in the products' order
+        const uint32_t my_s = tmem_s + 128 * (kScores == 2 ? st : number % 3) + lane_base;
+        const uint32_t turn = kScores == 2 ? 2 * turn_s : turn_s;
+        ++turn_s;
+        wait_all(ab, &sh->s_full[st][turn & 1], turn >> 1 & 1, a.status);
         fence_after_sync();
         if (j + 1 == nt) {  // the tile on the diagonal: -inf into S first, off the common path
           const int open = used ? row + 1 : 0;
@@ -281,7 +353,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f = !grow ? 1.f : k < 126.f ? __uint_as_float((127u - static_cast<uint32_t>(k)) << 23) : 0.f;
           if (grow) m = m == -INFINITY ? mn : m + k;
           l *= f;
-          if (j > 0) {  // the stream's O exists, and is complete: S of this tile was issued after it
+          if (j > 0) {
+            // The stream's O exists, and is complete where S of this tile was issued after it; else V of
+            // the tile before is given up when it is.
+            if (kScores == 3) {
+              const int64_t vpos = pos + 2 * j - 1;
+              wait_all(ab, &sh->empty[vpos % kSlots], static_cast<uint32_t>((vpos / kSlots) & 1), a.status);
+              fence_after_sync();
+            }
             uint32_t y[16];
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
@@ -314,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->p_ready[st]);
+        if (lane == 0) mbar_arrive(&sh->p_ready[st][turn & 1]);
       }
       pos += 2 * nk;
       if (nt == 0) continue;
