@@ -60,6 +60,18 @@ struct Shared {
   int abort_;
 };
 
+// A warpgroup's registers a thread, of those that the block was launched with.
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+constexpr int kLaunchRegs = 168, kFewRegs = 120, kManyRegs = 184;
+static_assert(128 * kFewRegs + 32 * kSoftmaxWarps * kManyRegs <= kThreads * kLaunchRegs, "a split above the launch's would wait for ever");
+
 // What every role knows of an item.
 struct Item {
   int lo, L, head, hk, row0;  // row0: first row of stream 0 in the sequence
@@ -127,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Item it;
 
   if (warp == kLoadWarp) {
+    registers_down<kFewRegs>();
     // ---- loads: Q, then K and V in turn ----
     Ring r;
     bool ok = true;
@@ -166,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (items > 0) settle_for(&sh->q_full, (items - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
+    registers_down<kFewRegs>();
     // ---- products, issued by one thread ----
     if (elect()) {
       const uint32_t q_at = desc_k(smem), k_at = desc_k(ring), v_at = desc_mn(ring);
@@ -290,7 +304,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       settle_for(&sh->drain, 0);
     }
     __syncwarp();
-  } else if (warp >= kSoftmaxWarp) {
+  } else if (warp < kSoftmaxWarp) {
+    registers_down<kFewRegs>();
+  } else {
+    registers_up<kManyRegs>();
     // ---- softmax: thread = row, warpgroup = stream ----
     const int st = (warp - kSoftmaxWarp) >> 2, row = tid & 127;
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
