@@ -44,14 +44,15 @@ constexpr float kRescale = 8.f;
 template <int D>
 struct Cfg {
   static constexpr int kTile = kRows * D * 2;              // bytes of 128 rows
-  static constexpr int kSlots = D == 128 ? 5 : 8;          // of K and V in turn
-  static constexpr int kBytes = (2 + kSlots) * kTile;
+  static constexpr int kEach = D == 128 ? 1 : 2;           // tiles of a slot: K and V in turn, or one of each
+  static constexpr int kSlots = D == 128 ? 5 : 6;
+  static constexpr int kBytes = (2 + kSlots * kEach) * kTile;
   static constexpr int kScores = D == 128 ? 2 : 3;         // tiles of S in TMEM, besides the streams' O
 };
 
 struct Shared {
   Handout items;
-  uint64_t full[8], empty[8];
+  uint64_t full[6], empty[6];
   uint64_t q_full, q_empty;
   uint64_t s_full[2][2], p_ready[2][2];  // of a stream's even and odd tiles
   uint64_t o_done[2], o_free[2];
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     kda_packed_fwd_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ CUtensorMap qmap,
                           const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                           const float sc) {
-  constexpr int kTile = Cfg<D>::kTile, kSlots = Cfg<D>::kSlots, kScores = Cfg<D>::kScores;
+  constexpr int kTile = Cfg<D>::kTile, kSlots = Cfg<D>::kSlots, kEach = Cfg<D>::kEach, kScores = Cfg<D>::kScores;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const ring = smem + 2 * kTile;  // behind the two query tiles
   Shared* const sh = reinterpret_cast<Shared*>(smem + Cfg<D>::kBytes);
@@ -159,12 +160,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++items;
       for (int j = 0; j < nk; ++j) {
-        for (int v = 0; v < 2; ++v) {
+        for (int v = 0; v < 2; v += kEach) {
           if (r.turn > 0) ok = ok && wait_all(ab, &sh->empty[r.slot], (r.turn - 1) & 1, a.status);
           if (!ok) break;
           if (elect()) {
-            mbar_expect_tx(&sh->full[r.slot], kTile);
-            load_rows<D>(ring + r.slot * kTile, v ? &vmap : &kmap, it.hk, it.lo + j * kRows, &sh->full[r.slot]);
+            mbar_expect_tx(&sh->full[r.slot], kEach * kTile);
+            uint8_t* const to = ring + r.slot * kEach * kTile;
+            load_rows<D>(to, v ? &vmap : &kmap, it.hk, it.lo + j * kRows, &sh->full[r.slot]);
+            if (kEach == 2) load_rows<D>(to + kTile, &vmap, it.hk, it.lo + j * kRows, &sh->full[r.slot]);
           }
           ++copies;
           r.next(kSlots);
@@ -182,11 +185,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     registers_down<kFewRegs>();
     // ---- products, issued by one thread ----
     if (elect()) {
-      const uint32_t q_at = desc_k(smem), k_at = desc_k(ring), v_at = desc_mn(ring);
+      const uint32_t q_at = desc_k(smem), k_at = desc_k(ring), v_at = desc_mn(ring + (kEach - 1) * kTile);
       constexpr uint32_t kStep = kTile >> 4;  // from a slot's descriptor to the next
       const uint32_t full = smem_addr(sh->full), p_ready = smem_addr(sh->p_ready);
       Ring rk;  // the ring's position of K(j); V(j) is the next one
-      uint32_t items = 0, turn_p[2] = {0, 0}, used_o[2] = {0, 0}, pos = 0;
+      uint32_t items = 0, turn_p[2] = {0, 0}, used_o[2] = {0, 0};
       bool ok = true;
       if constexpr (kScores == 3) {
         // Scores are issued three tiles ahead, in the place of the tile whose P has just been used. The order is
@@ -196,39 +199,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int n0 = it.n[0], nk = two ? it.n[1] : n0;
           ++items;
           if (!ok) continue;
-          auto slot_k = [&](int j) { return pos + 2 * j & kSlots - 1; };
-          auto turn_k = [&](int j) { return (pos + 2 * j) / kSlots; };
           auto scores = [&](int s, int j, uint32_t at) {
-            mma_scores<D>(at, q_at + s * kStep, k_at + slot_k(j) * kStep);
+            mma_scores<D>(at, q_at + s * kStep, k_at + rk.slot * 2 * kStep);
             mma_commit(&sh->s_full[s][turn_p[s] + j & 1]);
             if (s == two) {
-              mma_commit(&sh->empty[slot_k(j)]);
               if (j + 1 == nk) mma_commit(&sh->q_empty);
+              rk.next(kSlots);
             }
           };
+          auto wait1 = [&](uint32_t bar, uint32_t turn) {
+            return wait_for(ab, a.status, [&]() { return poll(bar, turn); });
+          };
           auto first = [&](int s, int j, uint32_t at) {
-            const uint32_t k_full = full + 8 * slot_k(j);
-            ok = ok && wait3(ab, a.status, smem_addr(&sh->q_full), items - 1, k_full, turn_k(j), k_full, turn_k(j));
+            ok = ok && wait1(smem_addr(&sh->q_full), items - 1) && wait1(full + 8 * rk.slot, rk.turn);
             if (!ok) return;
             fence_after_sync();
             scores(s, j, at);
           };
+          Ring rv = rk;
           uint32_t at = tmem_s;
-          // O (+)= P V of stream s, tile j; then scores of (ns, nj) if `more`
-          auto outputs = [&](int s, int j, bool more, int ns, int nj) {
+          // O (+)= P V of stream s, tile j; then scores of (ns, nj) if `more`, the first with those keys if `fresh`
+          auto outputs = [&](int s, int j, bool more, bool fresh, int ns, int nj) {
             if (!ok) return;
-            const uint32_t slot = slot_k(j) + 1, v_full = full + 8 * slot, turn = turn_p[s] + j;
-            const uint32_t k_full = more ? full + 8 * slot_k(nj) : v_full, k_turn = more ? turn_k(nj) : turn_k(j);
-            ok = wait3(ab, a.status, p_ready + 16 * s + 8 * (turn & 1), turn >> 1, v_full, turn_k(j), k_full, k_turn);
-            if (j == 0 && used_o[s]++ > 0) {
-              const uint32_t o_free = smem_addr(&sh->o_free[s]), free = used_o[s] - 2;
-              ok = ok && wait3(ab, a.status, o_free, free, o_free, free, o_free, free);
-            }
+            const uint32_t turn = turn_p[s] + j, p = p_ready + 16 * s + 8 * (turn & 1);
+            const bool wait_k = more && fresh;
+            const uint32_t k_full = wait_k ? full + 8 * rk.slot : p, k_turn = wait_k ? rk.turn : turn >> 1;
+            ok = wait_for(ab, a.status, [&]() { return fresh ? poll2(p, turn >> 1, k_full, k_turn) : poll(p, turn >> 1); });
+            if (j == 0 && used_o[s]++ > 0) ok = ok && wait1(smem_addr(&sh->o_free[s]), used_o[s] - 2);
             if (!ok) return;
             fence_after_sync();
-            mma_rows<D, 128>(tmem_o + D * s, at, v_at + slot * kStep, j > 0);
+            mma_rows<D, 128>(tmem_o + D * s, at, v_at + rv.slot * 2 * kStep, j > 0);
             if (more) scores(ns, nj, at);
-            if (s == two) mma_commit(&sh->empty[slot]);
+            if (s == two) {
+              mma_commit(&sh->empty[rv.slot]);
+              rv.next(kSlots);
+            }
             if (j + 1 == (s ? nk : n0)) mma_commit(&sh->o_done[s]);
             at = at == tmem_s + 256 ? tmem_s : at + 128;
           };
@@ -238,17 +243,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n0 > 1) first(0, 1, tmem_s + 256);
             else first(1, 1, tmem_s + 256);
             for (int j = 0; j < n0; ++j) {
-              outputs(0, j, j + 1 < n0, 1, j + 1);
-              if (j + 2 == n0) outputs(1, j, true, 1, n0);
-              else outputs(1, j, j + 2 < n0, 0, j + 2);
+              outputs(0, j, j + 1 < n0, false, 1, j + 1);
+              if (j + 2 == n0) outputs(1, j, true, true, 1, n0);
+              else outputs(1, j, j + 2 < n0, true, 0, j + 2);
             }
-            outputs(1, n0, false, 0, 0);
+            outputs(1, n0, false, false, 0, 0);
           } else {
             if (n0 > 1) first(0, 1, tmem_s + 128);
             if (n0 > 2) first(0, 2, tmem_s + 256);
-            for (int j = 0; j < n0; ++j) outputs(0, j, j + 3 < n0, 0, j + 3);
+            for (int j = 0; j < n0; ++j) outputs(0, j, j + 3 < n0, true, 0, j + 3);
           }
-          pos += 2 * nk;
           turn_p[0] += n0;
           turn_p[1] += it.n[1];
         }
@@ -341,10 +345,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_wait();
           const int past = it.L - j * kRows;  // rows of the tile from here on are another sequence's
           if (past < kRows) {
-            const int64_t vpos = pos + 2 * j + 1;
+            const int64_t vpos = kEach == 2 ? pos + j : pos + 2 * j + 1;
             const int slot = static_cast<int>(vpos % kSlots);
             if (wait_all(ab, &sh->full[slot], static_cast<uint32_t>((vpos / kSlots) & 1), a.status) && row >= past)
-              zero_row<D>(ring + slot * kTile, row);
+              zero_row<D>(ring + (slot * kEach + kEach - 1) * kTile, row);
             fence_async_smem();
           }
         }
@@ -374,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The stream's O exists, and is complete where S of this tile was issued after it; else V of
             // the tile before is given up when it is.
             if (kScores == 3) {
-              const int64_t vpos = pos + 2 * j - 1;
+              const int64_t vpos = pos + j - 1;
               wait_all(ab, &sh->empty[vpos % kSlots], static_cast<uint32_t>((vpos / kSlots) & 1), a.status);
               fence_after_sync();
             }
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->p_ready[st][turn & 1]);
       }
-      pos += 2 * nk;
+      pos += kEach == 2 ? nk : 2 * nk;
       if (nt == 0) continue;
       const bool fine = wait_all(ab, &sh->o_done[st], turn_d++ & 1, a.status);
       fence_after_sync();
