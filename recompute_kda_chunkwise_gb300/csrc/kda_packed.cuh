@@ -146,6 +146,17 @@ __device__ __forceinline__ bool settle_for(uint64_t* bar, uint32_t parity) {
   return false;
 }
 
+// A warpgroup's registers a thread, of those that the block was launched with. Called by all its warps,
+// in the branch that they take.
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Hands items to the CTA's warps. The first is the CTA's own number, every
 // further one the next that no CTA has taken, heaviest first: the order decides
 // when an item is worked on, not what comes out. One warp fetches a number when
@@ -285,10 +296,16 @@ inline bool rows_map(CUtensorMap* m, const void* base, int64_t S, int heads, int
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// SMs of the current device for a kernel's grid, with its shared memory allowed.
+// SMs of the current device for a kernel's grid, with its shared memory allowed. A kernel
+// that splits its registers between its warpgroups has to be launched with `regs`: with
+// fewer, a warpgroup would wait for its share for ever.
 template <typename K>
-cudaError_t packed_sms(PerDevice& kept, K kernel, size_t smem, int64_t* sms) {
+cudaError_t packed_sms(PerDevice& kept, K kernel, size_t smem, int64_t* sms, int regs = 0) {
   return kept.get(sms, [&](int dev, int64_t* n) {
+    cudaFuncAttributes built;
+    const cudaError_t read = regs > 0 ? cudaFuncGetAttributes(&built, kernel) : cudaSuccess;
+    if (read != cudaSuccess) return read;
+    if (regs > 0 && built.numRegs < regs) return cudaErrorInvalidConfiguration;
     const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     int count = 0;
     const cudaError_t got = cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev);

@@ -58,6 +58,10 @@ constexpr int kGroups = 4, kMathWarps = 4 * kGroups;
 constexpr int kCols = kRows / kGroups, kParts = kCols / 32;
 constexpr int kMmaWarp = 0, kLoadWarp = 1, kMathWarp = 4;
 constexpr int kThreads = 32 * (kMathWarp + kMathWarps);
+// Registers a thread of the dq kernel: what the block is launched with, and its split (2319 -> 2282 us
+// for the whole backward; that of dk and dv needs no more, and its other warps no fewer).
+constexpr int kLaunchRegs = 96, kFewRegs = 64, kManyRegs = 104;
+static_assert(128 * kFewRegs + 32 * kMathWarps * kManyRegs <= kThreads * kLaunchRegs, "a split above the launch's would wait for ever");
 
 // P x 32 columns of a tile, a thread's.
 template <int P>
@@ -550,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   QItem it;
 
   if (warp == kLoadWarp || warp == kLoadWarp + 1) {
+    registers_down<kFewRegs>();
     // ---- loads: a warp for q, d_o and K, another for V: neither waits for the other's slots ----
     const bool v = warp != kLoadWarp;
     uint64_t* const full = v ? sh->v_full : sh->k_full;
@@ -590,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rows) settle_for(&sh->q_full, (items - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
+    registers_down<kFewRegs>();
     // ---- products, issued by one thread ----
     if (elect()) {
       const uint32_t q_at = desc_k(smem), do_at = desc_k(smem + kTile), k_at = desc_k(kt), v_at = desc_k(vt),
@@ -647,7 +653,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       settle_for(&sh->drain, 0);
     }
     __syncwarp();
-  } else if (warp >= kMathWarp) {
+  } else if (warp < kMathWarp) {
+    registers_down<kFewRegs>();
+  } else {
+    registers_up<kManyRegs>();
     const int wg = (warp - kMathWarp) >> 2, row = tid & 127;
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;
     const uint32_t my_s = t_s + lane_base + kCols * wg;
@@ -786,7 +795,7 @@ cudaError_t launch(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap&
   static PerDevice kept_kv, kept_q;
   int64_t sms = 0;
   cudaError_t e = packed_sms(kept_kv, kda_packed_dkv_kernel<D>, smem_kv, &sms);
-  if (e == cudaSuccess) e = packed_sms(kept_q, kda_packed_dq_kernel<D>, smem_q, &sms);
+  if (e == cudaSuccess) e = packed_sms(kept_q, kda_packed_dq_kernel<D>, smem_q, &sms, kLaunchRegs);
   if (e != cudaSuccess) return e;
   if (sms > kPackedMaxCtas) sms = kPackedMaxCtas;
   const float sc = a.scale * 1.4426950408889634f;

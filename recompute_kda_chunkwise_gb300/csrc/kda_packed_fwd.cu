@@ -61,15 +61,7 @@ struct Shared {
   int abort_;
 };
 
-// A warpgroup's registers a thread, of those that the block was launched with.
-template <int N>
-__device__ __forceinline__ void registers_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void registers_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
+// Registers a thread: what the block is launched with, and its split.
 constexpr int kLaunchRegs = 168, kFewRegs = 120, kManyRegs = 184;
 static_assert(128 * kFewRegs + 32 * kSoftmaxWarps * kManyRegs <= kThreads * kLaunchRegs, "a split above the launch's would wait for ever");
 
@@ -455,7 +447,7 @@ cudaError_t launch(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap&
   const size_t smem = Cfg<D>::kBytes + sizeof(Shared);
   static PerDevice kept;
   int64_t sms = 0;
-  const cudaError_t e = packed_sms(kept, kda_packed_fwd_kernel<D>, smem, &sms);
+  const cudaError_t e = packed_sms(kept, kda_packed_fwd_kernel<D>, smem, &sms, kLaunchRegs);
   if (e != cudaSuccess) return e;
   const int64_t most = (a.S / (2 * kRows) + a.N) * a.Hq;  // items
   int64_t ctas = sms < kPackedMaxCtas ? sms : kPackedMaxCtas;

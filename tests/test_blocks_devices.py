@@ -84,3 +84,15 @@ def test_a_setting_that_failed_is_made_again(lib, call):
     lib.fake_fail(1)
     assert call(lib, 128) == KDA_ERR_CUDA
     assert call(lib, 128) == 0
+
+
+@pytest.mark.parametrize("call,regs", [(fwd, 168), (bwd, 96)])
+def test_a_kernel_built_with_too_few_registers_is_not_launched(lib, call, regs):
+    """One that splits them between its warpgroups would wait for the missing ones."""
+    lib.fake_device(0)
+    for D in (64, 128):
+        lib.fake_registers(regs - 8)
+        before = lib.fake_launches()
+        assert call(lib, D) == KDA_ERR_CUDA and lib.fake_launches() == before
+        lib.fake_registers(regs)
+        assert call(lib, D) == 0
