@@ -31,16 +31,17 @@
 // they would cost 40% more products.
 //
 // Bound: the tensor cores in principle, 512 cycles a product of 128 x 128 x 128: 3584
-// a tile for both passes; counters show them active 77% (dk, dv) and 67% (dq) of
+// a tile for both passes; counters show them active 77% (dk, dv) and 70% (dq) of
 // the time. What is left is latency: from a warpgroup's arrival to the product that
 // waited for it (300 to 400 cycles) and from there to the scores. 8192 tokens, 64
-// query heads on 8 of 128: 2296 us (40 for delta, 1040 dq, 1205 dk and dv), 1197
-// TFLOP/s counted as five products; 32768 tokens, 16 heads on 2: 1222. Heads of 64:
-// 1755 us, 783 TFLOP/s, bound by the arithmetic between the products. Without
+// query heads on 8 of 128: 2282 us (40 for delta, 1020 dq, 1205 dk and dv), 1204
+// TFLOP/s counted as five products; 32768 tokens, 16 heads on 2: 1210. Heads of 64:
+// 1689 us, 814 TFLOP/s, bound by the arithmetic between the products. Without
 // loads, or without exponentials, neither pass is more than 3% faster. What brought
 // it there, in us: a ring each for K and V 2995 -> 2505; descriptors of one addition
 // 2452; lse and delta in the ring with d_o instead of a barrier a step 2414; one
-// issuing thread with joint waits, dq's scores read a tile ahead 2296.
+// issuing thread with joint waits, dq's scores read a tile ahead 2296; registers for
+// dq's arithmetic 2319 -> 2282 on a slower day.
 #include <math.h>
 
 #include "kda_packed.cuh"

@@ -27,7 +27,8 @@
 // through heads without a division, and works on words of two values (171 us
 // before). Ten CTAs of 128 threads an SM hold that (104 us with five of 256, pairs 55
 // instead of 52, one head of 64 a token 83 instead of 68; 103, 53 and 64 with 64
-// threads), twelve half vectors; pairs and shorter items do better with sixteen.
+// threads), twelve half vectors and pairs of fp32; other pairs and shorter items do
+// better with sixteen.
 #include <math.h>
 
 #include "kda_blocks.h"
@@ -43,7 +44,7 @@ constexpr int64_t kMaxStride = 1 << 25;  // elements from a token to the next
 static_assert(kMaxStride * kMaxTile <= 1 << 30, "");
 constexpr int kTableBytes = 32768;    // sines and cosines of a tile
 constexpr int kTileVectors = 1024;    // 16-byte vectors of a CTA, about
-constexpr int kMinCtas = 608;
+constexpr int kMinCtas = 1216;
 
 struct RotaryArgs {
   const void *q, *k, *v;   // v: paged form only
@@ -134,7 +135,7 @@ __device__ __forceinline__ void store_words(void* p, const uint4& r) {
 // largest power of two up to a vector that divides R/2, elements of either half;
 // of the channels that pass, a vector, W elements only up to the first vector.
 template <typename T, int W, bool PAIRS, bool PAGED>
-__global__ void __launch_bounds__(kThreads, (W * sizeof(T) == 16 && !PAIRS) || sizeof(T) == 4 ? 10 : W * sizeof(T) == 8 ? 12 : 16)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? PAIRS ? 12 : 10 : W == 8 && !PAIRS ? 10 : W == 4 ? 12 : 16)
     kda_rotary_kernel(const RotaryArgs a) {
   constexpr bool kBf16 = sizeof(T) == 2;
   constexpr int kBytes = W * sizeof(T);
@@ -353,7 +354,7 @@ template <typename T, bool PAGED>
 cudaError_t launch(RotaryArgs a, bool pairs, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   // Tokens of a CTA: enough for a few rounds of its threads, but no fewer CTAs
-  // than four an SM; the table of a tile within its bytes.
+  // than eight an SM; the table of a tile within its bytes.
   const int64_t vectors = static_cast<int64_t>(a.Hq + a.Hk * (PAGED ? 2 : 1)) * a.D / V;
   int64_t tile = (kTileVectors + vectors - 1) / vectors;
   if (tile > a.S / kMinCtas) tile = a.S / kMinCtas;
