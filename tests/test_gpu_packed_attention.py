@@ -55,6 +55,20 @@ def test_sharp_and_flat_probabilities(scale, std):
     R.check_all(run(q, k, v, d_o, cu, scale), *R.attention(q, k, v, cu.tolist(), scale, d_o))
 
 
+@pytest.mark.parametrize("lens,Hq,Hk", [((1023,), 2, 1), ((640, 100, 897, 0, 128), 4, 2), ((260, 384, 129, 500), 48, 16)])
+@pytest.mark.parametrize("D", [128, 64])
+def test_maxima_that_rise_with_every_tile(lens, Hq, Hk, D):
+    """Scores that rise by some 17 octaves a tile, or fall, as the query's sign is: outputs are rescaled at every
+    tile, while other tiles' products are under way; items of one stream and of two, in turn on one CTA."""
+    q, k, v, d_o, cu = inputs(lens, Hq, Hk, D, seed=D, std=0.5)
+    u = torch.ones(D, device="cuda") * D ** -0.5
+    sign = torch.where(torch.rand(q.shape[:2], generator=torch.Generator().manual_seed(3)) < 0.7, 3.0, -3.0).cuda()
+    at = torch.cat([torch.arange(n) for n in lens]).cuda().float()
+    q = (q.float() + sign[..., None] * u).to(BF)
+    k = (k.float() + 0.25 * at[:, None, None] * u).to(BF)
+    R.check_all(run(q, k, v, d_o, cu, 0.125), *R.attention(q, k, v, cu.tolist(), 0.125, d_o))
+
+
 def test_slices_of_a_projection_and_autograd():
     from recompute_kda_chunkwise_gb300.attention import attention
     lens, Hq, Hk, D = (200, 131), 4, 2, 128
