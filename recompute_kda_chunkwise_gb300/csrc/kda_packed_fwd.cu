@@ -21,7 +21,7 @@
 // go stream by stream, and each tile's scores are issued three tiles ahead, into the
 // place of the tile whose P has just been used, so that they are there when their
 // warpgroup comes to them (595 -> 522); a tile of K and its V are one slot, so that a
-// product has one wait (506 -> 493).
+// product has one wait (506 -> 493; 472 with a barrier for each place of a stream).
 //
 // Items are handed out heaviest first to one CTA per SM. The next item's queries,
 // keys and values are fetched, and its first scores formed, while the last item's
@@ -31,7 +31,7 @@
 // chain scores -> probabilities -> products of each stream, of which two hide most.
 // 8192 tokens, 64 query heads on 8 of 128: 662 us, 1660 TFLOP/s, 86% of the measured
 // bf16 rate; 32768 tokens, 16 heads on 2: 1825. Heads of 64, with the same exponentials
-// for half the products: 493 us, 1115 TFLOP/s. One thread issues all products and its
+// for half the products: 472 us, 1165 TFLOP/s. One thread issues all products and its
 // instructions between them count: descriptors of one addition (771 -> 744 us), one
 // joint wait for all that a batch needs (662; 708 with two), the stream a constant (690;
 // 754 where it was computed). P handed over in two parts is no faster (686 and 695).
@@ -63,7 +63,8 @@ struct Shared {
   Handout items;
   uint64_t full[6], empty[6];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2][2], p_ready[2][2];  // of a stream's even and odd tiles
+  // of a stream's scores, by the place in TMEM where they lie (see below)
+  uint64_t s_full[2][3], p_ready[2][3];
   uint64_t o_done[2], o_free[2];
   uint64_t drain;
   uint32_t tmem;
@@ -117,9 +118,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh->q_full, 1);
     mbar_init(&sh->q_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      for (int odd = 0; odd < 2; ++odd) {
-        mbar_init(&sh->s_full[i][odd], 1);
-        mbar_init(&sh->p_ready[i][odd], 4);
+      for (int place = 0; place < 3; ++place) {
+        mbar_init(&sh->s_full[i][place], 1);
+        mbar_init(&sh->p_ready[i][place], 4);
       }
       mbar_init(&sh->o_done[i], 1);
       mbar_init(&sh->o_free[i], 4);
@@ -190,19 +191,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kStep = kTile >> 4;  // from a slot's descriptor to the next
       const uint32_t full = smem_addr(sh->full), p_ready = smem_addr(sh->p_ready);
       Ring rk;  // the ring's position of K(j); V(j) is the next one
-      uint32_t items = 0, turn_p[2] = {0, 0}, used_o[2] = {0, 0};
+      uint32_t items = 0, turn_p[2] = {0, 0}, used_o[2] = {0, 0};  // turn_p, three places: a bit for each
       bool ok = true;
       if constexpr (kScores == 3) {
         // Scores are issued three tiles ahead, in the place of the tile whose P has just been used. The order is
         // stream 0, stream 1 of the first keys, of the second, ...; stream 0 has no part in the last.
+        // A stream has a barrier for each place: scores come to one again only behind the wait for the P that was
+        // formed there, so neither barrier can complete twice before it is seen. (One for even and one for odd tiles
+        // could: an item of one stream has tiles 0 and 2 on their way at once. One for both streams would let
+        // a stream through that had no part in the item before.)
         while (item_at(a, tiles, handout_take_alone(&sh->items, items), it)) {
           const bool two = it.n[1] > 0;
           const int n0 = it.n[0], nk = two ? it.n[1] : n0;
           ++items;
           if (!ok) continue;
-          auto scores = [&](int s, int j, uint32_t at) {
-            mma_scores<D>(at, q_at + s * kStep, k_at + rk.slot * 2 * kStep);
-            mma_commit(&sh->s_full[s][turn_p[s] + j & 1]);
+          auto scores = [&](int s, int j, int place) {
+            mma_scores<D>(tmem_s + 128 * place, q_at + s * kStep, k_at + rk.slot * 2 * kStep);
+            mma_commit(&sh->s_full[s][place]);
             if (s == two) {
               if (j + 1 == nk) mma_commit(&sh->q_empty);
               rk.next(kSlots);
@@ -211,38 +216,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto wait1 = [&](uint32_t bar, uint32_t turn) {
             return wait_for(ab, a.status, [&]() { return poll(bar, turn); });
           };
-          auto first = [&](int s, int j, uint32_t at) {
+          auto first = [&](int s, int j, int place) {
             ok = ok && wait1(smem_addr(&sh->q_full), items - 1) && wait1(full + 8 * rk.slot, rk.turn);
             if (!ok) return;
             fence_after_sync();
-            scores(s, j, at);
+            scores(s, j, place);
           };
           Ring rv = rk;
-          uint32_t at = tmem_s;
+          int place = 0;
           // O (+)= P V of stream s, tile j; then scores of (ns, nj) if `more`, the first with those keys if `fresh`
           auto outputs = [&](int s, int j, bool more, bool fresh, int ns, int nj) {
             if (!ok) return;
-            const uint32_t turn = turn_p[s] + j, p = p_ready + 16 * s + 8 * (turn & 1);
+            const uint32_t turn = turn_p[s] >> place, p = p_ready + 24 * s + 8 * place;
+            turn_p[s] ^= 1u << place;
             const bool wait_k = more && fresh;
-            const uint32_t k_full = wait_k ? full + 8 * rk.slot : p, k_turn = wait_k ? rk.turn : turn >> 1;
-            ok = wait_for(ab, a.status, [&]() { return fresh ? poll2(p, turn >> 1, k_full, k_turn) : poll(p, turn >> 1); });
+            const uint32_t k_full = wait_k ? full + 8 * rk.slot : p, k_turn = wait_k ? rk.turn : turn;
+            ok = wait_for(ab, a.status, [&]() { return fresh ? poll2(p, turn, k_full, k_turn) : poll(p, turn); });
             if (j == 0 && used_o[s]++ > 0) ok = ok && wait1(smem_addr(&sh->o_free[s]), used_o[s] - 2);
             if (!ok) return;
             fence_after_sync();
-            mma_rows<D, 128>(tmem_o + D * s, at, v_at + rv.slot * 2 * kStep, j > 0);
-            if (more) scores(ns, nj, at);
+            mma_rows<D, 128>(tmem_o + D * s, tmem_s + 128 * place, v_at + rv.slot * 2 * kStep, j > 0);
+            if (more) scores(ns, nj, place);
             if (s == two) {
               mma_commit(&sh->empty[rv.slot]);
               rv.next(kSlots);
             }
             if (j + 1 == (s ? nk : n0)) mma_commit(&sh->o_done[s]);
-            at = at == tmem_s + 256 ? tmem_s : at + 128;
+            place = place == 2 ? 0 : place + 1;
           };
-          first(0, 0, tmem_s);
+          first(0, 0, 0);
           if (two) {
-            first(1, 0, tmem_s + 128);
-            if (n0 > 1) first(0, 1, tmem_s + 256);
-            else first(1, 1, tmem_s + 256);
+            first(1, 0, 1);
+            if (n0 > 1) first(0, 1, 2);
+            else first(1, 1, 2);
             for (int j = 0; j < n0; ++j) {
               outputs(0, j, j + 1 < n0, false, 1, j + 1);
               if (j + 2 == n0) outputs(1, j, true, true, 1, n0);
@@ -250,12 +256,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             outputs(1, n0, false, false, 0, 0);
           } else {
-            if (n0 > 1) first(0, 1, tmem_s + 128);
-            if (n0 > 2) first(0, 2, tmem_s + 256);
+            if (n0 > 1) first(0, 1, 1);
+            if (n0 > 2) first(0, 2, 2);
             for (int j = 0; j < n0; ++j) outputs(0, j, j + 3 < n0, true, 0, j + 3);
           }
-          turn_p[0] += n0;
-          turn_p[1] += it.n[1];
         }
       }
       auto qk = [&](int s, int slot) {
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int s = 0; s < 2; ++s) {
             if (!ok || j >= it.n[s]) continue;
             // P, V, the next K, and at an item's start O
-            ok = wait3(ab, a.status, p_ready + 16 * s, turn_p[s]++, v_full, rv.turn, k_full, k_turn);
+            ok = wait3(ab, a.status, p_ready + 24 * s, turn_p[s]++, v_full, rv.turn, k_full, k_turn);
             if (j == 0 && used_o[s]++ > 0) {
               const uint32_t o_free = smem_addr(&sh->o_free[s]), turn = used_o[s] - 2;
               ok = ok && wait3(ab, a.status, o_free, turn, o_free, turn, o_free, turn);
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int st = (warp - kSoftmaxWarp) >> 2, row = tid & 127;
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
     const uint32_t my_o = tmem_o + D * st + lane_base;
-    uint32_t turn_s = 0, turn_d = 0, items = 0;
+    uint32_t turn_s = 0, turn_d = 0, items = 0;  // turn_s: a bit for each place
     int64_t pos = 0;  // ring position of the item's K(0)
     while (item_at(a, tiles, handout_take(&sh->items, items++), it)) {
       const int nt = it.n[st], nk = it.n[1] ? it.n[1] : it.n[0];
@@ -326,10 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nt; ++j) {
         const int number = it.n[1] == 0 ? j : 2 * j + (j < it.n[0] ? st : 0);  // of the tile in the products' order
-        const uint32_t my_s = tmem_s + 128 * (kScores == 2 ? st : number % 3) + lane_base;
-        const uint32_t turn = kScores == 2 ? 2 * turn_s : turn_s;
-        ++turn_s;
-        wait_all(ab, &sh->s_full[st][turn & 1], turn >> 1 & 1, a.status);
+        const int place = kScores == 2 ? 0 : number % 3;
+        const uint32_t my_s = tmem_s + 128 * (kScores == 2 ? st : place) + lane_base;
+        wait_all(ab, &sh->s_full[st][place], turn_s >> place & 1, a.status);
+        turn_s ^= 1u << place;
         fence_after_sync();
         if (j + 1 == nt) {  // the tile on the diagonal: -inf into S first, off the common path
           const int open = used ? row + 1 : 0;
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->p_ready[st][turn & 1]);
+        if (lane == 0) mbar_arrive(&sh->p_ready[st][place]);
       }
       pos += kEach == 2 ? nk : 2 * nk;
       if (nt == 0) continue;
