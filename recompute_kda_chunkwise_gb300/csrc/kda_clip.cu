@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kda_squares_kernel(const
     const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     if (total > 0x1p-70f && total < 0x1p100f) {
       all += static_cast<double>(total);
-    } else if (any & 0x7fff7fffu) {  // out of fp32's range, or not finite; zeros of either sign add nothing
+    } else if (any & (t.bf16_in ? 0x7fff7fffu : 0x7fffffffu)) {  // out of fp32's range, or not finite; zeros of either sign add nothing
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {
         const uint4 y = j == 0 ? x[0] : j == 1 ? x[1] : j == 2 ? x[2] : x[3];

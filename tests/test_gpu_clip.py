@@ -185,3 +185,22 @@ def test_workspace_of_the_caller_shared_by_two_graphs():
                 g.replay()
     s.synchronize()
     assert [n.item() for n in norms] == want
+
+
+@pytest.mark.parametrize("dtype,bits", [(F32, [0x8000]), (F32, [0x8000, 0]), (F32, [1]), (F32, [0x10000, 0x8000]), (BF, [1]), (BF, [0x8000, 1])])
+def test_the_smallest_gradients_count(dtype, bits):
+    """fp32 whose only bit of 16 or more lies where bf16 has its sign, beside other subnormals; zeros of either sign."""
+    from recompute_kda_chunkwise_gb300 import grads as G
+    n = 100_000
+    word = torch.int32 if dtype == F32 else torch.int16
+    x = torch.tensor([b - (1 << 16) if dtype == BF and b >> 15 else b for b in bits], dtype=word, device="cuda")
+    t = x.repeat(n // len(bits)).view(dtype)
+    t[1::2].neg_()
+    ref = R.norm([t])
+    assert ref > 0
+    # the norm is a subnormal or near one: half a step there beside what check_norm allows
+    assert abs(G.grad_norm([t]).item() - ref) <= ref * 2.0 ** -20 + 2.0 ** -150
+    out = [torch.empty(n, device="cuda")]
+    G.clip_grads([t], ref / 2, out=out)
+    R.check(out[0], R.d(t) / 2, R.d(t).abs() * 2.0 ** -19 + 2.0 ** -150, "clipped")
+    assert G.grad_norm([torch.full((40,), -0.0, device="cuda", dtype=dtype)]).item() == 0
