@@ -134,6 +134,11 @@ int32_t* word(const Tensor& t, c10::DeviceIndex dev) {
   return static_cast<int32_t*>(fit(t, "status", {1}, at::kInt, dev));
 }
 
+// A caller's tensor was written behind autograd's back: a graph that saved it has to notice.
+void written(const Tensor& t) {
+  if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 template <typename F>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, const F& f) {
   if (n != want) {
@@ -428,13 +433,17 @@ PyObject* rotary(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     }
     int32_t* const status = word(a.maybe(10, "status"), dev);
     const c10::cuda::CUDAGuard on(dev);
-    Tensor qo = a.maybe(8, "q_out"), ko = a.maybe(9, "k_out");
+    const Tensor q_given = a.maybe(8, "q_out"), k_given = a.maybe(9, "k_out");
+    Tensor qo = q_given, ko = k_given;
     if (!k.defined() && ko.defined()) throw Refused("k_out without k");
     if (!qo.defined()) qo = at::empty(qs, q.options().requires_grad(false));
     if (k.defined() && !ko.defined()) ko = at::empty(ks, q.options().requires_grad(false));
     const kda_status r = g_entry.rotary(&p, qr.p, kr.p, fit(qo, "q_out", qs, dt, dev), fit(ko, "k_out", ks, dt, dev), status,
                                         stream_of(q));
-    return r == KDA_OK ? Py_BuildValue("(NN)", wrap(qo), wrap(ko)) : PyLong_FromLong(r);
+    if (r != KDA_OK) return PyLong_FromLong(r);
+    written(q_given);
+    written(k_given);
+    return Py_BuildValue("(NN)", wrap(qo), wrap(ko));
   });
 }
 
@@ -455,12 +464,17 @@ PyObject* append_rotary(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     p.k_stride = kr.stride;
     int32_t* const status = word(a.maybe(12, "status"), dev);
     const c10::cuda::CUDAGuard on(dev);
-    Tensor qo = a.maybe(11, "q_out");
+    const Tensor given = a.maybe(11, "q_out");
+    Tensor qo = given;
     if (!q.defined() && qo.defined()) throw Refused("q_out without q");
     if (q.defined() && !qo.defined()) qo = at::empty(qs, q.options().requires_grad(false));
     const kda_status r = g_entry.append_rotary(&g.p, &p, vr.stride, qr.p, kr.p, vr.p, fit(qo, "q_out", qs, at::kBFloat16, dev),
                                                g.k, g.v, status, stream_of(k));
-    return r == KDA_OK ? wrap(qo) : PyLong_FromLong(r);
+    if (r != KDA_OK) return PyLong_FromLong(r);
+    written(given);
+    written(a.at(6, "k_pages"));
+    written(a.at(7, "v_pages"));
+    return wrap(qo);
   });
 }
 
@@ -504,13 +518,16 @@ PyObject* packed_fwd(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     const Packed g = packed(q, a.at(1, "k"), a.at(2, "v"), a.at(3, "cu_seqlens"), v[4], v[4] == Py_None ? 0 : a.number(4));
     const auto dev = q.get_device();
     const c10::cuda::CUDAGuard on(dev);
-    Tensor out = a.maybe(5, "out"), ws = a.maybe(6, "workspace");
+    const Tensor given = a.maybe(5, "out");
+    Tensor out = given, ws = a.maybe(6, "workspace");
     if (!out.defined()) out = at::empty(g.qs, q.options().requires_grad(false));
     void* const op = fit(out, "out", g.qs, at::kBFloat16, dev);
     const Tensor lse = at::empty({g.qs[1], g.qs[0]}, q.options().dtype(at::kFloat).requires_grad(false));
     void* const wsp = buffer(ws, g_entry.packed_fwd_bytes(&g.p), q);
     const kda_status r = g_entry.packed_fwd(&g.p, g.q, g.k, g.v, op, static_cast<float*>(lse.data_ptr()), wsp, stream_of(q));
-    return r == KDA_OK ? Py_BuildValue("(NN)", wrap(out), wrap(lse)) : PyLong_FromLong(r);
+    if (r != KDA_OK) return PyLong_FromLong(r);
+    written(given);
+    return Py_BuildValue("(NN)", wrap(out), wrap(lse));
   });
 }
 
@@ -636,8 +653,7 @@ PyObject* clip(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     const kda_status r = g_entry.clip(num, g.p.data(), g.n.data(), g.dtype.data(), const_cast<void* const*>(o.p.data()),
                                       o.dtype.data(), a.number(1), static_cast<float*>(norm.data_ptr()), wsp, stream_of(norm));
     if (r != KDA_OK) return PyLong_FromLong(r);
-    for (const Tensor& x : o.t)  // written behind autograd's back: a graph that saved one has to notice
-      if (!x.is_inference()) x.unsafeGetTensorImpl()->bump_version();
+    for (const Tensor& x : o.t) written(x);
     return wrap(norm);
   });
 }
