@@ -51,7 +51,7 @@ typedef struct {
 } kda_rotary_problem;
 
 /* q_out [S, Hq, D] and k_out [S, Hkv, D] are contiguous; q_out may be q, and
- * k_out k, where that is contiguous too. Rows of tokens that cu_seqlens puts
+ * k_out k, where that is contiguous too; they overlap nothing else. Rows of tokens that cu_seqlens puts
  * into no sequence are not written (recorded in status). One launch. */
 kda_status kda_rotary(const kda_rotary_problem* p, const void* q, const void* k,
                       void* q_out, void* k_out, int32_t* status, void* stream);
@@ -60,7 +60,8 @@ kda_status kda_rotary(const kda_rotary_problem* p, const void* q, const void* k,
  * in the cache, kv_lens[n] - L + i, on their way there, and the new tokens'
  * queries beside them. r gives strides, rotary_dim, layout, magnitude and
  * freqs (its other fields are not read, inverse must be 0); v_stride as
- * q_stride. q NULL: keys and values only (q_out NULL then). q_out may be q.
+ * q_stride. q NULL: keys and values only (q_out NULL then). q_out may be q
+ * where that is contiguous; it and the pages overlap nothing else of the call.
  * What kda_paged_append skips is skipped, its row of q_out not written. */
 kda_status kda_paged_append_rotary(const kda_paged_problem* p, const kda_rotary_problem* r, int64_t v_stride,
                                    const void* q, const void* k, const void* v, void* q_out,
@@ -90,7 +91,8 @@ typedef struct {
   const int32_t* cu_seqlens;  /* device [N+1]: 0 .. S, not decreasing */
 } kda_attention_problem;
 
-/* o [S, Hq, D], lse fp32 [Hq, S]. The call's status word is the head of the
+/* o [S, Hq, D], lse fp32 [Hq, S]; o may be q where that is contiguous. Outputs
+ * and workspace overlap nothing else of the call. The call's status word is the head of the
  * workspace (kda_query_device_status): cu_seqlens that decrease or do not
  * reach from 0 to S leave the outputs unwritten. */
 size_t kda_attention_fwd_workspace_bytes(const kda_attention_problem* p);

@@ -18,7 +18,8 @@ from ._serving import AttentionProblem, bind, done, library
 def attention_fwd(q, k, v, cu_seqlens, *, scale=None, out=None, workspace=None):
     """Forward. cu_seqlens int32 [N+1]; scale: D ** -0.5 when None. workspace: a
     uint8 CUDA buffer of at least attention_workspace_bytes, whose head holds
-    the call's status word; allocated when None. Returns (o [S, Hq, D], lse
+    the call's status word; allocated when None. out may hold o, and may be a
+    contiguous q; it and the workspace overlap nothing else. Returns (o [S, Hq, D], lse
     fp32 [Hq, S]: the logarithm of each query's sum of exponentials)."""
     return done(bind().packed_fwd(q, k, v, cu_seqlens, scale, out, workspace), "kda_attention_fwd")
 

@@ -52,7 +52,7 @@ def _build_bind(force: bool = False) -> str:
 
     import torch
     src = os.path.join(CSRC, "kda_bind.cpp")
-    newest = max(os.path.getmtime(f) for f in [src, *(h for h in _headers() if h.startswith(INCLUDE)), torch.__file__])
+    newest = max(os.path.getmtime(f) for f in [src, os.path.join(CSRC, "kda_span.h"), *(h for h in _headers() if h.startswith(INCLUDE)), torch.__file__])
     if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= newest:
         return BIND
     at = os.path.dirname(torch.__file__)

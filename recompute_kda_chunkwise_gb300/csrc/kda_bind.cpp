@@ -28,6 +28,7 @@
 #include <vector>
 
 #include "kda_blocks.h"
+#include "kda_span.h"
 
 namespace {
 
@@ -390,6 +391,30 @@ Rows rows_of(const Tensor& t, const char* name, at::IntArrayRef shape, at::Scala
                   text(t.sizes()) + (t.is_cuda() ? "" : " on the CPU") + (shaped ? ", strided " + text(t.strides()) + ")" : ")"));
   return {t.data_ptr(), t.size(0) > 1 ? t.stride(0) : t.size(1) * t.size(2)};
 }
+// Memory of such a tensor, and of one that is contiguous.
+kda::Span span(const char* name, const Tensor& t, const Rows& r) {
+  if (!t.defined()) return kda::whole(name, nullptr, 0);
+  const int64_t elt = t.element_size();
+  const int64_t wide = t.size(1) * t.size(2);  // the entry points refuse shorter strides
+  return {name, reinterpret_cast<uintptr_t>(r.p), t.size(0), wide * elt, std::max(r.stride, std::max<int64_t>(wide, 1)) * elt};
+}
+kda::Span span(const char* name, const Tensor& t) {
+  return t.defined() ? kda::whole(name, t.data_ptr(), t.nbytes()) : kda::whole(name, nullptr, 0);
+}
+// What a call writes shares no memory with what else it writes, or reads: kernels
+// take both in any order. Output i may lie exactly over one contiguous input, the
+// one called over[i]. Outputs that the call itself makes need not be looked at.
+void apart(std::initializer_list<kda::Span> outs, std::initializer_list<kda::Span> ins, std::initializer_list<const char*> over = {}) {
+  auto own = over.begin();
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    const std::string input = own != over.end() ? *own++ : "";
+    for (auto x = o + 1; x != outs.end(); ++x)
+      if (kda::meet(*o, *x)) throw Refused(std::string(x->name) + " overlaps " + o->name);
+    for (const kda::Span& x : ins)
+      if (kda::meet(*o, x) && !(o->at == x.at && (x.rows == 1 || x.step == x.bytes) && input == x.name))
+        throw Refused(std::string(o->name) + " overlaps " + x.name);
+  }
+}
 
 // freqs interleaved magnitude
 kda_rotary_problem turn(const Args& a, int i, c10::DeviceIndex dev) {
@@ -438,8 +463,12 @@ PyObject* rotary(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     if (!k.defined() && ko.defined()) throw Refused("k_out without k");
     if (!qo.defined()) qo = at::empty(qs, q.options().requires_grad(false));
     if (k.defined() && !ko.defined()) ko = at::empty(ks, q.options().requires_grad(false));
-    const kda_status r = g_entry.rotary(&p, qr.p, kr.p, fit(qo, "q_out", qs, dt, dev), fit(ko, "k_out", ks, dt, dev), status,
-                                        stream_of(q));
+    void *const qop = fit(qo, "q_out", qs, dt, dev), *const kop = fit(ko, "k_out", ks, dt, dev);
+    if (q_given.defined() || k_given.defined())
+      apart({span("q_out", q_given), span("k_out", k_given)},
+            {span("q", q, qr), span("k", k, kr), span("frequencies", a.at(0, "frequencies")), span("positions", pos),
+             span("cu_seqlens", cu)}, {"q", "k"});
+    const kda_status r = g_entry.rotary(&p, qr.p, kr.p, qop, kop, status, stream_of(q));
     if (r != KDA_OK) return PyLong_FromLong(r);
     written(q_given);
     written(k_given);
@@ -458,8 +487,9 @@ PyObject* append_rotary(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     kda_rotary_problem p = turn(a, 0, dev);
     const Paged g = paged(a, 6, q.defined() ? q : k, q.defined() ? "q" : "k", k.size(1), 1.0);
     const std::array<int64_t, 3> ks{k.size(0), k.size(1), k.size(2)}, qs{ks[0], q.defined() ? q.size(1) : 0, ks[2]};
+    const Tensor val = a.at(5, "v"), kp = a.at(6, "k_pages"), vp = a.at(7, "v_pages");
     const Rows qr = rows_of(q, "q", qs, at::kBFloat16, dev), kr = rows_of(k, "k", ks, at::kBFloat16, dev),
-               vr = rows_of(a.at(5, "v"), "v", ks, at::kBFloat16, dev);
+               vr = rows_of(val, "v", ks, at::kBFloat16, dev);
     p.q_stride = qr.stride;
     p.k_stride = kr.stride;
     int32_t* const status = word(a.maybe(12, "status"), dev);
@@ -468,12 +498,16 @@ PyObject* append_rotary(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     Tensor qo = given;
     if (!q.defined() && qo.defined()) throw Refused("q_out without q");
     if (q.defined() && !qo.defined()) qo = at::empty(qs, q.options().requires_grad(false));
-    const kda_status r = g_entry.append_rotary(&g.p, &p, vr.stride, qr.p, kr.p, vr.p, fit(qo, "q_out", qs, at::kBFloat16, dev),
-                                               g.k, g.v, status, stream_of(k));
+    void* const qop = fit(qo, "q_out", qs, at::kBFloat16, dev);
+    apart({span("q_out", given), span("k_pages", kp), span("v_pages", vp)},
+          {span("q", q, qr), span("k", k, kr), span("v", val, vr), span("frequencies", a.at(0, "frequencies")),
+           span("page_table", a.at(8, "page_table")), span("kv_lens", a.at(9, "kv_lens")),
+           span("cu_seqlens", a.at(10, "cu_seqlens"))}, {"q"});
+    const kda_status r = g_entry.append_rotary(&g.p, &p, vr.stride, qr.p, kr.p, vr.p, qop, g.k, g.v, status, stream_of(k));
     if (r != KDA_OK) return PyLong_FromLong(r);
     written(given);
-    written(a.at(6, "k_pages"));
-    written(a.at(7, "v_pages"));
+    written(kp);
+    written(vp);
     return wrap(qo);
   });
 }
@@ -523,7 +557,14 @@ PyObject* packed_fwd(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     if (!out.defined()) out = at::empty(g.qs, q.options().requires_grad(false));
     void* const op = fit(out, "out", g.qs, at::kBFloat16, dev);
     const Tensor lse = at::empty({g.qs[1], g.qs[0]}, q.options().dtype(at::kFloat).requires_grad(false));
+    const bool own = !ws.defined();
     void* const wsp = buffer(ws, g_entry.packed_fwd_bytes(&g.p), q);
+    if (given.defined() || !own) {
+      const Tensor k = a.at(1, "k"), val = a.at(2, "v");
+      apart({span("out", given), own ? kda::whole("workspace", nullptr, 0) : span("workspace", ws)},
+            {span("q", q, {g.q, g.p.q_stride}), span("k", k, {g.k, g.p.k_stride}), span("v", val, {g.v, g.p.v_stride}),
+             span("cu_seqlens", a.at(3, "cu_seqlens"))}, {"q"});
+    }
     const kda_status r = g_entry.packed_fwd(&g.p, g.q, g.k, g.v, op, static_cast<float*>(lse.data_ptr()), wsp, stream_of(q));
     if (r != KDA_OK) return PyLong_FromLong(r);
     written(given);
@@ -543,7 +584,15 @@ PyObject* packed_bwd(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     void* const gp = fit(a.at(5, "d_o"), "d_o", g.qs, at::kBFloat16, dev);
     const c10::cuda::CUDAGuard on(dev);
     Tensor ws = a.maybe(8, "workspace");
+    const bool own = !ws.defined();
     void* const wsp = buffer(ws, g_entry.packed_bwd_bytes(&g.p), q);
+    if (!own) {
+      const Tensor k = a.at(1, "k"), val = a.at(2, "v");
+      apart({span("workspace", ws)},
+            {span("q", q, {g.q, g.p.q_stride}), span("k", k, {g.k, g.p.k_stride}), span("v", val, {g.v, g.p.v_stride}),
+             span("o", a.at(3, "o")), span("lse", a.at(4, "lse")), span("d_o", a.at(5, "d_o")),
+             span("cu_seqlens", a.at(6, "cu_seqlens"))});
+    }
     const auto opts = q.options().requires_grad(false);
     const Tensor dq = at::empty(g.qs, opts), dk = at::empty(g.ks, opts), dv = at::empty(g.ks, opts);
     const kda_status r = g_entry.packed_bwd(&g.p, g.q, g.k, g.v, op, lp, gp, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), wsp,

@@ -87,7 +87,7 @@ def rotary_fwd(rope, q, k=None, *, positions=None, cu_seqlens=None, out=None, st
     token's position is positions[s] (int32 [S]) or its index in its sequence
     of cu_seqlens (int32 [N+1]); one of the two is given. Returns (q', k'),
     contiguous; k' is None without k. ``out`` may hold (q', k'), either of
-    them None, and each may be its contiguous input."""
+    them None; each may be its contiguous input, and overlaps nothing else."""
     return _call(rope, q, k, 0, positions, cu_seqlens, out, status)
 
 

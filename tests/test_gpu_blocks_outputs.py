@@ -55,3 +55,51 @@ def test_attention_may_write_over_its_queries(D):
     x = q.clone()
     y, lse2 = A.attention_fwd(x, k, v, cu, out=x)
     assert y.data_ptr() == x.data_ptr() and torch.equal(x, o) and torch.equal(lse, lse2)
+
+
+def test_outputs_over_other_tensors_are_refused():
+    from recompute_kda_chunkwise_gb300 import attention as A, decode, rotary as T
+    rope, cu, S = T.Rotary(64), torch.tensor([0, 10], dtype=I32, device="cuda"), 10
+    pos = torch.arange(S, dtype=I32, device="cuda")
+    q, k, v, d_o = (rand(i, S, 4, 64) for i in range(4))
+    kp, vp, *rest = cache(4)
+    flat = rand(5, 4 * S * 256)
+    at = lambda i: flat[i:i + S * 256].view(S, 4, 64)  # noqa: E731
+    fused = rand(6, S, 3 * 256)
+    a, b, c = (fused[:, i * 256:(i + 1) * 256].view(S, 4, 64) for i in range(3))
+    first = fused[:1].view(3, 4, 64)[0:1]
+    keep = [t.clone() for t in (q, k, v, kp, vp, flat, fused, pos)]
+
+    def ints(n):  # int32 tensors inside an output
+        return flat.view(I32)[64:64 + n]
+
+    for call, what in (
+            (lambda: T.rotary_fwd(rope, q, k, positions=pos, out=(k, None)), "q_out overlaps k"),
+            (lambda: T.rotary_fwd(rope, q, k, positions=pos, out=(None, q)), "k_out overlaps q"),
+            (lambda: T.rotary_fwd(rope, q, q, positions=pos, out=(q, None)), "q_out overlaps k"),
+            (lambda: T.rotary_fwd(rope, q, k, positions=pos, out=(at(0), at(0))), "k_out overlaps q_out"),
+            (lambda: T.rotary_fwd(rope, q, k, positions=pos, out=(at(0), at(S * 256 - 8))), "k_out overlaps q_out"),
+            (lambda: T.rotary_fwd(rope, at(0), positions=pos, out=(at(8), None)), "q_out overlaps q"),
+            (lambda: T.rotary_bwd(rope, at(8), positions=pos, out=(at(0), None)), "q_out overlaps q"),
+            (lambda: T.rotary_fwd(rope, q, positions=ints(S), out=(at(0), None)), "q_out overlaps positions"),
+            (lambda: T.rotary_fwd(rope, a, positions=pos, out=(fused.view(-1)[:S * 256].view(S, 4, 64), None)), "q_out overlaps q"),
+            (lambda: decode.paged_append_rotary(rope, q, k, v, kp, vp, *rest, out=k), "q_out overlaps k"),
+            (lambda: decode.paged_append_rotary(rope, q, k, v, kp, vp, *rest, out=v), "q_out overlaps v"),
+            (lambda: decode.paged_append_rotary(rope, q, k, v, kp, kp, *rest), "v_pages overlaps k_pages"),
+            (lambda: decode.paged_append_rotary(rope, q, kp.view(-1, 4, 64)[:S], v, kp, vp, *rest), "k_pages overlaps k"),
+            (lambda: decode.paged_append_rotary(rope, q, k, v, kp, vp, *rest, out=vp.view(-1, 4, 64)[:S]), "v_pages overlaps q_out"),
+            (lambda: A.attention_fwd(q, k, v, cu, out=v), "out overlaps v"),
+            (lambda: A.attention_fwd(q, k, v, cu, out=k), "out overlaps k"),
+            (lambda: A.attention_fwd(a, b, c, cu, out=fused.view(-1)[:S * 256].view(S, 4, 64)), "out overlaps q"),
+            (lambda: A.attention_fwd(at(0), k, v, cu, out=at(8)), "out overlaps q"),
+            (lambda: A.attention_fwd(at(0), k, v, cu, workspace=flat.view(torch.uint8)), "workspace overlaps q"),
+            (lambda: A.attention_fwd(q, k, v, cu, out=at(0), workspace=flat.view(torch.uint8)), "workspace overlaps out"),
+            (lambda: A.attention_bwd(q, k, v, at(0), torch.zeros(4, S, device="cuda"), d_o, cu,
+                                     workspace=flat.view(torch.uint8)), "workspace overlaps o")):
+        with pytest.raises(ValueError, match=what):
+            call()
+    assert all(torch.equal(x, y) for x, y in zip(keep, (q, k, v, kp, vp, flat, fused, pos)))
+    # what lies beside one another, or in the gaps of a strided tensor, does not overlap
+    T.rotary_fwd(rope, q, k, positions=pos, out=(at(0), at(S * 256)))
+    T.rotary_fwd(rope, first, positions=pos[:1], out=(fused[:1, 256:512].view(1, 4, 64), None))
+    A.attention_fwd(q, k, v, cu, out=at(2 * S * 256), workspace=flat[:S * 256].view(torch.uint8))
