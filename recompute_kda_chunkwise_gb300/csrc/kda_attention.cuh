@@ -164,4 +164,18 @@ inline EncodeFn encode_fn() {
   return fn;
 }
 
+// make(): tensor maps, false where one could not be made. The encoder needs a current
+// context, and a thread has none before the first of its runtime calls that needs the
+// device (autograd's thread, where a gradient is its first work): such a call, which
+// changes nothing, and once more.
+template <typename F>
+bool in_context(const void* kernel, const F& make) {
+  if (make()) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutDefault) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return make();
+}
+
 }  // namespace kda

@@ -139,6 +139,16 @@ struct Maps {
   CUtensorMap q, k, v, d_o;
 };
 
+kda_status maps_of(const kda_attention_problem* p, const void* q, const void* k, const void* v, const void* d_o, Maps* m) {
+  const bool made = in_context(reinterpret_cast<const void*>(&kda_packed_list_kernel), [&]() {
+    return rows_map(&m->q, q, p->total_tokens, p->num_heads, p->head_dim, p->q_stride) &&
+           rows_map(&m->k, k, p->total_tokens, p->num_kv_heads, p->head_dim, p->k_stride) &&
+           rows_map(&m->v, v, p->total_tokens, p->num_kv_heads, p->head_dim, p->v_stride) &&
+           (!d_o || rows_map(&m->d_o, d_o, p->total_tokens, p->num_heads, p->head_dim, (int64_t)p->num_heads * p->head_dim));
+  });
+  return made ? KDA_OK : set_error(KDA_ERR_CUDA, "the tensor maps of q, k, v and d_o could not be made");
+}
+
 // Status word and list of tiles; the arguments that forward and backward share.
 kda_status begin(const kda_attention_problem* p, int rows, void* workspace, PackedArgs* a, cudaStream_t s) {
   *a = PackedArgs{};
@@ -175,14 +185,6 @@ kda_status begin(const kda_attention_problem* p, int rows, void* workspace, Pack
   return e == cudaSuccess ? KDA_OK : set_error(KDA_ERR_CUDA, "attention set-up failed: %s", cudaGetErrorString(e));
 }
 
-kda_status maps_of(const kda_attention_problem* p, const void* q, const void* k, const void* v, Maps* m) {
-  if (rows_map(&m->q, q, p->total_tokens, p->num_heads, p->head_dim, p->q_stride) &&
-      rows_map(&m->k, k, p->total_tokens, p->num_kv_heads, p->head_dim, p->k_stride) &&
-      rows_map(&m->v, v, p->total_tokens, p->num_kv_heads, p->head_dim, p->v_stride))
-    return KDA_OK;
-  return set_error(KDA_ERR_CUDA, "the tensor maps of q, k and v could not be made");
-}
-
 }  // namespace
 }  // namespace kda
 
@@ -208,7 +210,7 @@ kda_status kda_attention_fwd(const kda_attention_problem* p, const void* q, cons
   cudaStream_t s = (cudaStream_t)stream;
   PackedArgs a;
   Maps m;
-  if (p->total_tokens > 0) TRY(maps_of(p, q, k, v, &m));
+  if (p->total_tokens > 0) TRY(maps_of(p, q, k, v, nullptr, &m));
   TRY(begin(p, 256, workspace, &a, s));
   if (p->total_tokens == 0) return KDA_OK;
   a.o = static_cast<__nv_bfloat16*>(o);
@@ -235,9 +237,7 @@ kda_status kda_attention_bwd(const kda_attention_problem* p, const void* q, cons
                                                                {"d_o", d_o}, {"dq", dq}, {"dk", dk}, {"dv", dv}};
     for (const auto& t : all) TRY(tensor(t.name, t.t));
     TRY(tensor("lse", lse, 3u));
-    TRY(maps_of(p, q, k, v, &m));
-    if (!rows_map(&m.d_o, d_o, p->total_tokens, p->num_heads, p->head_dim, (int64_t)p->num_heads * p->head_dim))
-      return set_error(KDA_ERR_CUDA, "the tensor map of d_o could not be made");
+    TRY(maps_of(p, q, k, v, d_o, &m));
   }
   TRY(begin(p, 128, workspace, &a, s));
   if (p->total_tokens == 0) return KDA_OK;

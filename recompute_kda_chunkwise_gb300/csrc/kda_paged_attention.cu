@@ -914,7 +914,8 @@ kda_status launch_paged_attention(const PagedArgs& a, cudaStream_t s) {
   int box = kRows;
   while (a.page % box) box /= 2;  // the largest power of two up to 128 that divides the page: at least 8
   CUtensorMap k, v;
-  if (!page_map(&k, a.k, a, box) || !page_map(&v, a.v, a, box))
+  if (!in_context(reinterpret_cast<const void*>(&kda_paged_attention_kernel<64>),
+                  [&]() { return page_map(&k, a.k, a, box) && page_map(&v, a.v, a, box); }))
     return set_error(KDA_ERR_CUDA, "the tensor maps of the cache could not be made");
   const cudaError_t e = a.D == 128 ? launch<128>(a, k, v, box, s) : launch<64>(a, k, v, box, s);
   return e == cudaSuccess ? KDA_OK : set_error(KDA_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));

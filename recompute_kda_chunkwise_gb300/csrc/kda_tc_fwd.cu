@@ -1028,6 +1028,12 @@ size_t fwd_handoff_bytes(int items) {
 kda_status launch_fwd_tc(const kda_problem* p, const FwdArgs& a, cudaStream_t s) {
   if (p->head_dim != kD || p->dtype != KDA_DTYPE_BF16) return KDA_ERR_UNSUPPORTED;
   const bool cg = a.w != nullptr;  // GDN-2: b is the raw erase gate [S,H,D], w the raw write gate
+  void (*kern)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
+               const CUtensorMap, const TcFwdArgs) = cg ? kda_fwd_tc_kernel<true> : kda_fwd_tc_kernel<false>;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  // before the tensor maps, which need the thread's context: this call makes it current
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess)
+    return KDA_ERR_CUDA;
   CUtensorMap mq, mk, mv, mg, me, mw;
   if (!make_tma_map_bf16(&mq, a.q, p->total_tokens, p->num_heads) ||
       !make_tma_map_bf16(&mk, a.k, p->total_tokens, p->num_heads) ||
@@ -1042,8 +1048,6 @@ kda_status launch_fwd_tc(const kda_problem* p, const FwdArgs& a, cudaStream_t s)
     me = mq;  // unused
     mw = mq;
   }
-  void (*kern)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
-               const CUtensorMap, const TcFwdArgs) = cg ? kda_fwd_tc_kernel<true> : kda_fwd_tc_kernel<false>;
   TcFwdArgs t;
   t.b = static_cast<const __nv_bfloat16*>(a.b);
   t.A_log = a.A_log;
@@ -1064,9 +1068,6 @@ kda_status launch_fwd_tc(const kda_problem* p, const FwdArgs& a, cudaStream_t s)
   t.helpers = 0;
   t.xflags = a.xflags;
   t.xbuf = a.xbuf;
-  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess)
-    return KDA_ERR_CUDA;
   const int items = p->num_seqs * p->num_heads;
   // Split mode: with at least half as many spare SMs as items, helper CTAs
   // prepare every other chunk. Their hand-off waits need every CTA resident
