@@ -44,7 +44,7 @@ typedef struct {
   int32_t interleaved;
   int32_t inverse;
   float magnitude;
-  float reserved;             /* 0 */
+  int32_t fresh;              /* outputs that hold nothing yet: 1 q_out, 2 k_out, or both (3) */
   const int64_t* freqs;       /* device [R/2] */
   const int32_t* positions;   /* device [S]; NULL: a token's index in its sequence */
   const int32_t* cu_seqlens;  /* device [N+1], where positions is NULL */
@@ -52,17 +52,19 @@ typedef struct {
 
 /* q_out [S, Hq, D] and k_out [S, Hkv, D] are contiguous; q_out may be q, and
  * k_out k, where that is contiguous too; they overlap nothing else. Rows of tokens that cu_seqlens puts
- * into no sequence are not written (recorded in status). One launch. */
+ * into no sequence are not written, or, of a fresh output, zeros (recorded in
+ * status). One launch. */
 kda_status kda_rotary(const kda_rotary_problem* p, const void* q, const void* k,
                       void* q_out, void* k_out, int32_t* status, void* stream);
 
 /* kda_paged_append with rotary positions: keys are rotated by their position
  * in the cache, kv_lens[n] - L + i, on their way there, and the new tokens'
- * queries beside them. r gives strides, rotary_dim, layout, magnitude and
- * freqs (its other fields are not read, inverse must be 0); v_stride as
+ * queries beside them. r gives strides, rotary_dim, layout, magnitude,
+ * freqs and fresh (its other fields are not read, inverse must be 0); v_stride as
  * q_stride. q NULL: keys and values only (q_out NULL then). q_out may be q
  * where that is contiguous; it and the pages overlap nothing else of the call.
- * What kda_paged_append skips is skipped, its row of q_out not written. */
+ * What kda_paged_append skips is skipped, its row of q_out not written (zeros
+ * where that is fresh). */
 kda_status kda_paged_append_rotary(const kda_paged_problem* p, const kda_rotary_problem* r, int64_t v_stride,
                                    const void* q, const void* k, const void* v, void* q_out,
                                    void* k_pages, void* v_pages, int32_t* status, void* stream);
@@ -99,6 +101,13 @@ size_t kda_attention_fwd_workspace_bytes(const kda_attention_problem* p);
 kda_status kda_attention_fwd(const kda_attention_problem* p, const void* q, const void* k, const void* v,
                              void* o, float* lse, void* workspace, void* stream);
 
+/* The same for outputs that hold nothing yet, and with a status of the
+ * caller's. fresh: 1 o, 2 lse, or both (3): where cu_seqlens is refused these
+ * are filled with NaN. status: int32 on the device, zeroed by the caller, that
+ * takes the call's status word instead of the workspace's head (NULL: that). */
+kda_status kda_attention_fwd_fresh(const kda_attention_problem* p, const void* q, const void* k, const void* v,
+                                   void* o, float* lse, void* workspace, int32_t fresh, int32_t* status, void* stream);
+
 /* Gradients of o in q, k, v from the forward's inputs and outputs and d_o
  * [S, Hq, D]: dq [S, Hq, D], dk, dv [S, Hkv, D], contiguous, as o and d_o.
  * The probabilities are formed again from q, k and lse. */
@@ -106,6 +115,12 @@ size_t kda_attention_bwd_workspace_bytes(const kda_attention_problem* p);
 kda_status kda_attention_bwd(const kda_attention_problem* p, const void* q, const void* k, const void* v,
                              const void* o, const float* lse, const void* d_o,
                              void* dq, void* dk, void* dv, void* workspace, void* stream);
+
+/* The same for gradients that hold nothing yet (fresh 1; 0: as above), and with
+ * a status of the caller's. */
+kda_status kda_attention_bwd_fresh(const kda_attention_problem* p, const void* q, const void* k, const void* v,
+                                   const void* o, const float* lse, const void* d_o, void* dq, void* dk, void* dv,
+                                   void* workspace, int32_t fresh, int32_t* status, void* stream);
 
 /* ---- the global gradient norm, and clipping by it ---------------------------
  *

@@ -27,11 +27,16 @@ class PagedProblem(ctypes.Structure):
                 ("scale", _f32), ("cu_seqlens", _vp), ("page_table", _vp), ("kv_lens", _vp)]
 
 
+class _Fresh(ctypes.Union):
+    _fields_ = [("fresh", _i32), ("reserved", _f32)]  # the second: its name in programs from before it had a use, 0
+
+
 class RotaryProblem(ctypes.Structure):
     """Mirror of ``kda_rotary_problem``."""
+    _anonymous_ = ("_fresh",)
     _fields_ = [("total_tokens", _i64), ("q_stride", _i64), ("k_stride", _i64), ("num_seqs", _i32), ("num_heads", _i32),
                 ("num_kv_heads", _i32), ("head_dim", _i32), ("rotary_dim", _i32), ("dtype", _i32), ("interleaved", _i32),
-                ("inverse", _i32), ("magnitude", _f32), ("reserved", _f32), ("freqs", _vp), ("positions", _vp),
+                ("inverse", _i32), ("magnitude", _f32), ("_fresh", _Fresh), ("freqs", _vp), ("positions", _vp),
                 ("cu_seqlens", _vp)]
 
 
@@ -65,8 +70,10 @@ def library():
                 ("kda_paged_append_rotary", ctypes.c_int, [G, R, _i64] + [_vp] * 8),
                 ("kda_attention_fwd_workspace_bytes", ctypes.c_size_t, [A]),
                 ("kda_attention_fwd", ctypes.c_int, [A] + [_vp] * 7),
+                ("kda_attention_fwd_fresh", ctypes.c_int, [A] + [_vp] * 6 + [_i32] + [_vp] * 2),
                 ("kda_attention_bwd_workspace_bytes", ctypes.c_size_t, [A]),
                 ("kda_attention_bwd", ctypes.c_int, [A] + [_vp] * 11),
+                ("kda_attention_bwd_fresh", ctypes.c_int, [A] + [_vp] * 10 + [_i32] + [_vp] * 2),
                 ("kda_grad_norm_workspace_bytes", ctypes.c_size_t, [_i32]),
                 ("kda_grad_norm", ctypes.c_int, [_i32] + [_vp] * 6),
                 ("kda_clip_grads", ctypes.c_int, [_i32] + [_vp] * 5 + [ctypes.c_double] + [_vp] * 3)):
@@ -97,8 +104,8 @@ def bind():
         m.init(*(ctypes.cast(getattr(lib, n), _vp).value for n in (
             "kda_step", "kda_gdn2_step", "kda_block_norm_fwd", "kda_block_norm_workspace_bytes", "kda_block_norm_bwd",
             "kda_verify_drafts", "kda_paged_append", "kda_paged_attention_workspace_bytes", "kda_paged_attention",
-            "kda_rotary", "kda_paged_append_rotary", "kda_attention_fwd_workspace_bytes", "kda_attention_fwd",
-            "kda_attention_bwd_workspace_bytes", "kda_attention_bwd", "kda_grad_norm_workspace_bytes", "kda_grad_norm",
+            "kda_rotary", "kda_paged_append_rotary", "kda_attention_fwd_workspace_bytes", "kda_attention_fwd_fresh",
+            "kda_attention_bwd_workspace_bytes", "kda_attention_bwd_fresh", "kda_grad_norm_workspace_bytes", "kda_grad_norm",
             "kda_clip_grads")))
         _bind = m
     return _bind

@@ -47,9 +47,9 @@ struct Entry {
   decltype(&kda_rotary) rotary;
   decltype(&kda_paged_append_rotary) append_rotary;
   decltype(&kda_attention_fwd_workspace_bytes) packed_fwd_bytes;
-  decltype(&kda_attention_fwd) packed_fwd;
+  decltype(&kda_attention_fwd_fresh) packed_fwd;
   decltype(&kda_attention_bwd_workspace_bytes) packed_bwd_bytes;
-  decltype(&kda_attention_bwd) packed_bwd;
+  decltype(&kda_attention_bwd_fresh) packed_bwd;
   decltype(&kda_grad_norm_workspace_bytes) norm_of_grads_bytes;
   decltype(&kda_grad_norm) norm_of_grads;
   decltype(&kda_clip_grads) clip;
@@ -468,6 +468,7 @@ PyObject* rotary(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
       apart({span("q_out", q_given), span("k_out", k_given)},
             {span("q", q, qr), span("k", k, kr), span("frequencies", a.at(0, "frequencies")), span("positions", pos),
              span("cu_seqlens", cu)}, {"q", "k"});
+    p.fresh = (q_given.defined() ? 0 : 1) | (k.defined() && !k_given.defined() ? 2 : 0);
     const kda_status r = g_entry.rotary(&p, qr.p, kr.p, qop, kop, status, stream_of(q));
     if (r != KDA_OK) return PyLong_FromLong(r);
     written(q_given);
@@ -503,6 +504,7 @@ PyObject* append_rotary(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
           {span("q", q, qr), span("k", k, kr), span("v", val, vr), span("frequencies", a.at(0, "frequencies")),
            span("page_table", a.at(8, "page_table")), span("kv_lens", a.at(9, "kv_lens")),
            span("cu_seqlens", a.at(10, "cu_seqlens"))}, {"q"});
+    p.fresh = q.defined() && !given.defined() ? 1 : 0;
     const kda_status r = g_entry.append_rotary(&g.p, &p, vr.stride, qr.p, kr.p, vr.p, qop, g.k, g.v, status, stream_of(k));
     if (r != KDA_OK) return PyLong_FromLong(r);
     written(given);
@@ -544,9 +546,9 @@ Packed packed(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& c
   return r;
 }
 
-// q k v cu_seqlens scale|None out|None workspace|None
+// q k v cu_seqlens scale|None out|None workspace|None status|None
 PyObject* packed_fwd(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
-  return guarded(nargs, 7, [&]() -> PyObject* {
+  return guarded(nargs, 8, [&]() -> PyObject* {
     const Args a{v};
     const Tensor q = a.at(0, "q");
     const Packed g = packed(q, a.at(1, "k"), a.at(2, "v"), a.at(3, "cu_seqlens"), v[4], v[4] == Py_None ? 0 : a.number(4));
@@ -565,16 +567,17 @@ PyObject* packed_fwd(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
             {span("q", q, {g.q, g.p.q_stride}), span("k", k, {g.k, g.p.k_stride}), span("v", val, {g.v, g.p.v_stride}),
              span("cu_seqlens", a.at(3, "cu_seqlens"))}, {"q"});
     }
-    const kda_status r = g_entry.packed_fwd(&g.p, g.q, g.k, g.v, op, static_cast<float*>(lse.data_ptr()), wsp, stream_of(q));
+    const kda_status r = g_entry.packed_fwd(&g.p, g.q, g.k, g.v, op, static_cast<float*>(lse.data_ptr()), wsp,
+                                            given.defined() ? 2 : 3, word(a.maybe(7, "status"), dev), stream_of(q));
     if (r != KDA_OK) return PyLong_FromLong(r);
     written(given);
     return Py_BuildValue("(NN)", wrap(out), wrap(lse));
   });
 }
 
-// q k v o lse d_o cu_seqlens scale|None workspace|None
+// q k v o lse d_o cu_seqlens scale|None workspace|None status|None
 PyObject* packed_bwd(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
-  return guarded(nargs, 9, [&]() -> PyObject* {
+  return guarded(nargs, 10, [&]() -> PyObject* {
     const Args a{v};
     const Tensor q = a.at(0, "q");
     const Packed g = packed(q, a.at(1, "k"), a.at(2, "v"), a.at(6, "cu_seqlens"), v[7], v[7] == Py_None ? 0 : a.number(7));
@@ -595,8 +598,8 @@ PyObject* packed_bwd(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     }
     const auto opts = q.options().requires_grad(false);
     const Tensor dq = at::empty(g.qs, opts), dk = at::empty(g.ks, opts), dv = at::empty(g.ks, opts);
-    const kda_status r = g_entry.packed_bwd(&g.p, g.q, g.k, g.v, op, lp, gp, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), wsp,
-                                            stream_of(q));
+    const kda_status r = g_entry.packed_bwd(&g.p, g.q, g.k, g.v, op, lp, gp, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), wsp, 1,
+                                            word(a.maybe(9, "status"), dev), stream_of(q));
     return r == KDA_OK ? Py_BuildValue("(NNN)", wrap(dq), wrap(dk), wrap(dv)) : PyLong_FromLong(r);
   });
 }

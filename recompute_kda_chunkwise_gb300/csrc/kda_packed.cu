@@ -15,11 +15,11 @@ constexpr int kBuckets = 1024;
 // from the top, and places each tile. The order within a bucket is left open:
 // it decides when a tile is worked on, not what comes out.
 __global__ void __launch_bounds__(1024) kda_packed_list_kernel(const int32_t* cu, int N, int64_t S, int rows, int* list,
-                                                               int* status) {
+                                                               int* head, int* status) {
   __shared__ int count[kBuckets], sums[32], s_most;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   before_kernel();
-  if (tid < kClearBytes / 4) status[tid] = 0;
+  if (tid < kClearBytes / 4) head[tid] = 0;
   int bad = 0, most = 0;
   for (int n = tid; n < N; n += 1024) {
     const int lo = cu[n], hi = cu[n + 1];
@@ -150,11 +150,12 @@ kda_status maps_of(const kda_attention_problem* p, const void* q, const void* k,
 }
 
 // Status word and list of tiles; the arguments that forward and backward share.
-kda_status begin(const kda_attention_problem* p, int rows, void* workspace, PackedArgs* a, cudaStream_t s) {
+kda_status begin(const kda_attention_problem* p, int rows, void* workspace, int32_t* status, PackedArgs* a, cudaStream_t s) {
   *a = PackedArgs{};
   a->cu = p->cu_seqlens;
-  a->status = static_cast<int*>(workspace);
-  a->tickets = a->status + 4;
+  a->head = static_cast<int*>(workspace);
+  a->status = status ? status : a->head;
+  a->tickets = a->head + 4;
   a->S = p->total_tokens;
   a->N = p->num_seqs;
   a->Hq = p->num_heads;
@@ -173,12 +174,12 @@ kda_status begin(const kda_attention_problem* p, int rows, void* workspace, Pack
     return got;
   });
   if (e != cudaSuccess) return set_error(KDA_ERR_CUDA, "attention set-up failed: %s", cudaGetErrorString(e));
-  a->fresh = rows == 256 && a->N == 1 && a->S > 0 && (a->S + 255) / 256 * a->Hq <= (sms < kPackedMaxCtas ? sms : kPackedMaxCtas);
-  if (a->S == 0 || (a->N == 1 && rows == 256 && !a->fresh)) {
+  a->clears = rows == 256 && a->N == 1 && a->S > 0 && (a->S + 255) / 256 * a->Hq <= (sms < kPackedMaxCtas ? sms : kPackedMaxCtas);
+  if (a->S == 0 || (a->N == 1 && rows == 256 && !a->clears)) {
     e = cudaMemsetAsync(workspace, 0, kClearBytes, s);
   } else if (a->N > 1) {
     int* const list = reinterpret_cast<int*>(static_cast<char*>(workspace) + kHeaderBytes);
-    kda_packed_list_kernel<<<1, 1024, 0, s>>>(a->cu, a->N, a->S, rows, list, a->status);
+    kda_packed_list_kernel<<<1, 1024, 0, s>>>(a->cu, a->N, a->S, rows, list, a->head, a->status);
     e = cudaGetLastError();
     a->list = list;
   }
@@ -195,11 +196,13 @@ size_t kda_attention_fwd_workspace_bytes(const kda_attention_problem* p) {
   return validate(p, false) == KDA_OK ? kHeaderBytes + list_bytes(p, 256) : 0;
 }
 
-kda_status kda_attention_fwd(const kda_attention_problem* p, const void* q, const void* k, const void* v, void* o, float* lse,
-                             void* workspace, void* stream) {
+kda_status kda_attention_fwd_fresh(const kda_attention_problem* p, const void* q, const void* k, const void* v, void* o,
+                                   float* lse, void* workspace, int32_t fresh, int32_t* status, void* stream) {
   using namespace kda;
   TRY(validate(p, true));
   TRY(tensor("workspace", workspace));
+  if (fresh & ~3) return set_error(KDA_ERR_INVALID_ARG, "fresh %d is not 0 .. 3", fresh);
+  if ((uintptr_t)status & 3u) return set_error(KDA_ERR_INVALID_ARG, "status is not 4-byte aligned");
   if (p->total_tokens > 0) {
     TRY(tensor("q", q));
     TRY(tensor("k", k));
@@ -211,12 +214,18 @@ kda_status kda_attention_fwd(const kda_attention_problem* p, const void* q, cons
   PackedArgs a;
   Maps m;
   if (p->total_tokens > 0) TRY(maps_of(p, q, k, v, nullptr, &m));
-  TRY(begin(p, 256, workspace, &a, s));
+  TRY(begin(p, 256, workspace, status, &a, s));
   if (p->total_tokens == 0) return KDA_OK;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
+  a.fresh = fresh;
   const cudaError_t e = launch_packed_fwd(a, m.q, m.k, m.v, s);
   return e == cudaSuccess ? KDA_OK : set_error(KDA_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
+}
+
+kda_status kda_attention_fwd(const kda_attention_problem* p, const void* q, const void* k, const void* v, void* o, float* lse,
+                             void* workspace, void* stream) {
+  return kda_attention_fwd_fresh(p, q, k, v, o, lse, workspace, 0, nullptr, stream);
 }
 
 size_t kda_attention_bwd_workspace_bytes(const kda_attention_problem* p) {
@@ -224,11 +233,14 @@ size_t kda_attention_bwd_workspace_bytes(const kda_attention_problem* p) {
   return validate(p, false) == KDA_OK ? kHeaderBytes + list_bytes(p, 128) + delta_bytes(p) + stat_bytes(p) + part_bytes(p) : 0;
 }
 
-kda_status kda_attention_bwd(const kda_attention_problem* p, const void* q, const void* k, const void* v, const void* o,
-                             const float* lse, const void* d_o, void* dq, void* dk, void* dv, void* workspace, void* stream) {
+kda_status kda_attention_bwd_fresh(const kda_attention_problem* p, const void* q, const void* k, const void* v, const void* o,
+                                   const float* lse, const void* d_o, void* dq, void* dk, void* dv, void* workspace,
+                                   int32_t fresh, int32_t* status, void* stream) {
   using namespace kda;
   TRY(validate(p, true));
   TRY(tensor("workspace", workspace));
+  if (fresh & ~1) return set_error(KDA_ERR_INVALID_ARG, "fresh %d is not 0 or 1", fresh);
+  if ((uintptr_t)status & 3u) return set_error(KDA_ERR_INVALID_ARG, "status is not 4-byte aligned");
   cudaStream_t s = (cudaStream_t)stream;
   PackedArgs a;
   Maps m;
@@ -239,8 +251,9 @@ kda_status kda_attention_bwd(const kda_attention_problem* p, const void* q, cons
     TRY(tensor("lse", lse, 3u));
     TRY(maps_of(p, q, k, v, d_o, &m));
   }
-  TRY(begin(p, 128, workspace, &a, s));
+  TRY(begin(p, 128, workspace, status, &a, s));
   if (p->total_tokens == 0) return KDA_OK;
+  a.fresh = fresh;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.qs = p->q_stride;
   a.o_in = static_cast<const __nv_bfloat16*>(o);
@@ -257,6 +270,11 @@ kda_status kda_attention_bwd(const kda_attention_problem* p, const void* q, cons
   a.split = split_of(p);
   const cudaError_t e = launch_packed_bwd(a, m.q, m.k, m.v, m.d_o, s);
   return e == cudaSuccess ? KDA_OK : set_error(KDA_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
+}
+
+kda_status kda_attention_bwd(const kda_attention_problem* p, const void* q, const void* k, const void* v, const void* o,
+                             const float* lse, const void* d_o, void* dq, void* dk, void* dv, void* workspace, void* stream) {
+  return kda_attention_bwd_fresh(p, q, k, v, o, lse, d_o, dq, dk, dv, workspace, 0, nullptr, stream);
 }
 
 }  // extern "C"

@@ -13,7 +13,8 @@ constexpr int kPackedMaxCtas = 152;  // one per SM
 
 struct PackedArgs {
   const int32_t* cu;
-  int* status;
+  int* head;           // of the workspace: a status word, and the tickets
+  int* status;         // the call's status word: the head's, or the caller's
   int* tickets;        // items handed out, by kernel (zeroed before the call's first)
   const int* list;     // count, then from list + 4 on {first token, length, weight, sequence} of each tile; null: one sequence
   int64_t S;
@@ -28,7 +29,8 @@ struct PackedArgs {
   int64_t stat_tiles;
   float* part;         // gradients of k and v by parts of the head group: [2][split][S][Hkv][D]
   int split;
-  int fresh;           // forward of one short sequence: the kernel itself clears the header
+  int clears;          // forward of one short sequence: the kernel itself clears the header
+  int fresh;           // outputs to fill where cu_seqlens is refused: 1 o, 2 lse; of the backward 1 all
 };
 constexpr int kClearBytes = 32;  // of the workspace's header: the status word, and the tickets
 
@@ -55,6 +57,12 @@ __device__ __forceinline__ Tile tile_of(const PackedArgs& a, int tiles, int e) {
   if (!a.list) return {0, static_cast<int>(a.S), tiles - e, 0};
   const int4 t = reinterpret_cast<const int4*>(a.list + 4)[e];
   return {t.x, t.y, t.z, t.w};
+}
+// NaN (of either type) all over an output, by all CTAs: thread i of n in each. Work for
+// warps that have none: in front of the roles it would cost them registers.
+__device__ __forceinline__ void fill_nan(void* p, int64_t words, int i, int n) {
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * n + i; w < words; w += static_cast<int64_t>(gridDim.x) * n)
+    static_cast<uint32_t*>(p)[w] = 0x7fc07fc0u;
 }
 namespace tc {
 

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(256) kda_packed_delta_kernel(const __grid_cons
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 3;
   const int sub = threadIdx.x & 7;
   before_kernel();
-  if (!a.list && i < kClearBytes / 4 && sub == 0) a.status[i] = 0;
+  if (!a.list && i < kClearBytes / 4 && sub == 0) a.head[i] = 0;
   float sum = 0.f;
   if (i < a.S * a.Hq) {
     const uint4* const x = reinterpret_cast<const uint4*>(a.o_in + i * D);
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after_sync();
   before_kernel();
   after_kernel();
-  const int tiles = tiles_of(a, kRows);  // 0: no warp has work
+  const int tiles = tiles_of(a, kRows);  // 0: lengths that do not fit, no warp has work
   const uint32_t tmem = sh->tmem;
   const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
   KvItem it;
@@ -447,6 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->acc_free);
     }
+  } else if (tiles == 0 && a.fresh) {  // the one warp that has no other work
+    fill_nan(a.dk, a.S * a.Hkv * (D / 2), lane, 32);
+    fill_nan(a.dv, a.S * a.Hkv * (D / 2), lane, 32);
   }
   __syncthreads();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
@@ -549,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after_sync();
   before_kernel();
   after_kernel();
-  const int tiles = tiles_of(a, kRows);  // 0: no warp has work
+  const int tiles = tiles_of(a, kRows);  // 0: lengths that do not fit, no warp has work
   const uint32_t tmem = sh->tmem;
   const uint32_t t_s = tmem, t_dp = tmem + 128, t_dq = tmem + 384;  // dP at t_dp and t_dp + 128 in turn
   QItem it;
@@ -656,6 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < kMathWarp) {
     registers_down<kFewRegs>();
+    if (tiles == 0 && a.fresh) fill_nan(a.dq, a.S * a.Hq * (D / 2), lane, 32);
   } else {
     registers_up<kManyRegs>();
     const int wg = (warp - kMathWarp) >> 2, row = tid & 127;

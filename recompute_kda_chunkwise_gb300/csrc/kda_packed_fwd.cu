@@ -46,7 +46,7 @@ using namespace tc;
 
 constexpr int kRows = 128;
 constexpr int kSoftmaxWarps = 8;
-constexpr int kMmaWarp = 0, kLoadWarp = 1, kSoftmaxWarp = 4;  // warps 2 and 3 are idle
+constexpr int kMmaWarp = 0, kLoadWarp = 1, kSoftmaxWarp = 4;  // warps 2 and 3 have work where lengths are refused
 constexpr int kThreads = 32 * (kSoftmaxWarp + kSoftmaxWarps);
 constexpr float kRescale = 8.f;
 
@@ -134,9 +134,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after_sync();
   after_kernel();
-  if (a.fresh && blockIdx.x == 0 && tid < kClearBytes / 4) a.status[tid] = 0;
-  if (a.fresh) __syncthreads();
-  const int tiles = tiles_of(a, 2 * kRows);  // 0: no warp has work
+  if (a.clears && blockIdx.x == 0 && tid < kClearBytes / 4) a.head[tid] = 0;
+  if (a.clears) __syncthreads();
+  const int tiles = tiles_of(a, 2 * kRows);  // 0: lengths that do not fit, no warp has work
   const uint32_t tmem = sh->tmem;
   const uint32_t tmem_s = tmem, tmem_o = tmem + 128 * kScores;  // tile i of S (P over it) at + 128 i, O of stream i at + D i
   Item it;
@@ -315,6 +315,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < kSoftmaxWarp) {
     registers_down<kFewRegs>();
+    if (tiles == 0) {
+      if (a.fresh & 1) fill_nan(a.o, a.S * a.Hq * (D / 2), tid - 64, 64);
+      if (a.fresh & 2) fill_nan(a.lse, a.S * a.Hq, tid - 64, 64);
+    }
   } else {
     registers_up<kManyRegs>();
     // ---- softmax: thread = row, warpgroup = stream ----

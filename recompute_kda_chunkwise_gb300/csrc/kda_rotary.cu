@@ -56,7 +56,7 @@ struct RotaryArgs {
   int64_t S, pages;
   int N, Hq, Hk, D, R, tile, page, width;
   float mag;
-  int inverse;
+  int inverse, fresh;
 };
 
 // Number of sequences that end at or before token t, by a whole warp: every
@@ -128,6 +128,14 @@ __device__ __forceinline__ void store_words(void* p, const uint4& r) {
     *static_cast<uint32_t*>(p) = r.x;
   else
     *static_cast<uint16_t*>(p) = static_cast<uint16_t>(r.x);
+}
+
+// Zeros in n elements, whole vectors.
+template <typename T>
+__device__ __forceinline__ void zero_row(T* p, int n) {
+  constexpr int V = 16 / sizeof(T);
+#pragma unroll 1
+  for (int i = 0; i < n; i += V) *reinterpret_cast<uint4*>(p + i) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // How a head's channels are cut into items of work. PAIRS, channels (2i, 2i + 1)
@@ -304,7 +312,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? PAIRS ? 12 : 10 : W
       }
       if (!ok) {
         row = -1;
-        if (here) set_status(a.status, KDA_ERR_DEVICE_CHECK);
+        if (here) {  // a fresh row by its own lane: behind the tile's loop zeros cost every call (96.7 -> 99.1 us, append 41 -> 43)
+          set_status(a.status, KDA_ERR_DEVICE_CHECK);
+          if (a.fresh & 1) zero_row(static_cast<T*>(a.qo) + tok * a.Hq * a.D, a.Hq * a.D);
+          if (!PAGED && (a.fresh & 2)) zero_row(static_cast<T*>(a.ko) + tok * a.Hk * a.D, a.Hk * a.D);
+        }
       }
     }
     s_pos[lane] = pos;
@@ -394,6 +406,7 @@ kda_status validate_turn(const kda_rotary_problem* p, int D) {
     return set_error(KDA_ERR_INVALID_ARG, "rotary_dim %d must be even and within 2 .. head_dim %d", p->rotary_dim, D);
   if (!isfinite(p->magnitude)) return set_error(KDA_ERR_INVALID_ARG, "magnitude must be finite");
   if ((p->interleaved | p->inverse) & ~1) return set_error(KDA_ERR_INVALID_ARG, "interleaved and inverse are 0 or 1");
+  if (p->fresh & ~3) return set_error(KDA_ERR_INVALID_ARG, "fresh %d is not 0 .. 3", p->fresh);
   return tensor("freqs", p->freqs, 7u);
 }
 
@@ -440,7 +453,7 @@ kda_status kda_rotary(const kda_rotary_problem* p, const void* q, const void* k,
   a.q = q; a.k = k; a.qo = q_out; a.ko = k_out; a.qs = p->q_stride; a.ks = p->k_stride;
   a.freqs = p->freqs; a.positions = p->positions; a.cu = p->cu_seqlens; a.status = status;
   a.S = p->total_tokens; a.N = p->num_seqs; a.Hq = p->num_heads; a.Hk = p->num_kv_heads; a.D = p->head_dim;
-  a.R = p->rotary_dim; a.mag = p->magnitude; a.inverse = p->inverse;
+  a.R = p->rotary_dim; a.mag = p->magnitude; a.inverse = p->inverse; a.fresh = p->fresh;
   const cudaError_t r = e == 2 ? launch<__nv_bfloat16, false>(a, p->interleaved, (cudaStream_t)stream)
                                : launch<float, false>(a, p->interleaved, (cudaStream_t)stream);
   return r == cudaSuccess ? KDA_OK : set_error(KDA_ERR_CUDA, "rotary launch failed: %s", cudaGetErrorString(r));
@@ -476,6 +489,7 @@ kda_status kda_paged_append_rotary(const kda_paged_problem* p, const kda_rotary_
   a.freqs = r->freqs; a.cu = p->cu_seqlens; a.table = p->page_table; a.lens = p->kv_lens; a.status = status;
   a.S = p->total_tokens; a.pages = p->num_pages; a.N = p->num_seqs; a.Hq = q ? p->num_heads : 0; a.Hk = p->num_kv_heads;
   a.D = p->head_dim; a.R = r->rotary_dim; a.page = p->page_size; a.width = p->max_pages; a.mag = r->magnitude;
+  a.fresh = r->fresh;
   const cudaError_t st = launch<__nv_bfloat16, true>(a, r->interleaved, (cudaStream_t)stream);
   return st == cudaSuccess ? KDA_OK : set_error(KDA_ERR_CUDA, "append launch failed: %s", cudaGetErrorString(st));
 }

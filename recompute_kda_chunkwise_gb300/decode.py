@@ -57,7 +57,7 @@ def paged_append_rotary(rope, q, k, v, k_pages, v_pages, page_table, kv_lens, cu
     written as it is, and the rotated q [S, Hq, D] is returned (None where q
     is; ``out`` may hold it, and may be q; it and the pages overlap nothing else). rope: a ``rotary.Rotary``. q, k and
     v may be slices of a fused projection. Tokens that paged_append skips are
-    skipped: their rows of the result are not written."""
+    skipped: their rows of the result are zeros, or in a given ``out`` not written."""
     return done(bind().append_rotary(rope.turns, rope.interleaved, rope.magnitude, q, k, v, k_pages, v_pages, page_table,
                                      kv_lens, cu_seqlens, out, status), "kda_paged_append_rotary")
 

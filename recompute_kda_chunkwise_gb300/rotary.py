@@ -85,7 +85,10 @@ def rotary_fwd(rope, q, k=None, *, positions=None, cu_seqlens=None, out=None, st
     """Rotates q [S, Hq, D] and k [S, Hkv, D] (bf16 or fp32; slices of a fused
     projection fit: a token's heads and channels have to be contiguous). A
     token's position is positions[s] (int32 [S]) or its index in its sequence
-    of cu_seqlens (int32 [N+1]); one of the two is given. Returns (q', k'),
+    of cu_seqlens (int32 [N+1]); one of the two is given. Tokens that it puts into no
+    sequence (padding) are zeros in an output that the call makes, are left as they
+    were in a given one, and are recorded in status (an int32 CUDA tensor of one
+    zero, read with ``kda.query_device_status``). Returns (q', k'),
     contiguous; k' is None without k. ``out`` may hold (q', k'), either of
     them None; each may be its contiguous input, and overlaps nothing else."""
     return _call(rope, q, k, 0, positions, cu_seqlens, out, status)
@@ -100,10 +103,10 @@ class RotaryFunction(torch.autograd.Function):
     """Autograd wrapper. Differentiable once: a second derivative through it raises."""
 
     @staticmethod
-    def forward(ctx, rope, q, k, positions, cu_seqlens):
+    def forward(ctx, rope, q, k, positions, cu_seqlens, status=None):
         ctx.save_for_backward(positions, cu_seqlens)
-        ctx.rope = rope
-        qr, kr = rotary_fwd(rope, q, k, positions=positions, cu_seqlens=cu_seqlens)
+        ctx.rope, ctx.status = rope, status
+        qr, kr = rotary_fwd(rope, q, k, positions=positions, cu_seqlens=cu_seqlens, status=status)
         return qr if k is None else (qr, kr)
 
     @staticmethod
@@ -111,10 +114,12 @@ class RotaryFunction(torch.autograd.Function):
     def backward(ctx, dq, dk=None):
         positions, cu_seqlens = ctx.saved_tensors
         dq, dk = rotary_bwd(ctx.rope, dq.contiguous(), None if dk is None else dk.contiguous(), positions=positions,
-                            cu_seqlens=cu_seqlens)
-        return None, dq, dk, None, None
+                            cu_seqlens=cu_seqlens, status=ctx.status)
+        return None, dq, dk, None, None, None
 
 
-def rotary(rope, q, k=None, *, positions=None, cu_seqlens=None):
-    """Differentiable (once) rotation. Returns q', or (q', k') with k."""
-    return RotaryFunction.apply(rope, q, k, positions, cu_seqlens)
+def rotary(rope, q, k=None, *, positions=None, cu_seqlens=None, status=None):
+    """Differentiable (once) rotation. Returns q', or (q', k') with k. Tokens
+    that cu_seqlens puts into no sequence are zeros, and so are their gradients;
+    the forward and the backward record them in status."""
+    return RotaryFunction.apply(rope, q, k, positions, cu_seqlens, status)

@@ -172,3 +172,16 @@ def test_reference_gradients_against_differences():
     a = (R.turn(x, pos, f, 1.5, True)[0] * y).sum()
     b = (R.turn(y, pos, f, 1.5, True, -1)[0] * x).sum()
     assert a.item() == pytest.approx(b.item())
+
+
+def test_fresh_outputs_and_status_refusals(lib):
+    p = B.AttentionProblem(4, 256, 128, 128, 1, 4, 2, 64, 0, 0.1, 0x1000)
+    fwd = lambda fresh, status: lib.kda_attention_fwd_fresh(ctypes.byref(p), *([AL] * 6), fresh, status, NUL)  # noqa: E731
+    bwd = lambda fresh, status: lib.kda_attention_bwd_fresh(ctypes.byref(p), *([AL] * 10), fresh, status, NUL)  # noqa: E731
+    for call, bad in ((fwd, (-1, 4)), (bwd, (-1, 2))):
+        for fresh in bad:
+            assert call(fresh, NUL) == 1 and "fresh" in msg(lib)
+        assert call(1, MIS) == 1 and "status" in msg(lib)
+    r = rotary_problem(fresh=4)
+    assert lib.kda_rotary(ctypes.byref(r), AL, AL, AL, AL, NUL, NUL) == 1 and "fresh" in msg(lib)
+    assert B.RotaryProblem.fresh.offset == B.RotaryProblem.reserved.offset == 60

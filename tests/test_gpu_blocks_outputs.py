@@ -103,3 +103,103 @@ def test_outputs_over_other_tensors_are_refused():
     T.rotary_fwd(rope, q, k, positions=pos, out=(at(0), at(S * 256)))
     T.rotary_fwd(rope, first, positions=pos[:1], out=(fused[:1, 256:512].view(1, 4, 64), None))
     A.attention_fwd(q, k, v, cu, out=at(2 * S * 256), workspace=flat[:S * 256].view(torch.uint8))
+
+
+def spoil(*like):
+    """What the allocator hands out next holds sevens."""
+    t = [torch.full_like(x, 7.0) for x in like]
+    torch.cuda.synchronize()
+    del t
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hk", [(4, 2), (3, 3)])  # gradients of keys with and without parts to add up
+@pytest.mark.parametrize("ends", [[0, 90], [0, 40, 90], [0, 101], [0, 60, 40, 100], [1, 100]])
+def test_refused_lengths_reach_the_caller_of_attention(ends, Hq, Hk, D):
+    """Padding rows behind the last sequence, among others."""
+    from recompute_kda_chunkwise_gb300 import attention as A, kda as K
+    S = 100
+    q, k, v, d_o = rand(1, S, Hq, D), rand(2, S, Hk, D), rand(3, S, Hk, D), rand(4, S, Hq, D)
+    cu = torch.tensor(ends, dtype=I32, device="cuda")
+    leaves = [t.requires_grad_() for t in (q, k, v)]
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    spoil(q, k, v)
+    o = A.attention(q, k, v, cu, status=status)
+    assert K.query_device_status(status) == 6 and o.isnan().all()
+    status.zero_()
+    spoil(q, k, v)
+    grads = torch.autograd.grad(o, leaves, d_o)
+    assert K.query_device_status(status) == 6 and all(g.isnan().all() for g in grads)
+    # without a status; a given output is left as it was
+    assert A.attention(q, k, v, cu).isnan().all()
+    out = torch.full_like(q, 5.0)
+    ws = torch.empty(A.attention_workspace_bytes(q, k, cu), dtype=torch.uint8, device="cuda")
+    _, lse = A.attention_fwd(q.detach(), k.detach(), v.detach(), cu, out=out, workspace=ws)
+    assert (out == 5).all() and lse.isnan().all() and K.query_device_status(ws) == 6
+    # the caller's word takes it instead of the workspace's, and the first error stays
+    A.attention_fwd(q.detach(), k.detach(), v.detach(), cu, workspace=ws, status=status)
+    assert K.query_device_status(ws) == 0 and K.query_device_status(status) == 6
+    good = torch.tensor([0, 40, S], dtype=I32, device="cuda")
+    o = A.attention(q, k, v, good, status=status)
+    assert o.isfinite().all() and K.query_device_status(status) == 6
+    status.zero_()
+    torch.autograd.grad(A.attention(q, k, v, good, status=status), leaves, d_o)
+    assert K.query_device_status(status) == 0
+
+
+def test_refused_lengths_of_many_rows():
+    from recompute_kda_chunkwise_gb300 import attention as A
+    S, Hq, Hk, D = 20_000, 16, 4, 64
+    q, k, v, d_o = rand(1, S, Hq, D), rand(2, S, Hk, D), rand(3, S, Hk, D), rand(4, S, Hq, D)
+    for ends in ([0, S - 1], [0, 7000, S - 1]):
+        cu = torch.tensor(ends, dtype=I32, device="cuda")
+        o, lse = A.attention_fwd(q, k, v, cu)
+        assert o.isnan().all() and lse.isnan().all()
+        assert all(g.isnan().all() for g in A.attention_bwd(q, k, v, d_o, lse, d_o, cu))
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("S,D,dim", [(10, 64, 64), (10, 64, 42), (5000, 128, 96), (40, 512, 510)])
+def test_tokens_of_no_sequence_are_zeros_after_rotary(S, D, dim, interleaved, dtype):
+    """Padding rows in front, between and behind; their gradients are zeros too."""
+    from recompute_kda_chunkwise_gb300 import kda as K, rotary as T
+    rope = T.Rotary(dim, interleaved=interleaved)
+    q, k = rand(1, S, 3, D).to(dtype).requires_grad_(), rand(2, S, 2, D).to(dtype).requires_grad_()
+    cu = torch.tensor([2, 4, 4, S - 3], dtype=I32, device="cuda")
+    pad = torch.ones(S, dtype=torch.bool, device="cuda")
+    pad[2:S - 3] = False
+    pos = torch.cat([torch.arange(-2, 2), torch.arange(S - 4)]).to(I32).cuda()
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    spoil(q, k, q, k)
+    x, y = T.rotary(rope, q, k, cu_seqlens=cu, status=status)
+    assert K.query_device_status(status) == 6
+    want = T.rotary_fwd(rope, q, k, positions=pos)
+    for got, ref in zip((x, y), want):
+        assert (got[pad] == 0).all() and torch.equal(got[~pad], ref[~pad])
+    w, z = torch.randn_like(q), torch.randn_like(k)
+    want = T.rotary_bwd(rope, w, z, positions=pos)
+    status.zero_()
+    spoil(q, k, q, k)
+    for got, ref in zip(torch.autograd.grad((x, y), (q, k), (w, z)), want):
+        assert (got[pad] == 0).all() and torch.equal(got[~pad], ref[~pad])
+    assert K.query_device_status(status) == 6
+    # one output given, the other made by the call
+    out = torch.full_like(k, 9.0)
+    spoil(q)
+    x, _ = T.rotary_fwd(rope, q.detach(), k.detach(), cu_seqlens=cu, out=(None, out))
+    assert (x[pad] == 0).all() and (out[pad] == 9).all() and torch.equal(out[~pad], y[~pad])
+
+
+def test_skipped_queries_of_an_append_are_zeros():
+    from recompute_kda_chunkwise_gb300 import decode, kda as K, rotary as T
+    kp, vp, table, lens, _ = cache()
+    q, k, v = rand(1, 10, 6, 64), rand(2, 10, 2, 64), rand(3, 10, 2, 64)
+    table[0, 2] = 9  # positions 32 to 47 have no page
+    cu = torch.tensor([0, 10], dtype=I32, device="cuda")
+    keep, status = [t.clone() for t in (kp, vp)], torch.zeros(1, dtype=I32, device="cuda")
+    spoil(q)
+    x = decode.paged_append_rotary(T.Rotary(64), q, k, v, kp, vp, table, lens, cu, status=status)  # positions 30 to 39
+    assert K.query_device_status(status) == 6 and (x[2:] == 0).all() and (x[:2] != 0).any()
+    assert torch.equal(kp[2:], keep[0][2:]) and torch.equal(vp[2:], keep[1][2:])
+    assert torch.equal(vp[1, 14:], v[:2])
