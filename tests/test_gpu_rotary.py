@@ -254,3 +254,25 @@ def test_refusals():
         rotary.rotary_fwd(rope, torch.zeros(10, 132, dtype=BF, device="cuda")[:, :128].view(10, 2, 64), positions=pos)
     none = rotary.rotary_fwd(rope, x[:0], x[:0], cu_seqlens=cu * 0)
     assert none[0].shape == (0, 2, 64) and none[1].shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("dtype,D,dim", [(BF, 512, 510), (BF, 512, 300), (BF, 512, 302), (BF, 264, 262), (BF, 512, 508),
+                                         (torch.float32, 512, 510), (torch.float32, 512, 300), (torch.float32, 512, 506)])
+@pytest.mark.parametrize("S,Hq,Hk", [(1, 1, 0), (5, 3, 2), (130, 9, 1)])
+def test_heads_of_more_items_than_threads(S, Hq, Hk, dtype, D, dim):
+    """Halves that are cut into single elements or words: a CTA goes over its tile more than once."""
+    from recompute_kda_chunkwise_gb300 import rotary
+    g = gen(S + dim)
+    rope = make(dim, "half", "linear")
+    q, k = rand(g, S, Hq, D, dtype=dtype), rand(g, S, Hk, D, dtype=dtype) if Hk else None
+    cu = torch.tensor([0, S // 2, S], dtype=I32, device="cuda")
+    pos = list(range(S // 2)) + list(range(S - S // 2))
+    for fn, sign in ((rotary.rotary_fwd, 1), (rotary.rotary_bwd, -1)):
+        for x, y in zip((q, k), fn(rope, q, k, cu_seqlens=cu)):
+            if x is not None:
+                ref, bar = R.turn(x, pos, rope.frequencies, 1.0, False, sign)
+                R.check(y, ref, bar, "rotated")
+                assert torch.equal(y[..., dim:], x[..., dim:])
+    z = q.clone()
+    rotary.rotary_fwd(rope, z, cu_seqlens=cu, out=(z, None))
+    assert torch.equal(z, rotary.rotary_fwd(rope, q, cu_seqlens=cu)[0])
