@@ -254,8 +254,6 @@ kda_status kda_attention_bwd_fresh(const kda_attention_problem* p, const void* q
   TRY(begin(p, 128, workspace, status, &a, s));
   if (p->total_tokens == 0) return KDA_OK;
   a.fresh = fresh;
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.qs = p->q_stride;
   a.o_in = static_cast<const __nv_bfloat16*>(o);
   a.d_o = static_cast<const __nv_bfloat16*>(d_o);
   a.dq = static_cast<__nv_bfloat16*>(dq);

@@ -21,8 +21,7 @@ struct PackedArgs {
   int N, Hq, Hkv, D;
   float scale;
   __nv_bfloat16 *o, *dq, *dk, *dv;   // contiguous
-  const __nv_bfloat16 *q, *o_in, *d_o;
-  int64_t qs;          // elements from a token of q to the next
+  const __nv_bfloat16 *o_in, *d_o;
   float* lse;          // [Hq][S]
   float* delta;        // [Hq][S]
   float* stats;        // [Hq][stat_tiles][2][128]: -lse in base 2 and -delta of each tile's rows, zero past its sequence
@@ -260,17 +259,11 @@ __device__ __forceinline__ uint64_t desc_at(uint32_t lo, uint32_t bytes) { retur
 __host__ __device__ constexpr uint32_t k_step(int k) { return (k >> 2) * 128 * 128 + (k & 3) * 32; }
 constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // of an instruction: bf16 A and B
 
-// D = A B^T: A 128 rows of D in shared memory, or (_ta) as bf16 in TMEM, B 128
-// rows of D in shared memory (desc_k).
+// D = A B^T: A and B 128 rows of D in shared memory (desc_k).
 template <int D>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
 #pragma unroll
   for (int k = 0; k < D / 16; ++k) mma(d, desc_at(a, k_step(k)), desc_at(b, k_step(k)), idesc(128, 128) | kBf16, k > 0);
-}
-template <int D>
-__device__ __forceinline__ void mma_scores_ta(uint32_t d, uint32_t a, uint32_t b) {
-#pragma unroll
-  for (int k = 0; k < D / 16; ++k) mma_ta(d, a + 8 * k, desc_at(b, k_step(k)), idesc(128, 128) | kBf16, k > 0);
 }
 // D (+)= A B: A 128 columns of bf16 in TMEM, packed over the first half of each
 // run of `run` fp32 columns (128: all in one place), B 128 rows of D in shared
@@ -322,10 +315,6 @@ cudaError_t packed_sms(PerDevice& kept, K kernel, size_t smem, int64_t* sms, int
   });
 }
 
-struct PackedInputs {
-  const void *q, *k, *v;
-  int64_t qs, ks, vs;
-};
 cudaError_t launch_packed_fwd(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                               cudaStream_t s);
 cudaError_t launch_packed_bwd(const PackedArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
