@@ -27,8 +27,9 @@
 // through heads without a division, and works on words of two values (171 us
 // before). Ten CTAs of 128 threads an SM hold that (104 us with five of 256, pairs 55
 // instead of 52, one head of 64 a token 83 instead of 68; 103, 53 and 64 with 64
-// threads), twelve half vectors and pairs of fp32; other pairs and shorter items do
-// better with sixteen.
+// threads), twelve half vectors and pairs of fp32 (8192 tokens, 40 heads of 128, both
+// ways 118 us, 127 with ten; 1777 tokens, 12 + 3 heads of 64, 9.6 and 11.7, in a graph);
+// other pairs and shorter items do better with sixteen.
 #include <math.h>
 
 #include "kda_blocks.h"
@@ -44,7 +45,7 @@ constexpr int64_t kMaxStride = 1 << 25;  // elements from a token to the next
 static_assert(kMaxStride * kMaxTile <= 1 << 30, "");
 constexpr int kTableBytes = 32768;    // sines and cosines of a tile
 constexpr int kTileVectors = 1024;    // 16-byte vectors of a CTA, about
-constexpr int kMinCtas = 1216;
+constexpr int kSms = 152;
 
 struct RotaryArgs {
   const void *q, *k, *v;   // v: paged form only
@@ -142,8 +143,11 @@ __device__ __forceinline__ void zero_row(T* p, int n) {
 // turn together: an item is a 16-byte vector. Else, channels (i, i + R/2): W, the
 // largest power of two up to a vector that divides R/2, elements of either half;
 // of the channels that pass, a vector, W elements only up to the first vector.
+template <typename T, int W, bool PAIRS>
+constexpr int kCtasPerSm = sizeof(T) == 4 ? PAIRS ? 12 : 10 : W == 8 && !PAIRS ? 10 : W == 4 ? 12 : 16;
+
 template <typename T, int W, bool PAIRS, bool PAGED>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? PAIRS ? 12 : 10 : W == 8 && !PAIRS ? 10 : W == 4 ? 12 : 16)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<T, W, PAIRS>)
     kda_rotary_kernel(const RotaryArgs a) {
   constexpr bool kBf16 = sizeof(T) == 2;
   constexpr int kBytes = W * sizeof(T);
@@ -357,29 +361,32 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? PAIRS ? 12 : 10 : W
 }
 
 template <typename T, int W, bool PAIRS, bool PAGED>
-cudaError_t launch_as(const RotaryArgs& a, unsigned grid, size_t smem, cudaStream_t s) {
+cudaError_t launch_as(RotaryArgs a, cudaStream_t s) {
+  // Tokens of a CTA: enough for a few rounds of its threads, but of a call that all CTAs
+  // take at once no more than that needs (1777 tokens, 12 + 3 heads of 64, both ways: halves
+  // in bf16 8.3 us, where 1777 CTAs of one token take 11.1; fp32 pairs, of which 1824 CTAs
+  // fit, 9.6, and 10.3 with two tokens); the table of a tile within its bytes.
+  constexpr int V = 16 / sizeof(T), kWave = kSms * kCtasPerSm<T, W, PAIRS>;
+  const int64_t vectors = static_cast<int64_t>(a.Hq + a.Hk * (PAGED ? 2 : 1)) * a.D / V;
+  int64_t tile = (kTileVectors + vectors - 1) / vectors;
+  if (tile > (a.S + kWave - 1) / kWave) tile = (a.S + kWave - 1) / kWave;
+  if (tile > kTableBytes / (a.R / 2 * 8)) tile = kTableBytes / (a.R / 2 * 8);
+  a.tile = static_cast<int>(tile < 1 ? 1 : tile > kMaxTile ? kMaxTile : tile);
+  const unsigned grid = static_cast<unsigned>((a.S + a.tile - 1) / a.tile);
+  const size_t smem = static_cast<size_t>(a.tile) * (a.R / 2) * sizeof(float2);
   kda_rotary_kernel<T, W, PAIRS, PAGED><<<grid, kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
 template <typename T, bool PAGED>
-cudaError_t launch(RotaryArgs a, bool pairs, cudaStream_t s) {
+cudaError_t launch(const RotaryArgs& a, bool pairs, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  // Tokens of a CTA: enough for a few rounds of its threads, but no fewer CTAs
-  // than eight an SM; the table of a tile within its bytes.
-  const int64_t vectors = static_cast<int64_t>(a.Hq + a.Hk * (PAGED ? 2 : 1)) * a.D / V;
-  int64_t tile = (kTileVectors + vectors - 1) / vectors;
-  if (tile > a.S / kMinCtas) tile = a.S / kMinCtas;
-  if (tile > kTableBytes / (a.R / 2 * 8)) tile = kTableBytes / (a.R / 2 * 8);
-  a.tile = static_cast<int>(tile < 1 ? 1 : tile > kMaxTile ? kMaxTile : tile);
-  const unsigned grid = static_cast<unsigned>((a.S + a.tile - 1) / a.tile);
-  const size_t smem = static_cast<size_t>(a.tile) * (a.R / 2) * sizeof(float2);
   const int half = a.R / 2;
-  if (pairs) return launch_as<T, V, true, PAGED>(a, grid, smem, s);
-  if (half % V == 0) return launch_as<T, V, false, PAGED>(a, grid, smem, s);
+  if (pairs) return launch_as<T, V, true, PAGED>(a, s);
+  if (half % V == 0) return launch_as<T, V, false, PAGED>(a, s);
   if constexpr (V == 8)
-    if (half % 4 == 0) return launch_as<T, 4, false, PAGED>(a, grid, smem, s);
-  return half % 2 == 0 ? launch_as<T, 2, false, PAGED>(a, grid, smem, s) : launch_as<T, 1, false, PAGED>(a, grid, smem, s);
+    if (half % 4 == 0) return launch_as<T, 4, false, PAGED>(a, s);
+  return half % 2 == 0 ? launch_as<T, 2, false, PAGED>(a, s) : launch_as<T, 1, false, PAGED>(a, s);
 }
 
 kda_status tensor(const char* name, const void* p, unsigned align = 15u) {
