@@ -21,6 +21,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from ._serving import AttentionProblem, bind, done, library
+from .kda import _dense
 
 
 def attention_fwd(q, k, v, cu_seqlens, *, scale=None, out=None, workspace=None, status=None):
@@ -61,7 +62,7 @@ class AttentionFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, d_o):
         q, k, v, o, lse, cu_seqlens = ctx.saved_tensors
-        return *attention_bwd(q, k, v, o, lse, d_o.contiguous(), cu_seqlens, scale=ctx.scale, status=ctx.status), None, None, None
+        return *attention_bwd(q, k, v, o, lse, _dense(d_o), cu_seqlens, scale=ctx.scale, status=ctx.status), None, None, None
 
 
 def attention(q, k, v, cu_seqlens, *, scale=None, status=None):

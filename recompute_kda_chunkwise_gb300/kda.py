@@ -141,6 +141,13 @@ def _problem_from(q, beta, cu_seqlens, scale, lower_bound, eps, flags=0):
                         flags)
 
 
+def _dense(t):
+    """A gradient as the kernels read it: contiguous, and where 16-byte vectors begin (as a
+    slice of a larger gradient it need not be)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _check_tensors(q, *others, params=()):
     for t in (q,) + tuple(others):
         if not t.is_cuda or not t.is_contiguous() or t.dtype != q.dtype or t.device != q.device:
@@ -453,9 +460,9 @@ class GDN2Function(torch.autograd.Function):
     def backward(actx, dO, dht=None):
         q, k, v, g, erase, write, A_log, dt_bias, cu_seqlens, ctx = actx.saved_tensors
         scale, lower_bound, eps, has_h0 = actx.args
-        r = gdn2_bwd(q, k, v, g, erase, write, A_log, dt_bias, cu_seqlens, dO.contiguous(), ctx,
+        r = gdn2_bwd(q, k, v, g, erase, write, A_log, dt_bias, cu_seqlens, _dense(dO), ctx,
                      scale=scale, lower_bound=lower_bound, eps=eps,
-                     dht=None if dht is None else dht.contiguous(), want_dh0=has_h0)
+                     dht=None if dht is None else _dense(dht), want_dh0=has_h0)
         return (r["dq"], r["dk"], r["dv"], r["dg"], r["derase"], r["dwrite"], r["dA_log"],
                 r["ddt_bias"], None, r.get("dh0"), None, None, None, None)
 
@@ -489,9 +496,9 @@ class KDAFunction(torch.autograd.Function):
     def backward(actx, dO, dht=None):
         q, k, v, g, beta, A_log, dt_bias, cu_seqlens, ctx = actx.saved_tensors
         scale, lower_bound, eps, has_h0, _ = actx.args
-        r = kda_bwd(q, k, v, g, beta, A_log, dt_bias, cu_seqlens, dO.contiguous(), ctx,
+        r = kda_bwd(q, k, v, g, beta, A_log, dt_bias, cu_seqlens, _dense(dO), ctx,
                     scale=scale, lower_bound=lower_bound, eps=eps,
-                    dht=None if dht is None else dht.contiguous(), want_dh0=has_h0)
+                    dht=None if dht is None else _dense(dht), want_dh0=has_h0)
         return (r["dq"], r["dk"], r["dv"], r["dg"], r["dbeta"], r["dA_log"], r["ddt_bias"],
                 None, r.get("dh0"), None, None, None, None, None)
 

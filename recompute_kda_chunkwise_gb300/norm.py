@@ -13,6 +13,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from ._serving import bind, done
+from .kda import _dense
 
 
 def block_norm_fwd(y, *, z=None, h=None, w_post=None, w_pre=None, residual_scale: float = 1.0, block_scale: float = 1.0,
@@ -51,7 +52,7 @@ class BlockNormFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dh_out, dn=None):
         y, z, h, w_post, w_pre = ctx.saved_tensors
-        c = lambda t: None if t is None else t.contiguous()  # noqa: E731
+        c = lambda t: None if t is None else _dense(t)  # noqa: E731
         g = block_norm_bwd(y, z=z, h=h, w_post=w_post, w_pre=w_pre, dh_out=c(dh_out), dn=c(dn), **ctx.args)
         return g["dy"], g["dz"], g["dh"], g["dw_post"], g["dw_pre"], None, None, None
 

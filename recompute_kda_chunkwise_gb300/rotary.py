@@ -12,6 +12,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from ._serving import bind, done
+from .kda import _dense
 
 
 class Rotary:
@@ -113,7 +114,7 @@ class RotaryFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dq, dk=None):
         positions, cu_seqlens = ctx.saved_tensors
-        dq, dk = rotary_bwd(ctx.rope, dq.contiguous(), None if dk is None else dk.contiguous(), positions=positions,
+        dq, dk = rotary_bwd(ctx.rope, _dense(dq), None if dk is None else _dense(dk), positions=positions,
                             cu_seqlens=cu_seqlens, status=ctx.status)
         return None, dq, dk, None, None, None
 
