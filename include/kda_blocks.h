@@ -84,8 +84,8 @@ kda_status kda_paged_append_rotary(const kda_paged_problem* p, const kda_rotary_
 typedef struct {
   int64_t total_tokens;       /* S */
   int64_t q_stride, k_stride, v_stride;
-  int32_t num_seqs;           /* N >= 1 */
-  int32_t num_heads;          /* Hq */
+  int32_t num_seqs;           /* N: 1 .. 65536 */
+  int32_t num_heads;          /* Hq, at most 4096 */
   int32_t num_kv_heads;       /* Hkv */
   int32_t head_dim;           /* 64 or 128 */
   int32_t dtype;              /* KDA_DTYPE_BF16 */

@@ -41,7 +41,8 @@
 // it there, in us: a ring each for K and V 2995 -> 2505; descriptors of one addition
 // 2452; lse and delta in the ring with d_o instead of a barrier a step 2414; one
 // issuing thread with joint waits, dq's scores read a tile ahead 2296; registers for
-// dq's arithmetic (2319 before it by the same clock) 2282.
+// dq's arithmetic (2319 before it by the same clock: days differ by 1 to 2%) 2282, with
+// 48 bytes a thread spilled in dq's kernel for heads of 128 (-Xptxas -v).
 #include <math.h>
 
 #include "kda_packed.cuh"

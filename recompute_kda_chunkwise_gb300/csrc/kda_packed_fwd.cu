@@ -17,7 +17,7 @@
 // A thread takes its whole row into registers: the maximum first, then 128
 // exponentials without a branch between them (690 us for the case below where pieces
 // of 32 with a running maximum took 744). The registers come from the other warps
-// (690 -> 662). Heads of 64 leave TMEM room for a third tile of scores: the products
+// (687 -> 667). Heads of 64 leave TMEM room for a third tile of scores: the products
 // go stream by stream, and each tile's scores are issued three tiles ahead, into the
 // place of the tile whose P has just been used, so that they are there when their
 // warpgroup comes to them (595 -> 522); a tile of K and its V are one slot, so that a
@@ -30,7 +30,8 @@
 // Bound: the tensor cores (1024 cycles for a tile of 128 x 128 at D = 128), and the
 // chain scores -> probabilities -> products of each stream, of which two hide most.
 // 8192 tokens, 64 query heads on 8 of 128: 662 us, 1660 TFLOP/s, 86% of the measured
-// bf16 rate; 32768 tokens, 16 heads on 2: 1825. Heads of 64, with the same exponentials
+// bf16 rate; 32768 tokens, 16 heads on 2: 1825. (Clocks of different days differ by some
+// 2%: each pair of figures here is of one.) Heads of 64, with the same exponentials
 // for half the products: 472 us, 1165 TFLOP/s. One thread issues all products and its
 // instructions between them count: descriptors of one addition (771 -> 744 us), one
 // joint wait for all that a batch needs (662; 708 with two), the stream a constant (690;

@@ -6,8 +6,10 @@
 // Angles. A frequency is held as turns per position in units of 2^-64 of a
 // turn. The 64-bit product with a position, modulo 2^64, is the angle's
 // fraction of a turn: whole turns drop out without a rounding, where an fp32
-// product is off by 0.06 rad at position 10^6. Its upper 32 bits go to the
-// nearest quarter turn, whose rest is exact in fp32 to 2^-34 of a turn.
+// product is off by 0.06 rad at position 10^6. Its upper 32 bits (the rest, less
+// than 2^-32 of a turn, is cut off) go to the nearest quarter turn; what is left,
+// up to an eighth of a turn, is rounded to fp32: by 2^-28 of a turn at most, 2^-24 of
+// itself, which is what its sine is rounded by too.
 //
 // Bound: HBM, each element read and written once. 72 heads of 128 of 8192
 // tokens in bf16 (151 MB each way), rotated and, for the gradient, rotated back:

@@ -27,8 +27,9 @@ class Rotary:
                  by factor and leaves the fastest (dim > 2);
                  "by_parts": a pair that makes ``low`` turns or fewer within ``trained``
                  positions is divided by factor, one that makes ``high`` or more is
-                 left, with a ramp between; rotated channels are scaled by
-                 0.1 ln(factor) + 1
+                 left, with a ramp between that is linear in the number of turns;
+                 rotated channels are scaled by 0.1 ln(factor) + 1. (Weights that
+                 were trained with a ramp over the pairs' index want ``frequencies``.)
     frequencies  radians a position for each pair, instead of base and scaling
     magnitude    scales the rotated channels (None: 1, or by_parts' value)
 
