@@ -560,10 +560,11 @@ PyObject* packed_fwd(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     void* const op = fit(out, "out", g.qs, at::kBFloat16, dev);
     const Tensor lse = at::empty({g.qs[1], g.qs[0]}, q.options().dtype(at::kFloat).requires_grad(false));
     const bool own = !ws.defined();
-    void* const wsp = buffer(ws, g_entry.packed_fwd_bytes(&g.p), q);
+    const size_t bytes = g_entry.packed_fwd_bytes(&g.p);  // of a longer workspace the rest is not touched
+    void* const wsp = buffer(ws, bytes, q);
     if (given.defined() || !own) {
       const Tensor k = a.at(1, "k"), val = a.at(2, "v");
-      apart({span("out", given), own ? kda::whole("workspace", nullptr, 0) : span("workspace", ws)},
+      apart({span("out", given), kda::whole("workspace", wsp, own ? 0 : bytes)},
             {span("q", q, {g.q, g.p.q_stride}), span("k", k, {g.k, g.p.k_stride}), span("v", val, {g.v, g.p.v_stride}),
              span("cu_seqlens", a.at(3, "cu_seqlens"))}, {"q"});
     }
@@ -588,10 +589,11 @@ PyObject* packed_bwd(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     const c10::cuda::CUDAGuard on(dev);
     Tensor ws = a.maybe(8, "workspace");
     const bool own = !ws.defined();
-    void* const wsp = buffer(ws, g_entry.packed_bwd_bytes(&g.p), q);
+    const size_t bytes = g_entry.packed_bwd_bytes(&g.p);
+    void* const wsp = buffer(ws, bytes, q);
     if (!own) {
       const Tensor k = a.at(1, "k"), val = a.at(2, "v");
-      apart({span("workspace", ws)},
+      apart({kda::whole("workspace", wsp, bytes)},
             {span("q", q, {g.q, g.p.q_stride}), span("k", k, {g.k, g.p.k_stride}), span("v", val, {g.v, g.p.v_stride}),
              span("o", a.at(3, "o")), span("lse", a.at(4, "lse")), span("d_o", a.at(5, "d_o")),
              span("cu_seqlens", a.at(6, "cu_seqlens"))});

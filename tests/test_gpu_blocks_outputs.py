@@ -103,6 +103,8 @@ def test_outputs_over_other_tensors_are_refused():
     T.rotary_fwd(rope, q, k, positions=pos, out=(at(0), at(S * 256)))
     T.rotary_fwd(rope, first, positions=pos[:1], out=(fused[:1, 256:512].view(1, 4, 64), None))
     A.attention_fwd(q, k, v, cu, out=at(2 * S * 256), workspace=flat[:S * 256].view(torch.uint8))
+    # nor does what lies behind the part of a long workspace that the call needs
+    A.attention_fwd(q, k, v, cu, out=at(2 * S * 256), workspace=flat.view(torch.uint8))
 
 
 def spoil(*like):
