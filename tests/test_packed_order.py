@@ -1,5 +1,5 @@
-"""The barriers of the packed attention's forward (csrc/kda_packed_fwd.cu), as a model without a GPU: one
-CTA's loads, issuing thread, tensor pipe and softmax warps, stepped in any order. A barrier is what the
+"""The barriers of the packed attention's kernels (csrc/kda_packed_fwd.cu, kda_packed_bwd.cu), as models without a
+GPU: one CTA's loads, issuing thread, tensor pipe and warps of arithmetic, stepped in any order. A barrier is what the
 hardware has: a count of completed phases of which a wait sees the parity alone, so a wait for a phase is
 over too early if the one before it is not complete, and never if the one behind it is.
 
@@ -34,8 +34,36 @@ class Barrier:
         return True
 
 
-class Model:
-    """items: (key tiles of stream 0, of stream 1) of each. rescale: how often a warp rescales its outputs. places: tiles of scores in TMEM; three: heads of
+class Steps:
+    """What the models share: a pipe of products and commits in order, copies that land in any, and roles,
+    generators of what they wait for."""
+
+    def commit(self, bar):
+        self.pipe.append(bar.arrive)
+
+    def run(self, choose):
+        """choose(names of what can go on): the one that does."""
+        roles = dict(self.roles())
+        waits = {r: (lambda: True) for r in roles}
+        while roles or self.pipe or self.copies:
+            can = [r for r in roles if waits[r]()]
+            can += ["pipe"] * bool(self.pipe) + [f"copy {k}" for k in range(len(self.copies))]
+            if not can:
+                raise Stopped(sorted(roles))
+            r = choose(can)
+            if r == "pipe":
+                self.pipe.pop(0)()
+            elif r.startswith("copy"):
+                self.land(int(r.split()[1]))
+            else:
+                waits[r] = next(roles[r], None)
+                if waits[r] is None:
+                    del roles[r]
+        assert self.finished()
+
+
+class Model(Steps):
+    """The forward. items: (key tiles of stream 0, of stream 1) of each. rescale: how often a warp rescales its outputs. places: tiles of scores in TMEM; three: heads of
     64, two: heads of 128 (one for each stream). barriers of scores and probabilities: "own", one for each
     stream and place, as the kernel has; "shared", one for each place; "parity", two for each stream, by the parity of its tile."""
 
@@ -62,9 +90,6 @@ class Model:
         self.o, self.written = [None, None], []
 
     # ---- what is issued, and what runs when its turn comes ----
-    def commit(self, bar):
-        self.pipe.append(bar.arrive)
-
     def scores(self, item, s, j, place, slot):
         def run():
             assert self.ring[slot][:2] == (item, j) and self.q == item
@@ -229,28 +254,15 @@ class Model:
                 self.o[s] = None
             self.o_free[s].arrive()
 
-    def run(self, choose):
-        """choose(names of what can go on): the one that does."""
-        roles = {"load": self.load(), "issue": self.issue3() if self.places == 3 else self.issue2()}
+    def roles(self):
+        yield "load", self.load()
+        yield "issue", self.issue3() if self.places == 3 else self.issue2()
         for s in range(2):
             for w in range(self.warps):
-                roles[f"softmax {s} {w}"] = self.softmax(s)
-        waits = {r: (lambda: True) for r in roles}
-        while roles or self.pipe or self.copies:
-            can = [r for r in roles if waits[r]()]
-            can += ["pipe"] * bool(self.pipe) + [f"copy {k}" for k in range(len(self.copies))]
-            if not can:
-                raise Stopped(sorted(roles))
-            r = choose(can)
-            if r == "pipe":
-                self.pipe.pop(0)()
-            elif r.startswith("copy"):
-                self.land(int(r.split()[1]))
-            else:
-                waits[r] = next(roles[r], None)
-                if waits[r] is None:
-                    del roles[r]
-        assert sorted(set(self.written)) == [(i, s) for i, n in enumerate(self.items) for s in range(2) if n[s]]
+                yield f"softmax {s} {w}", self.softmax(s)
+
+    def finished(self):
+        return sorted(set(self.written)) == [(i, s) for i, n in enumerate(self.items) for s in range(2) if n[s]]
 
 
 def last(names):
@@ -263,14 +275,14 @@ def last(names):
 
 def at_random(seed):
     rng = random.Random(seed)
-    weight = {r: 4.0 ** rng.uniform(-3, 3) for r in ("load", "issue", "softmax 0", "softmax 1", "pipe", "copy")}
+    weight = {r: 4.0 ** rng.uniform(-3, 3) for r in ("load", "issue", "softmax 0", "softmax 1", "math", "pipe", "copy")}
     def choose(can):
         return rng.choices(can, [next(w for k, w in weight.items() if r.startswith(k)) for r in can])[0]
     return choose
 
 
 def orders(seeds):
-    for names in ("softmax", "softmax 0", "softmax 1", "softmax 0 0", "softmax 1 1", "load", "copy", "issue", "pipe",
+    for names in ("math", "math 0", "load q", "softmax", "softmax 0", "softmax 1", "softmax 0 0", "softmax 1 1", "load", "copy", "issue", "pipe",
                   ("copy", "load"), ("softmax", "load"), ("softmax", "copy"), ("issue", "pipe")):
         yield last(names)
     for seed in range(seeds):
@@ -311,3 +323,295 @@ def test_the_model_finds_waits_that_end_too_early():
     has not seen."""
     with pytest.raises(AssertionError, match="before its phase"):
         Model([(3, 0), (3, 4)], barriers="shared").run(last("pipe"))
+
+
+class Backward(Steps):
+    """What the backward's passes share. Every warp of arithmetic takes part in every tile."""
+
+    def __init__(self, items, warps=3):
+        self.items, self.warps = items, warps
+        self.pipe, self.copies, self.loaded = [], [], {}
+        self.s_full, self.done, self.acc_free = Barrier(1), Barrier(1), Barrier(warps)
+        self.acc, self.out = None, 0  # the accumulators' last step; items written, by each warp
+
+    def copy(self, key, what, bar):
+        """key: where; what: as the products name it."""
+        self.copies.append((key, what, bar))
+
+    def land(self, k):
+        key, what, bar = self.copies.pop(k)
+        self.loaded[key] = what
+        bar.arrive()
+
+    def finished(self):
+        return self.out == self.warps * len(self.items)
+
+
+class KeysAndValues(Backward):
+    """dk, dv. items: steps of each; every third step's last rows are another sequence's."""
+
+    def __init__(self, items, slots=(3, 2), warps=3):
+        super().__init__(items, warps)
+        self.q_full, self.q_empty = ([Barrier(1) for _ in range(slots[0])] for _ in range(2))
+        self.do_full, self.do_empty = [Barrier(1) for _ in range(slots[1])], [Barrier(1 + warps) for _ in range(slots[1])]
+        self.kv_full, self.kv_empty = Barrier(2), Barrier(1)
+        self.dp_full, self.p_ready, self.ds_ready = Barrier(1), Barrier(warps), Barrier(warps)
+        self.s = self.dp = None  # what lies there: ("S", step), or ("P", step) once every warp has written
+        self.wrote = {}
+
+    def roles(self):
+        yield "load q", self.load(self.q_full, self.q_empty, "q", True)
+        yield "load do", self.load(self.do_full, self.do_empty, "do", False)
+        yield "issue", self.issue()
+        for w in range(self.warps):
+            yield f"math {w}", self.math()
+
+    def load(self, full, empty, name, first):
+        t = 0
+        for i, steps in enumerate(self.items):
+            if first:
+                if i > 0:
+                    yield lambda: self.kv_empty.over(i - 1)
+                self.copy("k", i, self.kv_full)
+                self.copy("v", i, self.kv_full)
+            for _ in range(steps):
+                slot, turn = t % len(full), t // len(full)
+                if turn > 0:
+                    yield lambda: empty[slot].over(turn - 1)
+                self.copy((name, slot), t, full[slot])
+                t += 1
+
+    def issue(self):
+        def product(check, **to):
+            def run():
+                assert check()
+                vars(self).update(to)
+            self.pipe.append(run)
+
+        def full(bars, t):
+            return bars[t % len(bars)].over(t // len(bars))
+
+        def has(i, t, name):
+            n = len(self.q_full if name == "q" else self.do_full)
+            return self.loaded["k"] == i and self.loaded["v"] == i and self.loaded[name, t % n] == t
+
+        def scores(i, t):
+            product(lambda: has(i, t, "q") and self.s in (None, ("used",)), s=("S", t))
+            self.commit(self.s_full)
+
+        def dp(i, t):
+            product(lambda: has(i, t, "do") and self.dp in (None, ("used",)), dp=("S", t))
+            self.commit(self.dp_full)
+
+        t = 0
+        for i, steps in enumerate(self.items):
+            yield lambda: self.kv_full.over(i) and full(self.q_full, t) and full(self.do_full, t)
+            scores(i, t)
+            dp(i, t)
+            if steps == 1:
+                self.commit(self.kv_empty)
+            for n in range(steps):
+                more = n + 1 < steps
+                yield lambda: (self.p_ready.over(t) and (not more or full(self.q_full, t + 1))
+                               and (n > 0 or i == 0 or self.acc_free.over(i - 1)))
+                product(lambda t=t, n=n: self.s == ("P", t) and self.loaded["do", t % len(self.do_full)] == t
+                        and (self.acc is None if n == 0 else self.acc == t - 1), s=("used",))
+                self.commit(self.do_empty[t % len(self.do_empty)])
+                if more:
+                    scores(i, t + 1)
+                yield lambda: self.ds_ready.over(t) and (not more or full(self.do_full, t + 1))
+                product(lambda t=t: self.dp == ("P", t) and self.loaded["q", t % len(self.q_full)] == t, dp=("used",), acc=t)
+                self.commit(self.q_empty[t % len(self.q_empty)])
+                if more:
+                    dp(i, t + 1)
+                    if n + 2 == steps:
+                        self.commit(self.kv_empty)
+                else:
+                    self.commit(self.done)
+                t += 1
+
+    def write(self, name, t):
+        """A warp's probabilities over its scores."""
+        self.wrote[name, t] = self.wrote.get((name, t), 0) + 1
+        if self.wrote[name, t] == self.warps:
+            setattr(self, name, ("P", t))
+
+    def math(self):
+        t = 0
+        for i, steps in enumerate(self.items):
+            for _ in range(steps):
+                slot, turn = t % len(self.do_full), t // len(self.do_full)
+                yield lambda: self.do_full[slot].over(turn) and self.s_full.over(t)
+                if t % 3 == 0:
+                    yield lambda: self.dp_full.over(t)
+                    assert self.loaded["do", slot] == t and self.loaded["q", t % len(self.q_full)] == t
+                assert self.s == ("S", t)
+                yield lambda: True
+                self.write("s", t)
+                self.p_ready.arrive()
+                yield lambda: self.dp_full.over(t)
+                assert self.dp == ("S", t) and self.loaded["do", slot] == t  # lse and delta are in the slot
+                yield lambda: True
+                self.write("dp", t)
+                self.ds_ready.arrive()
+                self.do_empty[slot].arrive()
+                t += 1
+            yield lambda: self.done.over(i)
+            assert self.acc == t - 1
+            yield lambda: True
+            self.out += 1
+            if self.out == self.warps * (i + 1):
+                self.acc = None
+            self.acc_free.arrive()
+
+
+class Queries(Backward):
+    """dq. items: key tiles of each. ahead: scores are read a tile ahead (heads of 128)."""
+
+    def __init__(self, items, ahead, warps=3):
+        super().__init__(items, warps)
+        self.ahead = ahead
+        slots = (3, 2) if ahead else (5, 4)
+        self.k_full, self.k_empty = ([Barrier(1) for _ in range(slots[0])] for _ in range(2))
+        self.v_full, self.v_empty = ([Barrier(1) for _ in range(slots[1])] for _ in range(2))
+        self.q_full, self.q_empty, self.s_read = Barrier(2), Barrier(1), Barrier(warps)
+        self.dp_full, self.ds_ready = [Barrier(1) for _ in range(2)], [Barrier(warps) for _ in range(2)]
+        self.s, self.dp = None, [None, None]
+        self.seen, self.wrote = {}, {}
+
+    def roles(self):
+        yield "load q", self.load(self.k_full, self.k_empty, "k", True)
+        yield "load v", self.load(self.v_full, self.v_empty, "v", False)
+        yield "issue", self.issue()
+        for w in range(self.warps):
+            yield f"math {w}", self.math()
+
+    def load(self, full, empty, name, first):
+        t = 0
+        for i, tiles in enumerate(self.items):
+            if first:
+                if i > 0:
+                    yield lambda: self.q_empty.over(i - 1)
+                self.copy("q", i, self.q_full)
+                self.copy("do", i, self.q_full)
+            for _ in range(tiles):
+                slot, turn = t % len(full), t // len(full)
+                if turn > 0:
+                    yield lambda: empty[slot].over(turn - 1)
+                self.copy((name, slot), t, full[slot])
+                t += 1
+
+    def issue(self):
+        def full(bars, t):
+            return bars[t % len(bars)].over(t // len(bars))
+
+        def scores(i, t, last):
+            def s():
+                assert self.loaded["q"] == i and self.loaded["k", t % len(self.k_full)] == t
+                assert self.s is None, "scores over others"
+                self.s = t
+
+            def dp():
+                assert self.loaded["do"] == i and self.loaded["v", t % len(self.v_full)] == t
+                assert self.dp[t & 1] is None
+                self.dp[t & 1] = ("S", t)
+            self.pipe.append(s)
+            self.commit(self.s_full)
+            self.pipe.append(dp)
+            self.commit(self.dp_full[t & 1])
+            self.commit(self.v_empty[t % len(self.v_empty)])
+            if last:
+                self.commit(self.q_empty)
+
+        def keys(t):
+            return full(self.k_full, t) and full(self.v_full, t)
+
+        def dq(t, j):
+            def run():
+                assert self.dp[t & 1] == ("P", t) and self.loaded["k", t % len(self.k_full)] == t
+                assert self.acc is None if j == 0 else self.acc == t - 1
+                self.dp[t & 1], self.acc = None, t
+            self.pipe.append(run)
+
+        t = 0
+        for i, tiles in enumerate(self.items):
+            m = tiles - 1
+            yield lambda: self.q_full.over(i) and keys(t)
+            scores(i, t, m == 0)
+            if self.ahead and m > 0:
+                yield lambda: self.s_read.over(i) and keys(t + 1)
+                scores(i, t + 1, m == 1)
+            for j in range(tiles):
+                if not self.ahead and j < m:
+                    yield lambda: self.s_read.over(t) and keys(t + 1)
+                    scores(i, t + 1, j + 1 == m)
+                more = self.ahead and j + 2 <= m
+                yield lambda: self.ds_ready[t & 1].over(t >> 1) and (not more or keys(t + 2))
+                if j == 0 and i > 0:
+                    yield lambda: self.acc_free.over(i - 1)
+                dq(t, j)
+                self.commit(self.k_empty[t % len(self.k_empty)])
+                if j == m:
+                    self.commit(self.done)
+                if more:
+                    scores(i, t + 2, j + 2 == m)
+                t += 1
+
+    def math(self):
+        def read(t):
+            assert self.s == t
+            self.seen[t] = self.seen.get(t, 0) + 1
+            if self.seen[t] == self.warps:
+                self.s = None
+
+        t = 0
+        for i, tiles in enumerate(self.items):
+            m = tiles - 1
+            if self.ahead:
+                yield lambda: self.s_full.over(t)
+                read(t)
+                self.s_read.arrive()
+            for j in range(tiles):
+                if not self.ahead:
+                    yield lambda: self.s_full.over(t)
+                    read(t)
+                    self.s_read.arrive()
+                yield lambda: self.dp_full[t & 1].over(t >> 1)
+                assert self.dp[t & 1] == ("S", t)
+                yield lambda: True
+                self.wrote[t] = self.wrote.get(t, 0) + 1
+                if self.wrote[t] == self.warps:
+                    self.dp[t & 1] = ("P", t)
+                if self.ahead and j < m:
+                    yield lambda: self.s_full.over(t + 1)
+                    read(t + 1)
+                self.ds_ready[t & 1].arrive()
+                t += 1
+            yield lambda: self.done.over(i)
+            assert self.acc == t - 1
+            yield lambda: True
+            self.out += 1
+            if self.out == self.warps * (i + 1):
+                self.acc = None
+            self.acc_free.arrive()
+
+
+@pytest.mark.parametrize("make", [lambda n: KeysAndValues(n), lambda n: KeysAndValues(n, (5, 4)), lambda n: Queries(n, True),
+                                  lambda n: Queries(n, False)], ids=["dk dv 128", "dk dv 64", "dq 128", "dq 64"])
+def test_no_order_of_events_stops_the_backward(make):
+    for items in itertools.product((1, 2, 3, 4, 7), repeat=3):
+        for choose in orders(8):
+            make(items).run(choose)
+    rng = random.Random(1)
+    for seed in range(60):
+        make([rng.randrange(1, 9) for _ in range(8)]).run(at_random(seed))
+
+
+def test_the_model_finds_a_buffer_that_is_written_too_early():
+    """Without the wait for the warps that read the last scores."""
+    class Early(Queries):
+        def issue(self):
+            self.s_read.over = lambda phase: True
+            return super().issue()
+    with pytest.raises((AssertionError, Stopped)):
+        Early((3, 3), False).run(last("math 0"))
