@@ -84,3 +84,56 @@ g = torch.autograd.grad(attention(q, k, v, cu), (q, k, v), d_o)
 assert all(t.isfinite().all() for t in g)
 """
     subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
+
+
+@pytest.mark.parametrize("warm", [True, False])
+def test_autograd_captured_into_a_graph(warm):
+    """Forward and gradient through the autograd functions in a captured graph; warm False: autograd's thread has
+    done nothing before the capture."""
+    import subprocess
+    import sys
+    code = f"""
+import torch
+from recompute_kda_chunkwise_gb300 import attention as A, kda as K, rotary as T
+S, H, D = 300, 4, 64
+q, k, v = (torch.randn(S, h, D, device="cuda").bfloat16().requires_grad_() for h in (H, 2, 2))
+d_o = torch.randn(S, H, D, device="cuda").bfloat16()
+cu = torch.tensor([0, 130, S], dtype=torch.int32, device="cuda")
+status = torch.zeros(1, dtype=torch.int32, device="cuda")
+rope = T.Rotary(D)
+
+def step():
+    x, y = T.rotary(rope, q, k, cu_seqlens=cu, status=status)
+    o = A.attention(x, y, v, cu, status=status)
+    return (o, *torch.autograd.grad(o, (q, k, v), d_o))
+
+def plain():
+    x, y = T.rotary_fwd(rope, q, k, cu_seqlens=cu)
+    o, lse = A.attention_fwd(x, y, v, cu)
+    dx, dy, dv = A.attention_bwd(x, y, v, o, lse, d_o, cu)
+    return (o, *T.rotary_bwd(rope, dx, dy, cu_seqlens=cu), dv)
+
+want = [t.detach().clone() for t in plain()]
+s = torch.cuda.Stream()
+s.wait_stream(torch.cuda.current_stream())
+with torch.cuda.stream(s):
+    if {warm}:
+        step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = step()
+    for t in got:
+        t.detach().zero_()
+    graph.replay()
+    graph.replay()
+s.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+with torch.no_grad():
+    cu[2] = S - 1  # refused at the replay
+with torch.cuda.stream(s):
+    graph.replay()
+s.synchronize()
+assert K.query_device_status(status) == 6 and all(t.isnan().all() for t in (got[0], got[3]))
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
